@@ -201,9 +201,8 @@ def prepare(case, seed):
             t[a // BLOCK:a // BLOCK + -(-n // BLOCK)] for a, n in zip(s["starts"], s["sizes"])]
         if own:
             import dense_fp32_sgemm_gb300 as sg
-            s["grads"] = cut(s["g"])
-            s["opt"] = sg.AdamW(cut(s["p"]), cut(s["m"]), cut(s["v"]), m_scales=cut_scales(s["ms"]),
-                                v_scales=cut_scales(s["vs"]), lr=ADAMW["lr"],
+            s["opt"] = sg.AdamW(cut(s["p"]), cut(s["g"]), cut(s["m"]), cut(s["v"]),
+                                m_scales=cut_scales(s["ms"]), v_scales=cut_scales(s["vs"]), lr=ADAMW["lr"],
                                 betas=(ADAMW["beta1"], ADAMW["beta2"]), eps=ADAMW["eps"],
                                 weight_decay=ADAMW["weight_decay"])
     else:
@@ -337,7 +336,7 @@ def run(s):
     if case["op"] == "adamw":
         if not own:
             return _adamw_plain(s)
-        s["opt"].step(s["grads"], step=ADAMW["step"])
+        s["opt"].step(step=ADAMW["step"])
         return _adamw_outputs(s)
     return _ffn_own(s, case) if own else _ffn_plain(s, case)
 
