@@ -25,6 +25,8 @@ __all__ = [
     "VARIANT_AUTO", "VARIANT_GENERIC", "VARIANT_TILE", "VARIANT_STREAMK",
     "VARIANT_SKINNY", "VARIANT_MID", "VARIANT_MID64", "VARIANT_KSPLIT", "VARIANT_NARROW", "VARIANT_KSPLIT64", "VARIANT_SMALL",
     "STATUS",
+    "ffn_forward", "ffn_saved", "ffn_backward", "W4Matrix", "w4_quantize", "AdamW",
+    "GATE_SILU", "GATE_GELU", "GATE_RELU", "TYPE_F32", "TYPE_F16", "TYPE_BF16",
 ]
 
 STATUS = {
@@ -36,8 +38,11 @@ VARIANT_AUTO, VARIANT_GENERIC, VARIANT_TILE, VARIANT_STREAMK, VARIANT_SKINNY = -
 VARIANT_MID, VARIANT_MID64, VARIANT_KSPLIT, VARIANT_NARROW, VARIANT_KSPLIT64 = 4, 5, 6, 7, 8
 VARIANT_SMALL = 9
 ACT_NONE, ACT_RELU = 0, 1
+TYPE_F32, TYPE_F16, TYPE_BF16 = 0, 1, 2
+GATE_SILU, GATE_GELU, GATE_RELU = 0, 1, 2
 
 _i64, _f32, _vp, _int = ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_int
+_f64 = ctypes.c_double
 
 # name -> (restype, argtypes); one entry per function declared in include/*.h
 _SIGNATURES = {
@@ -67,6 +72,18 @@ _SIGNATURES = {
     "sgemm_probe_read": (_int, [_vp, _i64, _vp, _int, _vp]),
     "sgemm_probe_hold": (_int, [_i64, _vp]),
     "sgemm_probe_tf32": (_int, [_i64, _int, _vp]),
+    "sgemm_ffn_forward": (_int, [_i64, _i64, _i64, _int, _int, _vp, _i64, _vp, _i64, _vp, _i64,
+                                 _vp, _i64, _vp, _i64, _vp, _vp]),
+    "sgemm_ffn_saved_floats": (_i64, [_i64, _i64]),
+    "sgemm_ffn_backward": (_int, [_i64, _i64, _i64, _int, _int, _vp, _i64, _vp, _i64, _vp, _i64,
+                                  _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                  _i64, _vp]),
+    "sgemm_w4_matvec": (_int, [_i64, _i64, _i64, _i64, _int, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                               _i64, _vp, _i64, _vp]),
+    "sgemm_w4_quantize": (_int, [_i64, _i64, _i64, _int, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                 _i64, _vp]),
+    "sgemm_adamw_step": (_int, [_vp, _i64, _int, _int, _int, _int, _f64, _f64, _f64, _f64, _f64,
+                                _i64, _f64, _vp]),
 }
 EXPORTED_SYMBOLS = tuple(_SIGNATURES)
 
@@ -362,3 +379,7 @@ def probe_hold(ns: int, stream=None) -> None:
     """Queue a kernel that keeps `stream` busy for `ns` nanoseconds."""
     s = stream.cuda_stream if stream is not None else None
     _check(library().sgemm_probe_hold(int(ns), s), "sgemm_probe_hold")
+
+
+from .ffn import (AdamW, W4Matrix, ffn_backward, ffn_forward, ffn_saved,  # noqa: E402
+                  w4_quantize)

@@ -21,9 +21,11 @@ LIB_NAME = "libsgemm_gb300.so"
 LIB_PATH = os.path.join(BUILD, LIB_NAME)
 
 SOURCES = ["api.cu", "plan.cpp", "kernel_tile.cu", "kernel_skinny.cu", "kernel_generic.cu", "kernel_mid.cu",
-           "kernel_ksplit.cu", "kernel_narrow.cu", "kernel_small.cu", "probes.cu", "noalloc.cu", "kernel_3xtf32.cu"]
-HEADERS = ["device_common.cuh", "kernels.h", "kernels_3xtf32.h", "plan.h"]
-PUBLIC_HEADERS = ["sgemm.h", "sgemm_probe.h"]
+           "kernel_ksplit.cu", "kernel_narrow.cu", "kernel_small.cu", "probes.cu", "noalloc.cu", "kernel_3xtf32.cu",
+           "api_ffn.cu", "kernel_ffn.cu", "kernel_w4.cu", "kernel_adamw.cu"]
+HEADERS = ["device_common.cuh", "kernels.h", "kernels_3xtf32.h", "plan.h",
+           "kernels_ffn.h", "ops_internal.h", "ops_common.cuh"]
+PUBLIC_HEADERS = ["sgemm.h", "sgemm_probe.h", "sgemm_ffn.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

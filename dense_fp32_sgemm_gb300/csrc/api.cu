@@ -16,6 +16,7 @@
 #include "../../include/sgemm_probe.h"
 #include "kernels.h"
 #include "kernels_3xtf32.h"
+#include "ops_internal.h"
 #include "plan.h"
 
 namespace sgemm {
@@ -49,6 +50,8 @@ struct Workspace {
     size_t pack_bytes = 0;
     float *split = nullptr;  // 3xTF32 hi / lo operand copies
     size_t split_bytes = 0;
+    void *ops = nullptr;  // intermediates of the feed-forward operators
+    size_t ops_bytes = 0;
 };
 
 struct HostBuffers {
@@ -539,6 +542,63 @@ void wait_hooks(unsigned long long *timeout_ns, int *skip_loads_from) {
     *skip_loads_from = g_skip_loads_from.load();
 }
 
+std::mutex &api_mutex() { return g_mu; }
+
+sgemm_status_t op_device(OpDevice *out) {
+    DeviceState *d = nullptr;
+    const sgemm_status_t s = device_state(&d);
+    if (s != SGEMM_OK) return s;
+    if (cudaGetDevice(&out->index) != cudaSuccess) return SGEMM_ERR_NO_DEVICE;
+    out->num_sms = d->num_sms;
+    out->err = d->err;
+    wait_hooks(&out->timeout_ns, &out->skip_loads_from);
+    return SGEMM_OK;
+}
+
+sgemm_status_t op_workspace(cudaStream_t stream, size_t bytes, void **out) {
+    DeviceState *d = nullptr;
+    const sgemm_status_t s = device_state(&d);
+    if (s != SGEMM_OK) return s;
+    Workspace &w = d->ws[stream];
+    if (w.ops_bytes < bytes) {
+        if (w.ops) cudaFree(w.ops);
+        w.ops = nullptr;
+        w.ops_bytes = 0;
+        if (cudaMalloc(&w.ops, bytes) != cudaSuccess) {
+            cudaGetLastError();
+            return SGEMM_ERR_ALLOC;
+        }
+        w.ops_bytes = bytes;
+    }
+    *out = w.ops;
+    return SGEMM_OK;
+}
+
+sgemm_status_t op_counters(cudaStream_t stream, size_t count, int **out) {
+    DeviceState *d = nullptr;
+    sgemm_status_t s = device_state(&d);
+    if (s != SGEMM_OK) return s;
+    Workspace *w = nullptr;
+    s = ensure_workspace(*d, stream, 0, count, &w);
+    if (s == SGEMM_OK) *out = w->counters;
+    return s;
+}
+
+sgemm_status_t op_encode_2d(CUtensorMap *map, CUtensorMapDataType type, int elem, const void *base,
+                            int64_t rows, int64_t cols, int64_t ld, int box_cols, int box_rows,
+                            CUtensorMapSwizzle swizzle) {
+    if (!g_encode) return SGEMM_ERR_TMA;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * elem};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = g_encode(map, type, 2, const_cast<void *>(base), dims, strides, box, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SGEMM_OK : SGEMM_ERR_TMA;
+}
+
 }  // namespace sgemm
 
 using namespace sgemm;
@@ -940,6 +1000,7 @@ sgemm_status_t sgemm_release_workspace(void) {
             if (w.second.counters) cudaFree(w.second.counters);
             if (w.second.pack) cudaFree(w.second.pack);
             if (w.second.split) cudaFree(w.second.split);
+            if (w.second.ops) cudaFree(w.second.ops);
         }
         d.ws.clear();
         if (d.side) cudaStreamDestroy(d.side);

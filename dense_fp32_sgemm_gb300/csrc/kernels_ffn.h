@@ -1,0 +1,126 @@
+// Parameter blocks and launch wrappers of the feed-forward operators' kernels
+// (the gated block, products with 4-bit weights, the AdamW step).
+// Host-visible only.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace sgemm {
+
+// Element types and gate activations, as in include/sgemm_ffn.h.
+enum : int { kTypeF32 = 0, kTypeF16 = 1, kTypeBF16 = 2 };
+enum : int { kGateSilu = 0, kGateGelu = 1, kGateRelu = 2 };
+
+inline int type_bytes(int type) { return type == kTypeF32 ? 4 : 2; }
+
+// ---------------------------------------------------------------------------
+// Products with 4-bit weights.
+// ---------------------------------------------------------------------------
+constexpr int kW4Cols = 32;      // columns of W per CTA
+constexpr int kW4Warps = 8;      // warps of a CTA, each on its own part of K
+constexpr int kW4UnitK = 128;    // k per warp step: four 16-byte loads a lane
+constexpr int kW4MaxCluster = 8;
+
+struct W4Params {
+    int M, N, K;
+    int group;
+    const void *x;
+    long long ldx;
+    const uint32_t *q;
+    long long ldq;
+    const void *scales;
+    long long lds;
+    const uint8_t *zeros;  // nullptr: every zero point is 8
+    long long ldz;
+    void *y;
+    long long ldy;
+    int x_vec;         // 8 elements of x may be loaded at once
+    int units;         // ceil(K / kW4UnitK)
+    int cta_units;     // units of one CTA
+    int chunk_units;   // units whose x is staged at once
+};
+
+// vec: four columns of q, scales and zeros may be loaded at once.
+cudaError_t launch_w4(const W4Params &p, int type, bool vec, int cluster, cudaStream_t stream);
+// Rows of x one launch takes (FP32 rows take three of the instruction's each).
+int w4_max_rows(int type);
+// Bytes of shared memory a unit of staged x takes, and the limit for all of them.
+int w4_unit_bytes(int type, int M);
+constexpr int kW4StageBytes = 64 * 1024;
+
+struct W4QuantParams {
+    int N, K, group, type;
+    const void *W;
+    long long ldw;
+    uint32_t *q;
+    long long ldq;
+    void *scales;
+    long long lds;
+    uint8_t *zeros;
+    long long ldz;
+};
+cudaError_t launch_w4_quantize(const W4QuantParams &p, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// AdamW.
+// ---------------------------------------------------------------------------
+constexpr int kAdamBlock = 256;   // elements that share a scale of the 8-bit states
+constexpr int kAdamChunk = 4096;  // elements of one tensor a CTA takes
+constexpr int kAdamTensors = 400; // tensors of one launch
+
+struct AdamTensor {
+    void *p;
+    const void *g;
+    void *m, *v;
+    float *ms, *vs;
+    void *copy;
+    unsigned chunk0;  // first chunk of this tensor in the launch
+    unsigned vec;     // every array allows its widest loads
+    long long numel;
+};
+
+struct AdamHyper {
+    float beta1, omb1, beta2, omb2;  // omb: one minus beta
+    float decay;                     // 1 - lr * weight_decay
+    float step_size;                 // lr / (1 - beta1^step)
+    float inv_sqrt_bc2;              // 1 / sqrt(1 - beta2^step)
+    float eps;
+    float grad_scale;
+    int p_type, g_type, c_type;
+};
+
+// `tensors` (count <= kAdamTensors) with chunk0 filled in; `chunks` in all.
+cudaError_t launch_adamw(const AdamTensor *tensors, int count, unsigned chunks, int state_bits,
+                         const AdamHyper &h, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// The gated block's products.
+// ---------------------------------------------------------------------------
+// An operand as a strided matrix: element (i, j) at p[i * rs + j * cs].
+struct FfnView {
+    const void *p;
+    int type;
+    long long rs, cs;
+};
+
+enum : int {
+    kFfnStore = 0,     // C = A B (+ A2 B2), stored as C.type
+    kFfnGate = 1,      // h = act(A B) * (A B2); g and u kept when asked for
+    kFfnGateGrad = 2,  // dh = A B; dg, du and h from it and the kept g, u
+};
+
+struct FfnProduct {
+    int mode;
+    int M, N, K;
+    int act;
+    FfnView A, B, A2, B2;  // A2, B2: the second product, p null without
+    FfnView C;             // kFfnStore: C; kFfnGate: h; kFfnGateGrad: h
+    FfnView dg, du;        // kFfnGateGrad outputs
+    float *g, *u;          // kept g and u (M x ld), or null
+    long long ldgu;
+};
+cudaError_t launch_ffn_product(const FfnProduct &p, cudaStream_t stream);
+
+}  // namespace sgemm
