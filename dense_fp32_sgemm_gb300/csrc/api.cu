@@ -584,18 +584,19 @@ sgemm_status_t op_counters(cudaStream_t stream, size_t count, int **out) {
     return s;
 }
 
-sgemm_status_t op_encode_2d(CUtensorMap *map, CUtensorMapDataType type, int elem, const void *base,
-                            int64_t rows, int64_t cols, int64_t ld, int box_cols, int box_rows,
-                            CUtensorMapSwizzle swizzle) {
+sgemm_status_t op_encode_16(CUtensorMap *map, bool bf16, const void *base, int64_t rows,
+                            int64_t cols, int64_t ld, int64_t planes, int64_t plane_stride,
+                            int box_rows) {
     if (!g_encode) return SGEMM_ERR_TMA;
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld * elem};
-    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    const CUresult r = g_encode(map, type, 2, const_cast<void *>(base), dims, strides, box, estr,
-                                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)plane_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = g_encode(
+        map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+        const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? SGEMM_OK : SGEMM_ERR_TMA;
 }
 

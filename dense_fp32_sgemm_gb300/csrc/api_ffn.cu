@@ -58,32 +58,149 @@ sgemm_status_t check_ffn(const FfnArgs &a) {
 
 int64_t saved_ld(int64_t F) { return (F + 3) / 4 * 4; }
 
-FfnView view(const void *p, int type, int64_t ld) { return FfnView{p, type, ld, 1}; }
-FfnView transposed(const FfnView &v) { return FfnView{v.p, v.type, v.cs, v.rs}; }
+int64_t pad8(int64_t v) { return (v + 7) / 8 * 8; }
 
-// h (null: not wanted) and g, u (null: not kept) of the block's first half.
-sgemm_status_t run_gate(const FfnArgs &a, float *h, float *gu, cudaStream_t st) {
-    FfnProduct p = {};
-    p.mode = kFfnGate;
-    p.M = (int)a.T; p.N = (int)a.F; p.K = (int)a.D;
-    p.act = a.act;
-    p.A = p.A2 = view(a.x, a.type, a.ldx);
-    p.B = view(a.Wg, a.type, a.ldg);
-    p.B2 = view(a.Wu, a.type, a.ldu);
-    p.C = view(h, kTypeF32, a.F);
-    p.ldgu = saved_ld(a.F);
-    p.g = gu;
-    p.u = gu ? gu + a.T * p.ldgu : nullptr;
-    return status(launch_ffn_product(p, st));
+// Sizes of the pieces of one workspace, then their addresses.
+struct Arena {
+    size_t bytes = 0;
+    char *base = nullptr;
+    size_t take(size_t n) {
+        const size_t at = bytes;
+        bytes += (n + 255) / 256 * 256;
+        return at;
+    }
+    void *at(size_t offset) const { return base + offset; }
+};
+
+// A matrix as an operand of the tensor-core products: where it lies, or the
+// copy that has to be made of it first.
+struct Source {
+    FfnOperand op;
+    size_t offset = 0;  // of the copy in the workspace
+    bool copied = false;
+    const void *user = nullptr;
+    int64_t ld_user = 0;
+};
+
+// The user's rows x cols matrix: read in place where the TMA can (16-bit
+// values in 16-byte aligned rows), else through a copy.
+Source source(Arena &w, const void *p, int type, int64_t rows, int64_t cols, int64_t ld) {
+    Source s;
+    s.user = p;
+    s.ld_user = ld;
+    s.op = FfnOperand{p, rows, cols, ld, rows * ld, 1};
+    if (type == kTypeF32 || !aligned(p, 16) || ld % 8 != 0) {
+        s.copied = true;
+        s.op.ld = pad8(cols);
+        s.op.plane_stride = rows * s.op.ld;
+        s.op.planes = type == kTypeF32 ? 3 : 1;
+        s.offset = w.take((size_t)(s.op.planes * s.op.plane_stride) * 2);
+    }
+    return s;
 }
 
-sgemm_status_t run_product(int64_t M, int64_t N, int64_t K, const FfnView &A, const FfnView &B,
-                           const FfnView &C, cudaStream_t st, FfnView A2 = {}, FfnView B2 = {}) {
-    FfnProduct p = {};
-    p.mode = kFfnStore;
-    p.M = (int)M; p.N = (int)N; p.K = (int)K;
-    p.A = A; p.B = B; p.A2 = A2; p.B2 = B2; p.C = C;
-    return status(launch_ffn_product(p, st));
+// An intermediate matrix in the workspace.
+Source intermediate(Arena &w, int type, int64_t rows, int64_t cols) {
+    Source s;
+    const int planes = type == kTypeF32 ? 3 : 1;
+    s.op = FfnOperand{nullptr, rows, cols, pad8(cols), rows * pad8(cols), planes};
+    s.offset = w.take((size_t)(planes * s.op.plane_stride) * 2);
+    return s;
+}
+
+void place(const Arena &w, Source &s) {
+    if (s.copied || !s.op.p) s.op.p = w.at(s.offset);
+}
+
+sgemm_status_t make_copies(const Source *const *list, int n, int type, const OpDevice &dev,
+                           cudaStream_t st) {
+    FfnPrepJob jobs[kFfnPrepJobs];
+    int count = 0;
+    for (int i = 0; i < n; ++i) {
+        const Source &s = *list[i];
+        if (!s.copied) continue;
+        jobs[count++] = FfnPrepJob{s.user, s.ld_user, (int)s.op.rows, (int)s.op.cols,
+                                   const_cast<void *>(s.op.p), s.op.ld, s.op.plane_stride};
+    }
+    return status(launch_ffn_prep(jobs, count, type, dev.num_sms, st));
+}
+
+// Sets up and launches one product.  A and B (A2 and B2) as they lie in
+// memory; a_mn, b_mn: their rows run along k.
+struct Product {
+    const OpDevice &dev;
+    cudaStream_t st;
+    FfnGemmParams p = {};
+    FfnMaps maps;
+
+    Product(const OpDevice &d, cudaStream_t s, int mode, int type, int64_t M, int64_t N, int64_t K,
+            bool a_mn, bool b_mn)
+        : dev(d), st(s) {
+        p.mode = mode;
+        p.type = type;
+        p.M = (int)M; p.N = (int)N; p.K = (int)K;
+        p.segs = p.outs = 1;
+        p.a_mn = a_mn; p.b_mn = b_mn;
+        p.kblocks = (int)((K + kFfnBK - 1) / kFfnBK);
+        p.err = dev.err;
+        p.timeout_ns = dev.timeout_ns;
+        p.skip_loads_from = dev.skip_loads_from;
+    }
+
+    sgemm_status_t map(CUtensorMap *m, const FfnOperand &o, bool mn) {
+        return op_encode_16(m, p.type != kTypeF16, o.p, o.rows, o.cols, o.ld, o.planes,
+                            o.plane_stride, mn ? kFfnBK : kFfnBM);
+    }
+
+    sgemm_status_t run(const FfnOperand &A, const FfnOperand &B, const FfnOperand *A2 = nullptr,
+                       const FfnOperand *B2 = nullptr) {
+        const bool pair = p.type != kTypeF32 && p.M > kFfnBM;
+        const int cg = pair ? 2 : 1;
+        const int tile_n = (p.mode == kFfnGate ? kFfnBN / 2 : kFfnBN) * cg;
+        p.tiles_m = (p.M + kFfnBM * cg - 1) / (kFfnBM * cg);
+        p.tiles_n = (p.N + tile_n - 1) / tile_n;
+        const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * p.outs;
+        if (tiles > INT32_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
+        p.tiles = (int)tiles;
+        sgemm_status_t s = map(&maps.a[0], A, p.a_mn);
+        if (s == SGEMM_OK) s = map(&maps.a[1], A2 ? *A2 : A, p.a_mn);
+        if (s == SGEMM_OK) s = map(&maps.b[0], B, p.b_mn);
+        if (s == SGEMM_OK) s = map(&maps.b[1], B2 ? *B2 : B, p.b_mn);
+        if (s != SGEMM_OK) return s;
+        return status(launch_ffn_gemm(maps, p, pair, dev.num_sms, st));
+    }
+
+    void store(void *C, int64_t ld, void *C2 = nullptr, int64_t ld2 = 0) {
+        const int e = type_bytes(p.type);
+        p.C[0] = C; p.ldc[0] = ld;
+        p.C[1] = C2; p.ldc[1] = ld2;
+        p.c_vec = aligned(C, 16) && ld * e % 16 == 0 && (!C2 || (aligned(C2, 16) && ld2 * e % 16 == 0));
+    }
+    void store_planes(const FfnOperand &o) {
+        p.C[0] = const_cast<void *>(o.p);
+        p.ldc[0] = p.ldc[1] = o.ld;
+        p.c_plane = o.plane_stride;
+        p.c_vec = 1;
+    }
+};
+
+// The block's first half: h (when wanted) and g, u (when kept).
+sgemm_status_t run_gate(const OpDevice &dev, cudaStream_t st, const FfnArgs &a, const FfnOperand &x,
+                        const FfnOperand &Wg, const FfnOperand &Wu, const FfnOperand *h, float *gu) {
+    Product g(dev, st, kFfnGate, a.type, a.T, a.F, a.D, false, true);
+    g.p.act = a.act;
+    if (h) g.store_planes(*h);
+    g.p.ldgu = saved_ld(a.F);
+    g.p.g = gu;
+    g.p.u = gu ? gu + a.T * g.p.ldgu : nullptr;
+    return g.run(x, Wg, &x, &Wu);
+}
+
+sgemm_status_t zero_matrix(void *p, int64_t ld, int64_t rows, int64_t cols, int type,
+                           cudaStream_t st) {
+    const size_t e = type_bytes(type);
+    if (!p || rows == 0 || cols == 0) return SGEMM_OK;
+    return status(cudaMemset2DAsync(p, ld * e, 0, cols * e, rows, st));
 }
 
 }  // namespace
@@ -113,13 +230,23 @@ sgemm_status_t sgemm_ffn_forward(int64_t T, int64_t D, int64_t F, int type, int 
     OpDevice dev;
     s = op_device(&dev);
     if (s != SGEMM_OK) return s;
-    void *w = nullptr;
-    s = op_workspace(st, std::max<size_t>((size_t)(T * F) * 4, 16), &w);
+    if (F == 0) return zero_matrix(y, ldy, T, D, type, st);
+    Arena w;
+    Source vx = source(w, x, type, T, D, ldx), vg = source(w, Wg, type, D, F, ldg),
+           vu = source(w, Wu, type, D, F, ldu), vd = source(w, Wd, type, F, D, ldd),
+           h = intermediate(w, type, T, F);
+    void *base = nullptr;
+    s = op_workspace(st, w.bytes, &base);
     if (s != SGEMM_OK) return s;
-    float *h = static_cast<float *>(w);
-    s = run_gate(a, h, saved, st);
+    w.base = static_cast<char *>(base);
+    for (Source *v : {&vx, &vg, &vu, &vd, &h}) place(w, *v);
+    const Source *const inputs[] = {&vx, &vg, &vu, &vd};
+    s = make_copies(inputs, 4, type, dev, st);
+    if (s == SGEMM_OK) s = run_gate(dev, st, a, vx.op, vg.op, vu.op, &h.op, saved);
     if (s != SGEMM_OK) return s;
-    return run_product(T, D, F, view(h, kTypeF32, F), view(Wd, type, ldd), view(y, type, ldy), st);
+    Product down(dev, st, kFfnStore, type, T, D, F, false, true);
+    down.store(y, ldy);
+    return down.run(h.op, vd.op);
 }
 
 sgemm_status_t sgemm_ffn_backward(int64_t T, int64_t D, int64_t F, int type, int activation,
@@ -144,37 +271,56 @@ sgemm_status_t sgemm_ffn_backward(int64_t T, int64_t D, int64_t F, int type, int
     OpDevice dev;
     s = op_device(&dev);
     if (s != SGEMM_OK) return s;
-    const size_t tf = (size_t)(T * F), gu_floats = saved ? 0 : (size_t)(2 * T * saved_ld(F));
-    void *w = nullptr;
-    s = op_workspace(st, std::max<size_t>((3 * tf + gu_floats) * 4, 16), &w);
-    if (s != SGEMM_OK) return s;
-    float *gu = static_cast<float *>(w);
-    float *dg = gu + gu_floats, *du = dg + tf, *h = du + tf;
-    if (!saved) {
-        s = run_gate(a, nullptr, gu, st);
-        if (s != SGEMM_OK) return s;
+    if (T == 0 || F == 0) {
+        s = zero_matrix(dx, lddx, T, D, type, st);
+        if (s == SGEMM_OK && weights) s = zero_matrix(dWg, lddg, D, F, type, st);
+        if (s == SGEMM_OK && weights) s = zero_matrix(dWu, lddu, D, F, type, st);
+        if (s == SGEMM_OK && weights) s = zero_matrix(dWd, lddd, F, D, type, st);
+        return s;
     }
-    const float *kept = saved ? saved : gu;
-    const FfnView vx = view(x, type, ldx), vdy = view(dy, type, lddy);
-    const FfnView vdg = view(dg, kTypeF32, F), vdu = view(du, kTypeF32, F), vh = view(h, kTypeF32, F);
-    FfnProduct p = {};
-    p.mode = kFfnGateGrad;
-    p.M = (int)T; p.N = (int)F; p.K = (int)D;
-    p.act = activation;
-    p.A = vdy;
-    p.B = transposed(view(Wd, type, ldd));
-    p.C = vh; p.dg = vdg; p.du = vdu;
-    p.ldgu = saved_ld(F);
-    p.g = const_cast<float *>(kept);
-    p.u = p.g + T * p.ldgu;
-    s = status(launch_ffn_product(p, st));
-    if (s == SGEMM_OK && dx)
-        s = run_product(T, D, F, vdg, transposed(view(Wg, type, ldg)), view(dx, type, lddx), st, vdu,
-                        transposed(view(Wu, type, ldu)));
-    if (!weights) return s;
-    if (s == SGEMM_OK) s = run_product(D, F, T, transposed(vx), vdg, view(dWg, type, lddg), st);
-    if (s == SGEMM_OK) s = run_product(D, F, T, transposed(vx), vdu, view(dWu, type, lddu), st);
-    if (s == SGEMM_OK) s = run_product(F, D, T, transposed(vh), vdy, view(dWd, type, lddd), st);
+    Arena w;
+    Source vx = source(w, x, type, T, D, ldx), vg = source(w, Wg, type, D, F, ldg),
+           vu = source(w, Wu, type, D, F, ldu), vd = source(w, Wd, type, F, D, ldd),
+           vdy = source(w, dy, type, T, D, lddy), dg = intermediate(w, type, T, F),
+           du = intermediate(w, type, T, F), h = intermediate(w, type, T, F);
+    const size_t kept_at = saved ? 0 : w.take((size_t)sgemm_ffn_saved_floats(T, F) * 4);
+    void *base = nullptr;
+    s = op_workspace(st, w.bytes, &base);
+    if (s != SGEMM_OK) return s;
+    w.base = static_cast<char *>(base);
+    for (Source *v : {&vx, &vg, &vu, &vd, &vdy, &dg, &du, &h}) place(w, *v);
+    const Source *const inputs[] = {&vx, &vg, &vu, &vd, &vdy};
+    s = make_copies(inputs, 5, type, dev, st);
+    float *kept = saved ? const_cast<float *>(saved) : static_cast<float *>(w.at(kept_at));
+    if (s == SGEMM_OK && !saved) s = run_gate(dev, st, a, vx.op, vg.op, vu.op, nullptr, kept);
+    if (s != SGEMM_OK) return s;
+
+    Product grad(dev, st, kFfnGateGrad, type, T, F, D, false, false);
+    grad.p.act = activation;
+    grad.store_planes(h.op);
+    grad.p.C[1] = const_cast<void *>(dg.op.p);
+    grad.p.C[2] = const_cast<void *>(du.op.p);
+    grad.p.ldgu = saved_ld(F);
+    grad.p.g = kept;
+    grad.p.u = kept + T * grad.p.ldgu;
+    s = grad.run(vdy.op, vd.op);
+    if (s == SGEMM_OK && dx) {
+        Product p(dev, st, kFfnStore, type, T, D, F, false, false);
+        p.p.segs = 2;
+        p.store(dx, lddx);
+        s = p.run(dg.op, vg.op, &du.op, &vu.op);
+    }
+    if (s == SGEMM_OK && weights) {
+        Product p(dev, st, kFfnStore, type, D, F, T, true, true);
+        p.p.outs = 2;
+        p.store(dWg, lddg, dWu, lddu);
+        s = p.run(vx.op, dg.op, nullptr, &du.op);
+    }
+    if (s == SGEMM_OK && weights) {
+        Product p(dev, st, kFfnStore, type, F, D, T, true, true);
+        p.store(dWd, lddd);
+        s = p.run(h.op, vdy.op);
+    }
     return s;
 }
 

@@ -96,31 +96,74 @@ cudaError_t launch_adamw(const AdamTensor *tensors, int count, unsigned chunks, 
                          const AdamHyper &h, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
-// The gated block's products.
+// The gated block's products on the tensor cores (kernel_ffn.cu).
 // ---------------------------------------------------------------------------
-// An operand as a strided matrix: element (i, j) at p[i * rs + j * cs].
-struct FfnView {
+// An operand in memory: `planes` matrices of rows x cols 16-bit values, rows
+// ld elements apart (16-byte aligned), planes plane_rows rows apart.  16-bit
+// types have one plane; FP32 values are held as three bf16 planes that add up
+// to them.
+struct FfnOperand {
     const void *p;
-    int type;
-    long long rs, cs;
+    int64_t rows, cols, ld, plane_stride;  // plane_stride in elements
+    int planes;
 };
 
 enum : int {
-    kFfnStore = 0,     // C = A B (+ A2 B2), stored as C.type
+    kFfnStore = 0,     // C = A B, or A B + A2 B2, or two outputs A B and A B2
     kFfnGate = 1,      // h = act(A B) * (A B2); g and u kept when asked for
     kFfnGateGrad = 2,  // dh = A B; dg, du and h from it and the kept g, u
 };
 
-struct FfnProduct {
+constexpr int kFfnBM = 128;      // rows of a CTA's tile
+constexpr int kFfnBN = 128;      // columns of B each CTA brings in per k block
+constexpr int kFfnBK = 64;       // k per stage: one 128-byte swizzled row
+constexpr int kFfnStages = 6;
+constexpr int kFfnThreads = 384; // 4 warps of roles, 8 of epilogue
+
+struct FfnGemmParams {
     int mode;
+    int type;            // of the user's matrices
     int M, N, K;
     int act;
-    FfnView A, B, A2, B2;  // A2, B2: the second product, p null without
-    FfnView C;             // kFfnStore: C; kFfnGate: h; kFfnGateGrad: h
-    FfnView dg, du;        // kFfnGateGrad outputs
-    float *g, *u;          // kept g and u (M x ld), or null
+    int segs;            // products added up (2: A B + A2 B2)
+    int outs;            // outputs (2: A B -> C[0], A B2 -> C[1])
+    int a_mn, b_mn;      // operand is MN-major: its rows run along k
+    int tiles_m, tiles_n, tiles;
+    int kblocks;         // ceil(K / kFfnBK)
+    // kFfnStore: C, `type`.  kFfnGate: C[0] = h or null.  kFfnGateGrad: C[0] =
+    // h, C[1] = dg, C[2] = du.  h, dg and du are 16-bit operands for the next
+    // product: one plane of `type`, or three bf16 planes.
+    void *C[3];
+    long long ldc[2];    // kFfnStore: of each output; else ldc[0] of all
+    long long c_plane;
+    int c_vec;           // 16-byte stores allowed
+    float *g, *u;        // kept values, M x ldgu (a multiple of 4), or null
     long long ldgu;
+    int *err;
+    unsigned long long timeout_ns;
+    int skip_loads_from;
 };
-cudaError_t launch_ffn_product(const FfnProduct &p, cudaStream_t stream);
+
+// One operand's TMA descriptor as the kernel wants it: boxes of 64 along the
+// contiguous dimension by `rows` rows.
+struct FfnMaps {
+    CUtensorMap a[2], b[2];
+};
+// pair: 256-row tiles by pairs of CTAs.
+cudaError_t launch_ffn_gemm(const FfnMaps &maps, const FfnGemmParams &p, bool pair, int num_sms,
+                            cudaStream_t stream);
+
+// Copies that make operands of the user's matrices: FP32 split into three
+// bf16 planes, or 16-bit values moved to aligned rows.
+struct FfnPrepJob {
+    const void *src;
+    int64_t ld_src;
+    int rows, cols;
+    void *dst;
+    int64_t ld_dst, plane_stride;
+};
+constexpr int kFfnPrepJobs = 5;
+cudaError_t launch_ffn_prep(const FfnPrepJob *jobs, int count, int type, int num_sms,
+                            cudaStream_t stream);
 
 }  // namespace sgemm

@@ -35,10 +35,11 @@ sgemm_status_t op_workspace(cudaStream_t stream, size_t bytes, void **out);
 // cleared by sgemm_device_status() after a wait that gave up).
 sgemm_status_t op_counters(cudaStream_t stream, size_t count, int **out);
 
-// Row-major rows x cols matrix of `type` elements of `elem` bytes, rows
-// ld * elem bytes apart; boxes of box_rows x box_cols, zero outside.
-sgemm_status_t op_encode_2d(CUtensorMap *map, CUtensorMapDataType type, int elem, const void *base,
-                            int64_t rows, int64_t cols, int64_t ld, int box_cols, int box_rows,
-                            CUtensorMapSwizzle swizzle);
+// `planes` row-major rows x cols matrices of 16-bit elements (bf16 or fp16),
+// rows ld and planes plane_stride elements apart; boxes of one plane,
+// box_rows x 64, 128-byte swizzle, zero outside.
+sgemm_status_t op_encode_16(CUtensorMap *map, bool bf16, const void *base, int64_t rows,
+                            int64_t cols, int64_t ld, int64_t planes, int64_t plane_stride,
+                            int box_rows);
 
 }  // namespace sgemm
