@@ -74,7 +74,7 @@ _SIGNATURES = {
     "sgemm_probe_tf32": (_int, [_i64, _int, _vp]),
     "sgemm_ffn_forward": (_int, [_i64, _i64, _i64, _int, _int, _vp, _i64, _vp, _i64, _vp, _i64,
                                  _vp, _i64, _vp, _i64, _vp, _vp]),
-    "sgemm_ffn_saved_floats": (_i64, [_i64, _i64]),
+    "sgemm_ffn_saved_floats": (_i64, [_i64, _i64, _int]),
     "sgemm_ffn_backward": (_int, [_i64, _i64, _i64, _int, _int, _vp, _i64, _vp, _i64, _vp, _i64,
                                   _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
                                   _i64, _vp]),

@@ -579,9 +579,14 @@ sgemm_status_t op_counters(cudaStream_t stream, size_t count, int **out) {
     sgemm_status_t s = device_state(&d);
     if (s != SGEMM_OK) return s;
     Workspace *w = nullptr;
+    const bool grow = d->ws[stream].counter_count < count;
     s = ensure_workspace(*d, stream, 0, count, &w);
-    if (s == SGEMM_OK) *out = w->counters;
-    return s;
+    if (s != SGEMM_OK) return s;
+    // New counters are cleared on the default stream, which `stream` need not
+    // wait for.
+    if (grow && cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+    *out = w->counters;
+    return SGEMM_OK;
 }
 
 sgemm_status_t op_encode_16(CUtensorMap *map, bool bf16, const void *base, int64_t rows,

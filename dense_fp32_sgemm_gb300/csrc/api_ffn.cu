@@ -4,7 +4,7 @@
 #include <math.h>
 
 #include <algorithm>
-#include <vector>
+#include <initializer_list>
 
 #include "../../include/sgemm_ffn.h"
 #include "kernels_ffn.h"
@@ -56,8 +56,6 @@ sgemm_status_t check_ffn(const FfnArgs &a) {
     return SGEMM_OK;
 }
 
-int64_t saved_ld(int64_t F) { return (F + 3) / 4 * 4; }
-
 int64_t pad8(int64_t v) { return (v + 7) / 8 * 8; }
 
 // Sizes of the pieces of one workspace, then their addresses.
@@ -108,34 +106,85 @@ Source intermediate(Arena &w, int type, int64_t rows, int64_t cols) {
     return s;
 }
 
-void place(const Arena &w, Source &s) {
-    if (s.copied || !s.op.p) s.op.p = w.at(s.offset);
+// Where the cut tiles of a product's tail meet; the same for all products of a
+// call, which run one after the other.
+struct Tail {
+    size_t offset = 0;
+    float *partials = nullptr;
+    int *counters = nullptr;
+};
+constexpr int kMinShare = 8;  // steps
+
+size_t tail_bytes(const OpDevice &dev) {
+    return (size_t)2 * dev.num_sms * ffn_slot_floats(true) * sizeof(float);
+}
+// One per tail tile (fewer than workers), CTA of a worker and epilogue warp.
+size_t tail_counters(const OpDevice &dev) { return (size_t)dev.num_sms * 8; }
+
+// Takes the workspace (with room for the tail) and gives every piece its
+// address.
+sgemm_status_t place_all(Arena &w, Tail &tail, const OpDevice &dev, cudaStream_t st,
+                         std::initializer_list<Source *> list) {
+    tail.offset = w.take(tail_bytes(dev));
+    void *base = nullptr;
+    sgemm_status_t s = op_workspace(st, w.bytes, &base);
+    if (s == SGEMM_OK) s = op_counters(st, tail_counters(dev), &tail.counters);
+    if (s != SGEMM_OK) return s;
+    w.base = static_cast<char *>(base);
+    tail.partials = static_cast<float *>(w.at(tail.offset));
+    for (Source *v : list)
+        if (v->copied || !v->op.p) v->op.p = w.at(v->offset);
+    return SGEMM_OK;
 }
 
-sgemm_status_t make_copies(const Source *const *list, int n, int type, const OpDevice &dev,
-                           cudaStream_t st) {
+sgemm_status_t make_copies(std::initializer_list<const Source *> list, int type,
+                           const OpDevice &dev, cudaStream_t st) {
     FfnPrepJob jobs[kFfnPrepJobs];
     int count = 0;
-    for (int i = 0; i < n; ++i) {
-        const Source &s = *list[i];
-        if (!s.copied) continue;
-        jobs[count++] = FfnPrepJob{s.user, s.ld_user, (int)s.op.rows, (int)s.op.cols,
-                                   const_cast<void *>(s.op.p), s.op.ld, s.op.plane_stride};
+    for (const Source *s : list) {
+        if (!s->copied) continue;
+        jobs[count++] = FfnPrepJob{s->user, s->ld_user, (int)s->op.rows, (int)s->op.cols,
+                                   const_cast<void *>(s->op.p), s->op.ld, s->op.plane_stride};
     }
     return status(launch_ffn_prep(jobs, count, type, dev.num_sms, st));
 }
+
+// What the forward pass keeps for the backward pass: u act'(g) and act(g) in
+// blocks of 32 x 32 floats, then h as an operand.
+struct Kept {
+    int64_t keep_cols, block_floats, h_plane;
+    int planes;
+    int64_t floats() const { return 2 * block_floats + planes * h_plane / 2; }
+
+    Kept(int64_t T, int64_t F, int type) {
+        keep_cols = (F + 31) / 32;
+        block_floats = (T + 31) / 32 * keep_cols * 1024;
+        h_plane = T * pad8(F);
+        planes = type == kTypeF32 ? 3 : 1;
+    }
+    FfnOperand h(float *base, int64_t T, int64_t F) const {
+        return FfnOperand{base + 2 * block_floats, T, F, pad8(F), h_plane, planes};
+    }
+    void set(FfnGemmParams &p, float *base) const {
+        p.keep_cols = (int)keep_cols;
+        p.keep[0] = base;
+        p.keep[1] = base + block_floats;
+    }
+};
 
 // Sets up and launches one product.  A and B (A2 and B2) as they lie in
 // memory; a_mn, b_mn: their rows run along k.
 struct Product {
     const OpDevice &dev;
     cudaStream_t st;
+    float *partials;
+    int *counters;
     FfnGemmParams p = {};
     FfnMaps maps;
 
-    Product(const OpDevice &d, cudaStream_t s, int mode, int type, int64_t M, int64_t N, int64_t K,
+    Product(const OpDevice &d, cudaStream_t s, const Tail &t, int mode, int type, int64_t M, int64_t N, int64_t K,
             bool a_mn, bool b_mn)
-        : dev(d), st(s) {
+        : dev(d), st(s), partials(t.partials), counters(t.counters) {
         p.mode = mode;
         p.type = type;
         p.M = (int)M; p.N = (int)N; p.K = (int)K;
@@ -160,14 +209,23 @@ struct Product {
         p.tiles_m = (p.M + kFfnBM * cg - 1) / (kFfnBM * cg);
         p.tiles_n = (p.N + tile_n - 1) / tile_n;
         const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * p.outs;
+        const int64_t steps = (int64_t)p.kblocks * p.segs;
         if (tiles > INT32_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
-        p.tiles = (int)tiles;
         sgemm_status_t s = map(&maps.a[0], A, p.a_mn);
         if (s == SGEMM_OK) s = map(&maps.a[1], A2 ? *A2 : A, p.a_mn);
         if (s == SGEMM_OK) s = map(&maps.b[0], B, p.b_mn);
         if (s == SGEMM_OK) s = map(&maps.b[1], B2 ? *B2 : B, p.b_mn);
         if (s != SGEMM_OK) return s;
-        return status(launch_ffn_gemm(maps, p, pair, dev.num_sms, st));
+        p.workers = dev.num_sms / cg;
+        p.full_tiles = (int)(tiles / p.workers);
+        p.tail_tiles = (int)(tiles % p.workers);
+        // The tail's shares: at least kMinShare steps each, where there are
+        // as many, so that a share is worth its partial tile's way through L2.
+        p.tail_workers = (int)std::min<int64_t>(
+            p.workers, std::max<int64_t>(p.tail_tiles, p.tail_tiles * steps / kMinShare));
+        p.partials = partials;
+        p.counters = counters;
+        return status(launch_ffn_gemm(maps, p, pair, st));
     }
 
     void store(void *C, int64_t ld, void *C2 = nullptr, int64_t ld2 = 0) {
@@ -184,15 +242,14 @@ struct Product {
     }
 };
 
-// The block's first half: h (when wanted) and g, u (when kept).
-sgemm_status_t run_gate(const OpDevice &dev, cudaStream_t st, const FfnArgs &a, const FfnOperand &x,
-                        const FfnOperand &Wg, const FfnOperand &Wu, const FfnOperand *h, float *gu) {
-    Product g(dev, st, kFfnGate, a.type, a.T, a.F, a.D, false, true);
+// The block's first half: h, and the kept values where `keep` is given.
+sgemm_status_t run_gate(const OpDevice &dev, cudaStream_t st, const Tail &tail, const FfnArgs &a,
+                        const FfnOperand &x, const FfnOperand &Wg, const FfnOperand &Wu,
+                        const FfnOperand &h, const Kept &kept, float *keep) {
+    Product g(dev, st, tail, kFfnGate, a.type, a.T, a.F, a.D, false, true);
     g.p.act = a.act;
-    if (h) g.store_planes(*h);
-    g.p.ldgu = saved_ld(a.F);
-    g.p.g = gu;
-    g.p.u = gu ? gu + a.T * g.p.ldgu : nullptr;
+    g.store_planes(h);
+    if (keep) kept.set(g.p, keep);
     return g.run(x, Wg, &x, &Wu);
 }
 
@@ -210,9 +267,9 @@ using namespace sgemm;
 
 extern "C" {
 
-int64_t sgemm_ffn_saved_floats(int64_t T, int64_t F) {
-    if (T < 0 || F < 0 || T > kMaxFfnSize || F > kMaxFfnSize) return 0;
-    return 2 * T * saved_ld(F);
+int64_t sgemm_ffn_saved_floats(int64_t T, int64_t F, int type) {
+    if (T < 0 || F < 0 || T > kMaxFfnSize || F > kMaxFfnSize || !type_ok(type)) return 0;
+    return T == 0 || F == 0 ? 0 : Kept(T, F, type).floats();
 }
 
 sgemm_status_t sgemm_ffn_forward(int64_t T, int64_t D, int64_t F, int type, int activation,
@@ -232,19 +289,18 @@ sgemm_status_t sgemm_ffn_forward(int64_t T, int64_t D, int64_t F, int type, int 
     if (s != SGEMM_OK) return s;
     if (F == 0) return zero_matrix(y, ldy, T, D, type, st);
     Arena w;
+    Tail tail;
+    const Kept kept(T, F, type);
     Source vx = source(w, x, type, T, D, ldx), vg = source(w, Wg, type, D, F, ldg),
-           vu = source(w, Wu, type, D, F, ldu), vd = source(w, Wd, type, F, D, ldd),
-           h = intermediate(w, type, T, F);
-    void *base = nullptr;
-    s = op_workspace(st, w.bytes, &base);
+           vu = source(w, Wu, type, D, F, ldu), vd = source(w, Wd, type, F, D, ldd);
+    Source h = intermediate(w, type, T, F);
+    s = place_all(w, tail, dev, st, {&vx, &vg, &vu, &vd, &h});
     if (s != SGEMM_OK) return s;
-    w.base = static_cast<char *>(base);
-    for (Source *v : {&vx, &vg, &vu, &vd, &h}) place(w, *v);
-    const Source *const inputs[] = {&vx, &vg, &vu, &vd};
-    s = make_copies(inputs, 4, type, dev, st);
-    if (s == SGEMM_OK) s = run_gate(dev, st, a, vx.op, vg.op, vu.op, &h.op, saved);
+    if (saved) h.op = kept.h(saved, T, F);
+    s = make_copies({&vx, &vg, &vu, &vd}, type, dev, st);
+    if (s == SGEMM_OK) s = run_gate(dev, st, tail, a, vx.op, vg.op, vu.op, h.op, kept, saved);
     if (s != SGEMM_OK) return s;
-    Product down(dev, st, kFfnStore, type, T, D, F, false, true);
+    Product down(dev, st, tail, kFfnStore, type, T, D, F, false, true);
     down.store(y, ldy);
     return down.run(h.op, vd.op);
 }
@@ -279,47 +335,42 @@ sgemm_status_t sgemm_ffn_backward(int64_t T, int64_t D, int64_t F, int type, int
         return s;
     }
     Arena w;
+    Tail tail;
+    const Kept kept(T, F, type);
     Source vx = source(w, x, type, T, D, ldx), vg = source(w, Wg, type, D, F, ldg),
            vu = source(w, Wu, type, D, F, ldu), vd = source(w, Wd, type, F, D, ldd),
            vdy = source(w, dy, type, T, D, lddy), dg = intermediate(w, type, T, F),
-           du = intermediate(w, type, T, F), h = intermediate(w, type, T, F);
-    const size_t kept_at = saved ? 0 : w.take((size_t)sgemm_ffn_saved_floats(T, F) * 4);
-    void *base = nullptr;
-    s = op_workspace(st, w.bytes, &base);
+           du = intermediate(w, type, T, F);
+    const size_t kept_at = saved ? 0 : w.take((size_t)kept.floats() * sizeof(float));
+    s = place_all(w, tail, dev, st, {&vx, &vg, &vu, &vd, &vdy, &dg, &du});
     if (s != SGEMM_OK) return s;
-    w.base = static_cast<char *>(base);
-    for (Source *v : {&vx, &vg, &vu, &vd, &vdy, &dg, &du, &h}) place(w, *v);
-    const Source *const inputs[] = {&vx, &vg, &vu, &vd, &vdy};
-    s = make_copies(inputs, 5, type, dev, st);
-    float *kept = saved ? const_cast<float *>(saved) : static_cast<float *>(w.at(kept_at));
-    if (s == SGEMM_OK && !saved) s = run_gate(dev, st, a, vx.op, vg.op, vu.op, nullptr, kept);
+    float *keep = saved ? const_cast<float *>(saved) : static_cast<float *>(w.at(kept_at));
+    const FfnOperand h = kept.h(keep, T, F);
+    s = make_copies({&vx, &vg, &vu, &vd, &vdy}, type, dev, st);
+    if (s == SGEMM_OK && !saved) s = run_gate(dev, st, tail, a, vx.op, vg.op, vu.op, h, kept, keep);
     if (s != SGEMM_OK) return s;
 
-    Product grad(dev, st, kFfnGateGrad, type, T, F, D, false, false);
-    grad.p.act = activation;
-    grad.store_planes(h.op);
-    grad.p.C[1] = const_cast<void *>(dg.op.p);
-    grad.p.C[2] = const_cast<void *>(du.op.p);
-    grad.p.ldgu = saved_ld(F);
-    grad.p.g = kept;
-    grad.p.u = kept + T * grad.p.ldgu;
+    Product grad(dev, st, tail, kFfnGateGrad, type, T, F, D, false, false);
+    grad.store_planes(dg.op);
+    grad.p.C[1] = const_cast<void *>(du.op.p);
+    kept.set(grad.p, keep);
     s = grad.run(vdy.op, vd.op);
     if (s == SGEMM_OK && dx) {
-        Product p(dev, st, kFfnStore, type, T, D, F, false, false);
+        Product p(dev, st, tail, kFfnStore, type, T, D, F, false, false);
         p.p.segs = 2;
         p.store(dx, lddx);
         s = p.run(dg.op, vg.op, &du.op, &vu.op);
     }
     if (s == SGEMM_OK && weights) {
-        Product p(dev, st, kFfnStore, type, D, F, T, true, true);
+        Product p(dev, st, tail, kFfnStore, type, D, F, T, true, true);
         p.p.outs = 2;
         p.store(dWg, lddg, dWu, lddu);
         s = p.run(vx.op, dg.op, nullptr, &du.op);
     }
     if (s == SGEMM_OK && weights) {
-        Product p(dev, st, kFfnStore, type, F, D, T, true, true);
+        Product p(dev, st, tail, kFfnStore, type, F, D, T, true, true);
         p.store(dWd, lddd);
-        s = p.run(h.op, vdy.op);
+        s = p.run(h, vdy.op);
     }
     return s;
 }

@@ -4,9 +4,10 @@
 // tensor memory); what differs is which way round the operands lie and what
 // happens to the accumulators:
 //   gate       g = x Wg and u = x Wu into the two halves of one accumulator,
-//              h = act(g) * u stored (and g, u kept in FP32 when asked for)
+//              h = act(g) u stored (and u act'(g), act(g) kept in FP32 when
+//              asked for, in the order in which a warp holds them)
 //   down       y = h Wd
-//   gate grad  dh = dy Wd^T; dg = dh u act'(g), du = dh act(g), h stored
+//   gate grad  dh = dy Wd^T; dg = dh u act'(g), du = dh act(g)
 //   dx         dg Wg^T + du Wu^T, both products into one accumulator
 //   dW         x^T dg and x^T du (two outputs of one launch), h^T dy
 //
@@ -39,8 +40,9 @@ namespace {
 constexpr uint32_t kABytes = kFfnBM * kFfnBK * 2;
 constexpr uint32_t kBBytes = kFfnBN * kFfnBK * 2;
 constexpr uint32_t kStageBytes = kABytes + kBBytes;
-constexpr size_t kSmemBytes = (size_t)kFfnStages * kStageBytes + 1024;
 constexpr int kEpiWarps = 8;
+constexpr uint32_t kEpiBytes = 32 * 128;  // an epilogue warp's staging: 32 rows of 32 values
+constexpr size_t kSmemBytes = (size_t)kFfnStages * kStageBytes + kEpiWarps * kEpiBytes + 1024;
 constexpr uint32_t kBlockBytes = 64 * kFfnBK * 2;  // 64 of m or n by 64 k
 
 // FP32: which planes of A and B the six products take, smallest first.
@@ -68,47 +70,133 @@ __device__ __forceinline__ TileAt tile_at(const FfnGemmParams &p, int t) {
     return r;
 }
 
-// 32 consecutive FP32 values of a row to a matrix of TYPE, from column n on
-// (columns up to N).
-template <int TYPE>
-__device__ __forceinline__ void store_row(void *base, long long at, bool vec, int left,
-                                          const float (&v)[32]) {
-    if constexpr (TYPE == kTypeF32) {
-        float *c = static_cast<float *>(base) + at;
-        if (vec && left >= 32) {
+// A stretch of one tile's k steps (a step: one k block, with all its plane
+// products) that a worker computes.
+struct Unit {
+    int tile, s0, s1;   // steps [s0, s1)
+    int pieces, piece;  // the tile's stretches, and which this is
+    int first;          // the worker of piece 0
+};
+
+// The worker's u-th unit; false when there is none.  The tail's steps are
+// shared out evenly, so a worker's share touches at most two tiles.
+__device__ __forceinline__ bool unit_at(const FfnGemmParams &p, int worker, int u, int steps,
+                                        Unit &r) {
+    if (u < p.full_tiles) {
+        r = Unit{worker + u * p.workers, 0, steps, 1, 0, worker};
+        return true;
+    }
+    if (worker >= p.tail_workers) return false;
+    const long long all = (long long)p.tail_tiles * steps;
+    long long a = worker * all / p.tail_workers;
+    const long long e = (worker + 1) * all / p.tail_workers;
+    long long end = min(e, (a / steps + 1) * steps);
+    if (u > p.full_tiles) {
+        if (u > p.full_tiles + 1) return false;
+        a = end;
+        end = e;
+    }
+    if (a >= end) return false;
+    const int t = (int)(a / steps);
+    // Worker w starts at floor(w all / n), so step x is worker
+    // floor(((x + 1) n - 1) / all)'s.
+    const long long x0 = (long long)t * steps, n = p.tail_workers;
+    r.tile = p.full_tiles * p.workers + t;
+    r.s0 = (int)(a - x0);
+    r.s1 = (int)(end - x0);
+    r.first = (int)(((x0 + 1) * n - 1) / all);
+    r.pieces = (int)(((x0 + steps) * n - 1) / all) - r.first + 1;
+    r.piece = worker - r.first;
+    return true;
+}
+
+// Slot of piece q: a worker's first slot holds a piece that starts inside its
+// tile, the second one that starts with it.
+__device__ __forceinline__ int piece_slot(const Unit &u, int q) {
+    return 2 * (u.first + q) + (q == 0 ? 1 : 0);
+}
+
+// 32 values of each of a warp's lanes, as they lie in registers: 512
+// consecutive bytes per instruction.
+__device__ __forceinline__ void put_lanes(float *base, int lane, const float (&v)[32]) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                reinterpret_cast<float4 *>(c)[i] =
-                    make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        } else {
+    for (int i = 0; i < 8; ++i)
+        __stcg(reinterpret_cast<float4 *>(base) + i * 32 + lane,
+               make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+}
+__device__ __forceinline__ void get_lanes(const float *base, int lane, float (&v)[32]) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < left) c[i] = v[i];
-        }
-    } else {
-        uint16_t *c = static_cast<uint16_t *>(base) + at;
-        if (vec && left >= 32) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                reinterpret_cast<uint4 *>(c)[i] =
-                    make_uint4(pack16<TYPE>(v[8 * i], v[8 * i + 1]),
-                               pack16<TYPE>(v[8 * i + 2], v[8 * i + 3]),
-                               pack16<TYPE>(v[8 * i + 4], v[8 * i + 5]),
-                               pack16<TYPE>(v[8 * i + 6], v[8 * i + 7]));
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < left) c[i] = (uint16_t)(pack16<TYPE>(v[i], 0.0f) & 0xFFFFu);
-        }
+    for (int i = 0; i < 8; ++i) {
+        const float4 f = __ldcg(reinterpret_cast<const float4 *>(base) + i * 32 + lane);
+        v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
     }
 }
 
-// An intermediate matrix: 16-bit values, or FP32 values as three planes.
+// A warp's 32 x 32 block (lane = row, 32 columns each) to a row-major matrix
+// of TYPE: through shared memory, so that a row's 64 or 128 bytes are stored
+// by neighbouring lanes.  The 16-byte chunks of a row are permuted by its
+// number so that neither side has bank conflicts.  rows and cols are what is
+// left of the matrix from (row0, n) on.
 template <int TYPE>
-__device__ __forceinline__ void store_planes(void *base, long long at, long long plane, bool vec,
-                                             int left, const float (&v)[32]) {
+__device__ __forceinline__ void store_block(unsigned char *stage, int lane, void *base, long long ld,
+                                            long long row0, int n, int rows, int cols, bool vec,
+                                            const float (&v)[32]) {
+    constexpr int kElem = TYPE == kTypeF32 ? 4 : 2;
+    constexpr int kChunks = 32 * kElem / 16;  // of a row
+    constexpr int kPer = 16 / kElem;          // elements of a chunk
+    auto place = [&](int r, int c) {
+        return reinterpret_cast<uint4 *>(
+            stage + r * (16 * kChunks) + ((TYPE == kTypeF32 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4));
+    };
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        uint4 w;
+        if constexpr (TYPE == kTypeF32)
+            w = make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+                           __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+        else
+            w = make_uint4(pack16<TYPE>(v[8 * c], v[8 * c + 1]),
+                           pack16<TYPE>(v[8 * c + 2], v[8 * c + 3]),
+                           pack16<TYPE>(v[8 * c + 4], v[8 * c + 5]),
+                           pack16<TYPE>(v[8 * c + 6], v[8 * c + 7]));
+        *place(lane, c) = w;
+    }
+    __syncwarp();
+    const int c = lane % kChunks, left = cols - c * kPer;
+    unsigned char *out = static_cast<unsigned char *>(base) +
+                         ((row0 + lane / kChunks) * ld + n + c * kPer) * kElem;
+    const long long step = (long long)(32 / kChunks) * ld * kElem;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i, out += step) {
+        const int r = i * (32 / kChunks) + lane / kChunks;
+        const uint4 w = *place(r, c);
+        if (r < rows && left > 0) {
+            if (vec && left >= kPer) {
+                *reinterpret_cast<uint4 *>(out) = w;
+            } else {
+                const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    if (j < left) {
+                        if constexpr (TYPE == kTypeF32)
+                            reinterpret_cast<uint32_t *>(out)[j] = e[j];
+                        else
+                            reinterpret_cast<uint16_t *>(out)[j] = (uint16_t)(e[j / 2] >> (16 * (j % 2)));
+                    }
+            }
+        }
+    }
+    __syncwarp();
+}
+
+// The same to an intermediate matrix: 16-bit values, or FP32 values as three
+// planes.
+template <int TYPE>
+__device__ __forceinline__ void store_planes(unsigned char *stage, int lane, void *base, long long ld,
+                                             long long plane, long long row0, int n, int rows,
+                                             int cols, const float (&v)[32]) {
     if constexpr (TYPE != kTypeF32) {
-        store_row<TYPE>(base, at, vec, left, v);
+        store_block<TYPE>(stage, lane, base, ld, row0, n, rows, cols, true, v);
     } else {
         float rest[32];
 #pragma unroll
@@ -123,21 +211,9 @@ __device__ __forceinline__ void store_planes(void *base, long long at, long long
                 part[i] = s[0];
                 rest[i] = isfinite(s[0]) ? rest[i] - s[0] : 0.0f;
             }
-            store_row<kTypeBF16>(base, at + q * plane, vec, left, part);
+            store_block<kTypeBF16>(stage, lane, static_cast<uint16_t *>(base) + q * plane, ld, row0,
+                                   n, rows, cols, true, part);
         }
-    }
-}
-
-__device__ __forceinline__ void load_row(const float *c, int left, float (&v)[32]) {
-    if (left >= 32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float4 f = __ldg(reinterpret_cast<const float4 *>(c) + i);
-            v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = i < left ? __ldg(c + i) : 0.0f;
     }
 }
 
@@ -157,9 +233,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     const uint32_t raw = smem_addr(ffn_smem_raw);
     unsigned char *smem = ffn_smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     const uint32_t sbase = smem_addr(smem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t rank = CG == 2 ? cluster_rank() : 0;
-    const int worker = (int)blockIdx.x / CG, workers = (int)gridDim.x / CG;
+    const int worker = (int)blockIdx.x / CG;
 
     if (tid == 0) {
         for (int s = 0; s < kFfnStages; ++s) {
@@ -180,61 +257,73 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     tc_fence_after_sync();
     const uint32_t tmem = tmem_slot;
 
-    const int iters = p.kblocks * p.segs * kProducts;  // stages of a tile
-    // Stages that one accumulator takes before the epilogue reads it.
-    const int phase_iters = kSplit ? kProducts : iters;
-    const int phases = iters / phase_iters;
+    const int steps = p.kblocks * p.segs;  // of a tile; kProducts stages each
 
     if (warp == 0) {
         if (lane == 0) {
-            int it = 0;  // stages so far, over all tiles
+            // Stages so far over all tiles, the next one's place in the ring
+            // and the parity its release is waited for with (1: still new).
+            int it = 0, s = 0;
+            uint32_t parity = 1;
             bool ok = true;
-            for (int t = worker; ok && t < p.tiles; t += workers) {
-                const TileAt at = tile_at(p, t);
+            const uint32_t bar0 = CG == 2 ? cluster_addr(&full[0], 0) : smem_addr(&full[0]);
+            Unit unit;
+            for (int u = 0; ok && unit_at(p, worker, u, steps, unit); ++u) {
+                const TileAt at = tile_at(p, unit.tile);
                 const int m0 = at.m * (kFfnBM * CG) + (int)rank * kFfnBM;
                 const int n0 = at.n * kTileN;
-                for (int i = 0; i < iters; ++i, ++it) {
-                    if (p.skip_loads_from >= 0 && it >= p.skip_loads_from) {
-                        ok = false;
-                        break;
+                int seg = unit.s0 >= p.kblocks ? 1 : 0;
+                int k = (unit.s0 - seg * p.kblocks) * kFfnBK;
+                for (int step = unit.s0; ok && step < unit.s1; ++step, k += kFfnBK) {
+                    if (k >= p.kblocks * kFfnBK) {
+                        k = 0;
+                        seg = 1;
                     }
-                    const int s = it % kFfnStages, use = it / kFfnStages;
-                    if (use > 0 && !mbar_wait_bounded(&empty[s], (use - 1) & 1, p.timeout_ns)) {
-                        atomicOr(p.err, kErrWaitTimeout);
-                        s_abort = 1;
-                        ok = false;
-                        break;
-                    }
-                    const int prod = i % kProducts, kb = (i / kProducts) % p.kblocks;
-                    const int seg = i / (kProducts * p.kblocks);
-                    const int pa = kSplit ? kPlaneA[prod] : 0, pb = kSplit ? kPlaneB[prod] : 0;
-                    const int k = kb * kFfnBK;
-                    unsigned char *a = smem + (size_t)s * kStageBytes, *b = a + kABytes;
-                    // The pair's loads all complete on the first CTA's barrier.
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], kStageBytes * CG);
-                    const uint32_t bar = CG == 2 ? cluster_addr(&full[s], 0) : smem_addr(&full[s]);
-                    const CUtensorMap *ma = &maps.a[seg];
-                    if (p.a_mn) {
-                        tc_load_3d<CG>(a, ma, bar, m0, k, pa);
-                        tc_load_3d<CG>(a + kBlockBytes, ma, bar, m0 + 64, k, pa);
-                    } else {
-                        tc_load_3d<CG>(a, ma, bar, k, m0, pa);
-                    }
-                    if constexpr (MODE == kFfnGate) {
-                        // One CTA: 64 columns of each matrix.  A pair: the
-                        // first CTA brings 128 of Wg, the second of Wu.
-                        const CUtensorMap *m1 = CG == 2 ? &maps.b[rank] : &maps.b[0];
-                        const CUtensorMap *m2 = CG == 2 ? m1 : &maps.b[1];
-                        tc_load_3d<CG>(b, m1, bar, n0, k, pb);
-                        tc_load_3d<CG>(b + kBlockBytes, m2, bar, CG == 2 ? n0 + 64 : n0, k, pb);
-                    } else {
-                        const CUtensorMap *mb = &maps.b[seg + at.out];
-                        const int n = n0 + (int)rank * kFfnBN;
-                        if (p.b_mn) {
-                            tc_load_3d<CG>(b, mb, bar, n, k, pb);
-                            tc_load_3d<CG>(b + kBlockBytes, mb, bar, n + 64, k, pb);
-                        } else {
-                            tc_load_3d<CG>(b, mb, bar, k, n, pb);
+                    const CUtensorMap *ma = &maps.a[seg], *mb = &maps.b[seg + at.out];
+                    {
+#pragma unroll 1
+                        for (int prod = 0; prod < kProducts; ++prod, ++it) {
+                            if (p.skip_loads_from >= 0 && it >= p.skip_loads_from) {
+                                ok = false;
+                                break;
+                            }
+                            if (!tc_wait(&empty[s], parity, p.timeout_ns)) {
+                                atomicOr(p.err, kErrWaitTimeout);
+                                s_abort = 1;
+                                ok = false;
+                                break;
+                            }
+                            const int pa = kSplit ? kPlaneA[prod] : 0, pb = kSplit ? kPlaneB[prod] : 0;
+                            unsigned char *a = smem + s * kStageBytes, *b = a + kABytes;
+                            // The pair's loads all complete on the first CTA's barrier.
+                            if (rank == 0) mbar_arrive_expect_tx(&full[s], kStageBytes * CG);
+                            const uint32_t bar = bar0 + s * 8;
+                            if (p.a_mn) {
+                                tc_load_3d<CG>(a, ma, bar, m0, k, pa);
+                                tc_load_3d<CG>(a + kBlockBytes, ma, bar, m0 + 64, k, pa);
+                            } else {
+                                tc_load_3d<CG>(a, ma, bar, k, m0, pa);
+                            }
+                            if constexpr (MODE == kFfnGate) {
+                                // One CTA: 64 columns of each matrix.  A pair: the
+                                // first CTA brings 128 of Wg, the second of Wu.
+                                const CUtensorMap *m1 = CG == 2 ? &maps.b[rank] : &maps.b[0];
+                                const CUtensorMap *m2 = CG == 2 ? m1 : &maps.b[1];
+                                tc_load_3d<CG>(b, m1, bar, n0, k, pb);
+                                tc_load_3d<CG>(b + kBlockBytes, m2, bar, CG == 2 ? n0 + 64 : n0, k, pb);
+                            } else {
+                                const int n = n0 + (int)rank * kFfnBN;
+                                if (p.b_mn) {
+                                    tc_load_3d<CG>(b, mb, bar, n, k, pb);
+                                    tc_load_3d<CG>(b + kBlockBytes, mb, bar, n + 64, k, pb);
+                                } else {
+                                    tc_load_3d<CG>(b, mb, bar, k, n, pb);
+                                }
+                            }
+                            if (++s == kFfnStages) {
+                                s = 0;
+                                parity ^= 1;
+                            }
                         }
                     }
                 }
@@ -242,7 +331,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             // The last releases of the stages have to arrive before the CTA
             // leaves.
             for (int i = max(0, it - kFfnStages); ok && i < it; ++i)
-                if (!mbar_wait_bounded(&empty[i % kFfnStages], (i / kFfnStages) & 1, p.timeout_ns)) {
+                if (!tc_wait(&empty[i % kFfnStages], (i / kFfnStages) & 1, p.timeout_ns)) {
                     atomicOr(p.err, kErrDrainTimeout);
                     s_abort = 1;
                     ok = false;
@@ -250,172 +339,233 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        // The whole warp runs the loop, one elected lane issues: a loop of one
+        // lane alone keeps its descriptors in vector registers and spent some
+        // 650 clocks on a stage whose products take 512.
+        if (rank == 0) {
             const uint32_t idesc =
                 tc_idesc(kFfnBM * CG, kFfnBN * CG, TYPE != kTypeF16, p.a_mn != 0, p.b_mn != 0);
             // Per 16 k: two groups of eight rows (MN-major) or 32 bytes along
-            // the swizzled row (K-major).
-            const uint32_t a_step = p.a_mn ? 2048 : 32, b_step = p.b_mn ? 2048 : 32;
-            int it = 0, ph = 0;
+            // the swizzled row (K-major); units of 16 bytes.
+            const uint32_t a_step = (p.a_mn ? 2048 : 32) >> 4, b_step = (p.b_mn ? 2048 : 32) >> 4;
+            // Descriptors of the first stage; the others and the steps along
+            // k differ in the start address alone.
+            const uint64_t desc_a = tc_desc(sbase, kBlockBytes);
+            const uint64_t desc_b = tc_desc(sbase + kABytes, kBlockBytes);
+            int s = 0, buf = 0;
+            uint32_t parity = 0, acc_parity = 1;
             bool ok = true;
-            for (int t = worker; ok && t < p.tiles; t += workers) {
-                for (int q = 0; ok && q < phases; ++q, ++ph) {
-                    const int buf = ph & 1, use = ph >> 1;
-                    if (use > 0 && !mbar_wait_bounded(&acc_empty[buf], (use - 1) & 1, p.timeout_ns)) {
-                        atomicOr(p.err, kErrWaitTimeout);
-                        s_abort = 1;
-                        ok = false;
-                        break;
-                    }
+            Unit unit;
+            for (int u = 0; ok && unit_at(p, worker, u, steps, unit); ++u) {
+                // An accumulator takes the unit's steps, or (FP32) one.
+                const int phases = kSplit ? unit.s1 - unit.s0 : 1;
+                const int stages = kSplit ? kProducts : unit.s1 - unit.s0;
+                for (int q = 0; ok && q < phases; ++q) {
+                    ok = tc_wait_warp(&acc_empty[buf], acc_parity, p.timeout_ns);
+                    if (!ok) break;
                     tc_fence_after_sync();
                     const uint32_t d = tmem + buf * kAccCols;
-                    for (int i = 0; i < phase_iters; ++i, ++it) {
-                        const int s = it % kFfnStages;
-                        if (!mbar_wait_bounded(&full[s], (it / kFfnStages) & 1, p.timeout_ns)) {
-                            atomicOr(p.err, kErrWaitTimeout);
-                            s_abort = 1;
-                            ok = false;
-                            break;
-                        }
+                    for (int i = 0; i < stages; ++i) {
+                        ok = tc_wait_warp(&full[s], parity, p.timeout_ns);
+                        if (!ok) break;
                         tc_fence_after_sync();
-                        const uint32_t a = sbase + s * kStageBytes, b = a + kABytes;
+                        const uint64_t a = desc_a + s * (kStageBytes >> 4);
+                        const uint64_t b = desc_b + s * (kStageBytes >> 4);
+                        if (tc_elect()) {
 #pragma unroll
-                        for (int kk = 0; kk < kFfnBK / 16; ++kk)
-                            tc_mma<CG>(d, tc_desc(a + kk * a_step, kBlockBytes),
-                                       tc_desc(b + kk * b_step, kBlockBytes), idesc, (i | kk) != 0);
-                        tc_commit<CG>(&empty[s]);
+                            for (int kk = 0; kk < kFfnBK / 16; ++kk)
+                                tc_mma<CG>(d, a + kk * a_step, b + kk * b_step, idesc, (i | kk) != 0);
+                            tc_commit<CG>(&empty[s]);
+                        }
+                        __syncwarp();
+                        if (++s == kFfnStages) {
+                            s = 0;
+                            parity ^= 1;
+                        }
                     }
-                    if (ok) tc_commit<CG>(&acc_full[buf]);
+                    if (!ok) break;
+                    if (tc_elect()) tc_commit<CG>(&acc_full[buf]);
+                    __syncwarp();
+                    buf ^= 1;
+                    acc_parity ^= buf ^ 1;
                 }
+            }
+            if (!ok && lane == 0) {
+                atomicOr(p.err, kErrWaitTimeout);
+                s_abort = 1;
             }
         }
         __syncwarp();
     } else if (warp >= 4) {
         const int quad = warp & 3, half = (warp - 4) >> 2;
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
-        int ph = 0;
+        unsigned char *stage = smem + kFfnStages * kStageBytes + (warp - 4) * kEpiBytes;
+        // Part j is 32 accumulator columns; in the gate's product parts come
+        // in twos, the same columns of g and u.
+        constexpr int kTwo = MODE == kFfnGate ? 2 : 1;
+        auto part_col = [&](int j) {
+            return MODE == kFfnGate ? (j & 1) * 64 * CG + half * 32 * CG + 32 * (j >> 1)
+                                    : half * 64 * CG + 32 * j;
+        };
+        int buf = 0;
+        uint32_t parity = 0;
         bool ok = true;
-        for (int t = worker; ok && t < p.tiles; t += workers) {
-            const TileAt at = tile_at(p, t);
-            const int row = at.m * (kFfnBM * CG) + (int)rank * kFfnBM + quad * 32 + lane;
-            const int n_tile = at.n * kTileN;
-            const bool row_ok = row < p.M;
-            // Part j is 32 accumulator columns; in the gate's product parts
-            // come in twos, the same columns of g and u.
-            auto part_col = [&](int j) {
-                return MODE == kFfnGate ? (j & 1) * 64 * CG + half * 32 * CG + 32 * (j >> 1)
-                                        : half * 64 * CG + 32 * j;
-            };
-            auto emit = [&](int j, const float (&v)[32], const float (&v2)[32]) {
-                const int n = n_tile + part_col(j & (MODE == kFfnGate ? ~1 : ~0));
-                const int left = p.N - n;
-                if (!row_ok || left <= 0) return;
-                const long long c_at = (long long)row * p.ldc[MODE == kFfnStore ? at.out : 0] + n;
-                if constexpr (MODE == kFfnStore) {
-                    store_row<TYPE>(p.C[at.out], c_at, p.c_vec, left, v);
-                } else if constexpr (MODE == kFfnGate) {
-                    const long long gu = (long long)row * p.ldgu + n;
-                    if (p.g) {
-                        store_row<kTypeF32>(p.g, gu, true, left, v);
-                        store_row<kTypeF32>(p.u, gu, true, left, v2);
-                    }
-                    if (p.C[0]) {
-                        float h[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) h[i] = gate_act<kSplit>(v[i], p.act) * v2[i];
-                        store_planes<TYPE>(p.C[0], c_at, p.c_plane, p.c_vec, left, h);
-                    }
-                } else {
-                    const long long gu = (long long)row * p.ldgu + n;
-                    float g[32], u[32];
-                    load_row(p.g + gu, left, g);
-                    load_row(p.u + gu, left, u);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float a, slope;
-                        gate_act_slope<kSplit>(g[i], p.act, a, slope);
-                        const float ui = u[i];
-                        g[i] = v[i] * ui * slope;  // dg
-                        u[i] = v[i] * a;           // du
-                    }
-                    store_planes<TYPE>(p.C[1], c_at, p.c_plane, p.c_vec, left, g);
-                    store_planes<TYPE>(p.C[2], c_at, p.c_plane, p.c_vec, left, u);
-                    load_row(p.g + gu, left, g);
-                    load_row(p.u + gu, left, u);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) g[i] = gate_act<kSplit>(g[i], p.act) * u[i];
-                    store_planes<TYPE>(p.C[0], c_at, p.c_plane, p.c_vec, left, g);
-                }
-            };
+        Unit unit;
+        for (int u = 0; ok && unit_at(p, worker, u, steps, unit); ++u) {
+            const TileAt at = tile_at(p, unit.tile);
+            const int row0 = at.m * (kFfnBM * CG) + (int)rank * kFfnBM + quad * 32;
+            const int n_tile = at.n * kTileN, rows = p.M - row0;
             float sum[kSplit ? kParts : 1][32];
+            uint32_t d = t_lane;
             if constexpr (kSplit) {
 #pragma unroll
                 for (int j = 0; j < kParts; ++j)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) sum[j][i] = 0.0f;
-            }
-            for (int q = 0; q < phases; ++q, ++ph) {
-                const int buf = ph & 1;
-                int got = 1;
-                if (lane == 0) {
-                    got = mbar_wait_bounded(&acc_full[buf], (ph >> 1) & 1, p.timeout_ns) ? 1 : 0;
-                    if (!got) {
-                        atomicOr(p.err, kErrWaitTimeout);
-                        s_abort = 1;
-                    }
-                }
-                got = __shfl_sync(0xffffffffu, got, 0);
-                if (!got) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after_sync();
-                const uint32_t d = t_lane + buf * kAccCols;
-                if constexpr (kSplit) {
+                for (int q = unit.s0; q < unit.s1; ++q) {
+                    ok = tc_wait_warp(&acc_full[buf], parity, p.timeout_ns);
+                    if (!ok) break;
+                    tc_fence_after_sync();
 #pragma unroll
                     for (int j = 0; j < kParts; ++j) {
                         uint32_t r[32];
-                        tc_ld32(d + part_col(j), r);
+                        tc_ld32(t_lane + buf * kAccCols + part_col(j), r);
                         tc_wait_ld(r);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) sum[j][i] += __uint_as_float(r[i]);
                     }
-                } else {
-#pragma unroll 1
-                    for (int j = 0; j < kParts; j += MODE == kFfnGate ? 2 : 1) {
-                        uint32_t r[32], r2[32];
-                        float v[32], v2[32];
-                        tc_ld32(d + part_col(j), r);
-                        if constexpr (MODE == kFfnGate) {
-                            tc_ld32(d + part_col(j + 1), r2);
-                            tc_wait_ld(r2);
-                        }
-                        tc_wait_ld(r);
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) cluster_arrive(cluster_addr(&acc_empty[buf], 0));
+                    buf ^= 1;
+                    parity ^= buf ^ 1;
+                }
+            } else {
+                ok = tc_wait_warp(&acc_full[buf], parity, p.timeout_ns);
+                tc_fence_after_sync();
+                d = t_lane + buf * kAccCols;
+            }
+            if (!ok) break;
+            // This warp's part of the accumulator.
+            auto own = [&](int j, float (&v)[32]) {
+                if constexpr (kSplit) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            v[i] = __uint_as_float(r[i]);
-                            v2[i] = MODE == kFfnGate ? __uint_as_float(r2[i]) : 0.0f;
+                    for (int i = 0; i < 32; ++i) v[i] = sum[j][i];
+                } else {
+                    uint32_t r[32];
+                    tc_ld32(d + part_col(j), r);
+                    tc_wait_ld(r);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                }
+            };
+            // Where piece q of this tile keeps this warp's parts.
+            auto slot = [&](int q) {
+                return p.partials + (size_t)(piece_slot(unit, q) * CG + (int)rank) *
+                                        (kEpiWarps * kParts * 1024) +
+                       (warp - 4) * (kParts * 1024);
+            };
+            bool emit = rows > 0;
+            if (unit.pieces > 1 && rows > 0) {
+                float *mine = slot(unit.piece);
+#pragma unroll(kSplit ? kParts : 1)
+                for (int j = 0; j < kParts; ++j) {
+                    float v[32];
+                    own(j, v);
+                    put_lanes(mine + j * 1024, lane, v);
+                }
+                __threadfence();
+                __syncwarp();
+                int *counter = p.counters + ((unit.tile - p.full_tiles * p.workers) * CG + (int)rank) *
+                                                kEpiWarps + (warp - 4);
+                int arrived = 0;
+                if (lane == 0) {
+                    arrived = atomicAdd(counter, 1);
+                    if (arrived == unit.pieces - 1) *counter = 0;
+                }
+                emit = __shfl_sync(0xffffffffu, arrived, 0) == unit.pieces - 1;
+                __threadfence();
+            }
+            // The last to arrive adds the pieces (its own among them) in the
+            // order of k.
+            auto value = [&](int j, float (&v)[32]) {
+                if (unit.pieces == 1) {
+                    own(j, v);
+                    return;
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+#pragma unroll 1
+                for (int q = 0; q < unit.pieces; ++q) {
+                    float w[32];
+                    get_lanes(slot(q) + j * 1024, lane, w);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] += w[i];
+                }
+            };
+            if (emit) {
+#pragma unroll(kSplit ? kParts : 1)
+                for (int j = 0; j < kParts; j += kTwo) {
+                    const int n = n_tile + (MODE == kFfnGate ? half * 32 * CG + 16 * j : part_col(j));
+                    const int cols = p.N - n;
+                    if (cols <= 0) break;
+                    const long long kept =
+                        ((long long)(row0 >> 5) * p.keep_cols + (n >> 5)) * 1024;
+                    float v[32];
+                    if constexpr (MODE == kFfnStore) {
+                        value(j, v);
+                        store_block<TYPE>(stage, lane, p.C[at.out], p.ldc[at.out], row0, n, rows,
+                                          cols, p.c_vec, v);
+                    } else if constexpr (MODE == kFfnGate) {
+                        float w[32];
+                        value(j, v);
+                        value(j + 1, w);
+                        if (p.keep[0]) {
+                            float t[32];
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                float a, slope;
+                                gate_act_slope<kSplit>(v[i], p.act, a, slope);
+                                v[i] = a;
+                                t[i] = w[i] * slope;
+                                w[i] *= a;
+                            }
+                            put_lanes(p.keep[0] + kept, lane, t);
+                            put_lanes(p.keep[1] + kept, lane, v);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) w[i] *= gate_act<kSplit>(v[i], p.act);
                         }
-                        emit(j, v, v2);
+                        store_planes<TYPE>(stage, lane, p.C[0], p.ldc[0], p.c_plane, row0, n, rows,
+                                           cols, w);
+                    } else {
+                        float t[32];
+                        get_lanes(p.keep[0] + kept, lane, t);
+                        value(j, v);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) t[i] *= v[i];
+                        store_planes<TYPE>(stage, lane, p.C[0], p.ldc[0], p.c_plane, row0, n, rows,
+                                           cols, t);
+                        get_lanes(p.keep[1] + kept, lane, t);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) t[i] *= v[i];
+                        store_planes<TYPE>(stage, lane, p.C[1], p.ldc[0], p.c_plane, row0, n, rows,
+                                           cols, t);
                     }
                 }
+            }
+            if constexpr (!kSplit) {
                 // The accumulator may be overwritten.
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) {
-                    if constexpr (CG == 2)
-                        cluster_arrive(cluster_addr(&acc_empty[buf], 0));
-                    else
-                        mbar_arrive(&acc_empty[buf]);
-                }
+                if (lane == 0) cluster_arrive(cluster_addr(&acc_empty[buf], 0));
+                buf ^= 1;
+                parity ^= buf ^ 1;
             }
-            if constexpr (kSplit) {
-                if (ok) {
-#pragma unroll
-                    for (int j = 0; j < kParts; j += MODE == kFfnGate ? 2 : 1)
-                        emit(j, sum[j], sum[MODE == kFfnGate ? j + 1 : j]);
-                }
-            }
+        }
+        if (!ok && lane == 0) {
+            atomicOr(p.err, kErrWaitTimeout);
+            s_abort = 1;
         }
     }
 
@@ -424,8 +574,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     if (tid == 0 && (s_abort || p.skip_loads_from >= 0)) {
         // A role gave up: loads and products may still be in flight.  They
         // take microseconds; nothing here signals their end any more.
-        const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < 2000000ull) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < 4000000) {
         }
     }
     __syncthreads();
@@ -487,14 +637,13 @@ __global__ void __launch_bounds__(256) ffn_prep_kernel(const PrepTable t) {
 }
 
 template <int TYPE, int MODE, int CG>
-cudaError_t launch_one(const FfnMaps &maps, const FfnGemmParams &p, int num_sms,
-                       cudaStream_t stream) {
+cudaError_t launch_one(const FfnMaps &maps, const FfnGemmParams &p, cudaStream_t stream) {
     const auto kernel = ffn_gemm_kernel<TYPE, MODE, CG>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)kSmemBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(CG * std::min(p.tiles, num_sms / CG));
+    cfg.gridDim = dim3(CG * (p.full_tiles > 0 ? p.workers : p.tail_workers));
     cfg.blockDim = dim3(kFfnThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;
@@ -508,25 +657,24 @@ cudaError_t launch_one(const FfnMaps &maps, const FfnGemmParams &p, int num_sms,
 }
 
 template <int TYPE, int CG>
-cudaError_t launch_mode(const FfnMaps &maps, const FfnGemmParams &p, int num_sms,
-                        cudaStream_t stream) {
+cudaError_t launch_mode(const FfnMaps &maps, const FfnGemmParams &p, cudaStream_t stream) {
     switch (p.mode) {
-        case kFfnStore: return launch_one<TYPE, kFfnStore, CG>(maps, p, num_sms, stream);
-        case kFfnGate: return launch_one<TYPE, kFfnGate, CG>(maps, p, num_sms, stream);
-        default: return launch_one<TYPE, kFfnGateGrad, CG>(maps, p, num_sms, stream);
+        case kFfnStore: return launch_one<TYPE, kFfnStore, CG>(maps, p, stream);
+        case kFfnGate: return launch_one<TYPE, kFfnGate, CG>(maps, p, stream);
+        default: return launch_one<TYPE, kFfnGateGrad, CG>(maps, p, stream);
     }
 }
 
 }  // namespace
 
-cudaError_t launch_ffn_gemm(const FfnMaps &maps, const FfnGemmParams &p, bool pair, int num_sms,
+cudaError_t launch_ffn_gemm(const FfnMaps &maps, const FfnGemmParams &p, bool pair,
                             cudaStream_t stream) {
-    if (p.type == kTypeF32) return launch_mode<kTypeF32, 1>(maps, p, num_sms, stream);
+    if (p.type == kTypeF32) return launch_mode<kTypeF32, 1>(maps, p, stream);
     if (p.type == kTypeF16)
-        return pair ? launch_mode<kTypeF16, 2>(maps, p, num_sms, stream)
-                    : launch_mode<kTypeF16, 1>(maps, p, num_sms, stream);
-    return pair ? launch_mode<kTypeBF16, 2>(maps, p, num_sms, stream)
-                : launch_mode<kTypeBF16, 1>(maps, p, num_sms, stream);
+        return pair ? launch_mode<kTypeF16, 2>(maps, p, stream)
+                    : launch_mode<kTypeF16, 1>(maps, p, stream);
+    return pair ? launch_mode<kTypeBF16, 2>(maps, p, stream)
+                : launch_mode<kTypeBF16, 1>(maps, p, stream);
 }
 
 cudaError_t launch_ffn_prep(const FfnPrepJob *jobs, int count, int type, int num_sms,

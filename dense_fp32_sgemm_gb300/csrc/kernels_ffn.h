@@ -110,8 +110,8 @@ struct FfnOperand {
 
 enum : int {
     kFfnStore = 0,     // C = A B, or A B + A2 B2, or two outputs A B and A B2
-    kFfnGate = 1,      // h = act(A B) * (A B2); g and u kept when asked for
-    kFfnGateGrad = 2,  // dh = A B; dg, du and h from it and the kept g, u
+    kFfnGate = 1,      // g = A B, u = A B2; h = act(g) u; u act'(g) and act(g) kept when asked
+    kFfnGateGrad = 2,  // dh = A B; dg = dh u act'(g) and du = dh act(g) from the kept values
 };
 
 constexpr int kFfnBM = 128;      // rows of a CTA's tile
@@ -128,21 +128,32 @@ struct FfnGemmParams {
     int segs;            // products added up (2: A B + A2 B2)
     int outs;            // outputs (2: A B -> C[0], A B2 -> C[1])
     int a_mn, b_mn;      // operand is MN-major: its rows run along k
-    int tiles_m, tiles_n, tiles;
+    int tiles_m, tiles_n;
     int kblocks;         // ceil(K / kFfnBK)
-    // kFfnStore: C, `type`.  kFfnGate: C[0] = h or null.  kFfnGateGrad: C[0] =
-    // h, C[1] = dg, C[2] = du.  h, dg and du are 16-bit operands for the next
-    // product: one plane of `type`, or three bf16 planes.
-    void *C[3];
+    // Workers (CTAs or pairs) take whole tiles round-robin, full_tiles each;
+    // the tail_tiles left over are cut along k into tail_workers equal shares.
+    int workers, full_tiles, tail_tiles, tail_workers;
+    float *partials;     // 2 slots per worker of kFfnSlotFloats per CTA (tail)
+    int *counters;       // tail_tiles x CTAs of a worker x 8, zero at rest
+    // kFfnStore: C, `type`.  kFfnGate: C[0] = h.  kFfnGateGrad: C[0] = dg,
+    // C[1] = du.  h, dg and du are 16-bit operands for the next product: one
+    // plane of `type`, or three bf16 planes.
+    void *C[2];
     long long ldc[2];    // kFfnStore: of each output; else ldc[0] of all
     long long c_plane;
     int c_vec;           // 16-byte stores allowed
-    float *g, *u;        // kept values, M x ldgu (a multiple of 4), or null
-    long long ldgu;
+    // u act'(g) and act(g), or null: blocks of 32 x 32 values, block (i, j) at
+    // (i * keep_cols + j) * 1024, in it element (row r, column c) at
+    // (c / 4 * 32 + r) * 4 + c % 4: as a warp holds them.
+    float *keep[2];
+    int keep_cols;
     int *err;
     unsigned long long timeout_ns;
     int skip_loads_from;
 };
+
+// Floats of a CTA's accumulator; a worker's partial tile has one per CTA.
+inline int ffn_slot_floats(bool pair) { return kFfnBM * kFfnBN * (pair ? 2 : 1); }
 
 // One operand's TMA descriptor as the kernel wants it: boxes of 64 along the
 // contiguous dimension by `rows` rows.
@@ -150,7 +161,7 @@ struct FfnMaps {
     CUtensorMap a[2], b[2];
 };
 // pair: 256-row tiles by pairs of CTAs.
-cudaError_t launch_ffn_gemm(const FfnMaps &maps, const FfnGemmParams &p, bool pair, int num_sms,
+cudaError_t launch_ffn_gemm(const FfnMaps &maps, const FfnGemmParams &p, bool pair,
                             cudaStream_t stream);
 
 // Copies that make operands of the user's matrices: FP32 split into three

@@ -6,6 +6,38 @@
 
 namespace sgemm {
 
+// Waits for phase `parity` of `bar`, giving up after about `timeout_ns` (taken
+// as two SM clocks each: the clock register is cheaper to read than the
+// global timer).
+__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity,
+                                        unsigned long long timeout_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if ((unsigned long long)(clock64() - t0) > 2 * timeout_ns) return false;
+    }
+}
+
+// The same for a whole warp, with a result the compiler knows to be the same
+// in every lane: what follows stays convergent, so its addresses and
+// descriptors live in uniform registers.
+__device__ __forceinline__ bool tc_wait_warp(uint64_t *bar, uint32_t parity,
+                                             unsigned long long timeout_ns) {
+    return __all_sync(0xffffffffu, tc_wait(bar, parity, timeout_ns));
+}
+
+// True in one lane of a convergent warp.
+__device__ __forceinline__ bool tc_elect() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // Shared-memory matrix descriptor, 128-byte swizzle: start address, leading
 // and stride byte offsets (each in units of 16 bytes), fixed version bits
 // 46-47 = 1, layout type 2 in bits 61-63.

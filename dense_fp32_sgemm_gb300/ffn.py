@@ -67,19 +67,20 @@ def _block(x, w_gate, w_up, w_down):
     return T, D, F, kind, args
 
 
-def _saved_address(saved, T, F, device):
+def _saved_address(saved, T, F, kind, device):
     if saved is None:
         return None
-    need = _sg.library().sgemm_ffn_saved_floats(T, F)
+    need = _sg.library().sgemm_ffn_saved_floats(T, F, kind)
     if (saved.dtype != torch.float32 or saved.device != device or not saved.is_contiguous()
             or saved.numel() < need):
         raise ValueError(f"saved must be a contiguous float32 tensor of {need} elements on {device}")
     return saved.data_ptr()
 
 
-def ffn_saved(T: int, F: int, device="cuda"):
-    """A buffer for what the forward pass keeps for the backward pass."""
-    need = _sg.library().sgemm_ffn_saved_floats(int(T), int(F))
+def ffn_saved(T: int, F: int, device="cuda", dtype=torch.float32):
+    """A buffer for what the forward pass of ``dtype`` matrices keeps for the
+    backward pass (without ``dtype`` one that is large enough for any)."""
+    need = _sg.library().sgemm_ffn_saved_floats(int(T), int(F), _TYPES[dtype])
     return torch.empty(need, dtype=torch.float32, device=device)
 
 
@@ -96,7 +97,7 @@ def ffn_forward(x, w_gate, w_up, w_down, y=None, activation: int = 0, saved=None
     if y is None:
         y = torch.empty(T, D, dtype=x.dtype, device=x.device)
     _call(_sg.library().sgemm_ffn_forward, x.device, stream, T, D, F, kind, int(activation), *args,
-          *_matrix(y, "y", T, D, x.dtype, x.device), _saved_address(saved, T, F, x.device))
+          *_matrix(y, "y", T, D, x.dtype, x.device), _saved_address(saved, T, F, kind, x.device))
     return y
 
 
@@ -113,7 +114,7 @@ def ffn_backward(dy, x, w_gate, w_up, w_down, dx=None, dw_gate=None, dw_up=None,
     T, D, F, kind, args = _block(x, w_gate, w_up, w_down)
     dev, dtype = x.device, x.dtype
     dya = _matrix(dy, "dy", T, D, dtype, dev)
-    keep = _saved_address(saved, T, F, dev)
+    keep = _saved_address(saved, T, F, kind, dev)
 
     def out(t, name, rows, cols, wanted):
         if not wanted:

@@ -53,8 +53,9 @@ enum {
  * held in 32 bits.  With 16-bit types h is rounded to the type between the two
  * products (except where T is at most 8), with FP32 nothing is rounded below
  * 24 bits.
- * saved: NULL, or a device buffer (16-byte aligned) of sgemm_ffn_saved_floats(T, F)
- * floats that receives g and u in 32 bits for sgemm_ffn_backward.
+ * saved: NULL, or a device buffer (16-byte aligned) of sgemm_ffn_saved_floats(T, F,
+ * type) floats for sgemm_ffn_backward: it receives u act'(g) and act(g) in 32
+ * bits and h, in a layout of the library's own.
  * T == 0 or D == 0: nothing is done.  F == 0: y = 0.
  * Returns SGEMM_ERR_INVALID_ARG for a negative size, a leading dimension below
  * its row length, a NULL or misaligned pointer, an unknown type or activation;
@@ -65,8 +66,9 @@ SGEMM_API sgemm_status_t sgemm_ffn_forward(int64_t T, int64_t D, int64_t F, int 
                                            const void *Wu, int64_t ldu, const void *Wd, int64_t ldd,
                                            void *y, int64_t ldy, float *saved, void *stream);
 
-/* Floats of the `saved` buffer for T rows of F columns (0 for invalid sizes). */
-SGEMM_API int64_t sgemm_ffn_saved_floats(int64_t T, int64_t F);
+/* Floats of the `saved` buffer for T rows of F columns (0 for invalid sizes or
+ * an unknown type).  FP32 needs the most. */
+SGEMM_API int64_t sgemm_ffn_saved_floats(int64_t T, int64_t F, int type);
 
 /*
  * sgemm_ffn_backward -- gradients of the block for dy (T x D, lddy >= D):
@@ -75,8 +77,8 @@ SGEMM_API int64_t sgemm_ffn_saved_floats(int64_t T, int64_t F);
  *     dx = dg Wg^T + du Wu^T,  dWg = x^T dg,  dWu = x^T du,  dWd = h^T dy
  *
  * The first arguments are those of the forward call.  saved: the buffer the
- * forward call filled from the same x, Wg and Wu, or NULL: then g and u are
- * computed again.  dx: T x D, dWg and dWu: D x F, dWd: F x D, written whole.
+ * forward call filled from the same x, Wg and Wu, or NULL: then its contents
+ * are computed again.  dx: T x D, dWg and dWu: D x F, dWd: F x D, written whole.
  * dx may be NULL (no gradient of the input), and so may dWg, dWu and dWd, all
  * three together (frozen weights).  With 16-bit types h, dg and du are
  * rounded to the type before they enter the products.  T == 0: the weight
