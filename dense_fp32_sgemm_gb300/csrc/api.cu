@@ -605,6 +605,13 @@ sgemm_status_t op_encode_16(CUtensorMap *map, bool bf16, const void *base, int64
     return r == CUDA_SUCCESS ? SGEMM_OK : SGEMM_ERR_TMA;
 }
 
+sgemm_status_t op_encode_words(CUtensorMap *map, const uint32_t *base, int64_t rows, int64_t cols,
+                               int64_t ld, int box_cols, int box_rows) {
+    if (!g_encode) return SGEMM_ERR_TMA;
+    return encode_2d(map, reinterpret_cast<const float *>(base), rows, cols, ld, box_cols, box_rows,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 }  // namespace sgemm
 
 using namespace sgemm;

@@ -398,29 +398,56 @@ sgemm_status_t sgemm_w4_matvec(int64_t M, int64_t N, int64_t K, int64_t group, i
     W4Params p = {};
     p.N = (int)N; p.K = (int)K;
     p.group = (int)std::min<int64_t>(group, int64_t(1) << 30);
+    p.group_shift = -1;
+    for (int b = 5; b < 31; ++b)
+        if (p.group == 1 << b) p.group_shift = b;
     p.q = qweight; p.ldq = ldq;
     p.scales = scales; p.lds = lds;
     p.zeros = zeros; p.ldz = ldz;
     p.ldx = ldx; p.ldy = ldy;
-    p.x_vec = aligned(x, 16) && ldx % (16 / (int64_t)e) == 0;
+    p.x_vec = aligned(x, 16) && (M == 1 || ldx % (16 / (int64_t)e) == 0);
     p.units = (int)((K + kW4UnitK - 1) / kW4UnitK);
-    const bool vec = N % 4 == 0 && aligned(qweight, 16) && ldq % 4 == 0 && aligned(scales, 4 * e) &&
-                     lds % 4 == 0 && (!zeros || (aligned(zeros, 4) && ldz % 4 == 0));
-    // A cluster shares K where the columns alone leave SMs without work: at
-    // least two CTAs per SM, as long as every warp keeps a unit.
-    const int64_t tiles = (N + kW4Cols - 1) / kW4Cols;
-    int cluster = 1;
-    while (cluster < kW4MaxCluster && tiles * cluster < 2 * dev.num_sms &&
-           p.units >= 2 * cluster * kW4Warps)
-        cluster *= 2;
-    p.cta_units = (p.units + cluster - 1) / cluster;
+    const bool vec = N % 16 == 0 && aligned(qweight, 16) && ldq % 4 == 0 && aligned(scales, 16) &&
+                     lds * (int64_t)e % 16 == 0 && (!zeros || (aligned(zeros, 16) && ldz % 16 == 0));
+    CUtensorMap map = {};
+    if (vec && K > 0) {
+        const sgemm_status_t t = op_encode_words(&map, qweight, (K + 7) / 8, N, ldq, kW4BoxCols,
+                                                 kW4BoxRows);
+        if (t != SGEMM_OK) return t;
+    }
+    p.device = dev.index;
+    p.err = dev.err;
+    p.timeout_ns = dev.timeout_ns;
     const int max_rows = w4_max_rows(type);
     for (int64_t m0 = 0; m0 < M; m0 += max_rows) {
         p.M = (int)std::min<int64_t>(M - m0, max_rows);
         p.x = static_cast<const char *>(x) + m0 * ldx * e;
         p.y = static_cast<char *>(y) + m0 * ldy * e;
-        p.chunk_units = std::max(1, std::min(p.cta_units, kW4StageBytes / w4_unit_bytes(type, p.M)));
-        const cudaError_t err = launch_w4(p, type, vec, cluster, static_cast<cudaStream_t>(stream));
+        p.warps_n = p.M <= 4 ? 1 : 2;
+        // A cluster of CTAs shares K where that shortens the call.  Model, in SM
+        // clocks, fitted to GB300 times of 15 shapes with one to eight CTAs: an SM
+        // takes 270 a unit and 1500 a CTA, and a CTA by itself 3000 and 1000 a
+        // unit of its warps.  (1 x 4096 x 4096, bf16: 7.9, 6.0, 5.1, 7.3 us with 1,
+        // 2, 4, 8; 1 x 12288 x 4096: 19.6, 12.1, 10.0, 12.2; 1 x 16384 x 24576:
+        // 55, 57, 52, 64, and 49 with 3.)
+        const int64_t tiles = (N + kW4Cols * p.warps_n - 1) / (kW4Cols * p.warps_n);
+        const int warps_k = kW4Warps / p.warps_n;
+        int cluster = 1;
+        double least = 0.0;
+        for (int c = 1; c <= kW4MaxCluster && (c == 1 || c * warps_k <= p.units); ++c) {
+            const int64_t per_warp = (p.units + c * warps_k - 1) / (c * warps_k);
+            const double cost = (270.0 * tiles * p.warps_n * p.units + 1500.0 * tiles * c) / dev.num_sms +
+                                1000.0 * per_warp;
+            if (c == 1 || cost < least) {
+                least = cost;
+                cluster = c;
+            }
+        }
+        p.cta_units = (p.units + cluster - 1) / cluster;
+        p.chunk_units =
+            std::max(1, std::min(p.cta_units, kW4StageBytes / w4_unit_bytes(type, p.M)));
+        const cudaError_t err =
+            launch_w4(map, p, type, vec, cluster, static_cast<cudaStream_t>(stream));
         if (err != cudaSuccess) return SGEMM_ERR_LAUNCH;
     }
     return SGEMM_OK;

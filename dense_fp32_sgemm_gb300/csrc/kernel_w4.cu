@@ -3,50 +3,108 @@
 //   y[m][n] = sum over groups G of  s[G][n] * sum over k in G of x[m][k] (q[k][n] - z[G][n])
 //
 // Bound: HBM, K N / 2 bytes of q read once.  At the card's rate that is 13.6
-// weights per ns, about 2.4 instructions a lane for each, so the products go
-// to the warp-level matrix instruction and the lanes only expand the weights:
-// a word's eight values become four pairs of 16-bit floats with one shift,
-// four (and, or) instructions that drop the value into the mantissa of 1024
-// (or 128 for bf16) and four exact subtractions of zero point and offset,
-// about 1.2 instructions per weight.  The fifth-generation tensor cores would
-// need the expanded weights in shared memory and gain nothing at 16 columns.
+// weights per ns, so a lane has about 2.4 instructions for each, fewer where
+// they are logic (half rate).  So the products go to the warp-level matrix
+// instruction and the lanes only expand the weights: a word's eight values
+// become four pairs of 16-bit floats, each by one logic instruction (the forms
+// are described at expand).  The fifth-generation tensor cores would need the
+// expanded weights in shared memory and gain nothing at 16 columns.
 //
 // Layout.  The instruction (m16n8k16) takes the weights as its 16 x 16
 // operand, rows along n, and x as its 16 x 8 one, so up to eight rows of x
 // cost one instruction.  The order of k inside an instruction is free, so the
 // pairs come as a word gives them: (0,4), (1,5) in one instruction and (2,6),
-// (3,7) in the next; x is staged in shared memory in that order.  Lane (g, t)
-// = (lane / 4, lane % 4) of a warp reads four columns' words of word row t of
-// four: a warp reads 4 rows x 128 contiguous bytes for 32 columns x 32 k.
+// (3,7) in the next, and x read from shared memory is put in that order by four
+// byte permutations.  Lane (g, t) = (lane / 4, lane % 4) of a warp takes eight
+// columns' words of word row t of four; a unit is 128 k x 64 columns, 4 KB.
 //
-// Exactness.  q - z has at most five bits; 16-bit x enters as it is.  FP32 x
-// is the sum of three bf16 parts, each a row of its own of the x operand.
-// Sums are FP32; each group's sum is scaled in FP32.
+// Exactness.  q, z and q - z have at most five bits; 16-bit x enters as it is.
+// With 16-bit x the zero points' part, z (or 128 + z) times the sum of x, comes
+// off at the end of a group, its sum by one more instruction on a matrix of
+// ones: a quarter fewer instructions.  The cancellation costs bf16 five bits of
+// the FP32 sums' 24, far below the 8 bits of its y, and fp16 one or two.  FP32
+// x keeps the exact form; it is the sum of three bf16 parts, each a row of its
+// own of the x operand (made while x is staged).  Sums are FP32; each group's
+// sum is scaled in FP32.
 //
-// Split.  A CTA owns 32 columns and a range of K; its eight warps take every
-// eighth unit of 128 k and add up through shared memory in warp order.  Where
-// N alone gives too few CTAs, a cluster shares K and adds its CTAs' sums in
-// rank order through distributed shared memory: no atomics, no workspace.
+// Memory.  The time of such a product is a few round trips to HBM.  A warp
+// keeps a ring of units of its own under way in shared memory: two TMA boxes of
+// 32 columns each (128-byte swizzle; lanes take their columns in an order that
+// makes the reads free of bank conflicts) and bulk copies of the scales and
+// zero points, or, where rows do not start on 16 bytes, the aligned 16-byte
+// pieces that cover them.  TMA because it costs one lane two instructions: as
+// 16-byte copies by all lanes the first units alone held the warps up for 4000
+// clocks of a 13 us call, and one warp asking for all others' units took 800
+// clocks for each.
+//
+// Split.  A CTA's four warps stand side by side on 64 columns each
+// or behind one another along K (taking every n-th unit), or both: few rows of
+// x favour K (more CTAs), many rows columns (x is staged once per CTA).  Warps
+// along K add up through shared memory in warp order.  Where the columns give
+// too few CTAs, a cluster shares K and adds its CTAs' sums in rank order
+// through distributed shared memory: no atomics, no workspace.
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "ops_common.cuh"
+#include "tc_common.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace sgemm {
 namespace {
 
+constexpr int kMaxDevices = 64;
 constexpr int kThreads = kW4Warps * 32;
 constexpr int kSteps = kW4UnitK / 32;
+constexpr int kRows = kW4UnitK / 8;              // word rows of a unit
+constexpr int kBoxBytes = kRows * 128;           // 32 columns of a unit
+constexpr int kPlainPitch = 288;                 // bytes of a row of 64 + 3 words, banks apart
 
-__device__ __forceinline__ uint4 ld_stream(const uint32_t *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+// A unit in shared memory: q (two boxes, or 16 rows of pieces), then a row of
+// scales and one of zero points for each of its NG groups, as pieces.
+template <int TYPE, int NG>
+struct UnitLayout {
+    static constexpr int kElem = TYPE == kTypeF32 ? 4 : 2;
+    static constexpr int kScalePieces = kW4Cols * kElem / 16 + 1, kZeroPieces = kW4Cols / 16 + 1;
+    static constexpr int kScale = kRows * kPlainPitch;
+    static constexpr int kZero = kScale + NG * kScalePieces * 16;
+    static constexpr int kBytes = (kZero + NG * kZeroPieces * 16 + 1023) / 1024 * 1024;
+};
+static_assert(2 * kBoxBytes <= kRows * kPlainPitch, "boxes fit in the plain rows' place");
+
+// An aligned 16-byte piece of a row of a matrix into shared memory, as far as
+// it lies inside the row: up to `end`, and not before the matrix's first
+// element `base` (then element by element).
+__device__ __forceinline__ void copy_piece(unsigned char *dst, const unsigned char *piece,
+                                           const unsigned char *base, const unsigned char *end,
+                                           int elem) {
+    const long long left = end - piece;
+    if (left <= 0) return;
+    if (piece >= base && (left >= 16 || left % 4 == 0)) {
+        cp_async16(reinterpret_cast<float *>(dst), reinterpret_cast<const float *>(piece),
+                   left >= 16 ? 16 : (uint32_t)left);
+    } else {
+#pragma unroll 1
+        for (int e = 0; e < 16 && e < left; e += elem) {
+            if (piece + e < base) continue;
+            if (elem == 1)
+                dst[e] = piece[e];
+            else if (elem == 2)
+                *reinterpret_cast<uint16_t *>(dst + e) = *reinterpret_cast<const uint16_t *>(piece + e);
+            else
+                *reinterpret_cast<uint32_t *>(dst + e) = *reinterpret_cast<const uint32_t *>(piece + e);
+        }
+    }
+}
+__device__ __forceinline__ const unsigned char *piece_of(const unsigned char *p) {
+    return reinterpret_cast<const unsigned char *>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15));
+}
+// Where element n0 of the row starts in its first piece.
+__device__ __forceinline__ int piece_shift(const void *base, long long elements, int elem) {
+    return (int)((reinterpret_cast<uintptr_t>(base) + (unsigned long long)(elements * elem)) & 15);
 }
 
 template <bool BF16>
@@ -66,269 +124,451 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The four pairs (0,4), (1,5), (2,6), (3,7) of a word, minus the zero point.
-// z0 holds offset + z twice: 1024 + z in fp16, 128 + z in bf16.  z1 (fp16
-// only) holds -(64 + z) twice, for the pairs that sit four bits higher.
-template <bool BF16>
-__device__ __forceinline__ void expand(uint32_t w, uint32_t z0, uint32_t z1, uint32_t (&p)[4]) {
-    if constexpr (BF16) {
-        const __nv_bfloat162 z = *reinterpret_cast<const __nv_bfloat162 *>(&z0);
+// (w & mask) | magic in one instruction (left to itself the compiler makes two
+// of it, as an instruction has room for one constant).
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
+    return r;
+}
+
+// How the lanes expand a word into pairs of 16-bit floats, and what is left to
+// do for the zero points.
+//   kPlainInt (fp16 x): the bits of two values, masked, are fp16 numbers as
+//     they stand: subnormals, q 2^-24 for the low nibble of a byte and q 2^-20
+//     for the high one, both exact.  The two kinds keep sums of their own;
+//     z times the sum of x comes off at the end of a group.
+//   kOffset (bf16 x): bf16 has no such room below, so q enters as 128 + q, and
+//     128 + z times the sum of x comes off at the end.
+//   kExact (FP32 x): as kOffset, but 128 + z comes off every value.
+enum : int { kPlainInt, kOffset, kExact };
+
+// The pairs (0,4), (1,5), (2,6), (3,7) of a word.  magic: 128 twice in bf16;
+// zero: 128 + z twice (kExact).
+template <int FORM>
+__device__ __forceinline__ void expand(uint32_t w, uint32_t magic, uint32_t zero, uint32_t (&p)[4]) {
+    if constexpr (FORM == kPlainInt) {
+        const uint32_t s = w >> 8;
+        p[0] = w & 0x000F000Fu;
+        p[1] = w & 0x00F000F0u;
+        p[2] = s & 0x000F000Fu;
+        p[3] = s & 0x00F000F0u;
+    } else {
+        const __nv_bfloat162 z = *reinterpret_cast<const __nv_bfloat162 *>(&zero);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t v = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+            const uint32_t v = and_or(w >> (4 * i), 0x000F000Fu, magic);
             const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), z);
-            p[i] = *reinterpret_cast<const uint32_t *>(&d);
-        }
-    } else {
-        const __half2 z = *reinterpret_cast<const __half2 *>(&z0);
-        const __half2 zh = *reinterpret_cast<const __half2 *>(&z1);
-        const uint32_t sixteenth = 0x2C002C00u;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t s = w >> (8 * i);
-            const uint32_t lo = (s & 0x000F000Fu) | 0x64006400u;
-            const uint32_t hi = (s & 0x00F000F0u) | 0x64006400u;
-            const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&lo), z);
-            const __half2 b = __hfma2(*reinterpret_cast<const __half2 *>(&hi),
-                                      *reinterpret_cast<const __half2 *>(&sixteenth), zh);
-            p[2 * i] = *reinterpret_cast<const uint32_t *>(&a);
-            p[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&b);
+            p[i] = FORM == kOffset ? v : *reinterpret_cast<const uint32_t *>(&d);
         }
     }
 }
 
+// CTAs of one SM that the registers leave room for.
+constexpr int ctas_per_sm(int type, int nt, int gs) {
+    return nt == 1 && gs > 1 ? 4 : nt <= 2 && gs > 1 ? 3 : 2;
+}
+
 // TYPE: of x, scales and y.  NT: instructions' worth (8) of x rows.  GS: steps
-// of 32 k that share a scale inside a unit.  VEC: four columns are read at once.
+// of 32 k that share a scale inside a unit.  VEC: rows of q, scales and zeros
+// start on 16 bytes and N is a multiple of 16.
 template <int TYPE, int NT, int GS, bool VEC>
-__global__ void __launch_bounds__(kThreads, NT == 1 || (NT == 2 && TYPE != kTypeF32 && GS > 1) ? 2 : 1)
-    w4_kernel(const W4Params p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(TYPE, NT, GS))
+    w4_kernel(const __grid_constant__ CUtensorMap map, const W4Params p) {
     constexpr bool BF16 = TYPE != kTypeF16;
+    constexpr int FORM = TYPE == kTypeF16 ? kPlainInt : TYPE == kTypeBF16 ? kOffset : kExact;
+    constexpr int SUMS = FORM == kPlainInt ? 2 : 1;  // per accumulator
+    constexpr int T16 = TYPE == kTypeF16 ? kTypeF16 : kTypeBF16;
     constexpr int P = TYPE == kTypeF32 ? 3 : 1;
     constexpr int NG = kSteps / GS;  // scales of a unit
-    extern __shared__ __align__(16) unsigned char smem[];
+    using L = UnitLayout<TYPE, NG>;
+    extern __shared__ unsigned char w4_smem_raw[];
+    __shared__ uint64_t full[kW4Warps][kW4Stages];  // TMA boxes of a warp's stages
+    const uint32_t raw = smem_addr(w4_smem_raw);
+    unsigned char *smem = w4_smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    unsigned char *xs = smem + kW4Warps * kW4Stages * L::kBytes;
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
 
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
-    const int n0 = (int)(blockIdx.x / ranks) * kW4Cols;
-    const int rows = P * p.M;
+    const int tid = threadIdx.x, lane = tid % 32;
+    const int warp = __shfl_sync(0xffffffffu, tid / 32, 0);
+    const int warps_k = kW4Warps / p.warps_n;
+    const int cols = kW4Cols * p.warps_n;             // of this CTA
+    const int c0 = (int)(blockIdx.x / ranks) * cols;  // its first
     const int k_words = (p.K + 7) / 8;
     const int u0 = rank * p.cta_units, u1 = min(p.units, u0 + p.cta_units);
-    const int chunk_k = p.chunk_units * kW4UnitK;
-    const int pitch = chunk_k * 2 + 64;  // rows 64 bytes apart modulo 128: no bank conflicts
+    const int rows = P * p.M;
 
-    // The lane's four columns, as offsets from n0.
-    const int col0 = VEC ? 4 * g : g, col_step = VEC ? 1 : 8;
-    bool col_ok[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) col_ok[j] = n0 + col0 + j * col_step < p.N;
+    if (VEC && lane == 0) {
+        for (int i = 0; i < kW4Stages; ++i) mbar_init(&full[warp][i], 1);
+        fence_barrier_init();
+    }
+    __syncwarp();
 
-    auto load_words = [&](int unit, uint32_t (&w)[kSteps][4]) {
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int r = unit * (kW4UnitK / 8) + 4 * i + t;
-            const bool ok = unit < u1 && r < k_words;
-            const uint32_t *q = p.q + (long long)r * p.ldq + n0 + col0;
+    const int g = lane / 4, t = lane % 4;
+    const int wn = warp % p.warps_n, wk = warp / p.warps_n;
+    const int n0 = c0 + wn * kW4Cols;  // this warp's first column
+    const int pitch = p.chunk_units * kW4UnitK * 2 + 64;  // 64 bytes apart modulo 128
+    unsigned char *ring = smem + warp * (kW4Stages * L::kBytes);
+    // The lane's columns: VEC, two runs of four, else every eighth.
+    const int run = 4 * ((g >> 1) + 4 * (g & 1));
+
+    auto group_of = [&](int k) { return p.group_shift >= 0 ? k >> p.group_shift : k / p.group; };
+
+    // Asks for the warp's unit `u` (nothing when there is none).
+    auto fetch = [&](int u, int stage) {
+        if (u < u1 && n0 < p.N) {
+            unsigned char *to = ring + stage * L::kBytes;
             if constexpr (VEC) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (ok && col_ok[0]) v = ld_stream(q);
-                w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+                // Lane i brings group i's scales and zero points, lane 0 q.
+                const int groups = min(NG, (p.K - u * kW4UnitK + GS * 32 - 1) / (GS * 32));
+                const int cols_here = min(kW4Cols, p.N - n0);
+                const int zero_bytes = p.zeros ? cols_here : 0;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&full[warp][stage],
+                                          2 * kBoxBytes + groups * (cols_here * L::kElem + zero_bytes));
+                    tma_load_2d(to, &map, &full[warp][stage], n0, u * kRows);
+                    tma_load_2d(to + kBoxBytes, &map, &full[warp][stage], n0 + 32, u * kRows);
+                }
+                if (lane < groups) {
+                    const int group = group_of(u * kW4UnitK + lane * GS * 32);
+                    bulk_load(to + L::kScale + lane * (L::kScalePieces * 16),
+                              static_cast<const unsigned char *>(p.scales) +
+                                  (group * p.lds + n0) * L::kElem,
+                              cols_here * L::kElem, &full[warp][stage]);
+                    if (zero_bytes)
+                        bulk_load(to + L::kZero + lane * (L::kZeroPieces * 16),
+                                  p.zeros + group * p.ldz + n0, zero_bytes, &full[warp][stage]);
+                }
             } else {
+                // Two lanes to a row; 17 pieces cover 64 words wherever they
+                // start.
+                const int r = lane / 2, row = u * kRows + r;
+                if (row < k_words) {
+                    const uint32_t *q = p.q + row * p.ldq;
+                    const unsigned char *base = reinterpret_cast<const unsigned char *>(p.q);
+                    const unsigned char *end = reinterpret_cast<const unsigned char *>(q + p.N);
+                    const unsigned char *piece =
+                        piece_of(reinterpret_cast<const unsigned char *>(q + n0)) + (lane % 2) * 16;
+                    unsigned char *dst = to + r * kPlainPitch + (lane % 2) * 16;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[i][j] = ok && col_ok[j] ? __ldg(q + 8 * j) : 0u;
+                    for (int c = 0; c < 9; ++c)
+                        if (c < 8 || lane % 2 == 0)
+                            copy_piece(dst + c * 32, piece + c * 32, base, end, 4);
+                }
+                constexpr int kScaleJobs = NG * L::kScalePieces, kZeroJobs = NG * L::kZeroPieces;
+#pragma unroll 1
+                for (int j = lane; j < kScaleJobs + (p.zeros ? kZeroJobs : 0); j += 32) {
+                    const bool zero = j >= kScaleJobs;
+                    const int jj = zero ? j - kScaleJobs : j;
+                    const int per = zero ? L::kZeroPieces : L::kScalePieces;
+                    const int i = jj / per, c = jj - i * per, k = u * kW4UnitK + i * GS * 32;
+                    if (k < p.K) {
+                        const unsigned char *base =
+                            static_cast<const unsigned char *>(zero ? p.zeros : p.scales);
+                        const int elem = zero ? 1 : L::kElem;
+                        const unsigned char *row = base + group_of(k) * (zero ? p.ldz : p.lds) * elem;
+                        copy_piece(to + (zero ? L::kZero : L::kScale) + jj * 16,
+                                   piece_of(row + (long long)n0 * elem) + c * 16, base,
+                                   row + (long long)p.N * elem, elem);
+                    }
+                }
             }
         }
+        if constexpr (!VEC) cp_async_commit();
     };
-    auto load_scales = [&](int unit, float (&s)[NG][4], uint32_t (&z)[NG]) {
+    // Scale and zero point of the lane's columns of group i of unit u; what
+    // was not loaded (columns beyond N, groups beyond K) is not used or
+    // meets sums of zeros.
+    auto scales_of = [&](const unsigned char *w, int u, int i, float (&sc)[8], uint32_t (&z)[2]) {
+        const int k = u * kW4UnitK + i * GS * 32;
+        const bool there = k < p.K;
+        const unsigned char *s = w + L::kScale + i * L::kScalePieces * 16;
+        const unsigned char *zs = w + L::kZero + i * L::kZeroPieces * 16;
+        z[0] = z[1] = 0x08080808u;
+        if constexpr (VEC) {
+            s += run * L::kElem;
+            zs += run;
 #pragma unroll
-        for (int i = 0; i < NG; ++i) {
-            const int k = unit * kW4UnitK + i * GS * 32;
-            const bool ok = unit < u1 && k < p.K;
-            const long long at = (long long)(k / p.group) * p.lds + n0 + col0;
-            const long long zat = (long long)(k / p.group) * p.ldz + n0 + col0;
-            z[i] = 0x08080808u;
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (TYPE == kTypeF32) {
+                    const float4 f = *reinterpret_cast<const float4 *>(s + 128 * h);
+                    sc[4 * h] = f.x; sc[4 * h + 1] = f.y; sc[4 * h + 2] = f.z; sc[4 * h + 3] = f.w;
+                } else {
+                    const uint2 f = *reinterpret_cast<const uint2 *>(s + 64 * h);
+                    const float2 a = unpack16<T16>(f.x), b = unpack16<T16>(f.y);
+                    sc[4 * h] = a.x; sc[4 * h + 1] = a.y; sc[4 * h + 2] = b.x; sc[4 * h + 3] = b.y;
+                }
+                if (p.zeros) z[h] = *reinterpret_cast<const uint32_t *>(zs + 32 * h);
+            }
+        } else {
+            const int group = group_of(k);
+            s += piece_shift(p.scales, group * p.lds + n0, L::kElem) + g * L::kElem;
+            if (p.zeros) {
+                zs += piece_shift(p.zeros, group * p.ldz + n0, 1) + g;
+                z[0] = z[1] = 0;
+            }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
-            if constexpr (VEC) {
-                if (ok && col_ok[0]) {
-                    if constexpr (TYPE == kTypeF32) {
-                        const float4 f =
-                            __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.scales) + at));
-                        s[i][0] = f.x; s[i][1] = f.y; s[i][2] = f.z; s[i][3] = f.w;
+            for (int j = 0; j < 8; ++j) {
+                sc[j] = load_as_float(s, TYPE, 8 * j);
+                if (p.zeros) z[j / 4] |= (uint32_t)zs[8 * j] << (8 * (j % 4));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (!there) sc[j] = 0.0f;
+    };
+    // x of units [a, b) into shared memory, one row of 16-bit values per row
+    // of the x operand.  16-bit rows that start on 16 bytes are copied as they
+    // are, without a register in between.
+    const bool x_async = TYPE != kTypeF32 && p.x_vec;
+    auto stage_x = [&](int a, int b) {
+        const int octets = (b - a) * kRows, k0 = a * kW4UnitK;
+        for (int o = tid; o < octets; o += kThreads) {
+            const int left = p.K - k0 - o * 8;
+            const long long at = k0 + o * 8;
+            unsigned char *to = xs + o * 16;
+            if constexpr (TYPE != kTypeF32) {
+                const uint16_t *x = static_cast<const uint16_t *>(p.x) + at;
+                if (x_async) {
+                    const int n = min(max(left, 0), 8);
+                    for (int m = 0; m < p.M; ++m, x += p.ldx, to += pitch)
+                        cp_async16(reinterpret_cast<float *>(to),
+                                   reinterpret_cast<const float *>(n ? x : p.x), n * 2);
+                } else {
+#pragma unroll 2
+                    for (int m = 0; m < p.M; ++m) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            w[j] = (2 * j < left ? __ldg(x + m * p.ldx + 2 * j) : 0u) |
+                                   (2 * j + 1 < left ? (uint32_t)__ldg(x + m * p.ldx + 2 * j + 1) : 0u) << 16;
+                        *reinterpret_cast<uint4 *>(to + m * pitch) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            } else {
+                const float *x = static_cast<const float *>(p.x) + at;
+#pragma unroll 2
+                for (int m = 0; m < p.M; ++m) {
+                    float v[8];
+                    if (p.x_vec && left >= 8) {
+                        const float4 c = __ldg(reinterpret_cast<const float4 *>(x + m * p.ldx));
+                        const float4 d = __ldg(reinterpret_cast<const float4 *>(x + m * p.ldx) + 1);
+                        v[0] = c.x; v[1] = c.y; v[2] = c.z; v[3] = c.w;
+                        v[4] = d.x; v[5] = d.y; v[6] = d.z; v[7] = d.w;
                     } else {
-                        const uint2 f = __ldg(reinterpret_cast<const uint2 *>(
-                            static_cast<const uint16_t *>(p.scales) + at));
-                        const float2 a = unpack16<TYPE>(f.x), b = unpack16<TYPE>(f.y);
-                        s[i][0] = a.x; s[i][1] = a.y; s[i][2] = b.x; s[i][3] = b.y;
-                    }
-                    if (p.zeros) z[i] = __ldg(reinterpret_cast<const uint32_t *>(p.zeros + zat));
-                }
-            } else {
-                if (p.zeros) z[i] = 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (ok && col_ok[j]) {
-                        s[i][j] = load_as_float(p.scales, TYPE, at + 8 * j);
-                        if (p.zeros) z[i] |= (uint32_t)__ldg(p.zeros + zat + 8 * j) << (8 * j);
+                        for (int j = 0; j < 8; ++j) v[j] = j < left ? __ldg(x + m * p.ldx + j) : 0.0f;
                     }
+                    float part[8][3];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) split3(v[j], part[j]);
+#pragma unroll
+                    for (int q = 0; q < 3; ++q)
+                        *reinterpret_cast<uint4 *>(to + (q * p.M + m) * pitch) =
+                            make_uint4(pack16<T16>(part[0][q], part[1][q]),
+                                       pack16<T16>(part[2][q], part[3][q]),
+                                       pack16<T16>(part[4][q], part[5][q]),
+                                       pack16<T16>(part[6][q], part[7][q]));
                 }
             }
         }
     };
 
-    float total[NT][2][4];
+    // Where the lane reads: q of a step with even and odd number (the TMA's
+    // swizzle), and its row of x.
+    const int read_even = t * 128 + ((run << 2) ^ (t << 4));
+    const int read_odd = t * 128 + ((run << 2) ^ ((t + 4) << 4));
+    int x_row[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) x_row[j] = min(8 * j + g, rows - 1) * pitch;
+
+    float total[NT][4][4];
+    // Kept in a register: see and_or.
+    uint32_t magic;
+    asm volatile("mov.b32 %0, %1;" : "=r"(magic) : "n"(0x43004300u));
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < 4; ++b)
 #pragma unroll
             for (int e = 0; e < 4; ++e) total[j][b][e] = 0.0f;
 
-    uint32_t w[kSteps][4];
-    float s[NG][4];
-    uint32_t z[NG];
-    for (int c0 = u0; c0 < u1; c0 += p.chunk_units) {
-        const int c1 = min(u1, c0 + p.chunk_units);
-        // The first unit's weights are on their way while x is staged.
-        load_words(min(c0 + warp, c1), w);
-        load_scales(min(c0 + warp, c1), s, z);
-        if (c0 > u0) __syncthreads();
-        const int octets = (c1 - c0) * (kW4UnitK / 8);
-        for (int i = tid; i < p.M * octets; i += kThreads) {
-            const int m = i / octets, o = i % octets, k = c0 * kW4UnitK + o * 8;
-            float x[8];
-            const long long at = (long long)m * p.ldx + k;
-            if (p.x_vec && k + 8 <= p.K) {
-                if constexpr (TYPE == kTypeF32) {
-                    const float4 *f = reinterpret_cast<const float4 *>(static_cast<const float *>(p.x) + at);
-                    const float4 a = __ldg(f), b = __ldg(f + 1);
-                    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-                    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-                } else {
-                    const uint4 f = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + at));
-                    const float2 a = unpack16<TYPE>(f.x), b = unpack16<TYPE>(f.y);
-                    const float2 c = unpack16<TYPE>(f.z), d = unpack16<TYPE>(f.w);
-                    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
-                    x[4] = c.x; x[5] = c.y; x[6] = d.x; x[7] = d.y;
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[j] = k + j < p.K ? load_as_float(p.x, TYPE, at + j) : 0.0f;
-            }
-            unsigned char *to = smem + (size_t)m * pitch + o * 16;
-            if constexpr (P == 1) {
-                constexpr int T16 = TYPE == kTypeF16 ? kTypeF16 : kTypeBF16;
-                *reinterpret_cast<uint4 *>(to) =
-                    make_uint4(pack16<T16>(x[0], x[4]), pack16<T16>(x[1], x[5]),
-                               pack16<T16>(x[2], x[6]), pack16<T16>(x[3], x[7]));
-            } else {
-                float part[8][3];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) split3(x[j], part[j]);
-#pragma unroll
-                for (int q = 0; q < 3; ++q)
-                    *reinterpret_cast<uint4 *>(to + (size_t)q * p.M * pitch) =
-                        make_uint4(pack16<kTypeBF16>(part[0][q], part[4][q]),
-                                   pack16<kTypeBF16>(part[1][q], part[5][q]),
-                                   pack16<kTypeBF16>(part[2][q], part[6][q]),
-                                   pack16<kTypeBF16>(part[3][q], part[7][q]));
-            }
+    bool ok = true;
+    int stage = 0;
+    uint32_t parity = 0;
+    int u = u0 + wk;
+    if (x_async) stage_x(u0, min(u1, u0 + p.chunk_units));
+    cp_async_commit();
+#pragma unroll 1
+    for (int i = 0; i < kW4Stages; ++i) fetch(u + i * warps_k, i);
+    for (int a = u0; a < u1; a += p.chunk_units) {
+        const int b = min(u1, a + p.chunk_units);
+        if (a > u0) {
+            __syncthreads();
+            stage_x(a, b);
+            cp_async_commit();
+            cp_async_wait<0>();
+        } else {
+            if (!x_async) stage_x(a, b);
+            cp_async_wait<VEC ? 0 : kW4Stages>();  // x; the units' copies came after it
         }
         __syncthreads();
-
-        for (int u = c0 + warp; u < c1; u += kW4Warps) {
-            // The next unit's loads go out before this one is computed.
-            uint32_t w2[kSteps][4];
-            float s2[NG][4];
-            uint32_t z2[NG];
-            const int next = u + kW4Warps < c1 ? u + kW4Warps : u1;
-            load_words(next, w2);
-            load_scales(next, s2, z2);
-            const unsigned char *xu = smem + (size_t)(u - c0) * kW4UnitK * 2 + t * 16;
+        for (; ok && u < b; u += warps_k) {
+            if constexpr (VEC) {
+                if (n0 < p.N) ok = tc_wait(&full[warp][stage], parity, p.timeout_ns);
+            } else {
+                cp_async_wait<kW4Stages - 1>();
+            }
+            __syncwarp();
+            if (!ok) break;
+            const unsigned char *w = ring + stage * L::kBytes;
+            const unsigned char *xu = xs + (size_t)(u - a) * kW4UnitK * 2 + t * 16;
 #pragma unroll
             for (int gi = 0; gi < NG; ++gi) {
-                float sum[NT][2][4];
+                float sum[SUMS][NT][4][4], ones[NT][4], sc[8];
+                uint32_t z[2];
+                scales_of(w, u, gi, sc, z);
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)
+                    for (int e = 0; e < 4; ++e) {
+                        ones[j][e] = 0.0f;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sum[j][b][e] = 0.0f;
-                uint32_t z0[4], z1[4];
+                        for (int b2 = 0; b2 < 4; ++b2)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t zj = (z[gi] >> (8 * j)) & 15u;
-                    z0[j] = (BF16 ? 0x43004300u : 0x64006400u) | zj * 0x00010001u;
-                    z1[j] = 0xD400D400u + zj * 0x00100010u;
-                }
+                            for (int k = 0; k < SUMS; ++k) sum[k][j][b2][e] = 0.0f;
+                    }
 #pragma unroll
                 for (int st = 0; st < GS; ++st) {
-                    const int i = gi * GS + st;
-                    uint32_t e[4][4];
+                    const int i = gi * GS + st, r = 4 * i + t;
+                    uint32_t wi[8];
+                    if constexpr (VEC) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) expand<BF16>(w[i][j], z0[j], z1[j], e[j]);
+                        for (int h = 0; h < 2; ++h) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(
+                                w + h * kBoxBytes + i * 512 + (i % 2 ? read_odd : read_even));
+                            wi[4 * h] = v.x; wi[4 * h + 1] = v.y;
+                            wi[4 * h + 2] = v.z; wi[4 * h + 3] = v.w;
+                        }
+                    } else {
+                        // Where the row's first word lies in its first piece.
+                        const int shift = piece_shift(p.q, (u * kRows + r) * p.ldq + n0, 4) / 4;
+                        const uint32_t *from =
+                            reinterpret_cast<const uint32_t *>(w + r * kPlainPitch) + shift + g;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) wi[j] = from[8 * j];
+                    }
+                    // x04, x15, x26, x37.  Columns beyond the rows of x
+                    // repeat the last one; nobody reads what they add up to.
+                    uint32_t xv[NT][4];
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
-                        uint4 b = make_uint4(0, 0, 0, 0);
-                        if (8 * j + g < rows)
-                            b = *reinterpret_cast<const uint4 *>(xu + (size_t)(8 * j + g) * pitch +
-                                                                 i * 64);
+                        const uint4 v = *reinterpret_cast<const uint4 *>(xu + x_row[j] + i * 64);
+                        xv[j][0] = __byte_perm(v.x, v.z, 0x5410);
+                        xv[j][1] = __byte_perm(v.x, v.z, 0x7632);
+                        xv[j][2] = __byte_perm(v.y, v.w, 0x5410);
+                        xv[j][3] = __byte_perm(v.y, v.w, 0x7632);
+                        if constexpr (FORM != kExact) {
+                            constexpr uint32_t kOne = BF16 ? 0x3F803F80u : 0x3C003C00u;
+                            const uint32_t one[4] = {kOne, kOne, kOne, kOne};
+                            mma<BF16>(ones[j], one, xv[j][0], xv[j][1]);
+                            mma<BF16>(ones[j], one, xv[j][2], xv[j][3]);
+                        }
+                    }
 #pragma unroll
-                        for (int blk = 0; blk < 2; ++blk) {
-                            const uint32_t a0[4] = {e[2 * blk][0], e[2 * blk + 1][0],
-                                                    e[2 * blk][1], e[2 * blk + 1][1]};
-                            const uint32_t a1[4] = {e[2 * blk][2], e[2 * blk + 1][2],
-                                                    e[2 * blk][3], e[2 * blk + 1][3]};
-                            mma<BF16>(sum[j][blk], a0, b.x, b.y);
-                            mma<BF16>(sum[j][blk], a1, b.z, b.w);
+                    for (int blk = 0; blk < 4; ++blk) {
+                        uint32_t e0[4], e1[4], zero[2] = {};
+                        if constexpr (FORM == kExact) {
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                zero[c] = 0x43004300u |
+                                          ((z[blk / 2] >> (8 * (2 * (blk % 2) + c))) & 15u) * 0x00010001u;
+                        }
+                        expand<FORM>(wi[2 * blk], magic, zero[0], e0);
+                        expand<FORM>(wi[2 * blk + 1], magic, zero[1], e1);
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            if constexpr (FORM == kPlainInt) {
+                                // Low nibbles' pairs together, high nibbles' together.
+                                const uint32_t lo[4] = {e0[0], e1[0], e0[2], e1[2]};
+                                const uint32_t hi[4] = {e0[1], e1[1], e0[3], e1[3]};
+                                mma<BF16>(sum[0][j][blk], lo, xv[j][0], xv[j][2]);
+                                mma<BF16>(sum[SUMS - 1][j][blk], hi, xv[j][1], xv[j][3]);
+                            } else {
+                                const uint32_t a0[4] = {e0[0], e1[0], e0[1], e1[1]};
+                                const uint32_t a1[4] = {e0[2], e1[2], e0[3], e1[3]};
+                                mma<BF16>(sum[0][j][blk], a0, xv[j][0], xv[j][1]);
+                                mma<BF16>(sum[0][j][blk], a1, xv[j][2], xv[j][3]);
+                            }
                         }
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+                for (int c = 0; c < 8; ++c) {
+                    // z, or 128 + z: the byte dropped into the mantissa of 2^23.
+                    const float off =
+                        __uint_as_float(0x4B000000u | ((z[c / 4] >> (8 * (c % 4))) & 15u)) -
+                        (FORM == kOffset ? 8388480.0f : 8388608.0f);
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)
+                    for (int j = 0; j < NT; ++j)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            total[j][b][e] = fmaf(s[gi][2 * b + e / 2], sum[j][b][e], total[j][b][e]);
+                        for (int e = 0; e < 2; ++e) {
+                            const int at = 2 * (c % 2) + e;
+                            float v = sum[0][j][c / 2][at];
+                            if constexpr (FORM == kPlainInt)
+                                v = fmaf(16777216.0f, v, 1048576.0f * sum[SUMS - 1][j][c / 2][at]);
+                            if constexpr (FORM != kExact) v = fmaf(-off, ones[j][e], v);
+                            total[j][c / 2][at] = fmaf(sc[c], v, total[j][c / 2][at]);
+                        }
+                }
             }
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) w[i][j] = w2[i][j];
-#pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                z[i] = z2[i];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[i][j] = s2[i][j];
+            __syncwarp();
+            fetch(u + kW4Stages * warps_k, stage);
+            if (++stage == kW4Stages) {
+                stage = 0;
+                parity ^= 1;
             }
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!ok && lane == 0) atomicOr(p.err, kErrWaitTimeout);
+    if (__syncthreads_or(!ok)) {
+        // Copies may still be under way: let them land before the staging
+        // memory is used again.
+        const long long start = clock64();
+        while (clock64() - start < 4000000) {
+        }
+        __syncthreads();
+    }
 
     // The warps' sums, then the cluster's, in order.
-    __syncthreads();
-    float *red = reinterpret_cast<float *>(smem);  // [warp][row of x][column]
+    float *red = reinterpret_cast<float *>(smem);  // [warp along K][row of x][column]
+    {
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+            for (int e = 0; e < 2; ++e) {
+                const int c = 8 * j + 2 * t + e;
+                if (c < rows) {
+                    float *to = red + (wk * rows + c) * cols + wn * kW4Cols;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = 8 * j + 2 * t + e % 2;
-                const int col = col0 + (2 * b + e / 2) * col_step;
-                if (c < rows) red[(warp * rows + c) * kW4Cols + col] = total[j][b][e];
+                    for (int w = 0; w < 8; ++w)
+                        to[VEC ? (w / 4) * 32 + run + w % 4 : 8 * w + g] = total[j][w / 2][2 * (w % 2) + e];
+                }
             }
+    }
     __syncthreads();
-    float *mine = red + kW4Warps * rows * kW4Cols;  // [row of x][column], this CTA's sums
-    const int outs = p.M * kW4Cols;
+    float *mine = red + warps_k * rows * cols;  // [row of x][column], this CTA's sums
+    const int outs = p.M * cols, shift = 31 - __clz(cols);
     for (int i = tid; i < outs; i += kThreads) {
         float v = 0.0f;
+#pragma unroll 1
         for (int q = 0; q < P; ++q)
-            for (int k = 0; k < kW4Warps; ++k) v += red[k * rows * kW4Cols + q * outs + i];
+            for (int k = 0; k < warps_k; ++k) v += red[k * rows * cols + q * outs + i];
         if (ranks == 1) {
-            const int n = n0 + i % kW4Cols;
-            if (n < p.N) store_from_float(p.y, TYPE, (long long)(i / kW4Cols) * p.ldy + n, v);
+            const int n = c0 + (i & (cols - 1));
+            if (n < p.N) store_from_float(p.y, TYPE, (long long)(i >> shift) * p.ldy + n, v);
         } else {
             mine[i] = v;
         }
@@ -338,48 +578,57 @@ __global__ void __launch_bounds__(kThreads, NT == 1 || (NT == 2 && TYPE != kType
     for (int i = rank * kThreads + tid; i < outs; i += ranks * kThreads) {
         float v = 0.0f;
         for (int r = 0; r < ranks; ++r) v += cluster.map_shared_rank(mine, r)[i];
-        const int n = n0 + i % kW4Cols;
-        if (n < p.N) store_from_float(p.y, TYPE, (long long)(i / kW4Cols) * p.ldy + n, v);
+        const int n = c0 + (i & (cols - 1));
+        if (n < p.N) store_from_float(p.y, TYPE, (long long)(i >> shift) * p.ldy + n, v);
     }
     cluster.sync();  // no CTA leaves while another reads its sums
 }
 
 template <int TYPE, int NT, int GS, bool VEC>
-cudaError_t launch_one(const W4Params &p, int cluster, cudaStream_t stream) {
+cudaError_t launch_one(const CUtensorMap &map, const W4Params &p, int cluster, cudaStream_t stream) {
     constexpr int P = TYPE == kTypeF32 ? 3 : 1;
-    const int rows = P * p.M;
-    const size_t stage = (size_t)rows * (p.chunk_units * kW4UnitK * 2 + 64);
-    const size_t reduce = (size_t)(kW4Warps * rows + p.M) * kW4Cols * sizeof(float);
+    const int rows = P * p.M, cols = kW4Cols * p.warps_n;
+    const size_t ring = kW4Warps * kW4Stages * UnitLayout<TYPE, kSteps / GS>::kBytes;
+    const size_t x = (size_t)rows * (p.chunk_units * kW4UnitK * 2 + 64);
+    const size_t reduce = (size_t)(kW4Warps / p.warps_n * rows + p.M) * cols * sizeof(float);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.N + kW4Cols - 1) / kW4Cols) * cluster);
+    cfg.gridDim = dim3((unsigned)((p.N + cols - 1) / cols) * cluster);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = std::max(stage, reduce);
+    cfg.dynamicSmemBytes = std::max(ring + x, reduce) + 1024;
     cfg.stream = stream;
-    if (cfg.dynamicSmemBytes > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(w4_kernel<TYPE, NT, GS, VEC>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   kW4StageBytes + 16 * 1024);
+    static std::atomic<size_t> limit[kMaxDevices];  // set up so far, per device
+    if (p.device >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (limit[p.device].load() < cfg.dynamicSmemBytes) {
+        const size_t most = ring + kW4StageBytes + 8192 + 1024;
+        const size_t want = std::max(cfg.dynamicSmemBytes, std::max(most, reduce + 1024));
+        cudaError_t e = cudaFuncSetAttribute(w4_kernel<TYPE, NT, GS, VEC>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)want);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(w4_kernel<TYPE, NT, GS, VEC>,
+                                     cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         if (e != cudaSuccess) return e;
+        limit[p.device].store(want);
     }
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, w4_kernel<TYPE, NT, GS, VEC>, p);
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, w4_kernel<TYPE, NT, GS, VEC>, map, p);
 }
 
 template <int TYPE, int NT>
-cudaError_t launch_nt(const W4Params &p, bool vec, int cluster, cudaStream_t stream) {
+cudaError_t launch_nt(const CUtensorMap &map, const W4Params &p, bool vec, int cluster,
+                      cudaStream_t stream) {
     if (p.group % 128 == 0)
-        return vec ? launch_one<TYPE, NT, 4, true>(p, cluster, stream)
-                   : launch_one<TYPE, NT, 4, false>(p, cluster, stream);
+        return vec ? launch_one<TYPE, NT, 4, true>(map, p, cluster, stream)
+                   : launch_one<TYPE, NT, 4, false>(map, p, cluster, stream);
     if (p.group % 64 == 0)
-        return vec ? launch_one<TYPE, NT, 2, true>(p, cluster, stream)
-                   : launch_one<TYPE, NT, 2, false>(p, cluster, stream);
-    return vec ? launch_one<TYPE, NT, 1, true>(p, cluster, stream)
-               : launch_one<TYPE, NT, 1, false>(p, cluster, stream);
+        return vec ? launch_one<TYPE, NT, 2, true>(map, p, cluster, stream)
+                   : launch_one<TYPE, NT, 2, false>(map, p, cluster, stream);
+    return vec ? launch_one<TYPE, NT, 1, true>(map, p, cluster, stream)
+               : launch_one<TYPE, NT, 1, false>(map, p, cluster, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -426,17 +675,18 @@ int w4_max_rows(int type) { return type == kTypeF32 ? 8 : 16; }
 
 int w4_unit_bytes(int type, int M) { return (type == kTypeF32 ? 3 : 1) * M * kW4UnitK * 2; }
 
-cudaError_t launch_w4(const W4Params &p, int type, bool vec, int cluster, cudaStream_t stream) {
+cudaError_t launch_w4(const CUtensorMap &map, const W4Params &p, int type, bool vec, int cluster,
+                      cudaStream_t stream) {
     if (type == kTypeF32) {
-        if (3 * p.M <= 8) return launch_nt<kTypeF32, 1>(p, vec, cluster, stream);
-        if (3 * p.M <= 16) return launch_nt<kTypeF32, 2>(p, vec, cluster, stream);
-        return launch_nt<kTypeF32, 3>(p, vec, cluster, stream);
+        if (3 * p.M <= 8) return launch_nt<kTypeF32, 1>(map, p, vec, cluster, stream);
+        if (3 * p.M <= 16) return launch_nt<kTypeF32, 2>(map, p, vec, cluster, stream);
+        return launch_nt<kTypeF32, 3>(map, p, vec, cluster, stream);
     }
     if (type == kTypeF16)
-        return p.M <= 8 ? launch_nt<kTypeF16, 1>(p, vec, cluster, stream)
-                        : launch_nt<kTypeF16, 2>(p, vec, cluster, stream);
-    return p.M <= 8 ? launch_nt<kTypeBF16, 1>(p, vec, cluster, stream)
-                    : launch_nt<kTypeBF16, 2>(p, vec, cluster, stream);
+        return p.M <= 8 ? launch_nt<kTypeF16, 1>(map, p, vec, cluster, stream)
+                        : launch_nt<kTypeF16, 2>(map, p, vec, cluster, stream);
+    return p.M <= 8 ? launch_nt<kTypeBF16, 1>(map, p, vec, cluster, stream)
+                    : launch_nt<kTypeBF16, 2>(map, p, vec, cluster, stream);
 }
 
 cudaError_t launch_w4_quantize(const W4QuantParams &p, cudaStream_t stream) {

@@ -18,14 +18,16 @@ inline int type_bytes(int type) { return type == kTypeF32 ? 4 : 2; }
 // ---------------------------------------------------------------------------
 // Products with 4-bit weights.
 // ---------------------------------------------------------------------------
-constexpr int kW4Cols = 32;      // columns of W per CTA
-constexpr int kW4Warps = 8;      // warps of a CTA, each on its own part of K
-constexpr int kW4UnitK = 128;    // k per warp step: four 16-byte loads a lane
+constexpr int kW4Cols = 64;      // columns of W per warp
+constexpr int kW4Warps = 4;      // computing warps of a CTA, along the columns and along K
+constexpr int kW4UnitK = 128;    // k of a unit
+constexpr int kW4Stages = 3;     // units a warp has under way
+constexpr int kW4BoxCols = 32, kW4BoxRows = kW4UnitK / 8;  // TMA box of words
 constexpr int kW4MaxCluster = 8;
 
 struct W4Params {
     int M, N, K;
-    int group;
+    int group, group_shift;  // group_shift: log2 of group, or -1
     const void *x;
     long long ldx;
     const uint32_t *q;
@@ -40,10 +42,15 @@ struct W4Params {
     int units;         // ceil(K / kW4UnitK)
     int cta_units;     // units of one CTA
     int chunk_units;   // units whose x is staged at once
+    int warps_n;       // warps side by side along the columns (1, 2 or 4)
+    int device;
+    int *err;
+    unsigned long long timeout_ns;
 };
 
-// vec: four columns of q, scales and zeros may be loaded at once.
-cudaError_t launch_w4(const W4Params &p, int type, bool vec, int cluster, cudaStream_t stream);
+// vec: rows of q, scales and zeros start on 16 bytes, N % 16 == 0; q through
+// `map` (boxes of kW4BoxRows x kW4BoxCols words, 128-byte swizzle).
+cudaError_t launch_w4(const CUtensorMap &map, const W4Params &p, int type, bool vec, int cluster, cudaStream_t stream);
 // Rows of x one launch takes (FP32 rows take three of the instruction's each).
 int w4_max_rows(int type);
 // Bytes of shared memory a unit of staged x takes, and the limit for all of them.

@@ -42,4 +42,9 @@ sgemm_status_t op_encode_16(CUtensorMap *map, bool bf16, const void *base, int64
                             int64_t cols, int64_t ld, int64_t planes, int64_t plane_stride,
                             int box_rows);
 
+// Row-major rows x cols matrix of 32-bit words, rows ld words apart; boxes of
+// box_rows x box_cols, 128-byte swizzle, zero outside.
+sgemm_status_t op_encode_words(CUtensorMap *map, const uint32_t *base, int64_t rows, int64_t cols,
+                               int64_t ld, int box_cols, int box_rows);
+
 }  // namespace sgemm

@@ -41,17 +41,20 @@ def _type_of(t, name):
 def _call(fn, device, stream, *args):
     """One C-ABI call with `device` current and the stream as last argument."""
     index = device.index
-    if stream is None:
-        raw = torch.cuda.current_stream(device).cuda_stream
-    else:
-        raw = stream.cuda_stream
-    if index is None or index == torch.cuda.current_device():
+    # The raw handle: torch.cuda.current_stream() makes an object first, which
+    # takes as long as the whole C call.
+    raw = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
         status = fn(*args, raw)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             status = fn(*args, raw)
     if status != 0:
         raise _sg.SgemmError(status, fn.__name__)
+
+
+def _raw_stream(index):
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _block(x, w_gate, w_up, w_down):
@@ -158,17 +161,25 @@ class W4Matrix:
         self.K, self.N, self.group, self.device, self.dtype = K, N, group, dev, scales.dtype
         self.qweight, self.scales, self.zeros = qweight, scales, zeros
         self._weights = (q, ldq, s, lds, z, ldz)
+        self._index = dev.index
         self._fn = _sg.library().sgemm_w4_matvec
 
     def matvec(self, x, y=None, stream=None):
         """y = x @ W for M x K rows x (M is meant to be small: the weights are
         read once per 16 rows, 8 with float32).  Returns y (allocated when not given)."""
         M = x.shape[0]
-        a = _matrix(x, "x", M, self.K, self.dtype, self.device)
         if y is None:
             y = torch.empty(M, self.N, dtype=self.dtype, device=self.device)
-        _call(self._fn, self.device, stream, M, self.N, self.K, self.group, self.type, *a,
-              *self._weights, *_matrix(y, "y", M, self.N, self.dtype, self.device))
+        if (x.shape == (M, self.K) and y.shape == (M, self.N) and x.dtype is self.dtype
+                and y.dtype is self.dtype and x.get_device() == y.get_device() == self._index
+                and x.is_contiguous() and y.is_contiguous()):
+            # The usual call, a few microseconds long on the device.
+            xa, ldx, ya, ldy = x.data_ptr(), max(self.K, 1), y.data_ptr(), max(self.N, 1)
+        else:
+            xa, ldx = _matrix(x, "x", M, self.K, self.dtype, self.device)
+            ya, ldy = _matrix(y, "y", M, self.N, self.dtype, self.device)
+        _call(self._fn, self.device, stream, M, self.N, self.K, self.group, self.type, xa, ldx,
+              *self._weights, ya, ldy)
         return y
 
 
