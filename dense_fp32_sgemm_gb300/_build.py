@@ -22,9 +22,10 @@ LIB_PATH = os.path.join(BUILD, LIB_NAME)
 
 SOURCES = ["api.cu", "plan.cpp", "kernel_tile.cu", "kernel_skinny.cu", "kernel_generic.cu", "kernel_mid.cu",
            "kernel_ksplit.cu", "kernel_narrow.cu", "kernel_small.cu", "probes.cu", "noalloc.cu", "kernel_3xtf32.cu",
-           "api_ffn.cu", "kernel_ffn.cu", "kernel_w4.cu", "kernel_adamw.cu"]
+           "api_ffn.cu", "kernel_ffn.cu", "kernel_ffn_stream.cu", "kernel_w4.cu", "kernel_adamw.cu"]
 HEADERS = ["device_common.cuh", "kernels.h", "kernels_3xtf32.h", "plan.h",
-           "kernels_ffn.h", "ops_internal.h", "ops_common.cuh"]
+           "kernels_ffn.h", "ops_internal.h", "ops_common.cuh",
+           "tc_common.cuh", "ffn_gate.cuh"]
 PUBLIC_HEADERS = ["sgemm.h", "sgemm_probe.h", "sgemm_ffn.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

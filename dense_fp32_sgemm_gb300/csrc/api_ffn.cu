@@ -253,6 +253,34 @@ sgemm_status_t run_gate(const OpDevice &dev, cudaStream_t st, const Tail &tail, 
     return g.run(x, Wg, &x, &Wu);
 }
 
+// The whole block for a few rows: two passes over weights.
+sgemm_status_t run_stream(const OpDevice &dev, cudaStream_t st, const FfnArgs &a, void *y,
+                          int64_t ldy) {
+    void *h = nullptr;
+    const sgemm_status_t s = op_workspace(st, (size_t)(a.T * a.F) * sizeof(float), &h);
+    if (s != SGEMM_OK) return s;
+    const int64_t e = type_bytes(a.type);
+    auto vec = [&](const void *p, int64_t ld, int64_t n) {
+        return aligned(p, 16) && ld * e % 16 == 0 && n * e % 16 == 0;
+    };
+    FfnStreamParams p = {};
+    p.T = (int)a.T; p.N = (int)a.F; p.K = (int)a.D;
+    p.act = a.act;
+    p.x = a.x; p.ldx = a.ldx;
+    p.W = a.Wg; p.ldw = a.ldg;
+    p.W2 = a.Wu; p.ldw2 = a.ldu;
+    p.y = h; p.ldy = a.F;
+    p.device = dev.index;
+    if (launch_ffn_stream(p, a.type, true, vec(a.Wg, a.ldg, a.F) && vec(a.Wu, a.ldu, a.F),
+                          dev.num_sms, st) != cudaSuccess)
+        return SGEMM_ERR_LAUNCH;
+    p.N = (int)a.D; p.K = (int)a.F;
+    p.x = h; p.ldx = a.F;
+    p.W = a.Wd; p.ldw = a.ldd;
+    p.y = y; p.ldy = ldy;
+    return status(launch_ffn_stream(p, a.type, false, vec(a.Wd, a.ldd, a.D), dev.num_sms, st));
+}
+
 sgemm_status_t zero_matrix(void *p, int64_t ld, int64_t rows, int64_t cols, int type,
                            cudaStream_t st) {
     const size_t e = type_bytes(type);
@@ -288,6 +316,12 @@ sgemm_status_t sgemm_ffn_forward(int64_t T, int64_t D, int64_t F, int type, int 
     s = op_device(&dev);
     if (s != SGEMM_OK) return s;
     if (F == 0) return zero_matrix(y, ldy, T, D, type, st);
+    // Few rows: one pass over the weights on the FP32 pipe.  From five rows of
+    // 16-bit weights on that is the slower way (8 x 4096 x 12288: 167 us, the
+    // tensor cores 91), unless they would have to be copied to aligned rows.
+    const bool in_place = type != kTypeF32 && aligned(Wg, 16) && aligned(Wu, 16) &&
+                          aligned(Wd, 16) && ldg % 8 == 0 && ldu % 8 == 0 && ldd % 8 == 0;
+    if (!saved && (T <= 4 || (T <= kFfnStreamRows && !in_place))) return run_stream(dev, st, a, y, ldy);
     Arena w;
     Tail tail;
     const Kept kept(T, F, type);
@@ -516,6 +550,12 @@ sgemm_status_t sgemm_adamw_step(const sgemm_adamw_tensor_t *tensors, int64_t cou
     h.grad_scale = (float)grad_scale;
     h.p_type = param_type; h.g_type = grad_type; h.c_type = copy_type;
     const size_t state_vec = state_bits == 8 ? 8 : 16;
+    // Long chunks keep a warp's ring filled; short ones (down to one block per
+    // warp) give every SM eight CTAs where there is little to do.
+    int64_t total = 0;
+    for (int64_t i = 0; i < count; ++i) total += tensors[i].numel;
+    h.chunk = kAdamChunk;
+    while (h.chunk > kAdamMinChunk && total / h.chunk < 8 * dev.num_sms) h.chunk /= 2;
     AdamTensor batch[kAdamTensors];
     int n = 0;
     uint64_t chunks = 0;
@@ -523,9 +563,9 @@ sgemm_status_t sgemm_adamw_step(const sgemm_adamw_tensor_t *tensors, int64_t cou
     for (int64_t i = 0; i < count; ++i) {
         const sgemm_adamw_tensor_t &t = tensors[i];
         if (t.numel == 0) continue;
-        const uint64_t need = (uint64_t)((t.numel + kAdamChunk - 1) / kAdamChunk);
+        const uint64_t need = (uint64_t)((t.numel + h.chunk - 1) / h.chunk);
         if (n == kAdamTensors || (n > 0 && chunks + need > INT32_MAX)) {
-            if (launch_adamw(batch, n, (unsigned)chunks, state_bits, h, st) != cudaSuccess)
+            if (launch_adamw(batch, n, (unsigned)chunks, state_bits, h, dev.index, st) != cudaSuccess)
                 return SGEMM_ERR_LAUNCH;
             n = 0;
             chunks = 0;
@@ -539,7 +579,7 @@ sgemm_status_t sgemm_adamw_step(const sgemm_adamw_tensor_t *tensors, int64_t cou
                 aligned(t.v, state_vec) && (!t.copy || aligned(t.copy, 16));
         chunks += need;
     }
-    return status(n ? launch_adamw(batch, n, (unsigned)chunks, state_bits, h, st) : cudaSuccess);
+    return status(n ? launch_adamw(batch, n, (unsigned)chunks, state_bits, h, dev.index, st) : cudaSuccess);
 }
 
 }  // extern "C"

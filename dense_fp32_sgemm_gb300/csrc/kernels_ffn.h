@@ -74,7 +74,7 @@ cudaError_t launch_w4_quantize(const W4QuantParams &p, cudaStream_t stream);
 // AdamW.
 // ---------------------------------------------------------------------------
 constexpr int kAdamBlock = 256;   // elements that share a scale of the 8-bit states
-constexpr int kAdamChunk = 4096;  // elements of one tensor a CTA takes
+constexpr int kAdamMinChunk = 2048, kAdamChunk = 16384;  // elements of one tensor a CTA takes
 constexpr int kAdamTensors = 400; // tensors of one launch
 
 struct AdamTensor {
@@ -96,11 +96,12 @@ struct AdamHyper {
     float eps;
     float grad_scale;
     int p_type, g_type, c_type;
+    int chunk;  // elements of one tensor a CTA takes
 };
 
 // `tensors` (count <= kAdamTensors) with chunk0 filled in; `chunks` in all.
 cudaError_t launch_adamw(const AdamTensor *tensors, int count, unsigned chunks, int state_bits,
-                         const AdamHyper &h, cudaStream_t stream);
+                         const AdamHyper &h, int device, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
 // The gated block's products on the tensor cores (kernel_ffn.cu).
@@ -183,5 +184,27 @@ struct FfnPrepJob {
 constexpr int kFfnPrepJobs = 5;
 cudaError_t launch_ffn_prep(const FfnPrepJob *jobs, int count, int type, int num_sms,
                             cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// The gated block for a few rows (kernel_ffn_stream.cu).
+// ---------------------------------------------------------------------------
+constexpr int kFfnStreamRows = 8;  // most rows it takes
+
+struct FfnStreamParams {
+    int T, N, K;
+    int act;
+    const void *x;        // T x K: of the weights' type (gate) or FP32 (down)
+    long long ldx;
+    const void *W, *W2;   // K x N; W2 of the gate's two
+    long long ldw, ldw2;
+    void *y;              // T x N: FP32 (gate: h) or of the weights' type
+    long long ldy;
+    int device;
+    // set by launch_ffn_stream
+    int lanes_per_row, cta_rows, chunk_rows;
+};
+// vec: 16 bytes of a row's columns may be loaded at once (N a multiple too).
+cudaError_t launch_ffn_stream(const FfnStreamParams &p, int type, bool gate, bool vec, int num_sms,
+                              cudaStream_t stream);
 
 }  // namespace sgemm

@@ -51,7 +51,7 @@ enum {
  * one D x 2F matrix); Wd: F x D (ldd >= D); y: T x D (ldy >= D), not
  * overlapping any input.  All matrices are of `type` (SGEMM_TYPE_*); sums are
  * held in 32 bits.  With 16-bit types h is rounded to the type between the two
- * products (except where T is at most 8), with FP32 nothing is rounded below
+ * products (except in the form for few rows, T <= 8), with FP32 nothing is rounded below
  * 24 bits.
  * saved: NULL, or a device buffer (16-byte aligned) of sgemm_ffn_saved_floats(T, F,
  * type) floats for sgemm_ffn_backward: it receives u act'(g) and act(g) in 32
