@@ -116,7 +116,7 @@ struct Tail {
 constexpr int kMinShare = 8;  // steps
 
 size_t tail_bytes(const OpDevice &dev) {
-    return (size_t)2 * dev.num_sms * ffn_slot_floats(true) * sizeof(float);
+    return (size_t)2 * dev.num_sms * ffn_slot_floats(false, true) * sizeof(float);
 }
 // One per tail tile (fewer than workers), CTA of a worker and epilogue warp.
 size_t tail_counters(const OpDevice &dev) { return (size_t)dev.num_sms * 8; }
@@ -180,7 +180,7 @@ struct Product {
     float *partials;
     int *counters;
     FfnGemmParams p = {};
-    FfnMaps maps;
+    FfnMaps maps = {};
 
     Product(const OpDevice &d, cudaStream_t s, const Tail &t, int mode, int type, int64_t M, int64_t N, int64_t K,
             bool a_mn, bool b_mn)
@@ -196,25 +196,30 @@ struct Product {
         p.skip_loads_from = dev.skip_loads_from;
     }
 
-    sgemm_status_t map(CUtensorMap *m, const FfnOperand &o, bool mn) {
+    sgemm_status_t map(CUtensorMap *m, const FfnOperand &o, int box_rows) {
         return op_encode_16(m, p.type != kTypeF16, o.p, o.rows, o.cols, o.ld, o.planes,
-                            o.plane_stride, mn ? kFfnBK : kFfnBM);
+                            o.plane_stride, box_rows);
     }
 
     sgemm_status_t run(const FfnOperand &A, const FfnOperand &B, const FfnOperand *A2 = nullptr,
                        const FfnOperand *B2 = nullptr) {
-        const bool pair = p.type != kTypeF32 && p.M > kFfnBM;
-        const int cg = pair ? 2 : 1;
-        const int tile_n = (p.mode == kFfnGate ? kFfnBN / 2 : kFfnBN) * cg;
+        const bool pair = p.M > kFfnBM;
+        const int cg = pair ? 2 : 1, b_cols = ffn_b_cols(p.type == kTypeF32, pair);
+        const int tile_n = b_cols * cg / (p.mode == kFfnGate ? 2 : 1);
+        // Rows of a short A that do not exist are not brought in: what they
+        // would add goes into rows of the accumulator that nobody reads.
+        const int a_rows = p.a_mn ? kFfnBK : std::min(kFfnBM, (p.M + 7) / 8 * 8);
+        const int b_rows = p.b_mn ? kFfnBK : b_cols;
+        p.a_bytes = (p.a_mn ? kFfnBM : a_rows) * kFfnBK * 2;
         p.tiles_m = (p.M + kFfnBM * cg - 1) / (kFfnBM * cg);
         p.tiles_n = (p.N + tile_n - 1) / tile_n;
         const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * p.outs;
         const int64_t steps = (int64_t)p.kblocks * p.segs;
         if (tiles > INT32_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
-        sgemm_status_t s = map(&maps.a[0], A, p.a_mn);
-        if (s == SGEMM_OK) s = map(&maps.a[1], A2 ? *A2 : A, p.a_mn);
-        if (s == SGEMM_OK) s = map(&maps.b[0], B, p.b_mn);
-        if (s == SGEMM_OK) s = map(&maps.b[1], B2 ? *B2 : B, p.b_mn);
+        sgemm_status_t s = map(&maps.a[0], A, a_rows);
+        if (s == SGEMM_OK && A2) s = map(&maps.a[1], *A2, a_rows);
+        if (s == SGEMM_OK) s = map(&maps.b[0], B, b_rows);
+        if (s == SGEMM_OK && B2) s = map(&maps.b[1], *B2, b_rows);
         if (s != SGEMM_OK) return s;
         p.workers = dev.num_sms / cg;
         p.full_tiles = (int)(tiles / p.workers);
@@ -250,7 +255,7 @@ sgemm_status_t run_gate(const OpDevice &dev, cudaStream_t st, const Tail &tail, 
     g.p.act = a.act;
     g.store_planes(h);
     if (keep) kept.set(g.p, keep);
-    return g.run(x, Wg, &x, &Wu);
+    return g.run(x, Wg, nullptr, &Wu);
 }
 
 // The whole block for a few rows: two passes over weights.

@@ -25,8 +25,10 @@
 //   warp 1       one thread issues tcgen05.mma and releases stages by commit
 //   warp 2       allocates and frees tensor memory
 //   warps 4-11   epilogue, from one of two accumulators while the other fills
-// CG = 2: a pair of CTAs on one 256 x 256 tile, each holding half of A's rows
-// and half of B's columns; the first CTA's thread issues for both.
+// CG = 2: a pair of CTAs on one 256 x 256 tile (FP32: 256 x 128, as a thread
+// holds its sums in registers), each holding half of A's rows and half of B's
+// columns; the first CTA's thread issues for both.  A launch may start while the
+// one before it on the stream drains (programmatic dependent launch).
 // Every wait is bounded; a role that gives up flags the error word, the others
 // run out in turn, and the CTA lets its copies land before it leaves.
 #include <algorithm>
@@ -38,11 +40,20 @@ namespace sgemm {
 namespace {
 
 constexpr uint32_t kABytes = kFfnBM * kFfnBK * 2;
-constexpr uint32_t kBBytes = kFfnBN * kFfnBK * 2;
-constexpr uint32_t kStageBytes = kABytes + kBBytes;
 constexpr int kEpiWarps = 8;
 constexpr uint32_t kEpiBytes = 32 * 128;  // an epilogue warp's staging: 32 rows of 32 values
-constexpr size_t kSmemBytes = (size_t)kFfnStages * kStageBytes + kEpiWarps * kEpiBytes + 1024;
+
+// Sizes of a form: type and CTAs to a tile.
+template <int TYPE, int CG>
+struct Form {
+    static constexpr int kBCols = ffn_b_cols(TYPE == kTypeF32, CG == 2);  // of B per CTA
+    static constexpr uint32_t kBBytes = kBCols * kFfnBK * 2;
+    static constexpr uint32_t kStageBytes = kABytes + kBBytes;
+    static constexpr int kStages = 192 * 1024 / kStageBytes;
+    static constexpr int kAccCols = kBCols * CG;  // tensor-memory columns of an accumulator
+    static constexpr int kParts = kAccCols / 64;  // groups of 32 columns of an epilogue warp
+    static constexpr size_t kSmem = (size_t)kStages * kStageBytes + kEpiWarps * kEpiBytes + 1024;
+};
 constexpr uint32_t kBlockBytes = 64 * kFfnBK * 2;  // 64 of m or n by 64 k
 
 // FP32: which planes of A and B the six products take, smallest first.
@@ -222,11 +233,12 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const FfnGemmParams p) {
     constexpr bool kSplit = TYPE == kTypeF32;         // three planes, sums in registers
     constexpr int kProducts = kSplit ? 6 : 1;
-    constexpr int kAccCols = 128 * CG;                // tensor-memory columns of an accumulator
-    constexpr int kTileN = MODE == kFfnGate ? 64 * CG : 128 * CG;
-    constexpr int kParts = 2 * CG;                    // groups of 32 columns of an epilogue warp
+    using Fm = Form<TYPE, CG>;
+    constexpr int kAccCols = Fm::kAccCols, kStages = Fm::kStages, kParts = Fm::kParts;
+    constexpr uint32_t kStageBytes = Fm::kStageBytes;
+    constexpr int kTileN = MODE == kFfnGate ? kAccCols / 2 : kAccCols;
     extern __shared__ unsigned char ffn_smem_raw[];
-    __shared__ uint64_t full[kFfnStages], empty[kFfnStages], acc_full[2], acc_empty[2];
+    __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int s_abort;
 
@@ -239,7 +251,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     const int worker = (int)blockIdx.x / CG;
 
     if (tid == 0) {
-        for (int s = 0; s < kFfnStages; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -250,12 +262,16 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         s_abort = 0;
         fence_barrier_init();
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 2) tc_alloc<CG, 2 * kAccCols>(&tmem_slot);
     tc_fence_before_sync();
     __syncthreads();
     if constexpr (CG == 2) cluster_barrier();
     tc_fence_after_sync();
     const uint32_t tmem = tmem_slot;
+    // Up to here nothing touched memory that the kernel before this one on the
+    // stream reads or writes; its results are complete after this.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     const int steps = p.kblocks * p.segs;  // of a tile; kProducts stages each
 
@@ -296,7 +312,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                             const int pa = kSplit ? kPlaneA[prod] : 0, pb = kSplit ? kPlaneB[prod] : 0;
                             unsigned char *a = smem + s * kStageBytes, *b = a + kABytes;
                             // The pair's loads all complete on the first CTA's barrier.
-                            if (rank == 0) mbar_arrive_expect_tx(&full[s], kStageBytes * CG);
+                            if (rank == 0) mbar_arrive_expect_tx(&full[s], (p.a_bytes + Fm::kBBytes) * CG);
                             const uint32_t bar = bar0 + s * 8;
                             if (p.a_mn) {
                                 tc_load_3d<CG>(a, ma, bar, m0, k, pa);
@@ -306,21 +322,23 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                             }
                             if constexpr (MODE == kFfnGate) {
                                 // One CTA: 64 columns of each matrix.  A pair: the
-                                // first CTA brings 128 of Wg, the second of Wu.
+                                // first CTA brings Wg's columns, the second Wu's.
                                 const CUtensorMap *m1 = CG == 2 ? &maps.b[rank] : &maps.b[0];
                                 const CUtensorMap *m2 = CG == 2 ? m1 : &maps.b[1];
                                 tc_load_3d<CG>(b, m1, bar, n0, k, pb);
-                                tc_load_3d<CG>(b + kBlockBytes, m2, bar, CG == 2 ? n0 + 64 : n0, k, pb);
+                                if constexpr (Fm::kBCols == 128)
+                                    tc_load_3d<CG>(b + kBlockBytes, m2, bar, CG == 2 ? n0 + 64 : n0, k, pb);
                             } else {
-                                const int n = n0 + (int)rank * kFfnBN;
+                                const int n = n0 + (int)rank * Fm::kBCols;
                                 if (p.b_mn) {
                                     tc_load_3d<CG>(b, mb, bar, n, k, pb);
-                                    tc_load_3d<CG>(b + kBlockBytes, mb, bar, n + 64, k, pb);
+                                    if constexpr (Fm::kBCols == 128)
+                                        tc_load_3d<CG>(b + kBlockBytes, mb, bar, n + 64, k, pb);
                                 } else {
                                     tc_load_3d<CG>(b, mb, bar, k, n, pb);
                                 }
                             }
-                            if (++s == kFfnStages) {
+                            if (++s == kStages) {
                                 s = 0;
                                 parity ^= 1;
                             }
@@ -330,8 +348,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             }
             // The last releases of the stages have to arrive before the CTA
             // leaves.
-            for (int i = max(0, it - kFfnStages); ok && i < it; ++i)
-                if (!tc_wait(&empty[i % kFfnStages], (i / kFfnStages) & 1, p.timeout_ns)) {
+            for (int i = max(0, it - kStages); ok && i < it; ++i)
+                if (!tc_wait(&empty[i % kStages], (i / kStages) & 1, p.timeout_ns)) {
                     atomicOr(p.err, kErrDrainTimeout);
                     s_abort = 1;
                     ok = false;
@@ -344,7 +362,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         // 650 clocks on a stage whose products take 512.
         if (rank == 0) {
             const uint32_t idesc =
-                tc_idesc(kFfnBM * CG, kFfnBN * CG, TYPE != kTypeF16, p.a_mn != 0, p.b_mn != 0);
+                tc_idesc(kFfnBM * CG, kAccCols, TYPE != kTypeF16, p.a_mn != 0, p.b_mn != 0);
             // Per 16 k: two groups of eight rows (MN-major) or 32 bytes along
             // the swizzled row (K-major); units of 16 bytes.
             const uint32_t a_step = (p.a_mn ? 2048 : 32) >> 4, b_step = (p.b_mn ? 2048 : 32) >> 4;
@@ -378,7 +396,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                             tc_commit<CG>(&empty[s]);
                         }
                         __syncwarp();
-                        if (++s == kFfnStages) {
+                        if (++s == kStages) {
                             s = 0;
                             parity ^= 1;
                         }
@@ -399,13 +417,13 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     } else if (warp >= 4) {
         const int quad = warp & 3, half = (warp - 4) >> 2;
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
-        unsigned char *stage = smem + kFfnStages * kStageBytes + (warp - 4) * kEpiBytes;
+        unsigned char *stage = smem + kStages * kStageBytes + (warp - 4) * kEpiBytes;
         // Part j is 32 accumulator columns; in the gate's product parts come
         // in twos, the same columns of g and u.
         constexpr int kTwo = MODE == kFfnGate ? 2 : 1;
         auto part_col = [&](int j) {
-            return MODE == kFfnGate ? (j & 1) * 64 * CG + half * 32 * CG + 32 * (j >> 1)
-                                    : half * 64 * CG + 32 * j;
+            return MODE == kFfnGate ? (j & 1) * (kAccCols / 2) + half * (kAccCols / 4) + 32 * (j >> 1)
+                                    : half * (kAccCols / 2) + 32 * j;
         };
         int buf = 0;
         uint32_t parity = 0;
@@ -506,7 +524,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             if (emit) {
 #pragma unroll(kSplit ? kParts : 1)
                 for (int j = 0; j < kParts; j += kTwo) {
-                    const int n = n_tile + (MODE == kFfnGate ? half * 32 * CG + 16 * j : part_col(j));
+                    const int n = n_tile + (MODE == kFfnGate ? half * (kAccCols / 4) + 16 * j : part_col(j));
                     const int cols = p.N - n;
                     if (cols <= 0) break;
                     const long long kept =
@@ -640,19 +658,21 @@ template <int TYPE, int MODE, int CG>
 cudaError_t launch_one(const FfnMaps &maps, const FfnGemmParams &p, cudaStream_t stream) {
     const auto kernel = ffn_gemm_kernel<TYPE, MODE, CG>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kSmemBytes);
+                                         (int)Form<TYPE, CG>::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(CG * (p.full_tiles > 0 ? p.workers : p.tail_workers));
     cfg.blockDim = dim3(kFfnThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.dynamicSmemBytes = Form<TYPE, CG>::kSmem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = CG;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, maps, p);
 }
 
@@ -669,7 +689,9 @@ cudaError_t launch_mode(const FfnMaps &maps, const FfnGemmParams &p, cudaStream_
 
 cudaError_t launch_ffn_gemm(const FfnMaps &maps, const FfnGemmParams &p, bool pair,
                             cudaStream_t stream) {
-    if (p.type == kTypeF32) return launch_mode<kTypeF32, 1>(maps, p, stream);
+    if (p.type == kTypeF32)
+        return pair ? launch_mode<kTypeF32, 2>(maps, p, stream)
+                    : launch_mode<kTypeF32, 1>(maps, p, stream);
     if (p.type == kTypeF16)
         return pair ? launch_mode<kTypeF16, 2>(maps, p, stream)
                     : launch_mode<kTypeF16, 1>(maps, p, stream);

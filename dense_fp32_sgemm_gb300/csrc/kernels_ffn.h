@@ -123,9 +123,9 @@ enum : int {
 };
 
 constexpr int kFfnBM = 128;      // rows of a CTA's tile
-constexpr int kFfnBN = 128;      // columns of B each CTA brings in per k block
+// Columns of B that each CTA brings in per k block.
+constexpr int ffn_b_cols(bool f32, bool pair) { return f32 && pair ? 64 : 128; }
 constexpr int kFfnBK = 64;       // k per stage: one 128-byte swizzled row
-constexpr int kFfnStages = 6;
 constexpr int kFfnThreads = 384; // 4 warps of roles, 8 of epilogue
 
 struct FfnGemmParams {
@@ -136,6 +136,7 @@ struct FfnGemmParams {
     int segs;            // products added up (2: A B + A2 B2)
     int outs;            // outputs (2: A B -> C[0], A B2 -> C[1])
     int a_mn, b_mn;      // operand is MN-major: its rows run along k
+    uint32_t a_bytes;    // of A per CTA and stage: rows of `a` boxes, 128 bytes each
     int tiles_m, tiles_n;
     int kblocks;         // ceil(K / kFfnBK)
     // Workers (CTAs or pairs) take whole tiles round-robin, full_tiles each;
@@ -161,7 +162,9 @@ struct FfnGemmParams {
 };
 
 // Floats of a CTA's accumulator; a worker's partial tile has one per CTA.
-inline int ffn_slot_floats(bool pair) { return kFfnBM * kFfnBN * (pair ? 2 : 1); }
+inline int ffn_slot_floats(bool f32, bool pair) {
+    return kFfnBM * ffn_b_cols(f32, pair) * (pair ? 2 : 1);
+}
 
 // One operand's TMA descriptor as the kernel wants it: boxes of 64 along the
 // contiguous dimension by `rows` rows.
