@@ -113,8 +113,6 @@ struct Tail {
     float *partials = nullptr;
     int *counters = nullptr;
 };
-constexpr int kMinShare = 8;  // steps
-
 size_t tail_bytes(const OpDevice &dev) {
     return (size_t)2 * dev.num_sms * ffn_slot_floats(false, true) * sizeof(float);
 }
@@ -172,6 +170,58 @@ struct Kept {
     }
 };
 
+// Single CTAs or pairs, and how the tiles left over after whole rounds are cut
+// along k: the least of a model of SM clocks, fitted to GB300 times.  A step (64 k)
+// of a 256 x 256 pair tile takes 512, of a 128 x 128 tile 330 (its operands pass
+// through shared memory at the full rate); FP32 steps are six of 330.  Cutting a
+// tile in n pieces costs 128 KB a CTA written (6500 clocks on all SMs at once) and
+// n times as much read by the last to finish, half of both for single CTAs: at 333 x
+// 1000 x 1504 the cut products took 12 us longer than their steps.
+struct FfnPlan {
+    bool pair;
+    int tiles_m, tiles_n, workers, full_tiles, tail_tiles, tail_workers;
+};
+
+FfnPlan ffn_plan(const FfnGemmParams &p, int num_sms) {
+    FfnPlan best = {};
+    double least = -1.0;
+    const bool f32 = p.type == kTypeF32;
+    for (int pair = 0; pair <= (p.M > kFfnBM ? 1 : 0); ++pair) {
+        const int cg = pair ? 2 : 1, b_cols = ffn_b_cols(f32, pair != 0);
+        const int tile_n = b_cols * cg / (p.mode == kFfnGate ? 2 : 1);
+        FfnPlan q;
+        q.pair = pair != 0;
+        q.tiles_m = (p.M + kFfnBM * cg - 1) / (kFfnBM * cg);
+        q.tiles_n = (p.N + tile_n - 1) / tile_n;
+        q.workers = num_sms / cg;
+        const int64_t tiles = (int64_t)q.tiles_m * q.tiles_n * p.outs;
+        const int64_t steps = (int64_t)p.kblocks * p.segs;
+        q.full_tiles = (int)(tiles / q.workers);
+        q.tail_tiles = (int)(tiles % q.workers);
+        const double step = f32 ? 6 * 330.0 : pair ? 512.0 : 330.0;
+        const double size = ffn_slot_floats(f32, pair != 0) / 32768.0;
+        const double whole = 4000.0 + (pair ? 5000.0 : 2500.0) + step * (double)(q.full_tiles * steps);
+        // n whole pieces a tile, or (n = 0) even shares for all workers, whose
+        // ends meet inside tiles.
+        for (int n = 0; n <= std::max(1, q.workers / std::max(1, q.tail_tiles)); ++n) {
+            if (n > steps || (n == 0 && q.tail_tiles * steps < 4 * q.workers)) continue;
+            q.tail_workers = n == 0 ? q.workers : q.tail_tiles * n;
+            if (q.tail_tiles == 0) q.tail_workers = 0;
+            double cost = whole;
+            if (q.tail_tiles) {
+                const double pieces = n == 0 ? (double)q.workers / q.tail_tiles + 1.0 : n;
+                cost += step * (double)(q.tail_tiles * steps) / q.tail_workers +
+                        (n == 1 ? 0.0 : size * (f32 ? 3000.0 + 1500.0 * pieces : 8000.0 + 3500.0 * pieces));
+            }
+            if (least < 0.0 || cost < least) {
+                least = cost;
+                best = q;
+            }
+        }
+    }
+    return best;
+}
+
 // Sets up and launches one product.  A and B (A2 and B2) as they lie in
 // memory; a_mn, b_mn: their rows run along k.
 struct Product {
@@ -191,6 +241,7 @@ struct Product {
         p.segs = p.outs = 1;
         p.a_mn = a_mn; p.b_mn = b_mn;
         p.kblocks = (int)((K + kFfnBK - 1) / kFfnBK);
+        p.device = dev.index;
         p.err = dev.err;
         p.timeout_ns = dev.timeout_ns;
         p.skip_loads_from = dev.skip_loads_from;
@@ -203,34 +254,28 @@ struct Product {
 
     sgemm_status_t run(const FfnOperand &A, const FfnOperand &B, const FfnOperand *A2 = nullptr,
                        const FfnOperand *B2 = nullptr) {
-        const bool pair = p.M > kFfnBM;
-        const int cg = pair ? 2 : 1, b_cols = ffn_b_cols(p.type == kTypeF32, pair);
-        const int tile_n = b_cols * cg / (p.mode == kFfnGate ? 2 : 1);
+        const FfnPlan plan = ffn_plan(p, dev.num_sms);
+        const int b_cols = ffn_b_cols(p.type == kTypeF32, plan.pair);
         // Rows of a short A that do not exist are not brought in: what they
         // would add goes into rows of the accumulator that nobody reads.
         const int a_rows = p.a_mn ? kFfnBK : std::min(kFfnBM, (p.M + 7) / 8 * 8);
         const int b_rows = p.b_mn ? kFfnBK : b_cols;
         p.a_bytes = (p.a_mn ? kFfnBM : a_rows) * kFfnBK * 2;
-        p.tiles_m = (p.M + kFfnBM * cg - 1) / (kFfnBM * cg);
-        p.tiles_n = (p.N + tile_n - 1) / tile_n;
-        const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * p.outs;
-        const int64_t steps = (int64_t)p.kblocks * p.segs;
-        if (tiles > INT32_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
+        p.tiles_m = plan.tiles_m;
+        p.tiles_n = plan.tiles_n;
+        if ((int64_t)plan.tiles_m * plan.tiles_n * p.outs > INT32_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
         sgemm_status_t s = map(&maps.a[0], A, a_rows);
         if (s == SGEMM_OK && A2) s = map(&maps.a[1], *A2, a_rows);
         if (s == SGEMM_OK) s = map(&maps.b[0], B, b_rows);
         if (s == SGEMM_OK && B2) s = map(&maps.b[1], *B2, b_rows);
         if (s != SGEMM_OK) return s;
-        p.workers = dev.num_sms / cg;
-        p.full_tiles = (int)(tiles / p.workers);
-        p.tail_tiles = (int)(tiles % p.workers);
-        // The tail's shares: at least kMinShare steps each, where there are
-        // as many, so that a share is worth its partial tile's way through L2.
-        p.tail_workers = (int)std::min<int64_t>(
-            p.workers, std::max<int64_t>(p.tail_tiles, p.tail_tiles * steps / kMinShare));
+        p.workers = plan.workers;
+        p.full_tiles = plan.full_tiles;
+        p.tail_tiles = plan.tail_tiles;
+        p.tail_workers = plan.tail_workers;
         p.partials = partials;
         p.counters = counters;
-        return status(launch_ffn_gemm(maps, p, pair, st));
+        return status(launch_ffn_gemm(maps, p, plan.pair, st));
     }
 
     void store(void *C, int64_t ld, void *C2 = nullptr, int64_t ld2 = 0) {

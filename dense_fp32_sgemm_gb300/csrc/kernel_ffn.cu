@@ -32,6 +32,7 @@
 // Every wait is bounded; a role that gives up flags the error word, the others
 // run out in turn, and the CTA lets its copies land before it leaves.
 #include <algorithm>
+#include <atomic>
 
 #include "ffn_gate.cuh"
 #include "tc_common.cuh"
@@ -40,6 +41,7 @@ namespace sgemm {
 namespace {
 
 constexpr uint32_t kABytes = kFfnBM * kFfnBK * 2;
+constexpr int kMaxDevices = 64;
 constexpr int kEpiWarps = 8;
 constexpr uint32_t kEpiBytes = 32 * 128;  // an epilogue warp's staging: 32 rows of 32 values
 
@@ -657,9 +659,14 @@ __global__ void __launch_bounds__(256) ffn_prep_kernel(const PrepTable t) {
 template <int TYPE, int MODE, int CG>
 cudaError_t launch_one(const FfnMaps &maps, const FfnGemmParams &p, cudaStream_t stream) {
     const auto kernel = ffn_gemm_kernel<TYPE, MODE, CG>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)Form<TYPE, CG>::kSmem);
-    if (e != cudaSuccess) return e;
+    static std::atomic<bool> configured[kMaxDevices];
+    if (p.device >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!configured[p.device].load()) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Form<TYPE, CG>::kSmem);
+        if (e != cudaSuccess) return e;
+        configured[p.device].store(true);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(CG * (p.full_tiles > 0 ? p.workers : p.tail_workers));
     cfg.blockDim = dim3(kFfnThreads);

@@ -144,6 +144,7 @@ struct FfnGemmParams {
     int workers, full_tiles, tail_tiles, tail_workers;
     float *partials;     // 2 slots per worker of kFfnSlotFloats per CTA (tail)
     int *counters;       // tail_tiles x CTAs of a worker x 8, zero at rest
+    int device;
     // kFfnStore: C, `type`.  kFfnGate: C[0] = h.  kFfnGateGrad: C[0] = dg,
     // C[1] = du.  h, dg and du are 16-bit operands for the next product: one
     // plane of `type`, or three bf16 planes.
