@@ -179,39 +179,71 @@ struct Kept {
 // 1000 x 1504 the cut products took 12 us longer than their steps.
 struct FfnPlan {
     bool pair;
-    int tiles_m, tiles_n, workers, full_tiles, tail_tiles, tail_workers;
+    int workers, long_tiles, extra, full_tiles, tail_tiles, tail_workers;
 };
 
-FfnPlan ffn_plan(const FfnGemmParams &p, int num_sms) {
+void tile_problems(FfnGemmParams &p, bool pair) {
+    const int bm = kFfnBM * (pair ? 2 : 1);
+    const int tile_n = ffn_b_cols(p.type == kTypeF32, pair) * (pair ? 2 : 1) / (p.mode == kFfnGate ? 2 : 1);
+    p.tiles = 0;
+    for (int i = 0; i < p.count; ++i) {
+        FfnProblem &q = p.prob[i];
+        q.tiles_m = (q.M + bm - 1) / bm;
+        q.tiles_n = (q.N + tile_n - 1) / tile_n;
+        q.tile0 = p.tiles;
+        p.tiles += q.tiles_m * q.tiles_n;
+    }
+}
+
+FfnPlan ffn_plan(FfnGemmParams &p, int num_sms) {
     FfnPlan best = {};
     double least = -1.0;
     const bool f32 = p.type == kTypeF32;
-    for (int pair = 0; pair <= (p.M > kFfnBM ? 1 : 0); ++pair) {
-        const int cg = pair ? 2 : 1, b_cols = ffn_b_cols(f32, pair != 0);
-        const int tile_n = b_cols * cg / (p.mode == kFfnGate ? 2 : 1);
+    bool tall = false;
+    for (int i = 0; i < p.count; ++i) tall = tall || p.prob[i].M > kFfnBM;
+    auto steps_of = [&](int i) { return (int64_t)p.prob[i].kblocks * p.prob[i].segs; };
+    // At most two lengths of tiles: the products up to `others` have the longer.
+    int others = 0;
+    for (int i = 1; i < p.count; ++i)
+        if (steps_of(i) != steps_of(0)) {
+            others = i;
+            break;
+        }
+    for (int pair = 0; pair <= (tall ? 1 : 0); ++pair) {
+        tile_problems(p, pair != 0);
         FfnPlan q;
         q.pair = pair != 0;
-        q.tiles_m = (p.M + kFfnBM * cg - 1) / (kFfnBM * cg);
-        q.tiles_n = (p.N + tile_n - 1) / tile_n;
-        q.workers = num_sms / cg;
-        const int64_t tiles = (int64_t)q.tiles_m * q.tiles_n * p.outs;
-        const int64_t steps = (int64_t)p.kblocks * p.segs;
-        q.full_tiles = (int)(tiles / q.workers);
-        q.tail_tiles = (int)(tiles % q.workers);
+        q.workers = num_sms / (pair ? 2 : 1);
+        const int64_t steps = steps_of(p.count - 1);
         const double step = f32 ? 6 * 330.0 : pair ? 512.0 : 330.0;
         const double size = ffn_slot_floats(f32, pair != 0) / 32768.0;
-        const double whole = 4000.0 + (pair ? 5000.0 : 2500.0) + step * (double)(q.full_tiles * steps);
+        double whole = 4000.0 + (pair ? 5000.0 : 2500.0);
+        q.long_tiles = others ? p.prob[others].tile0 : 0;
+        const int more = q.long_tiles % q.workers, fewer = q.workers - more;
+        q.extra = 0;
+        if (others) {
+            // Who has one long tile fewer takes as many others as fit its length.
+            const int64_t longer = steps_of(0);
+            const int rest = p.tiles - q.long_tiles;
+            if (more) q.extra = (int)std::min<int64_t>(longer / steps, rest / fewer);
+            whole += step * (double)(q.long_tiles / q.workers * longer + (more ? longer : 0));
+        }
+        const int rest = p.tiles - q.long_tiles - q.extra * fewer;
+        q.full_tiles = rest / q.workers;
+        q.tail_tiles = rest % q.workers;
+        whole += step * (double)(q.full_tiles * steps);
         // n whole pieces a tile, or (n = 0) even shares for all workers, whose
         // ends meet inside tiles.
-        for (int n = 0; n <= std::max(1, q.workers / std::max(1, q.tail_tiles)); ++n) {
+        const int most = std::max(1, q.workers / std::max(1, q.tail_tiles));
+        for (int n = 0; n <= most; ++n) {
             if (n > steps || (n == 0 && q.tail_tiles * steps < 4 * q.workers)) continue;
-            q.tail_workers = n == 0 ? q.workers : q.tail_tiles * n;
-            if (q.tail_tiles == 0) q.tail_workers = 0;
+            q.tail_workers = n == 1 || q.tail_tiles == 0 ? 0 : n == 0 ? q.workers : q.tail_tiles * n;
             double cost = whole;
-            if (q.tail_tiles) {
+            if (n == 1 && q.tail_tiles) cost += step * (double)steps;
+            if (q.tail_workers) {
                 const double pieces = n == 0 ? (double)q.workers / q.tail_tiles + 1.0 : n;
                 cost += step * (double)(q.tail_tiles * steps) / q.tail_workers +
-                        (n == 1 ? 0.0 : size * (f32 ? 3000.0 + 1500.0 * pieces : 8000.0 + 3500.0 * pieces));
+                        size * (f32 ? 3000.0 + 1500.0 * pieces : 8000.0 + 3500.0 * pieces);
             }
             if (least < 0.0 || cost < least) {
                 least = cost;
@@ -222,73 +254,86 @@ FfnPlan ffn_plan(const FfnGemmParams &p, int num_sms) {
     return best;
 }
 
-// Sets up and launches one product.  A and B (A2 and B2) as they lie in
-// memory; a_mn, b_mn: their rows run along k.
-struct Product {
+// A launch of up to kFfnProblems products.  Operands as they lie in memory; a_mn,
+// b_mn: their rows run along k.  Those with the longest tiles come first.
+struct Launch {
     const OpDevice &dev;
     cudaStream_t st;
-    float *partials;
-    int *counters;
     FfnGemmParams p = {};
     FfnMaps maps = {};
+    FfnOperand operand[kFfnMaps];
+    int operands = 0;
 
-    Product(const OpDevice &d, cudaStream_t s, const Tail &t, int mode, int type, int64_t M, int64_t N, int64_t K,
-            bool a_mn, bool b_mn)
-        : dev(d), st(s), partials(t.partials), counters(t.counters) {
+    Launch(const OpDevice &d, cudaStream_t s, const Tail &t, int mode, int type) : dev(d), st(s) {
         p.mode = mode;
         p.type = type;
-        p.M = (int)M; p.N = (int)N; p.K = (int)K;
-        p.segs = p.outs = 1;
-        p.a_mn = a_mn; p.b_mn = b_mn;
-        p.kblocks = (int)((K + kFfnBK - 1) / kFfnBK);
+        p.partials = t.partials;
+        p.counters = t.counters;
         p.device = dev.index;
         p.err = dev.err;
         p.timeout_ns = dev.timeout_ns;
         p.skip_loads_from = dev.skip_loads_from;
     }
 
-    sgemm_status_t map(CUtensorMap *m, const FfnOperand &o, int box_rows) {
-        return op_encode_16(m, p.type != kTypeF16, o.p, o.rows, o.cols, o.ld, o.planes,
-                            o.plane_stride, box_rows);
+    FfnProblem &add(int64_t M, int64_t N, int64_t K, const FfnOperand &A, bool a_mn,
+                    const FfnOperand &B, bool b_mn, const FfnOperand *A2 = nullptr,
+                    const FfnOperand *B2 = nullptr) {
+        FfnProblem &q = p.prob[p.count++];
+        q.M = (int)M; q.N = (int)N;
+        q.segs = A2 ? 2 : 1;
+        q.a_mn = a_mn; q.b_mn = b_mn;
+        q.kblocks = (int)((K + kFfnBK - 1) / kFfnBK);
+        q.a = operands;
+        operand[operands++] = A;
+        if (A2) operand[operands++] = *A2;
+        q.b = operands;
+        operand[operands++] = B;
+        if (B2) operand[operands++] = *B2;
+        return q;
     }
 
-    sgemm_status_t run(const FfnOperand &A, const FfnOperand &B, const FfnOperand *A2 = nullptr,
-                       const FfnOperand *B2 = nullptr) {
+    sgemm_status_t run() {
+        int64_t tiles = 0;  // of the smallest kind
+        for (int i = 0; i < p.count; ++i)
+            tiles += ((int64_t)p.prob[i].M / kFfnBM + 1) * ((int64_t)p.prob[i].N / 64 + 1);
+        if (tiles > INT32_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
         const FfnPlan plan = ffn_plan(p, dev.num_sms);
-        const int b_cols = ffn_b_cols(p.type == kTypeF32, plan.pair);
-        // Rows of a short A that do not exist are not brought in: what they
-        // would add goes into rows of the accumulator that nobody reads.
-        const int a_rows = p.a_mn ? kFfnBK : std::min(kFfnBM, (p.M + 7) / 8 * 8);
-        const int b_rows = p.b_mn ? kFfnBK : b_cols;
-        p.a_bytes = (p.a_mn ? kFfnBM : a_rows) * kFfnBK * 2;
-        p.tiles_m = plan.tiles_m;
-        p.tiles_n = plan.tiles_n;
-        if ((int64_t)plan.tiles_m * plan.tiles_n * p.outs > INT32_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
-        sgemm_status_t s = map(&maps.a[0], A, a_rows);
-        if (s == SGEMM_OK && A2) s = map(&maps.a[1], *A2, a_rows);
-        if (s == SGEMM_OK) s = map(&maps.b[0], B, b_rows);
-        if (s == SGEMM_OK && B2) s = map(&maps.b[1], *B2, b_rows);
-        if (s != SGEMM_OK) return s;
+        tile_problems(p, plan.pair);
         p.workers = plan.workers;
+        p.long_tiles = plan.long_tiles;
+        p.extra = plan.extra;
         p.full_tiles = plan.full_tiles;
         p.tail_tiles = plan.tail_tiles;
         p.tail_workers = plan.tail_workers;
-        p.partials = partials;
-        p.counters = counters;
+        for (int i = 0; i < p.count; ++i) {
+            FfnProblem &q = p.prob[i];
+            // Rows of a short A that do not exist are not brought in: what they
+            // would add goes into rows of the accumulator that nobody reads.
+            const int a_rows = q.a_mn ? kFfnBK : std::min(kFfnBM, (q.M + 7) / 8 * 8);
+            const int b_rows = q.b_mn ? kFfnBK : ffn_b_cols(p.type == kTypeF32, plan.pair);
+            q.a_bytes = (q.a_mn ? kFfnBM : a_rows) * kFfnBK * 2;
+            const int end = i + 1 < p.count ? p.prob[i + 1].a : operands;
+            for (int m = q.a; m < end; ++m) {
+                const FfnOperand &o = operand[m];
+                const sgemm_status_t s =
+                    op_encode_16(&maps.m[m], p.type != kTypeF16, o.p, o.rows, o.cols, o.ld, o.planes,
+                                 o.plane_stride, m < q.b ? a_rows : b_rows);
+                if (s != SGEMM_OK) return s;
+            }
+        }
         return status(launch_ffn_gemm(maps, p, plan.pair, st));
     }
 
-    void store(void *C, int64_t ld, void *C2 = nullptr, int64_t ld2 = 0) {
-        const int e = type_bytes(p.type);
-        p.C[0] = C; p.ldc[0] = ld;
-        p.C[1] = C2; p.ldc[1] = ld2;
-        p.c_vec = aligned(C, 16) && ld * e % 16 == 0 && (!C2 || (aligned(C2, 16) && ld2 * e % 16 == 0));
+    void store(FfnProblem &q, void *C, int64_t ld) const {
+        q.C[0] = C;
+        q.ldc = ld;
+        q.c_vec = aligned(C, 16) && ld * type_bytes(p.type) % 16 == 0;
     }
-    void store_planes(const FfnOperand &o) {
-        p.C[0] = const_cast<void *>(o.p);
-        p.ldc[0] = p.ldc[1] = o.ld;
-        p.c_plane = o.plane_stride;
-        p.c_vec = 1;
+    static void store_planes(FfnProblem &q, const FfnOperand &o) {
+        q.C[0] = const_cast<void *>(o.p);
+        q.ldc = o.ld;
+        q.c_plane = o.plane_stride;
+        q.c_vec = 1;
     }
 };
 
@@ -296,11 +341,11 @@ struct Product {
 sgemm_status_t run_gate(const OpDevice &dev, cudaStream_t st, const Tail &tail, const FfnArgs &a,
                         const FfnOperand &x, const FfnOperand &Wg, const FfnOperand &Wu,
                         const FfnOperand &h, const Kept &kept, float *keep) {
-    Product g(dev, st, tail, kFfnGate, a.type, a.T, a.F, a.D, false, true);
+    Launch g(dev, st, tail, kFfnGate, a.type);
     g.p.act = a.act;
-    g.store_planes(h);
+    Launch::store_planes(g.add(a.T, a.F, a.D, x, false, Wg, true, nullptr, &Wu), h);
     if (keep) kept.set(g.p, keep);
-    return g.run(x, Wg, nullptr, &Wu);
+    return g.run();
 }
 
 // The whole block for a few rows: two passes over weights.
@@ -384,9 +429,9 @@ sgemm_status_t sgemm_ffn_forward(int64_t T, int64_t D, int64_t F, int type, int 
     s = make_copies({&vx, &vg, &vu, &vd}, type, dev, st);
     if (s == SGEMM_OK) s = run_gate(dev, st, tail, a, vx.op, vg.op, vu.op, h.op, kept, saved);
     if (s != SGEMM_OK) return s;
-    Product down(dev, st, tail, kFfnStore, type, T, D, F, false, true);
-    down.store(y, ldy);
-    return down.run(h.op, vd.op);
+    Launch down(dev, st, tail, kFfnStore, type);
+    down.store(down.add(T, D, F, h.op, false, vd.op, true), y, ldy);
+    return down.run();
 }
 
 sgemm_status_t sgemm_ffn_backward(int64_t T, int64_t D, int64_t F, int type, int activation,
@@ -434,29 +479,28 @@ sgemm_status_t sgemm_ffn_backward(int64_t T, int64_t D, int64_t F, int type, int
     if (s == SGEMM_OK && !saved) s = run_gate(dev, st, tail, a, vx.op, vg.op, vu.op, h, kept, keep);
     if (s != SGEMM_OK) return s;
 
-    Product grad(dev, st, tail, kFfnGateGrad, type, T, F, D, false, false);
-    grad.store_planes(dg.op);
-    grad.p.C[1] = const_cast<void *>(du.op.p);
+    Launch grad(dev, st, tail, kFfnGateGrad, type);
+    FfnProblem &q = grad.add(T, F, D, vdy.op, false, vd.op, false);
+    Launch::store_planes(q, dg.op);
+    q.C[1] = const_cast<void *>(du.op.p);
     kept.set(grad.p, keep);
-    s = grad.run(vdy.op, vd.op);
-    if (s == SGEMM_OK && dx) {
-        Product p(dev, st, tail, kFfnStore, type, T, D, F, false, false);
-        p.p.segs = 2;
-        p.store(dx, lddx);
-        s = p.run(dg.op, vg.op, &du.op, &vu.op);
+    s = grad.run();
+    if (s != SGEMM_OK) return s;
+    // The gradients wait for nothing but dg and du: one launch, the longest
+    // tiles first (dx sums over 2 F, the weights' over T).
+    Launch rest(dev, st, tail, kFfnStore, type);
+    const bool dx_first = 2 * ((F + kFfnBK - 1) / kFfnBK) >= (T + kFfnBK - 1) / kFfnBK;
+    auto add_dx = [&]() {
+        rest.store(rest.add(T, D, F, dg.op, false, vg.op, false, &du.op, &vu.op), dx, lddx);
+    };
+    if (dx && dx_first) add_dx();
+    if (weights) {
+        rest.store(rest.add(D, F, T, vx.op, true, dg.op, true), dWg, lddg);
+        rest.store(rest.add(D, F, T, vx.op, true, du.op, true), dWu, lddu);
+        rest.store(rest.add(F, D, T, h, true, vdy.op, true), dWd, lddd);
     }
-    if (s == SGEMM_OK && weights) {
-        Product p(dev, st, tail, kFfnStore, type, D, F, T, true, true);
-        p.p.outs = 2;
-        p.store(dWg, lddg, dWu, lddu);
-        s = p.run(vx.op, dg.op, nullptr, &du.op);
-    }
-    if (s == SGEMM_OK && weights) {
-        Product p(dev, st, tail, kFfnStore, type, F, D, T, true, true);
-        p.store(dWd, lddd);
-        s = p.run(h, vdy.op);
-    }
-    return s;
+    if (dx && !dx_first) add_dx();
+    return rest.run();
 }
 
 sgemm_status_t sgemm_w4_matvec(int64_t M, int64_t N, int64_t K, int64_t group, int type,

@@ -9,7 +9,8 @@
 //   down       y = h Wd
 //   gate grad  dh = dy Wd^T; dg = dh u act'(g), du = dh act(g)
 //   dx         dg Wg^T + du Wu^T, both products into one accumulator
-//   dW         x^T dg and x^T du (two outputs of one launch), h^T dy
+//   dW         x^T dg, x^T du and h^T dy
+// Products that do not wait for one another share a launch (dx and the three of dW).
 //
 // Types.  16-bit operands enter as they are.  FP32 operands are three bf16
 // planes (kernel below) whose sum they are to 24 bits; six of the nine plane
@@ -62,50 +63,64 @@ constexpr uint32_t kBlockBytes = 64 * kFfnBK * 2;  // 64 of m or n by 64 k
 __constant__ const int kPlaneA[6] = {2, 0, 1, 1, 0, 0};
 __constant__ const int kPlaneB[6] = {0, 2, 1, 0, 1, 0};
 
-struct TileAt {
-    int out, m, n;  // output, tile row, tile column
-};
-
-// Tiles in groups of eight tile rows, column by column inside a group, so
-// that the CTAs at work share rows of A and columns of B in L2.
-__device__ __forceinline__ TileAt tile_at(const FfnGemmParams &p, int t) {
-    constexpr int kGroup = 8;
-    TileAt r;
-    const int per_out = p.tiles_m * p.tiles_n;
-    r.out = t / per_out;
-    t -= r.out * per_out;
-    const int per_group = kGroup * p.tiles_n;
-    const int first = t / per_group * kGroup;
-    const int rows = min(kGroup, p.tiles_m - first);
-    t -= first * p.tiles_n;
-    r.m = first + t % rows;
-    r.n = t / rows;
-    return r;
-}
-
 // A stretch of one tile's k steps (a step: one k block, with all its plane
 // products) that a worker computes.
 struct Unit {
-    int tile, s0, s1;   // steps [s0, s1)
+    int prob, m, n;     // product, tile row and column
+    int s0, s1;         // steps [s0, s1)
     int pieces, piece;  // the tile's stretches, and which this is
     int first;          // the worker of piece 0
+    int tail;           // the tile's number in the tail (cut tiles)
 };
+
+// Tiles of a product in groups of eight tile rows, column by column inside a
+// group, so that the CTAs at work share rows of A and columns of B in L2.
+__device__ __forceinline__ void locate(const FfnGemmParams &p, int t, Unit &r) {
+    constexpr int kGroup = 8;
+    r.prob = 0;
+#pragma unroll
+    for (int i = 1; i < kFfnProblems; ++i)
+        if (i < p.count && t >= p.prob[i].tile0) r.prob = i;
+    const FfnProblem &q = p.prob[r.prob];
+    t -= q.tile0;
+    const int per_group = kGroup * q.tiles_n;
+    const int first = t / per_group * kGroup;
+    const int rows = min(kGroup, q.tiles_m - first);
+    t -= first * q.tiles_n;
+    r.m = first + t % rows;
+    r.n = t / rows;
+}
 
 // The worker's u-th unit; false when there is none.  The tail's steps are
 // shared out evenly, so a worker's share touches at most two tiles.
-__device__ __forceinline__ bool unit_at(const FfnGemmParams &p, int worker, int u, int steps,
-                                        Unit &r) {
-    if (u < p.full_tiles) {
-        r = Unit{worker + u * p.workers, 0, steps, 1, 0, worker};
+__device__ __forceinline__ bool unit_at(const FfnGemmParams &p, int worker, int u, Unit &r) {
+    const int longs = p.long_tiles > worker ? (p.long_tiles - worker - 1) / p.workers + 1 : 0;
+    const int more = p.long_tiles % p.workers, fewer = p.workers - more;  // one long tile more, fewer
+    const int extra = worker >= more ? p.extra : 0;
+    const int base = p.long_tiles + p.extra * fewer;
+    const int v = u - longs - extra;  // of the tiles that all share
+    if (v < p.full_tiles || p.tail_workers == 0) {
+        const int t = u < longs ? worker + u * p.workers
+                      : v < 0   ? p.long_tiles + (u - longs) * fewer + worker - more
+                                : base + worker + v * p.workers;
+        if (t >= p.tiles) return false;
+        locate(p, t, r);
+        r.s0 = 0;
+        r.s1 = p.prob[r.prob].kblocks * p.prob[r.prob].segs;
+        r.pieces = 1;
+        r.piece = r.tail = 0;
+        r.first = worker;
         return true;
     }
     if (worker >= p.tail_workers) return false;
+    const FfnProblem &last = p.prob[p.count - 1];
+    const int steps = last.kblocks * last.segs;
     const long long all = (long long)p.tail_tiles * steps;
     long long a = worker * all / p.tail_workers;
     const long long e = (worker + 1) * all / p.tail_workers;
     long long end = min(e, (a / steps + 1) * steps);
-    if (u > p.full_tiles) {
-        if (u > p.full_tiles + 1) return false;
+    if (v > p.full_tiles) {
+        if (v > p.full_tiles + 1) return false;
         a = end;
         end = e;
     }
@@ -114,7 +129,8 @@ __device__ __forceinline__ bool unit_at(const FfnGemmParams &p, int worker, int 
     // Worker w starts at floor(w all / n), so step x is worker
     // floor(((x + 1) n - 1) / all)'s.
     const long long x0 = (long long)t * steps, n = p.tail_workers;
-    r.tile = p.full_tiles * p.workers + t;
+    locate(p, base + p.full_tiles * p.workers + t, r);
+    r.tail = t;
     r.s0 = (int)(a - x0);
     r.s1 = (int)(end - x0);
     r.first = (int)(((x0 + 1) * n - 1) / all);
@@ -149,11 +165,12 @@ __device__ __forceinline__ void get_lanes(const float *base, int lane, float (&v
 // of TYPE: through shared memory, so that a row's 64 or 128 bytes are stored
 // by neighbouring lanes.  The 16-byte chunks of a row are permuted by its
 // number so that neither side has bank conflicts.  rows and cols are what is
-// left of the matrix from (row0, n) on.
-template <int TYPE>
+// left of the matrix from (row0, n) on.  v(i), called once for each i in order, is
+// the lane's value in column i.
+template <int TYPE, class Values>
 __device__ __forceinline__ void store_block(unsigned char *stage, int lane, void *base, long long ld,
                                             long long row0, int n, int rows, int cols, bool vec,
-                                            const float (&v)[32]) {
+                                            Values &&v) {
     constexpr int kElem = TYPE == kTypeF32 ? 4 : 2;
     constexpr int kChunks = 32 * kElem / 16;  // of a row
     constexpr int kPer = 16 / kElem;          // elements of a chunk
@@ -164,14 +181,15 @@ __device__ __forceinline__ void store_block(unsigned char *stage, int lane, void
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
         uint4 w;
+        float e[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) e[i] = v(kPer * c + i);
         if constexpr (TYPE == kTypeF32)
-            w = make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
-                           __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+            w = make_uint4(__float_as_uint(e[0]), __float_as_uint(e[1]), __float_as_uint(e[2]),
+                           __float_as_uint(e[3]));
         else
-            w = make_uint4(pack16<TYPE>(v[8 * c], v[8 * c + 1]),
-                           pack16<TYPE>(v[8 * c + 2], v[8 * c + 3]),
-                           pack16<TYPE>(v[8 * c + 4], v[8 * c + 5]),
-                           pack16<TYPE>(v[8 * c + 6], v[8 * c + 7]));
+            w = make_uint4(pack16<TYPE>(e[0], e[1]), pack16<TYPE>(e[2], e[3]),
+                           pack16<TYPE>(e[4 % kPer], e[5 % kPer]), pack16<TYPE>(e[6 % kPer], e[7 % kPer]));
         *place(lane, c) = w;
     }
     __syncwarp();
@@ -207,26 +225,20 @@ __device__ __forceinline__ void store_block(unsigned char *stage, int lane, void
 template <int TYPE>
 __device__ __forceinline__ void store_planes(unsigned char *stage, int lane, void *base, long long ld,
                                              long long plane, long long row0, int n, int rows,
-                                             int cols, const float (&v)[32]) {
+                                             int cols, float (&v)[32]) {
     if constexpr (TYPE != kTypeF32) {
-        store_block<TYPE>(stage, lane, base, ld, row0, n, rows, cols, true, v);
+        store_block<TYPE>(stage, lane, base, ld, row0, n, rows, cols, true, [&](int i) { return v[i]; });
     } else {
-        float rest[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) rest[i] = v[i];
+        // v becomes what is left of it.
 #pragma unroll 1
-        for (int q = 0; q < 3; ++q) {
-            float part[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                float s[3];
-                split3(rest[i], s);
-                part[i] = s[0];
-                rest[i] = isfinite(s[0]) ? rest[i] - s[0] : 0.0f;
-            }
-            store_block<kTypeBF16>(stage, lane, static_cast<uint16_t *>(base) + q * plane, ld, row0,
-                                   n, rows, cols, true, part);
-        }
+        for (int q = 0; q < 3; ++q)
+            store_block<kTypeBF16>(stage, lane, static_cast<uint16_t *>(base) + q * plane, ld, row0, n,
+                                   rows, cols, true, [&](int i) {
+                                       float s[3];
+                                       split3(v[i], s);
+                                       v[i] = isfinite(s[0]) ? v[i] - s[0] : 0.0f;
+                                       return s[0];
+                                   });
     }
 }
 
@@ -275,8 +287,6 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     // stream reads or writes; its results are complete after this.
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    const int steps = p.kblocks * p.segs;  // of a tile; kProducts stages each
-
     if (warp == 0) {
         if (lane == 0) {
             // Stages so far over all tiles, the next one's place in the ring
@@ -286,18 +296,20 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             bool ok = true;
             const uint32_t bar0 = CG == 2 ? cluster_addr(&full[0], 0) : smem_addr(&full[0]);
             Unit unit;
-            for (int u = 0; ok && unit_at(p, worker, u, steps, unit); ++u) {
-                const TileAt at = tile_at(p, unit.tile);
-                const int m0 = at.m * (kFfnBM * CG) + (int)rank * kFfnBM;
-                const int n0 = at.n * kTileN;
-                int seg = unit.s0 >= p.kblocks ? 1 : 0;
-                int k = (unit.s0 - seg * p.kblocks) * kFfnBK;
+            for (int u = 0; ok && unit_at(p, worker, u, unit); ++u) {
+                const FfnProblem &pr = p.prob[MODE == kFfnStore ? unit.prob : 0];
+                const int m0 = unit.m * (kFfnBM * CG) + (int)rank * kFfnBM;
+                const int n0 = unit.n * kTileN, k_end = pr.kblocks * kFfnBK;
+                const bool a_mn = pr.a_mn, b_mn = pr.b_mn;
+                const uint32_t bytes = (pr.a_bytes + Fm::kBBytes) * CG;
+                int seg = unit.s0 >= pr.kblocks ? 1 : 0;
+                int k = unit.s0 * kFfnBK - seg * k_end;
                 for (int step = unit.s0; ok && step < unit.s1; ++step, k += kFfnBK) {
-                    if (k >= p.kblocks * kFfnBK) {
+                    if (k >= k_end) {
                         k = 0;
                         seg = 1;
                     }
-                    const CUtensorMap *ma = &maps.a[seg], *mb = &maps.b[seg + at.out];
+                    const CUtensorMap *ma = &maps.m[pr.a + seg], *mb = &maps.m[pr.b + seg];
                     {
 #pragma unroll 1
                         for (int prod = 0; prod < kProducts; ++prod, ++it) {
@@ -314,9 +326,9 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                             const int pa = kSplit ? kPlaneA[prod] : 0, pb = kSplit ? kPlaneB[prod] : 0;
                             unsigned char *a = smem + s * kStageBytes, *b = a + kABytes;
                             // The pair's loads all complete on the first CTA's barrier.
-                            if (rank == 0) mbar_arrive_expect_tx(&full[s], (p.a_bytes + Fm::kBBytes) * CG);
+                            if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
                             const uint32_t bar = bar0 + s * 8;
-                            if (p.a_mn) {
+                            if (a_mn) {
                                 tc_load_3d<CG>(a, ma, bar, m0, k, pa);
                                 tc_load_3d<CG>(a + kBlockBytes, ma, bar, m0 + 64, k, pa);
                             } else {
@@ -325,14 +337,14 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                             if constexpr (MODE == kFfnGate) {
                                 // One CTA: 64 columns of each matrix.  A pair: the
                                 // first CTA brings Wg's columns, the second Wu's.
-                                const CUtensorMap *m1 = CG == 2 ? &maps.b[rank] : &maps.b[0];
-                                const CUtensorMap *m2 = CG == 2 ? m1 : &maps.b[1];
+                                const CUtensorMap *m1 = CG == 2 ? mb + rank : mb;
+                                const CUtensorMap *m2 = CG == 2 ? m1 : mb + 1;
                                 tc_load_3d<CG>(b, m1, bar, n0, k, pb);
                                 if constexpr (Fm::kBCols == 128)
                                     tc_load_3d<CG>(b + kBlockBytes, m2, bar, CG == 2 ? n0 + 64 : n0, k, pb);
                             } else {
                                 const int n = n0 + (int)rank * Fm::kBCols;
-                                if (p.b_mn) {
+                                if (b_mn) {
                                     tc_load_3d<CG>(b, mb, bar, n, k, pb);
                                     if constexpr (Fm::kBCols == 128)
                                         tc_load_3d<CG>(b + kBlockBytes, mb, bar, n + 64, k, pb);
@@ -363,11 +375,6 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         // lane alone keeps its descriptors in vector registers and spent some
         // 650 clocks on a stage whose products take 512.
         if (rank == 0) {
-            const uint32_t idesc =
-                tc_idesc(kFfnBM * CG, kAccCols, TYPE != kTypeF16, p.a_mn != 0, p.b_mn != 0);
-            // Per 16 k: two groups of eight rows (MN-major) or 32 bytes along
-            // the swizzled row (K-major); units of 16 bytes.
-            const uint32_t a_step = (p.a_mn ? 2048 : 32) >> 4, b_step = (p.b_mn ? 2048 : 32) >> 4;
             // Descriptors of the first stage; the others and the steps along
             // k differ in the start address alone.
             const uint64_t desc_a = tc_desc(sbase, kBlockBytes);
@@ -376,7 +383,13 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             uint32_t parity = 0, acc_parity = 1;
             bool ok = true;
             Unit unit;
-            for (int u = 0; ok && unit_at(p, worker, u, steps, unit); ++u) {
+            for (int u = 0; ok && unit_at(p, worker, u, unit); ++u) {
+                const FfnProblem &pr = p.prob[MODE == kFfnStore ? unit.prob : 0];
+                const uint32_t idesc = tc_idesc(kFfnBM * CG, kAccCols, TYPE != kTypeF16, pr.a_mn != 0,
+                                                pr.b_mn != 0);
+                // Per 16 k: two groups of eight rows (MN-major) or 32 bytes
+                // along the swizzled row (K-major); units of 16 bytes.
+                const uint32_t a_step = (pr.a_mn ? 2048 : 32) >> 4, b_step = (pr.b_mn ? 2048 : 32) >> 4;
                 // An accumulator takes the unit's steps, or (FP32) one.
                 const int phases = kSplit ? unit.s1 - unit.s0 : 1;
                 const int stages = kSplit ? kProducts : unit.s1 - unit.s0;
@@ -431,10 +444,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         uint32_t parity = 0;
         bool ok = true;
         Unit unit;
-        for (int u = 0; ok && unit_at(p, worker, u, steps, unit); ++u) {
-            const TileAt at = tile_at(p, unit.tile);
-            const int row0 = at.m * (kFfnBM * CG) + (int)rank * kFfnBM + quad * 32;
-            const int n_tile = at.n * kTileN, rows = p.M - row0;
+        for (int u = 0; ok && unit_at(p, worker, u, unit); ++u) {
+            const FfnProblem &pr = p.prob[MODE == kFfnStore ? unit.prob : 0];
+            const int row0 = unit.m * (kFfnBM * CG) + (int)rank * kFfnBM + quad * 32;
+            const int n_tile = unit.n * kTileN, rows = pr.M - row0;
             float sum[kSplit ? kParts : 1][32];
             uint32_t d = t_lane;
             if constexpr (kSplit) {
@@ -496,8 +509,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 }
                 __threadfence();
                 __syncwarp();
-                int *counter = p.counters + ((unit.tile - p.full_tiles * p.workers) * CG + (int)rank) *
-                                                kEpiWarps + (warp - 4);
+                int *counter = p.counters + (unit.tail * CG + (int)rank) * kEpiWarps + (warp - 4);
                 int arrived = 0;
                 if (lane == 0) {
                     arrived = atomicAdd(counter, 1);
@@ -513,50 +525,68 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                     own(j, v);
                     return;
                 }
+                // (with FP32 half the columns at a time, for the registers' sake)
+                constexpr int kAtOnce = kSplit ? 4 : 8;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+                for (int i0 = 0; i0 < 8; i0 += kAtOnce) {
+#pragma unroll
+                    for (int i = 4 * i0; i < 4 * (i0 + kAtOnce); ++i) v[i] = 0.0f;
 #pragma unroll 1
-                for (int q = 0; q < unit.pieces; ++q) {
-                    float w[32];
-                    get_lanes(slot(q) + j * 1024, lane, w);
+                    for (int q = 0; q < unit.pieces; ++q) {
+                        const float4 *from = reinterpret_cast<const float4 *>(slot(q) + j * 1024) + lane;
+                        float4 w[kAtOnce];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] += w[i];
+                        for (int i = 0; i < kAtOnce; ++i) w[i] = __ldcg(from + (i0 + i) * 32);
+#pragma unroll
+                        for (int i = 0; i < kAtOnce; ++i) {
+                            v[4 * (i0 + i)] += w[i].x;
+                            v[4 * (i0 + i) + 1] += w[i].y;
+                            v[4 * (i0 + i) + 2] += w[i].z;
+                            v[4 * (i0 + i) + 3] += w[i].w;
+                        }
+                    }
                 }
             };
             if (emit) {
 #pragma unroll(kSplit ? kParts : 1)
                 for (int j = 0; j < kParts; j += kTwo) {
                     const int n = n_tile + (MODE == kFfnGate ? half * (kAccCols / 4) + 16 * j : part_col(j));
-                    const int cols = p.N - n;
+                    const int cols = pr.N - n;
                     if (cols <= 0) break;
                     const long long kept =
                         ((long long)(row0 >> 5) * p.keep_cols + (n >> 5)) * 1024;
                     float v[32];
                     if constexpr (MODE == kFfnStore) {
                         value(j, v);
-                        store_block<TYPE>(stage, lane, p.C[at.out], p.ldc[at.out], row0, n, rows,
-                                          cols, p.c_vec, v);
+                        store_block<TYPE>(stage, lane, pr.C[0], pr.ldc, row0, n, rows, cols, pr.c_vec,
+                                          [&](int i) { return v[i]; });
                     } else if constexpr (MODE == kFfnGate) {
                         float w[32];
                         value(j, v);
                         value(j + 1, w);
                         if (p.keep[0]) {
-                            float t[32];
+                            // Four columns at a time, as put_lanes would lay
+                            // them: 32 more values would not fit the registers.
+                            float4 *k0 = reinterpret_cast<float4 *>(p.keep[0] + kept) + lane;
+                            float4 *k1 = reinterpret_cast<float4 *>(p.keep[1] + kept) + lane;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                float a, slope;
-                                gate_act_slope<kSplit>(v[i], p.act, a, slope);
-                                v[i] = a;
-                                t[i] = w[i] * slope;
-                                w[i] *= a;
+                            for (int i = 0; i < 8; ++i) {
+                                float a[4], t[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    float slope;
+                                    gate_act_slope<kSplit>(v[4 * i + e], p.act, a[e], slope);
+                                    t[e] = w[4 * i + e] * slope;
+                                    w[4 * i + e] *= a[e];
+                                }
+                                __stcg(k0 + i * 32, make_float4(t[0], t[1], t[2], t[3]));
+                                __stcg(k1 + i * 32, make_float4(a[0], a[1], a[2], a[3]));
                             }
-                            put_lanes(p.keep[0] + kept, lane, t);
-                            put_lanes(p.keep[1] + kept, lane, v);
                         } else {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) w[i] *= gate_act<kSplit>(v[i], p.act);
                         }
-                        store_planes<TYPE>(stage, lane, p.C[0], p.ldc[0], p.c_plane, row0, n, rows,
+                        store_planes<TYPE>(stage, lane, pr.C[0], pr.ldc, pr.c_plane, row0, n, rows,
                                            cols, w);
                     } else {
                         float t[32];
@@ -564,13 +594,13 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                         value(j, v);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) t[i] *= v[i];
-                        store_planes<TYPE>(stage, lane, p.C[0], p.ldc[0], p.c_plane, row0, n, rows,
+                        store_planes<TYPE>(stage, lane, pr.C[0], pr.ldc, pr.c_plane, row0, n, rows,
                                            cols, t);
                         get_lanes(p.keep[1] + kept, lane, t);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) t[i] *= v[i];
-                        store_planes<TYPE>(stage, lane, p.C[1], p.ldc[0], p.c_plane, row0, n, rows,
-                                           cols, t);
+                        for (int i = 0; i < 32; ++i) v[i] *= t[i];
+                        store_planes<TYPE>(stage, lane, pr.C[1], pr.ldc, pr.c_plane, row0, n, rows,
+                                           cols, v);
                     }
                 }
             }
@@ -668,7 +698,8 @@ cudaError_t launch_one(const FfnMaps &maps, const FfnGemmParams &p, cudaStream_t
         configured[p.device].store(true);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(CG * (p.full_tiles > 0 ? p.workers : p.tail_workers));
+    cfg.gridDim = dim3(CG * (p.full_tiles + p.long_tiles > 0 ? p.workers
+                             : p.tail_workers ? p.tail_workers : p.tail_tiles));
     cfg.blockDim = dim3(kFfnThreads);
     cfg.dynamicSmemBytes = Form<TYPE, CG>::kSmem;
     cfg.stream = stream;

@@ -117,7 +117,7 @@ struct FfnOperand {
 };
 
 enum : int {
-    kFfnStore = 0,     // C = A B, or A B + A2 B2, or two outputs A B and A B2
+    kFfnStore = 0,     // C = A B, or A B + A2 B2
     kFfnGate = 1,      // g = A B, u = A B2; h = act(g) u; u act'(g) and act(g) kept when asked
     kFfnGateGrad = 2,  // dh = A B; dg = dh u act'(g) and du = dh act(g) from the kept values
 };
@@ -128,30 +128,43 @@ constexpr int ffn_b_cols(bool f32, bool pair) { return f32 && pair ? 64 : 128; }
 constexpr int kFfnBK = 64;       // k per stage: one 128-byte swizzled row
 constexpr int kFfnThreads = 384; // 4 warps of roles, 8 of epilogue
 
-struct FfnGemmParams {
-    int mode;
-    int type;            // of the user's matrices
-    int M, N, K;
-    int act;
+constexpr int kFfnProblems = 4;  // products of one launch (kFfnStore)
+constexpr int kFfnMaps = 10;     // operands of one launch
+
+// One product of a launch.  Its operands are maps a, a + 1 (second product of a
+// sum) and b, b + 1.
+struct FfnProblem {
+    int M, N;
+    int a, b;
     int segs;            // products added up (2: A B + A2 B2)
-    int outs;            // outputs (2: A B -> C[0], A B2 -> C[1])
     int a_mn, b_mn;      // operand is MN-major: its rows run along k
     uint32_t a_bytes;    // of A per CTA and stage: rows of `a` boxes, 128 bytes each
-    int tiles_m, tiles_n;
     int kblocks;         // ceil(K / kFfnBK)
-    // Workers (CTAs or pairs) take whole tiles round-robin, full_tiles each;
-    // the tail_tiles left over are cut along k into tail_workers equal shares.
-    int workers, full_tiles, tail_tiles, tail_workers;
-    float *partials;     // 2 slots per worker of kFfnSlotFloats per CTA (tail)
-    int *counters;       // tail_tiles x CTAs of a worker x 8, zero at rest
-    int device;
-    // kFfnStore: C, `type`.  kFfnGate: C[0] = h.  kFfnGateGrad: C[0] = dg,
+    int tiles_m, tiles_n, tile0;  // tiles, and the first one's number in the launch
+    // kFfnStore: C[0], `type`.  kFfnGate: C[0] = h.  kFfnGateGrad: C[0] = dg,
     // C[1] = du.  h, dg and du are 16-bit operands for the next product: one
     // plane of `type`, or three bf16 planes.
     void *C[2];
-    long long ldc[2];    // kFfnStore: of each output; else ldc[0] of all
-    long long c_plane;
+    long long ldc, c_plane;
     int c_vec;           // 16-byte stores allowed
+};
+
+struct FfnGemmParams {
+    int mode;
+    int type;            // of the user's matrices
+    int act;
+    int count;           // products, those with the longest tiles first
+    FfnProblem prob[kFfnProblems];
+    int tiles;           // of all products
+    // Workers (CTAs or pairs) take whole tiles round-robin: first the long_tiles
+    // of the products with the longest tiles, where there are two lengths; then
+    // those that got one long tile fewer take `extra` of the others; then all
+    // take full_tiles each.  The tail_tiles left over are cut along k into
+    // tail_workers equal shares (tail_workers 0: taken whole).
+    int workers, long_tiles, extra, full_tiles, tail_tiles, tail_workers;
+    float *partials;     // 2 slots per worker of ffn_slot_floats() per CTA (tail)
+    int *counters;       // tail_tiles x CTAs of a worker x 8, zero at rest
+    int device;
     // u act'(g) and act(g), or null: blocks of 32 x 32 values, block (i, j) at
     // (i * keep_cols + j) * 1024, in it element (row r, column c) at
     // (c / 4 * 32 + r) * 4 + c % 4: as a warp holds them.
@@ -167,10 +180,9 @@ inline int ffn_slot_floats(bool f32, bool pair) {
     return kFfnBM * ffn_b_cols(f32, pair) * (pair ? 2 : 1);
 }
 
-// One operand's TMA descriptor as the kernel wants it: boxes of 64 along the
-// contiguous dimension by `rows` rows.
+// The operands' TMA descriptors: boxes of 64 along the contiguous dimension.
 struct FfnMaps {
-    CUtensorMap a[2], b[2];
+    CUtensorMap m[kFfnMaps];
 };
 // pair: 256-row tiles by pairs of CTAs.
 cudaError_t launch_ffn_gemm(const FfnMaps &maps, const FfnGemmParams &p, bool pair,
