@@ -348,32 +348,38 @@ sgemm_status_t run_gate(const OpDevice &dev, cudaStream_t st, const Tail &tail, 
     return g.run();
 }
 
-// The whole block for a few rows: two passes over weights.
+// The whole block for a few rows: one pass over the weights for every eight.
 sgemm_status_t run_stream(const OpDevice &dev, cudaStream_t st, const FfnArgs &a, void *y,
                           int64_t ldy) {
     void *h = nullptr;
-    const sgemm_status_t s = op_workspace(st, (size_t)(a.T * a.F) * sizeof(float), &h);
+    const sgemm_status_t s =
+        op_workspace(st, (size_t)(std::min<int64_t>(a.T, kFfnStreamRows) * a.F) * sizeof(float), &h);
     if (s != SGEMM_OK) return s;
     const int64_t e = type_bytes(a.type);
     auto vec = [&](const void *p, int64_t ld, int64_t n) {
         return aligned(p, 16) && ld * e % 16 == 0 && n * e % 16 == 0;
     };
-    FfnStreamParams p = {};
-    p.T = (int)a.T; p.N = (int)a.F; p.K = (int)a.D;
-    p.act = a.act;
-    p.x = a.x; p.ldx = a.ldx;
-    p.W = a.Wg; p.ldw = a.ldg;
-    p.W2 = a.Wu; p.ldw2 = a.ldu;
-    p.y = h; p.ldy = a.F;
-    p.device = dev.index;
-    if (launch_ffn_stream(p, a.type, true, vec(a.Wg, a.ldg, a.F) && vec(a.Wu, a.ldu, a.F),
-                          dev.num_sms, st) != cudaSuccess)
-        return SGEMM_ERR_LAUNCH;
-    p.N = (int)a.D; p.K = (int)a.F;
-    p.x = h; p.ldx = a.F;
-    p.W = a.Wd; p.ldw = a.ldd;
-    p.y = y; p.ldy = ldy;
-    return status(launch_ffn_stream(p, a.type, false, vec(a.Wd, a.ldd, a.D), dev.num_sms, st));
+    for (int64_t t = 0; t < a.T; t += kFfnStreamRows) {
+        FfnStreamParams p = {};
+        p.T = (int)std::min<int64_t>(a.T - t, kFfnStreamRows);
+        p.N = (int)a.F; p.K = (int)a.D;
+        p.act = a.act;
+        p.x = static_cast<const char *>(a.x) + t * a.ldx * e; p.ldx = a.ldx;
+        p.W = a.Wg; p.ldw = a.ldg;
+        p.W2 = a.Wu; p.ldw2 = a.ldu;
+        p.y = h; p.ldy = a.F;
+        p.device = dev.index;
+        if (launch_ffn_stream(p, a.type, true, vec(a.Wg, a.ldg, a.F) && vec(a.Wu, a.ldu, a.F),
+                              dev.num_sms, st) != cudaSuccess)
+            return SGEMM_ERR_LAUNCH;
+        p.N = (int)a.D; p.K = (int)a.F;
+        p.x = h; p.ldx = a.F;
+        p.W = a.Wd; p.ldw = a.ldd;
+        p.y = static_cast<char *>(y) + t * ldy * e; p.ldy = ldy;
+        if (launch_ffn_stream(p, a.type, false, vec(a.Wd, a.ldd, a.D), dev.num_sms, st) != cudaSuccess)
+            return SGEMM_ERR_LAUNCH;
+    }
+    return SGEMM_OK;
 }
 
 sgemm_status_t zero_matrix(void *p, int64_t ld, int64_t rows, int64_t cols, int type,
@@ -411,12 +417,15 @@ sgemm_status_t sgemm_ffn_forward(int64_t T, int64_t D, int64_t F, int type, int 
     s = op_device(&dev);
     if (s != SGEMM_OK) return s;
     if (F == 0) return zero_matrix(y, ldy, T, D, type, st);
-    // Few rows: one pass over the weights on the FP32 pipe.  From five rows of
-    // 16-bit weights on that is the slower way (8 x 4096 x 12288: 167 us, the
-    // tensor cores 91), unless they would have to be copied to aligned rows.
+    // Few rows: passes over the weights on the FP32 pipe, one for every eight.
+    // From five rows of 16-bit weights on that is the slower way (8 x 4096 x 12288:
+    // 167 us, the tensor cores 73), unless they would have to be copied to
+    // aligned rows; with FP32 weights, which the tensor cores need split in
+    // three first, from 25 (12 x 2048 x 8192: 212 us that way).
     const bool in_place = type != kTypeF32 && aligned(Wg, 16) && aligned(Wu, 16) &&
                           aligned(Wd, 16) && ldg % 8 == 0 && ldu % 8 == 0 && ldd % 8 == 0;
-    if (!saved && (T <= 4 || (T <= kFfnStreamRows && !in_place))) return run_stream(dev, st, a, y, ldy);
+    const int64_t few = type == kTypeF32 ? 24 : in_place ? 4 : 8;
+    if (!saved && T <= few) return run_stream(dev, st, a, y, ldy);
     Arena w;
     Tail tail;
     const Kept kept(T, F, type);

@@ -17,8 +17,8 @@
 // products are taken, smallest first, the three left out are below 2^-24 of
 // the product.  The tensor core adds without rounding to nearest, so an
 // accumulator that runs over all of K would drift by some 10^-5; FP32 sums
-// are therefore taken out of tensor memory after every k block and added up
-// in registers in FP32.
+// are therefore taken out of tensor memory after every k block and added
+// up in registers in FP32.
 //
 // Structure, 384 threads a CTA, one CTA per SM:
 //   warp 0       one thread issues the TMA loads of 64-deep operand blocks
@@ -59,9 +59,12 @@ struct Form {
 };
 constexpr uint32_t kBlockBytes = 64 * kFfnBK * 2;  // 64 of m or n by 64 k
 
-// FP32: which planes of A and B the six products take, smallest first.
-__constant__ const int kPlaneA[6] = {2, 0, 1, 1, 0, 0};
-__constant__ const int kPlaneB[6] = {0, 2, 1, 0, 1, 0};
+// FP32: the planes of a k block in the order in which they are brought in (and
+// then used), each with A's and B's in one stage of the ring; and the k blocks
+// that pass through an accumulator before its sums are taken out.
+constexpr int kPlanes = 3;
+__device__ __forceinline__ int plane_at(int i) { return i == 0 ? 0 : 3 - i; }  // 0, 2, 1
+constexpr int kPhaseSteps = 1;
 
 // A stretch of one tile's k steps (a step: one k block, with all its plane
 // products) that a worker computes.
@@ -246,7 +249,7 @@ template <int TYPE, int MODE, int CG>
 __global__ void __launch_bounds__(kFfnThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const FfnGemmParams p) {
     constexpr bool kSplit = TYPE == kTypeF32;         // three planes, sums in registers
-    constexpr int kProducts = kSplit ? 6 : 1;
+    constexpr int kLoads = kSplit ? kPlanes : 1;      // stages of a step
     using Fm = Form<TYPE, CG>;
     constexpr int kAccCols = Fm::kAccCols, kStages = Fm::kStages, kParts = Fm::kParts;
     constexpr uint32_t kStageBytes = Fm::kStageBytes;
@@ -312,7 +315,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                     const CUtensorMap *ma = &maps.m[pr.a + seg], *mb = &maps.m[pr.b + seg];
                     {
 #pragma unroll 1
-                        for (int prod = 0; prod < kProducts; ++prod, ++it) {
+                        for (int load = 0; load < kLoads; ++load, ++it) {
                             if (p.skip_loads_from >= 0 && it >= p.skip_loads_from) {
                                 ok = false;
                                 break;
@@ -323,33 +326,33 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                                 ok = false;
                                 break;
                             }
-                            const int pa = kSplit ? kPlaneA[prod] : 0, pb = kSplit ? kPlaneB[prod] : 0;
+                            const int plane = kSplit ? plane_at(load) : 0;
                             unsigned char *a = smem + s * kStageBytes, *b = a + kABytes;
                             // The pair's loads all complete on the first CTA's barrier.
                             if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
                             const uint32_t bar = bar0 + s * 8;
                             if (a_mn) {
-                                tc_load_3d<CG>(a, ma, bar, m0, k, pa);
-                                tc_load_3d<CG>(a + kBlockBytes, ma, bar, m0 + 64, k, pa);
+                                tc_load_3d<CG>(a, ma, bar, m0, k, plane);
+                                tc_load_3d<CG>(a + kBlockBytes, ma, bar, m0 + 64, k, plane);
                             } else {
-                                tc_load_3d<CG>(a, ma, bar, k, m0, pa);
+                                tc_load_3d<CG>(a, ma, bar, k, m0, plane);
                             }
                             if constexpr (MODE == kFfnGate) {
                                 // One CTA: 64 columns of each matrix.  A pair: the
                                 // first CTA brings Wg's columns, the second Wu's.
                                 const CUtensorMap *m1 = CG == 2 ? mb + rank : mb;
                                 const CUtensorMap *m2 = CG == 2 ? m1 : mb + 1;
-                                tc_load_3d<CG>(b, m1, bar, n0, k, pb);
+                                tc_load_3d<CG>(b, m1, bar, n0, k, plane);
                                 if constexpr (Fm::kBCols == 128)
-                                    tc_load_3d<CG>(b + kBlockBytes, m2, bar, CG == 2 ? n0 + 64 : n0, k, pb);
+                                    tc_load_3d<CG>(b + kBlockBytes, m2, bar, CG == 2 ? n0 + 64 : n0, k, plane);
                             } else {
                                 const int n = n0 + (int)rank * Fm::kBCols;
                                 if (b_mn) {
-                                    tc_load_3d<CG>(b, mb, bar, n, k, pb);
+                                    tc_load_3d<CG>(b, mb, bar, n, k, plane);
                                     if constexpr (Fm::kBCols == 128)
-                                        tc_load_3d<CG>(b + kBlockBytes, mb, bar, n + 64, k, pb);
+                                        tc_load_3d<CG>(b + kBlockBytes, mb, bar, n + 64, k, plane);
                                 } else {
-                                    tc_load_3d<CG>(b, mb, bar, k, n, pb);
+                                    tc_load_3d<CG>(b, mb, bar, k, n, plane);
                                 }
                             }
                             if (++s == kStages) {
@@ -390,31 +393,64 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 // Per 16 k: two groups of eight rows (MN-major) or 32 bytes
                 // along the swizzled row (K-major); units of 16 bytes.
                 const uint32_t a_step = (pr.a_mn ? 2048 : 32) >> 4, b_step = (pr.b_mn ? 2048 : 32) >> 4;
-                // An accumulator takes the unit's steps, or (FP32) one.
-                const int phases = kSplit ? unit.s1 - unit.s0 : 1;
-                const int stages = kSplit ? kProducts : unit.s1 - unit.s0;
-                for (int q = 0; ok && q < phases; ++q) {
+                // An accumulator takes the unit's steps, or (FP32) a few.
+                constexpr int kMost = kSplit ? kPhaseSteps : 1 << 30;
+                for (int step = unit.s0; ok && step < unit.s1;) {
+                    const int end = kSplit ? min(step + kMost, unit.s1) : unit.s1;
                     ok = tc_wait_warp(&acc_empty[buf], acc_parity, p.timeout_ns);
                     if (!ok) break;
                     tc_fence_after_sync();
                     const uint32_t d = tmem + buf * kAccCols;
-                    for (int i = 0; i < stages; ++i) {
-                        ok = tc_wait_warp(&full[s], parity, p.timeout_ns);
-                        if (!ok) break;
+                    // Waits for the next stage and returns its number.
+                    auto take = [&]() {
+                        const int at = s;
+                        ok = ok && tc_wait_warp(&full[s], parity, p.timeout_ns);
                         tc_fence_after_sync();
-                        const uint64_t a = desc_a + s * (kStageBytes >> 4);
-                        const uint64_t b = desc_b + s * (kStageBytes >> 4);
-                        if (tc_elect()) {
-#pragma unroll
-                            for (int kk = 0; kk < kFfnBK / 16; ++kk)
-                                tc_mma<CG>(d, a + kk * a_step, b + kk * b_step, idesc, (i | kk) != 0);
-                            tc_commit<CG>(&empty[s]);
-                        }
-                        __syncwarp();
                         if (++s == kStages) {
                             s = 0;
                             parity ^= 1;
                         }
+                        return at;
+                    };
+                    // A of stage i times B of stage j.
+                    auto product = [&](int i, int j, bool first) {
+                        const uint64_t a = desc_a + i * (kStageBytes >> 4);
+                        const uint64_t b = desc_b + j * (kStageBytes >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < kFfnBK / 16; ++kk)
+                            tc_mma<CG>(d, a + kk * a_step, b + kk * b_step, idesc, !first || kk != 0);
+                    };
+                    for (bool first = true; step < end; ++step, first = false) {
+                        const int s0 = take();
+                        if constexpr (kSplit) {
+                            // Six products of the planes, smallest first; a
+                            // stage is released after its last use.
+                            const int s2 = take();
+                            if (!ok) break;
+                            if (tc_elect()) {
+                                product(s2, s0, first);
+                                product(s0, s2, false);
+                                tc_commit<CG>(&empty[s2]);
+                            }
+                            __syncwarp();
+                            const int s1 = take();
+                            if (!ok) break;
+                            if (tc_elect()) {
+                                product(s1, s1, false);
+                                product(s1, s0, false);
+                                product(s0, s1, false);
+                                tc_commit<CG>(&empty[s1]);
+                                product(s0, s0, false);
+                                tc_commit<CG>(&empty[s0]);
+                            }
+                        } else {
+                            if (!ok) break;
+                            if (tc_elect()) {
+                                product(s0, s0, first);
+                                tc_commit<CG>(&empty[s0]);
+                            }
+                        }
+                        __syncwarp();
                     }
                     if (!ok) break;
                     if (tc_elect()) tc_commit<CG>(&acc_full[buf]);
@@ -455,7 +491,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 for (int j = 0; j < kParts; ++j)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) sum[j][i] = 0.0f;
-                for (int q = unit.s0; q < unit.s1; ++q) {
+                for (int q = unit.s0; q < unit.s1; q += kPhaseSteps) {
                     ok = tc_wait_warp(&acc_full[buf], parity, p.timeout_ns);
                     if (!ok) break;
                     tc_fence_after_sync();

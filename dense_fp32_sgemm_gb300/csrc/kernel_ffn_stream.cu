@@ -1,4 +1,4 @@
-// The gated block for a few rows (T <= 8, decoding): one pass over the weights.
+// The gated block for up to eight rows (decoding): one pass over the weights.
 //
 //   gate   g = x Wg, u = x Wu, h = act(g) u   (h stays FP32, T x F)
 //   down   y = h Wd
