@@ -3,7 +3,9 @@
 Argument marshalling only: every step of C = alpha*A*B + beta*C runs in the
 library's CUDA kernels.  The functions mirror the C ABI in include/sgemm.h
 and include/sgemm_probe.h; ``run`` and ``run_host`` add the conversion from
-torch tensors / numpy arrays to pointers and leading dimensions.
+torch tensors / numpy arrays to pointers and leading dimensions.  The
+feed-forward operators (include/sgemm_ffn.h: the gated block and its gradients,
+products with 4-bit weights, the AdamW step) take torch tensors: ffn.py.
 
 There is no fallback: if the library has not been built, or no sm_103 GPU is
 present, calls raise.
@@ -381,5 +383,14 @@ def probe_hold(ns: int, stream=None) -> None:
     _check(library().sgemm_probe_hold(int(ns), s), "sgemm_probe_hold")
 
 
-from .ffn import (AdamW, W4Matrix, ffn_backward, ffn_forward, ffn_saved,  # noqa: E402
-                  w4_quantize)
+# The feed-forward operators work on torch tensors: their module is imported
+# with the first of its names that is used, so that the rest needs no torch.
+_FFN_NAMES = ("ffn_forward", "ffn_saved", "ffn_backward", "W4Matrix", "w4_quantize", "AdamW")
+
+
+def __getattr__(name):
+    if name in _FFN_NAMES:
+        from . import ffn
+        value = globals()[name] = getattr(ffn, name)
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -22,7 +22,7 @@
 //
 // Structure, 384 threads a CTA, one CTA per SM:
 //   warp 0       one thread issues the TMA loads of 64-deep operand blocks
-//                (128-byte swizzle) into a ring of 32 KB stages
+//                (128-byte swizzle) into a ring of 32 KB (FP32 pairs: 24 KB) stages
 //   warp 1       one thread issues tcgen05.mma and releases stages by commit
 //   warp 2       allocates and frees tensor memory
 //   warps 4-11   epilogue, from one of two accumulators while the other fills
