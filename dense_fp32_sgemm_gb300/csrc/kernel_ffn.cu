@@ -21,9 +21,9 @@
 // up in registers in FP32.
 //
 // Structure, 384 threads a CTA, one CTA per SM:
-//   warp 0       one thread issues the TMA loads of 64-deep operand blocks
+//   warp 0       one elected thread issues the TMA loads of 64-deep operand blocks
 //                (128-byte swizzle) into a ring of 32 KB (FP32 pairs: 24 KB) stages
-//   warp 1       one thread issues tcgen05.mma and releases stages by commit
+//   warp 1       one elected thread issues tcgen05.mma and releases stages by commit
 //   warp 2       allocates and frees tensor memory
 //   warps 4-11   epilogue, from one of two accumulators while the other fills
 // CG = 2: a pair of CTAs on one 256 x 256 tile (FP32: 256 x 128, as a thread
@@ -291,86 +291,91 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp == 0) {
-        if (lane == 0) {
-            // Stages so far over all tiles, the next one's place in the ring
-            // and the parity its release is waited for with (1: still new).
-            int it = 0, s = 0;
-            uint32_t parity = 1;
-            bool ok = true;
-            const uint32_t bar0 = CG == 2 ? cluster_addr(&full[0], 0) : smem_addr(&full[0]);
-            Unit unit;
-            for (int u = 0; ok && unit_at(p, worker, u, unit); ++u) {
-                const FfnProblem &pr = p.prob[MODE == kFfnStore ? unit.prob : 0];
-                const int m0 = unit.m * (kFfnBM * CG) + (int)rank * kFfnBM;
-                const int n0 = unit.n * kTileN, k_end = pr.kblocks * kFfnBK;
-                const bool a_mn = pr.a_mn, b_mn = pr.b_mn;
-                const uint32_t bytes = (pr.a_bytes + Fm::kBBytes) * CG;
-                int seg = unit.s0 >= pr.kblocks ? 1 : 0;
-                int k = unit.s0 * kFfnBK - seg * k_end;
-                for (int step = unit.s0; ok && step < unit.s1; ++step, k += kFfnBK) {
-                    if (k >= k_end) {
-                        k = 0;
-                        seg = 1;
-                    }
-                    const CUtensorMap *ma = &maps.m[pr.a + seg], *mb = &maps.m[pr.b + seg];
-                    {
+        // The whole warp runs the loop, as in the next branch, and one elected
+        // lane issues: alone in the loop, a lane took some 700 clocks to issue
+        // a stage's loads.
+        // Stages so far over all tiles, the next one's place in the ring
+        // and the parity its release is waited for with (1: still new).
+        int it = 0, s = 0;
+        uint32_t parity = 1;
+        bool ok = true;
+        const uint32_t bar0 = CG == 2 ? cluster_addr(&full[0], 0) : smem_addr(&full[0]);
+        Unit unit;
+        for (int u = 0; ok && unit_at(p, worker, u, unit); ++u) {
+            const FfnProblem &pr = p.prob[MODE == kFfnStore ? unit.prob : 0];
+            const int m0 = unit.m * (kFfnBM * CG) + (int)rank * kFfnBM;
+            const int n0 = unit.n * kTileN, k_end = pr.kblocks * kFfnBK;
+            const bool a_mn = pr.a_mn, b_mn = pr.b_mn;
+            const uint32_t bytes = (pr.a_bytes + Fm::kBBytes) * CG;
+            int seg = unit.s0 >= pr.kblocks ? 1 : 0;
+            int k = unit.s0 * kFfnBK - seg * k_end;
+            for (int step = unit.s0; ok && step < unit.s1; ++step, k += kFfnBK) {
+                if (k >= k_end) {
+                    k = 0;
+                    seg = 1;
+                }
+                const CUtensorMap *ma = &maps.m[pr.a + seg], *mb = &maps.m[pr.b + seg];
 #pragma unroll 1
-                        for (int load = 0; load < kLoads; ++load, ++it) {
-                            if (p.skip_loads_from >= 0 && it >= p.skip_loads_from) {
-                                ok = false;
-                                break;
-                            }
-                            if (!tc_wait(&empty[s], parity, p.timeout_ns)) {
-                                atomicOr(p.err, kErrWaitTimeout);
-                                s_abort = 1;
-                                ok = false;
-                                break;
-                            }
-                            const int plane = kSplit ? plane_at(load) : 0;
-                            unsigned char *a = smem + s * kStageBytes, *b = a + kABytes;
-                            // The pair's loads all complete on the first CTA's barrier.
-                            if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-                            const uint32_t bar = bar0 + s * 8;
-                            if (a_mn) {
-                                tc_load_3d<CG>(a, ma, bar, m0, k, plane);
-                                tc_load_3d<CG>(a + kBlockBytes, ma, bar, m0 + 64, k, plane);
-                            } else {
-                                tc_load_3d<CG>(a, ma, bar, k, m0, plane);
-                            }
-                            if constexpr (MODE == kFfnGate) {
-                                // One CTA: 64 columns of each matrix.  A pair: the
-                                // first CTA brings Wg's columns, the second Wu's.
-                                const CUtensorMap *m1 = CG == 2 ? mb + rank : mb;
-                                const CUtensorMap *m2 = CG == 2 ? m1 : mb + 1;
-                                tc_load_3d<CG>(b, m1, bar, n0, k, plane);
+                for (int load = 0; load < kLoads; ++load, ++it) {
+                    if (p.skip_loads_from >= 0 && it >= p.skip_loads_from) {
+                        ok = false;
+                        break;
+                    }
+                    ok = tc_wait_warp(&empty[s], parity, p.timeout_ns);
+                    if (!ok) {
+                        if (lane == 0) {
+                            atomicOr(p.err, kErrWaitTimeout);
+                            s_abort = 1;
+                        }
+                        break;
+                    }
+                    if (tc_elect()) {
+                        const int plane = kSplit ? plane_at(load) : 0;
+                        const uint32_t a = sbase + s * kStageBytes, b = a + kABytes;
+                        // The pair's loads all complete on the first CTA's barrier.
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+                        const uint32_t bar = bar0 + s * 8;
+                        if (a_mn) {
+                            tc_load_3d<CG>(a, ma, bar, m0, k, plane);
+                            tc_load_3d<CG>(a + kBlockBytes, ma, bar, m0 + 64, k, plane);
+                        } else {
+                            tc_load_3d<CG>(a, ma, bar, k, m0, plane);
+                        }
+                        if constexpr (MODE == kFfnGate) {
+                            // One CTA: 64 columns of each matrix.  A pair: the
+                            // first CTA brings Wg's columns, the second Wu's.
+                            const CUtensorMap *m1 = CG == 2 ? mb + rank : mb;
+                            const CUtensorMap *m2 = CG == 2 ? m1 : mb + 1;
+                            tc_load_3d<CG>(b, m1, bar, n0, k, plane);
+                            if constexpr (Fm::kBCols == 128)
+                                tc_load_3d<CG>(b + kBlockBytes, m2, bar, CG == 2 ? n0 + 64 : n0, k, plane);
+                        } else {
+                            const int n = n0 + (int)rank * Fm::kBCols;
+                            if (b_mn) {
+                                tc_load_3d<CG>(b, mb, bar, n, k, plane);
                                 if constexpr (Fm::kBCols == 128)
-                                    tc_load_3d<CG>(b + kBlockBytes, m2, bar, CG == 2 ? n0 + 64 : n0, k, plane);
+                                    tc_load_3d<CG>(b + kBlockBytes, mb, bar, n + 64, k, plane);
                             } else {
-                                const int n = n0 + (int)rank * Fm::kBCols;
-                                if (b_mn) {
-                                    tc_load_3d<CG>(b, mb, bar, n, k, plane);
-                                    if constexpr (Fm::kBCols == 128)
-                                        tc_load_3d<CG>(b + kBlockBytes, mb, bar, n + 64, k, plane);
-                                } else {
-                                    tc_load_3d<CG>(b, mb, bar, k, n, plane);
-                                }
-                            }
-                            if (++s == kStages) {
-                                s = 0;
-                                parity ^= 1;
+                                tc_load_3d<CG>(b, mb, bar, k, n, plane);
                             }
                         }
                     }
+                    __syncwarp();
+                    if (++s == kStages) {
+                        s = 0;
+                        parity ^= 1;
+                    }
                 }
             }
-            // The last releases of the stages have to arrive before the CTA
-            // leaves.
-            for (int i = max(0, it - kStages); ok && i < it; ++i)
-                if (!tc_wait(&empty[i % kStages], (i / kStages) & 1, p.timeout_ns)) {
-                    atomicOr(p.err, kErrDrainTimeout);
-                    s_abort = 1;
-                    ok = false;
-                }
+        }
+        // The last releases of the stages have to arrive before the CTA
+        // leaves.
+        for (int i = max(0, it - kStages); ok && i < it; ++i) {
+            ok = tc_wait_warp(&empty[i % kStages], (i / kStages) & 1, p.timeout_ns);
+            if (!ok && lane == 0) {
+                atomicOr(p.err, kErrDrainTimeout);
+                s_abort = 1;
+            }
         }
         __syncwarp();
     } else if (warp == 1) {

@@ -165,18 +165,18 @@ __device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32]) {
 // CG == 2 the pair's first CTA's).  c0 times the element size is a multiple
 // of 16 bytes.
 template <int CG>
-__device__ __forceinline__ void tc_load_3d(void *dst, const CUtensorMap *map, uint32_t bar, int c0,
+__device__ __forceinline__ void tc_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0,
                                            int c1, int c2) {
     if constexpr (CG == 1)
         asm volatile(
             "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
+            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
             : "memory");
     else
         asm volatile(
             "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            ".cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
+            ".cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
             : "memory");
 }
@@ -196,9 +196,11 @@ __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                      : "memory");
 }
-// Arrive on a barrier of any CTA of the cluster.
+// Arrive on a barrier of any CTA of the cluster, about tensor memory: what it
+// orders are tcgen05 operations already waited for, so CTA scope is enough
+// (cluster scope also waits for the thread's stores: 2000 clocks).
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 }  // namespace sgemm
