@@ -215,7 +215,7 @@ FfnPlan ffn_plan(FfnGemmParams &p, int num_sms) {
         q.pair = pair != 0;
         q.workers = num_sms / (pair ? 2 : 1);
         const int64_t steps = steps_of(p.count - 1);
-        const double step = f32 ? 6 * 330.0 : pair ? 512.0 : 330.0;
+        const double step = f32 ? (pair ? 1800.0 : 2300.0) : pair ? 512.0 : 330.0;
         const double size = ffn_slot_floats(f32, pair != 0) / 32768.0;
         double whole = 4000.0 + (pair ? 5000.0 : 2500.0);
         q.long_tiles = others ? p.prob[others].tile0 : 0;

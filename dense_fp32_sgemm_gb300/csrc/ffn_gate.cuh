@@ -12,19 +12,16 @@ template <bool ACCURATE>
 __device__ __forceinline__ float gate_exp(float x) {
     return ACCURATE ? expf(x) : __expf(x);
 }
-template <bool ACCURATE>
-__device__ __forceinline__ float gate_div(float a, float b) {
-    return ACCURATE ? a / b : __fdividef(a, b);
-}
-
 constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluK = 0.044715f;
 
 // 1 / (1 + exp(-x)).  exp(-x) may reach infinity (the result is then 0);
-// __fdividef returns 0 for divisors above 2^126, which is the same.
+// __fdividef returns 0 for divisors above 2^126, which is the same.  Its two
+// units of the last place are as good as the exponential's, and unlike the
+// exact division it has no branch, so that a lane's elements overlap.
 template <bool ACCURATE>
 __device__ __forceinline__ float gate_sigmoid(float x) {
-    return gate_div<ACCURATE>(1.0f, 1.0f + gate_exp<ACCURATE>(-x));
+    return __fdividef(1.0f, 1.0f + gate_exp<ACCURATE>(-x));
 }
 
 // act(g).  GELU's tanh form is g * sigmoid(2 c (g + k g^3)).

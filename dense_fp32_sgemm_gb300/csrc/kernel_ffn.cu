@@ -237,10 +237,9 @@ __device__ __forceinline__ void store_planes(unsigned char *stage, int lane, voi
         for (int q = 0; q < 3; ++q)
             store_block<kTypeBF16>(stage, lane, static_cast<uint16_t *>(base) + q * plane, ld, row0, n,
                                    rows, cols, true, [&](int i) {
-                                       float s[3];
-                                       split3(v[i], s);
-                                       v[i] = isfinite(s[0]) ? v[i] - s[0] : 0.0f;
-                                       return s[0];
+                                       const float part = bf16_part(v[i]);
+                                       v[i] = bf16_rest(v[i], part);
+                                       return part;
                                    });
     }
 }

@@ -48,25 +48,24 @@ __device__ __forceinline__ float2 unpack16(uint32_t w) {
     }
 }
 
-// x as the sum of three bf16 values (its 24 significant bits in parts of 8):
-// the first is x rounded to nearest, each next one rounds what is left, which
-// FP32 subtraction forms exactly.  A finite x that would round to infinity is
-// cut instead; an infinity or NaN is its first part alone.
+// x rounded to bf16; a finite x that would round to infinity is cut instead.
+__device__ __forceinline__ float bf16_part(float x) {
+    const float hi = __bfloat162float(__float2bfloat16_rn(x));
+    return fabsf(hi) == INFINITY ? __uint_as_float(__float_as_uint(x) & 0xFFFF0000u) : hi;
+}
+// What is left of x after its part, exact in FP32: nothing of an infinity or NaN.
+// (Selects, no branches: with branches a lane's elements go one after the other.)
+__device__ __forceinline__ float bf16_rest(float x, float part) {
+    return fabsf(part) < INFINITY ? x - part : 0.0f;
+}
+// x as the sum of three bf16 values (its 24 significant bits in parts of 8),
+// each the rounded rest of those before it; an infinity or NaN is its first part
+// alone.
 __device__ __forceinline__ void split3(float x, float (&part)[3]) {
-    float hi = __bfloat162float(__float2bfloat16_rn(x));
-    if (!isfinite(hi)) {
-        if (!isfinite(x)) {
-            part[0] = x;
-            part[1] = part[2] = 0.0f;
-            return;
-        }
-        hi = __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
-    }
-    const float r = x - hi;
-    const float mid = __bfloat162float(__float2bfloat16_rn(r));
-    part[0] = hi;
-    part[1] = mid;
-    part[2] = r - mid;
+    part[0] = bf16_part(x);
+    const float r = bf16_rest(x, part[0]);
+    part[1] = __bfloat162float(__float2bfloat16_rn(r));
+    part[2] = r - part[1];
 }
 
 }  // namespace sgemm
