@@ -60,11 +60,9 @@ struct Form {
 constexpr uint32_t kBlockBytes = 64 * kFfnBK * 2;  // 64 of m or n by 64 k
 
 // FP32: the planes of a k block in the order in which they are brought in (and
-// then used), each with A's and B's in one stage of the ring; and the k blocks
-// that pass through an accumulator before its sums are taken out.
+// then used), each with A's and B's in one stage of the ring.
 constexpr int kPlanes = 3;
 __device__ __forceinline__ int plane_at(int i) { return i == 0 ? 0 : 3 - i; }  // 0, 2, 1
-constexpr int kPhaseSteps = 1;
 
 // A stretch of one tile's k steps (a step: one k block, with all its plane
 // products) that a worker computes.
@@ -397,68 +395,74 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 // Per 16 k: two groups of eight rows (MN-major) or 32 bytes
                 // along the swizzled row (K-major); units of 16 bytes.
                 const uint32_t a_step = (pr.a_mn ? 2048 : 32) >> 4, b_step = (pr.b_mn ? 2048 : 32) >> 4;
-                // An accumulator takes the unit's steps, or (FP32) a few.
-                constexpr int kMost = kSplit ? kPhaseSteps : 1 << 30;
-                for (int step = unit.s0; ok && step < unit.s1;) {
-                    const int end = kSplit ? min(step + kMost, unit.s1) : unit.s1;
-                    ok = tc_wait_warp(&acc_empty[buf], acc_parity, p.timeout_ns);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    const uint32_t d = tmem + buf * kAccCols;
-                    // Waits for the next stage and returns its number.
-                    auto take = [&]() {
-                        const int at = s;
-                        ok = ok && tc_wait_warp(&full[s], parity, p.timeout_ns);
-                        tc_fence_after_sync();
-                        if (++s == kStages) {
-                            s = 0;
-                            parity ^= 1;
-                        }
-                        return at;
-                    };
-                    // A of stage i times B of stage j.
-                    auto product = [&](int i, int j, bool first) {
-                        const uint64_t a = desc_a + i * (kStageBytes >> 4);
-                        const uint64_t b = desc_b + j * (kStageBytes >> 4);
+                // Waits for the next stage and returns its number.
+                auto take = [&]() {
+                    const int at = s;
+                    ok = ok && tc_wait_warp(&full[s], parity, p.timeout_ns);
+                    if (++s == kStages) {
+                        s = 0;
+                        parity ^= 1;
+                    }
+                    return at;
+                };
+                // A of stage i times B of stage j into accumulator d.
+                auto product = [&](uint32_t d, int i, int j, bool first) {
+                    const uint64_t a = desc_a + i * (kStageBytes >> 4);
+                    const uint64_t b = desc_b + j * (kStageBytes >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < kFfnBK / 16; ++kk)
-                            tc_mma<CG>(d, a + kk * a_step, b + kk * b_step, idesc, !first || kk != 0);
-                    };
-                    for (bool first = true; step < end; ++step, first = false) {
-                        const int s0 = take();
-                        if constexpr (kSplit) {
-                            // Six products of the planes, smallest first; a
-                            // stage is released after its last use.
-                            const int s2 = take();
-                            if (!ok) break;
-                            if (tc_elect()) {
-                                product(s2, s0, first);
-                                product(s0, s2, false);
-                                tc_commit<CG>(&empty[s2]);
-                            }
-                            __syncwarp();
-                            const int s1 = take();
-                            if (!ok) break;
-                            if (tc_elect()) {
-                                product(s1, s1, false);
-                                product(s1, s0, false);
-                                product(s0, s1, false);
-                                tc_commit<CG>(&empty[s1]);
-                                product(s0, s0, false);
-                                tc_commit<CG>(&empty[s0]);
-                            }
-                        } else {
-                            if (!ok) break;
-                            if (tc_elect()) {
-                                product(s0, s0, first);
-                                tc_commit<CG>(&empty[s0]);
-                            }
+                    for (int kk = 0; kk < kFfnBK / 16; ++kk)
+                        tc_mma<CG>(d, a + kk * a_step, b + kk * b_step, idesc, !first || kk != 0);
+                };
+                ok = tc_wait_warp(&acc_empty[buf], acc_parity, p.timeout_ns);
+                if constexpr (kSplit) {
+                    // An accumulator takes one step: six products of the
+                    // planes, smallest first; a stage is released after its
+                    // last use.  What the next step starts with is waited for
+                    // while the last products stand in the tensor core's queue
+                    // (of about four MMAs).
+                    int s0 = take(), s2 = take();
+                    for (int step = unit.s0; ok; ++step) {
+                        tc_fence_after_sync();
+                        const uint32_t d = tmem + buf * kAccCols;
+                        if (tc_elect()) {
+                            product(d, s2, s0, true);
+                            product(d, s0, s2, false);
+                            tc_commit<CG>(&empty[s2]);
+                        }
+                        __syncwarp();
+                        const int s1 = take();
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        if (tc_elect()) {
+                            product(d, s1, s1, false);
+                            product(d, s1, s0, false);
+                            product(d, s0, s1, false);
+                            tc_commit<CG>(&empty[s1]);
+                            product(d, s0, s0, false);
+                            tc_commit<CG>(&empty[s0]);
+                            tc_commit<CG>(&acc_full[buf]);
+                        }
+                        __syncwarp();
+                        buf ^= 1;
+                        acc_parity ^= buf ^ 1;
+                        if (step + 1 == unit.s1) break;
+                        ok = tc_wait_warp(&acc_empty[buf], acc_parity, p.timeout_ns);
+                        s0 = take();
+                        s2 = take();
+                    }
+                } else {
+                    const uint32_t d = tmem + buf * kAccCols;
+                    for (int step = unit.s0; ok && step < unit.s1; ++step) {
+                        const int at = take();
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        if (tc_elect()) {
+                            product(d, at, at, step == unit.s0);
+                            tc_commit<CG>(&empty[at]);
+                            if (step + 1 == unit.s1) tc_commit<CG>(&acc_full[buf]);
                         }
                         __syncwarp();
                     }
-                    if (!ok) break;
-                    if (tc_elect()) tc_commit<CG>(&acc_full[buf]);
-                    __syncwarp();
                     buf ^= 1;
                     acc_parity ^= buf ^ 1;
                 }
@@ -495,7 +499,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 for (int j = 0; j < kParts; ++j)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) sum[j][i] = 0.0f;
-                for (int q = unit.s0; q < unit.s1; q += kPhaseSteps) {
+                for (int q = unit.s0; q < unit.s1; ++q) {
                     ok = tc_wait_warp(&acc_full[buf], parity, p.timeout_ns);
                     if (!ok) break;
                     tc_fence_after_sync();
@@ -522,8 +526,11 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             // This warp's part of the accumulator.
             auto own = [&](int j, float (&v)[32]) {
                 if constexpr (kSplit) {
+                    // Chosen by value: unrolled over the parts, the code below
+                    // is so long that fetching it takes longer than running it.
+                    static_assert(kParts == 2, "");
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = sum[j][i];
+                    for (int i = 0; i < 32; ++i) v[i] = j ? sum[kParts - 1][i] : sum[0][i];
                 } else {
                     uint32_t r[32];
                     tc_ld32(d + part_col(j), r);
@@ -541,7 +548,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             bool emit = rows > 0;
             if (unit.pieces > 1 && rows > 0) {
                 float *mine = slot(unit.piece);
-#pragma unroll(kSplit ? kParts : 1)
+#pragma unroll 1
                 for (int j = 0; j < kParts; ++j) {
                     float v[32];
                     own(j, v);
@@ -588,7 +595,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 }
             };
             if (emit) {
-#pragma unroll(kSplit ? kParts : 1)
+#pragma unroll 1
                 for (int j = 0; j < kParts; j += kTwo) {
                     const int n = n_tile + (MODE == kFfnGate ? half * (kAccCols / 4) + 16 * j : part_col(j));
                     const int cols = pr.N - n;
@@ -629,18 +636,16 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                         store_planes<TYPE>(stage, lane, pr.C[0], pr.ldc, pr.c_plane, row0, n, rows,
                                            cols, w);
                     } else {
-                        float t[32];
-                        get_lanes(p.keep[0] + kept, lane, t);
                         value(j, v);
+#pragma unroll 1
+                        for (int w = 0; w < 2; ++w) {
+                            float t[32];
+                            get_lanes(p.keep[w] + kept, lane, t);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) t[i] *= v[i];
-                        store_planes<TYPE>(stage, lane, pr.C[0], pr.ldc, pr.c_plane, row0, n, rows,
-                                           cols, t);
-                        get_lanes(p.keep[1] + kept, lane, t);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] *= t[i];
-                        store_planes<TYPE>(stage, lane, pr.C[1], pr.ldc, pr.c_plane, row0, n, rows,
-                                           cols, v);
+                            for (int i = 0; i < 32; ++i) t[i] *= v[i];
+                            store_planes<TYPE>(stage, lane, pr.C[w], pr.ldc, pr.c_plane, row0, n, rows,
+                                               cols, t);
+                        }
                     }
                 }
             }
