@@ -215,7 +215,7 @@ FfnPlan ffn_plan(FfnGemmParams &p, int num_sms) {
         q.pair = pair != 0;
         q.workers = num_sms / (pair ? 2 : 1);
         const int64_t steps = steps_of(p.count - 1);
-        const double step = f32 ? (pair ? 1800.0 : 2300.0) : pair ? 512.0 : 330.0;
+        const double step = f32 ? (pair ? 1800.0 : 2300.0) : pair ? 512.0 : 450.0;
         const double size = ffn_slot_floats(f32, pair != 0) / 32768.0;
         double whole = 4000.0 + (pair ? 5000.0 : 2500.0);
         q.long_tiles = others ? p.prob[others].tile0 : 0;
@@ -419,12 +419,15 @@ sgemm_status_t sgemm_ffn_forward(int64_t T, int64_t D, int64_t F, int type, int 
     if (F == 0) return zero_matrix(y, ldy, T, D, type, st);
     // Few rows: passes over the weights on the FP32 pipe, one for every eight.
     // From five rows of 16-bit weights on that is the slower way (8 x 4096 x 12288:
-    // 167 us, the tensor cores 73), unless they would have to be copied to
-    // aligned rows; with FP32 weights, which the tensor cores need split in
-    // three first, from 25 (12 x 2048 x 8192: 212 us that way).
+    // 94 us, the tensor cores 72; 8 x 2048 x 8192: 53 and 39), unless the products
+    // are small (8 x 1024 x 4096: 22 us, the tensor cores 29) or the weights would
+    // have to be copied to aligned rows (8 x 2047 x 5461: 49 us, 67 and more that
+    // way); with FP32 weights, which the tensor cores need split in three first, from
+    // 25 (2048 x 5464: 24 rows 100 us, 32 rows on the tensor cores 144).
     const bool in_place = type != kTypeF32 && aligned(Wg, 16) && aligned(Wu, 16) &&
                           aligned(Wd, 16) && ldg % 8 == 0 && ldu % 8 == 0 && ldd % 8 == 0;
-    const int64_t few = type == kTypeF32 ? 24 : in_place ? 4 : 8;
+    const bool small = D * F <= 6 << 20;
+    const int64_t few = type == kTypeF32 ? 24 : in_place && !small ? 4 : 8;
     if (!saved && T <= few) return run_stream(dev, st, a, y, ldy);
     Arena w;
     Tail tail;

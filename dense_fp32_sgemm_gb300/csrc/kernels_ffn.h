@@ -218,6 +218,8 @@ struct FfnStreamParams {
     int device;
     // set by launch_ffn_stream
     int lanes_per_row, cta_rows, chunk_rows;
+    int safe_rows;           // see ffn_stream_kernel
+    const void *end, *end2;  // of W and W2
 };
 // vec: 16 bytes of a row's columns may be loaded at once (N a multiple too).
 cudaError_t launch_ffn_stream(const FfnStreamParams &p, int type, bool gate, bool vec, int num_sms,
