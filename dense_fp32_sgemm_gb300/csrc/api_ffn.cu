@@ -558,26 +558,35 @@ sgemm_status_t sgemm_w4_matvec(int64_t M, int64_t N, int64_t K, int64_t group, i
     p.device = dev.index;
     p.err = dev.err;
     p.timeout_ns = dev.timeout_ns;
+    p.safe_rows = (int)(72 / at_least_one(ldq)) + 1;  // 288 bytes
     const int max_rows = w4_max_rows(type);
     for (int64_t m0 = 0; m0 < M; m0 += max_rows) {
         p.M = (int)std::min<int64_t>(M - m0, max_rows);
         p.x = static_cast<const char *>(x) + m0 * ldx * e;
         p.y = static_cast<char *>(y) + m0 * ldy * e;
         p.warps_n = p.M <= 4 ? 1 : 2;
-        // A cluster of CTAs shares K where that shortens the call.  Model, in SM
-        // clocks, fitted to GB300 times of 15 shapes with one to eight CTAs: an SM
-        // takes 270 a unit and 1500 a CTA, and a CTA by itself 3000 and 1000 a
-        // unit of its warps.  (1 x 4096 x 4096, bf16: 7.9, 6.0, 5.1, 7.3 us with 1,
-        // 2, 4, 8; 1 x 12288 x 4096: 19.6, 12.1, 10.0, 12.2; 1 x 16384 x 24576:
-        // 55, 57, 52, 64, and 49 with 3.)
+        // A cluster of CTAs shares K where that shortens the call.  Model, in
+        // microseconds, fitted to GB300 times of 11 shapes with one to eight CTAs, of
+        // which it takes the best in every one: a wave takes 2.9 and 0.9 for each unit
+        // of a warp, an SM 0.028 a unit and 0.24 a CTA.  (8 x 4096 x 12288, bf16: 15.2,
+        // 14.5, 12.5, 16.7 us with 1 to 4; 1 x 4096 x 4096: 7.9, 6.0, 6.1, 5.1, and 7.3
+        // with 8; 16 x 12288 x 4096: 57, 33, 24, 19, and 16 with 8.)
         const int64_t tiles = (N + kW4Cols * p.warps_n - 1) / (kW4Cols * p.warps_n);
         const int warps_k = kW4Warps / p.warps_n;
+        const int parts = type == SGEMM_TYPE_F32 ? 3 : 1;
+        // What is left of an SM's places to clusters, which stay inside a group
+        // of SMs.
+        constexpr double kPlaced[kW4MaxCluster + 1] = {0, 1, 1, .96, .97, .96, .92, .88, .95};
         int cluster = 1;
         double least = 0.0;
         for (int c = 1; c <= kW4MaxCluster && (c == 1 || c * warps_k <= p.units); ++c) {
-            const int64_t per_warp = (p.units + c * warps_k - 1) / (c * warps_k);
-            const double cost = (270.0 * tiles * p.warps_n * p.units + 1500.0 * tiles * c) / dev.num_sms +
-                                1000.0 * per_warp;
+            const int units = (p.units + c - 1) / c;
+            const int staged = std::max(1, std::min(units, kW4StageBytes / w4_unit_bytes(type, p.M)));
+            const double places = kPlaced[c] * dev.num_sms * w4_ctas_per_sm(type, p.M, p.group, staged);
+            const double waves = ceil(tiles / std::max(1.0, floor(places / c)));
+            const double per_warp = (units + warps_k - 1) / warps_k;
+            const double cost = waves * (2.87 + 0.92 * per_warp * sqrt((parts * p.M + 7) / 8)) +
+                                tiles * (0.0276 * p.warps_n * p.units + 0.24 * c) / dev.num_sms;
             if (c == 1 || cost < least) {
                 least = cost;
                 cluster = c;

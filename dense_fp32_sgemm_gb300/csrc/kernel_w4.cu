@@ -47,6 +47,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "ops_common.cuh"
 #include "tc_common.cuh"
@@ -244,14 +245,21 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(TYPE, NT, GS))
                 // Two lanes to a row; 17 pieces cover 64 words wherever they
                 // start.
                 const int r = lane / 2, row = u * kRows + r;
-                if (row < k_words) {
-                    const uint32_t *q = p.q + row * p.ldq;
+                const uint32_t *q = p.q + row * p.ldq;
+                const unsigned char *piece =
+                    piece_of(reinterpret_cast<const unsigned char *>(q + n0)) + (lane % 2) * 16;
+                unsigned char *dst = to + r * kPlainPitch + (lane % 2) * 16;
+                if (u * kRows >= p.safe_rows && (u + 1) * kRows <= k_words - p.safe_rows) {
+                    // All pieces lie inside the matrix.
+#pragma unroll
+                    for (int c = 0; c < 9; ++c)
+                        if (c < 8 || lane % 2 == 0)
+                            cp_async16(reinterpret_cast<float *>(dst + c * 32),
+                                       reinterpret_cast<const float *>(piece + c * 32), 16);
+                } else if (row < k_words) {
                     const unsigned char *base = reinterpret_cast<const unsigned char *>(p.q);
                     const unsigned char *end = reinterpret_cast<const unsigned char *>(q + p.N);
-                    const unsigned char *piece =
-                        piece_of(reinterpret_cast<const unsigned char *>(q + n0)) + (lane % 2) * 16;
-                    unsigned char *dst = to + r * kPlainPitch + (lane % 2) * 16;
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < 9; ++c)
                         if (c < 8 || lane % 2 == 0)
                             copy_piece(dst + c * 32, piece + c * 32, base, end, 4);
@@ -674,6 +682,22 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const W4QuantParams p)
 int w4_max_rows(int type) { return type == kTypeF32 ? 8 : 16; }
 
 int w4_unit_bytes(int type, int M) { return (type == kTypeF32 ? 3 : 1) * M * kW4UnitK * 2; }
+
+int w4_ctas_per_sm(int type, int M, int group, int units) {
+    const int parts = type == kTypeF32 ? 3 : 1, nt = (parts * M + 7) / 8;
+    const int gs = group % 128 == 0 ? 4 : group % 64 == 0 ? 2 : 1;
+    auto ring = [&](auto type_of) {
+        constexpr int t = decltype(type_of)::value;
+        return gs == 4   ? UnitLayout<t, kSteps / 4>::kBytes
+               : gs == 2 ? UnitLayout<t, kSteps / 2>::kBytes
+                         : UnitLayout<t, kSteps>::kBytes;
+    };
+    const int stage = type == kTypeF32 ? ring(std::integral_constant<int, kTypeF32>())
+                                       : ring(std::integral_constant<int, kTypeF16>());
+    const int bytes = kW4Warps * kW4Stages * stage + parts * M * (units * kW4UnitK * 2 + 64) + 1024;
+    // An SM's 228 KB, of which each CTA takes one for itself.
+    return std::max(1, std::min(ctas_per_sm(type, nt, gs), 228 * 1024 / (bytes + 1024)));
+}
 
 cudaError_t launch_w4(const CUtensorMap &map, const W4Params &p, int type, bool vec, int cluster,
                       cudaStream_t stream) {

@@ -43,6 +43,7 @@ struct W4Params {
     int cta_units;     // units of one CTA
     int chunk_units;   // units whose x is staged at once
     int warps_n;       // warps side by side along the columns (1, 2 or 4)
+    int safe_rows;     // of q, at either end, from whose inside a piece may reach outside
     int device;
     int *err;
     unsigned long long timeout_ns;
@@ -56,6 +57,8 @@ int w4_max_rows(int type);
 // Bytes of shared memory a unit of staged x takes, and the limit for all of them.
 int w4_unit_bytes(int type, int M);
 constexpr int kW4StageBytes = 64 * 1024;
+// CTAs that an SM holds with x of `units` units staged.
+int w4_ctas_per_sm(int type, int M, int group, int units);
 
 struct W4QuantParams {
     int N, K, group, type;
