@@ -172,11 +172,14 @@ struct Kept {
 
 // Single CTAs or pairs, and how the tiles left over after whole rounds are cut
 // along k: the least of a model of SM clocks, fitted to GB300 times.  A step (64 k)
-// of a 256 x 256 pair tile takes 512, of a 128 x 128 tile 330 (its operands pass
-// through shared memory at the full rate); FP32 steps are six of 330.  Cutting a
-// tile in n pieces costs 128 KB a CTA written (6500 clocks on all SMs at once) and
-// n times as much read by the last to finish, half of both for single CTAs: at 333 x
-// 1000 x 1504 the cut products took 12 us longer than their steps.
+// of a 256 x 256 pair tile takes 512, of a 128 x 128 tile 450 (256 of products, but
+// its operands pass through shared memory twice in that time; 330 and 560 in its
+// place: 64 and 69 us against 60 for the training step 200 x 1000 x 2000).  FP32:
+// 1800 of a 256 x 128 pair tile, 2300 of a 128 x 128 one (2048 x 2048 x 8192 step
+// 2.20 and 2.67 ms).  Cutting a tile in n pieces costs 128 KB a CTA written (6500
+// clocks on all SMs at once) and n times as much read by the last to finish, half
+// of both for single CTAs: at 333 x 1000 x 1504 the cut products took 12 us longer
+// than their steps.
 struct FfnPlan {
     bool pair;
     int workers, long_tiles, extra, full_tiles, tail_tiles, tail_workers;
