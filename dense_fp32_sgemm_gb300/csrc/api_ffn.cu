@@ -179,7 +179,8 @@ struct Kept {
 // 2.20 and 2.67 ms).  Cutting a tile in n pieces costs 128 KB a CTA written (6500
 // clocks on all SMs at once) and n times as much read by the last to finish, half
 // of both for single CTAs: at 333 x 1000 x 1504 the cut products took 12 us longer
-// than their steps.
+// than their steps.  With FP32 the last to finish also has the longer epilogue (3000
+// and 1500 in place of 15000 and 4000: 777 x 1500 x 3000 405 us, so 382).
 struct FfnPlan {
     bool pair;
     int workers, long_tiles, extra, full_tiles, tail_tiles, tail_workers;
@@ -246,7 +247,7 @@ FfnPlan ffn_plan(FfnGemmParams &p, int num_sms) {
             if (q.tail_workers) {
                 const double pieces = n == 0 ? (double)q.workers / q.tail_tiles + 1.0 : n;
                 cost += step * (double)(q.tail_tiles * steps) / q.tail_workers +
-                        size * (f32 ? 3000.0 + 1500.0 * pieces : 8000.0 + 3500.0 * pieces);
+                        size * (f32 ? 15000.0 + 4000.0 * pieces : 8000.0 + 3500.0 * pieces);
             }
             if (least < 0.0 || cost < least) {
                 least = cost;
