@@ -34,7 +34,7 @@
 // power), shared memory in single CTAs and FP32.  Measured per call: 4096 x 4096 x
 // 12288 bf16 619-643 us (1.9-2.0 PFLOP/s), the training step 8192 x 2048 x 8192 bf16
 // 1345-1394 us (1.8), 2048 x 2048 x 8192 FP32 2130 us (290 TFLOP/s, 1.7 PFLOP/s of
-// plane products), 333 x 2000 x 5336 fp16 48-53 us.
+// plane products), 333 x 2000 x 5336 fp16 47-53 us.
 // Every wait is bounded; a role that gives up flags the error word, the others
 // run out in turn, and the CTA lets its copies land before it leaves.
 #include <algorithm>
