@@ -272,10 +272,11 @@ class AdamW:
     def _fill(self, field, tensors, dtype, counts):
         if len(tensors) != len(self._table):
             raise ValueError(f"{field}: {len(tensors)} tensors for {len(self._table)} parameters")
+        index = self.device.index if self.device.type == "cuda" else None
         for entry, t, n in zip(self._table, tensors, counts):
-            if t.dtype != dtype:
+            if t.dtype is not dtype:
                 raise TypeError(f"every {field} must be {dtype}")
-            if t.device != self.device or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+            if t.get_device() != index or not t.is_contiguous() or t.numel() != n:
                 raise ValueError(f"every {field} must be a contiguous tensor of its parameter's "
                                  f"size on {self.device}")
             setattr(entry, field, t.data_ptr())
