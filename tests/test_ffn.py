@@ -411,6 +411,48 @@ def test_wrapper_refuses_what_is_not_a_cuda_matrix():
         sg.ffn_forward(x[0], w, w, w)
 
 
+class OnDevice:
+    """What the wrapper reads of a CUDA tensor, without one."""
+
+    def __init__(self, t):
+        self.dtype, self.shape, self.device = t.dtype, t.shape, torch.device("cuda", 0)
+        self.dim, self.stride, self.data_ptr = t.dim, t.stride, lambda: 4096
+
+
+def test_overlapping_rows_are_refused():
+    # Rows with less than their length between them (a broadcast gradient's, say)
+    # end outside the memory that the tensor has.
+    from dense_fp32_sgemm_gb300.ffn import _matrix
+    f32, dev = torch.float32, torch.device("cuda", 0)
+
+    def ld(t):
+        return _matrix(OnDevice(t), "dy", *t.shape, f32, dev)[1]
+
+    one = torch.ones(1, 8)
+    for t in (one.expand(4, 8), torch.ones(64).as_strided((4, 8), (7, 1)), torch.ones(1, 1).expand(3, 1)):
+        with pytest.raises(ValueError, match="dy has overlapping rows"):
+            ld(t)
+    assert ld(one) == 8 and ld(torch.ones(4, 8)) == 8 and ld(torch.ones(4, 12)[:, :8]) == 12
+    assert ld(one.expand(1, 8)) == 8 and ld(one[:, :0].expand(4, 0)) >= 1
+    assert ld(torch.ones(64).as_strided((1, 8), (3, 1))) == 8  # one row: its stride means nothing
+
+
+@gpu
+def test_broadcast_tensors_are_refused(device):
+    T, D, F = 6, 16, 24
+    x, w, d = (torch.ones(s, device="cuda") for s in ((T, D), (D, F), (F, D)))
+    for bad in ((x[:1].expand(T, D), w, w, d), (x, w[:1].expand(D, F), w, d), (x, w, w, d[:1].expand(F, D))):
+        with pytest.raises(ValueError):
+            sg.ffn_forward(*bad)
+    with pytest.raises(ValueError):
+        sg.ffn_forward(x, w, w, d, y=torch.empty(1, D, device="cuda").expand(T, D))
+    for over in (dict(dy=x[:1].expand(T, D)), dict(dx=x[:1].expand(T, D)), dict(dw_gate=w[:1].expand(D, F)),
+                 dict(dw_down=d[:1].expand(F, D))):
+        dy = over.pop("dy", x)
+        with pytest.raises(ValueError):
+            sg.ffn_backward(dy, x, w, w, d, **over)
+
+
 @gpu
 def test_wrapper_refuses_wrong_shapes_and_types(device):
     x, w, d = (torch.ones(s, device="cuda") for s in ((4, 8), (8, 16), (16, 8)))

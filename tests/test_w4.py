@@ -283,3 +283,18 @@ def test_wrapper_refuses(device):
         w.matvec(x, torch.empty(2, 31, device="cuda", dtype=torch.bfloat16))
     with pytest.raises(ValueError):
         w.matvec(x.cpu())
+
+
+@gpu
+def test_broadcast_tensors_are_refused(device):
+    x, q, s, z = make(2, 64, 32, 32, "bf16", True)
+    for a in ((q[:1].expand(8, 32), s, z), (q, s[:1].expand(2, 32), z), (q, s, z[:1].expand(2, 32))):
+        with pytest.raises(ValueError):
+            sg.W4Matrix(a[0], a[1], 64, 32, zeros=a[2])
+    w = sg.W4Matrix(q, s, 64, 32, zeros=z)
+    with pytest.raises(ValueError):
+        w.matvec(x[:1].expand(2, 64))
+    with pytest.raises(ValueError):
+        w.matvec(x, torch.empty(1, 32, device="cuda", dtype=torch.bfloat16).expand(2, 32))
+    with pytest.raises(ValueError):
+        sg.w4_quantize(x[:1].expand(64, 64), 32)
