@@ -3,7 +3,10 @@ backward pass, products with 4-bit weights, and the AdamW step.
 
 Argument checks and marshalling only; all arithmetic runs in the library's
 CUDA kernels (include/sgemm_ffn.h).  Work is queued on ``stream`` (a
-torch.cuda.Stream) or the current stream; nothing here synchronises.
+torch.cuda.Stream) or the current stream; no call waits for it.  Outputs that
+are made here are allocated on the stream that writes them, as torch does under
+``torch.cuda.stream(stream)``: to use one on another stream, let that stream wait
+for ``stream`` and tell the allocator by ``record_stream``.
 """
 from __future__ import annotations
 
@@ -34,6 +37,16 @@ def _matrix(t, name, rows, cols, dtype, device):
         raise ValueError(f"{name} has overlapping rows ({step} elements apart, {cols} long): "
                          "pass a contiguous copy")
     return t.data_ptr(), max(step if rows > 1 else cols, cols, 1)
+
+
+def _empty(rows, cols, dtype, device, stream):
+    """A new rows x cols tensor from the memory of the stream that will write it.
+    (From the current stream's, the allocator could hand out memory that work queued
+    there still uses, and give it away again while `stream` still writes.)"""
+    if stream is None:
+        return torch.empty(rows, cols, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(rows, cols, dtype=dtype, device=device)
 
 
 def _type_of(t, name):
@@ -103,7 +116,7 @@ def ffn_forward(x, w_gate, w_up, w_down, y=None, activation: int = 0, saved=None
     """
     T, D, F, kind, args = _block(x, w_gate, w_up, w_down)
     if y is None:
-        y = torch.empty(T, D, dtype=x.dtype, device=x.device)
+        y = _empty(T, D, x.dtype, x.device, stream)
     _call(_sg.library().sgemm_ffn_forward, x.device, stream, T, D, F, kind, int(activation), *args,
           *_matrix(y, "y", T, D, x.dtype, x.device), _saved_address(saved, T, F, kind, x.device))
     return y
@@ -128,7 +141,7 @@ def ffn_backward(dy, x, w_gate, w_up, w_down, dx=None, dw_gate=None, dw_up=None,
         if not wanted:
             return None, (None, max(cols, 1))
         if t is None:
-            t = torch.empty(rows, cols, dtype=dtype, device=dev)
+            t = _empty(rows, cols, dtype, dev, stream)
         return t, _matrix(t, name, rows, cols, dtype, dev)
 
     dx, a = out(dx, "dx", T, D, need_dx)
@@ -174,7 +187,7 @@ class W4Matrix:
         read once per 16 rows, 8 with float32).  Returns y (allocated when not given)."""
         M = x.shape[0]
         if y is None:
-            y = torch.empty(M, self.N, dtype=self.dtype, device=self.device)
+            y = _empty(M, self.N, self.dtype, self.device, stream)
         if (x.shape == (M, self.K) and y.shape == (M, self.N) and x.dtype is self.dtype
                 and y.dtype is self.dtype and x.get_device() == y.get_device() == self._index
                 and x.is_contiguous() and y.is_contiguous()):
@@ -200,9 +213,9 @@ def w4_quantize(w, group: int = 128, zeros: bool = True, stream=None) -> W4Matri
     kind, dev = _type_of(w, "w"), w.device
     a = _matrix(w, "w", K, N, w.dtype, dev)
     groups = -(-K // group)
-    q = torch.empty(-(-K // 8), N, dtype=torch.int32, device=dev)
-    s = torch.empty(groups, N, dtype=w.dtype, device=dev)
-    z = torch.empty(groups, N, dtype=torch.uint8, device=dev) if zeros else None
+    q = _empty(-(-K // 8), N, torch.int32, dev, stream)
+    s = _empty(groups, N, w.dtype, dev, stream)
+    z = _empty(groups, N, torch.uint8, dev, stream) if zeros else None
     _call(_sg.library().sgemm_w4_quantize, dev, stream, N, K, group, kind, *a, q.data_ptr(),
           max(N, 1), s.data_ptr(), max(N, 1), z.data_ptr() if zeros else None, max(N, 1))
     return W4Matrix(q, s, K, group, zeros=z)

@@ -1,0 +1,132 @@
+"""Memory and order where the feed-forward operators run on another stream than
+the current one: outputs made by a call come from the memory of the stream that
+writes them.
+"""
+import contextlib
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import dense_fp32_sgemm_gb300 as sg
+
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def device():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    sg.build()
+    return torch.device("cuda", 0)
+
+
+class OnDevice:
+    """What the wrappers read of a CUDA tensor, without one."""
+
+    def __init__(self, *shape, dtype=torch.float32, empty=torch.empty):
+        t = empty(*shape, dtype=dtype)
+        self.dtype, self.shape, self.device = dtype, t.shape, torch.device("cuda", 0)
+        self.dim, self.stride, self.numel = t.dim, t.stride, t.numel
+        self.is_contiguous, self.requires_grad = t.is_contiguous, False
+
+    def data_ptr(self):
+        return 4096
+
+    def get_device(self):
+        return 0
+
+
+def calls(make):
+    """name -> a call on `stream` that makes its outputs, with tensors from make(rows, cols, dtype)."""
+    x, w, d = make(40, 64, torch.float32), make(64, 96, torch.float32), make(96, 64, torch.float32)
+    q, s = make(8, 96, torch.int32), make(2, 96, torch.float32)
+    w4 = sg.W4Matrix(q, s, 64, 32)
+    return {
+        "forward": lambda stream: sg.ffn_forward(x, w, w, d, stream=stream),
+        "backward": lambda stream: sg.ffn_backward(x, x, w, w, d, stream=stream),
+        "matvec": lambda stream: w4.matvec(x, stream=stream),
+        "quantize": lambda stream: sg.w4_quantize(w, 32, stream=stream),
+    }
+
+
+NAMES = ("forward", "backward", "matvec", "quantize")
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_outputs_are_allocated_under_their_stream(monkeypatch, name):
+    from dense_fp32_sgemm_gb300 import ffn
+    sg.build()
+    call = calls(lambda rows, cols, dtype: OnDevice(rows, cols, dtype=dtype))[name]
+    current, made = ["current"], []
+
+    @contextlib.contextmanager
+    def under(stream):
+        current.append(stream)
+        yield
+        current.pop()
+
+    def empty(*shape, dtype=None, device=None):
+        made.append(current[-1])
+        return OnDevice(*shape, dtype=dtype)
+
+    with monkeypatch.context() as m:
+        m.setattr(torch.cuda, "stream", under)
+        m.setattr(ffn, "_call", lambda *a: None)
+        m.setattr(torch, "empty", empty)
+        call("side")
+        assert made and set(made) == {"side"}
+        made.clear()
+        call(None)
+        assert made and set(made) == {"current"}
+
+
+def outputs(result):
+    if isinstance(result, sg.W4Matrix):
+        return [result.qweight, result.scales, result.zeros]
+    return list(result) if isinstance(result, tuple) else [result]
+
+
+def spans(tensors):
+    return [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors]
+
+
+def meet(a, b):
+    return any(p < v and u < q for p, q in a for u, v in b)
+
+
+@gpu
+@pytest.mark.parametrize("name", NAMES)
+def test_no_memory_in_use_on_another_stream_is_taken(device, name):
+    gen = torch.Generator("cuda").manual_seed(8)
+
+    def make(rows, cols, dtype):
+        if dtype == torch.int32:
+            return torch.zeros(rows, cols, dtype=dtype, device="cuda")
+        return torch.randn(rows, cols, generator=gen, device="cuda")
+
+    call, side = calls(make)[name], torch.cuda.Stream()
+    want = [t.clone() for t in outputs(call(None))]
+    torch.cuda.synchronize()
+    call(side)  # workspace first: what follows does not wait for the device
+    torch.cuda.synchronize()
+    sizes = [(t.numel(), t.dtype) for t in want]
+
+    def others():
+        return [torch.empty(n, dtype=dtype, device="cuda") for n, dtype in sizes for _ in range(3)]
+
+    # A result dropped before its stream has come to write it: its memory is not
+    # the current stream's to use.
+    sg.probe_hold(20_000_000, side)
+    held = spans(outputs(call(side)))
+    assert not side.query()
+    assert not meet(held, spans(others()))
+    torch.cuda.synchronize()
+    # Memory that the current stream has freed but still works on is not the other's.
+    sg.probe_hold(20_000_000, torch.cuda.current_stream())
+    freed = spans(others())
+    got = outputs(call(side))
+    assert not torch.cuda.current_stream().query()
+    assert not meet(freed, spans(got))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
