@@ -3,7 +3,7 @@ backward pass, products with 4-bit weights, and the AdamW step.
 
 Argument checks and marshalling only; all arithmetic runs in the library's
 CUDA kernels (include/sgemm_ffn.h).  Work is queued on ``stream`` (a
-torch.cuda.Stream) or the current stream; no call waits for it.  Outputs that
+torch.cuda.Stream) or the current stream; no call that queues work waits for it.  Outputs that
 are made here are allocated on the stream that writes them, as torch does under
 ``torch.cuda.stream(stream)``: to use one on another stream, let that stream wait
 for ``stream`` and tell the allocator by ``record_stream``.
@@ -235,7 +235,8 @@ class AdamW:
     grads: buffers of one type, read by every step (set_grads() replaces
     them).  m, v: the states, float32, or float8_e4m3fn together with m_scales
     and v_scales (float32, one value per 256 elements of a tensor) for states
-    of 8 bits; left out, they are made here with ``state_bits``.  copies:
+    of 8 bits; left out, they are made here with ``state_bits`` (which waits for the
+    current stream: their zeros are there for a step on any stream).  copies:
     None, or tensors of one type that receive the updated parameters (16-bit
     weights beside FP32 parameters).  The tensors are kept: their storage must
     stay where it is.  ``steps`` counts the steps taken.
@@ -261,6 +262,9 @@ class AdamW:
             if state_bits == 8:
                 m_scales, v_scales = ([torch.zeros(-(-p.numel() // ADAMW_BLOCK), device=p.device)
                                        for p in self.params] for _ in range(2))
+            if self.device.type == "cuda":
+                # Steps may run on any stream: the zeros are there before the first.
+                torch.cuda.current_stream(self.device).synchronize()
         self.m, self.v = list(m), list(v)
         self.state_bits = 32 if self.m[0].dtype == torch.float32 else 8
         state = torch.float32 if self.state_bits == 32 else torch.float8_e4m3fn

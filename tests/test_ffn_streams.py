@@ -1,6 +1,6 @@
 """Memory and order where the feed-forward operators run on another stream than
 the current one: outputs made by a call come from the memory of the stream that
-writes them.
+writes them, and an optimizer's states are zero before the first step on any.
 """
 import contextlib
 
@@ -130,3 +130,46 @@ def test_no_memory_in_use_on_another_stream_is_taken(device, name):
     assert not meet(freed, spans(got))
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@gpu
+@pytest.mark.parametrize("bits", [8, 32])
+def test_states_are_zero_before_a_step_on_any_stream(device, bits):
+    # The memory that the states get held ones before; the fill is queued behind work
+    # that keeps the current stream busy while the step runs on another.
+    n, side = 100_000, torch.cuda.Stream()
+    p, g = (torch.ones(n, device="cuda") for _ in range(2))
+    want = sg.AdamW([p.clone()], [g], state_bits=bits, lr=0.5)
+    want.step()
+    dirty = [torch.ones(n, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    del dirty
+    sg.probe_hold(20_000_000, torch.cuda.current_stream())
+    opt = sg.AdamW([p], [g], state_bits=bits, lr=0.5)
+    opt.step(stream=side)
+    torch.cuda.synchronize()
+    for a, b in zip(opt.params + opt.m + opt.v, want.params + want.m + want.v):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_states_wait_for_their_fill(monkeypatch):
+    # Without a device: the handle waits for the stream that fills them.
+    from dense_fp32_sgemm_gb300 import ffn
+    sg.build()
+    log = []
+
+    class Stream:
+        def synchronize(self):
+            log.append("wait")
+
+    def zeros(n, dtype=torch.float32, device=None):
+        log.append("fill")
+        t = OnDevice(n, dtype=dtype)
+        t.view = lambda kind: OnDevice(n, dtype=kind)
+        return t
+
+    with monkeypatch.context() as m:
+        m.setattr(torch, "zeros", zeros)
+        m.setattr(torch.cuda, "current_stream", lambda device=None: Stream())
+        ffn.AdamW([OnDevice(300)], [OnDevice(300)], state_bits=8)
+    assert log == ["fill"] * 4 + ["wait"]
