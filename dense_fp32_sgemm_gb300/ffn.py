@@ -292,19 +292,23 @@ class AdamW:
         self.set_grads(grads)
 
     def _fill(self, field, tensors, dtype, counts):
+        """Puts the tensors' addresses into the table: all of them, or none where one is
+        refused."""
         if len(tensors) != len(self._table):
             raise ValueError(f"{field}: {len(tensors)} tensors for {len(self._table)} parameters")
         index = self.device.index if self.device.type == "cuda" else None
-        for entry, t, n in zip(self._table, tensors, counts):
+        for t, n in zip(tensors, counts):
             if t.dtype is not dtype:
                 raise TypeError(f"every {field} must be {dtype}")
             if t.get_device() != index or not t.is_contiguous() or t.numel() != n:
                 raise ValueError(f"every {field} must be a contiguous tensor of its parameter's "
                                  f"size on {self.device}")
+        for entry, t in zip(self._table, tensors):
             setattr(entry, field, t.data_ptr())
 
     def set_grads(self, grads):
-        """Take the gradients from these buffers from now on."""
+        """Take the gradients from these buffers from now on.  Where one of them is refused,
+        the handle stays as it was."""
         grads = list(grads)
         kind = _type_of(grads[0], "grads") if grads else 0
         self._fill("grad", grads, grads[0].dtype if grads else None,

@@ -306,3 +306,24 @@ def test_wrapper_refuses(device):
         sg.AdamW([p], [g], [f8], [f8])
     with pytest.raises(sg.SgemmError):
         sg.AdamW([p], [g]).step(step=0)
+
+
+@gpu
+def test_refused_gradients_leave_the_handle_as_it_was(device):
+    def made():
+        return make([700, 33, 4096], "fp32", "fp32", 32, seed=21)
+
+    s, clean = made(), made()
+    opt, want = (sg.AdamW(t["p"], t["g"], t["m"], t["v"], **HYPER) for t in (s, clean))
+    before = [bytes(e) for e in opt._table]
+    others = [torch.full_like(g, 3.0) for g in s["g"]]
+    for bad in (others[:2] + [others[2][:-1]], others[:2] + [others[2].cpu()], others[:2] + [others[2].bfloat16()],
+                [g.bfloat16() for g in others[:2]] + [others[2]], others[:2]):
+        with pytest.raises((TypeError, ValueError)):
+            opt.set_grads(bad)
+        assert [bytes(e) for e in opt._table] == before
+        assert all(a is b for a, b in zip(opt.grads, s["g"]))
+    for o in (opt, want):
+        o.step(step=5)
+    for k in ("p", "m", "v"):
+        assert all(torch.equal(a, b) for a, b in zip(s[k], clean[k]))
