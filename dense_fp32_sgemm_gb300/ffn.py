@@ -260,7 +260,8 @@ class AdamW:
 
             m, v = states(), states()
             if state_bits == 8:
-                m_scales, v_scales = ([torch.zeros(-(-p.numel() // ADAMW_BLOCK), device=p.device)
+                m_scales, v_scales = ([torch.zeros(-(-p.numel() // ADAMW_BLOCK), dtype=torch.float32,
+                                                   device=p.device)
                                        for p in self.params] for _ in range(2))
             if self.device.type == "cuda":
                 # Steps may run on any stream: the zeros are there before the first.

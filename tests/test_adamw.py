@@ -327,3 +327,15 @@ def test_refused_gradients_leave_the_handle_as_it_was(device):
         o.step(step=5)
     for k in ("p", "m", "v"):
         assert all(torch.equal(a, b) for a, b in zip(s[k], clean[k]))
+
+
+@gpu
+def test_states_do_not_go_by_the_default_type(device):
+    p, g = torch.ones(300, device="cuda"), torch.ones(300, device="cuda")
+    torch.set_default_dtype(torch.float64)
+    try:
+        opt = sg.AdamW([p], [g], state_bits=8, lr=0.5, weight_decay=0.0)
+    finally:
+        torch.set_default_dtype(torch.float32)
+    opt.step()
+    assert opt.m_scales[0].dtype == torch.float32 and bool(((p - 0.5).abs() < 1e-6).all())
