@@ -11,6 +11,7 @@
 #include <mutex>
 #include <set>
 #include <utility>
+#include <vector>
 
 #include "../../include/sgemm.h"
 #include "../../include/sgemm_probe.h"
@@ -41,17 +42,26 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// Device memory that grows with the calls of a stream.  A captured graph holds the
+// address that its calls were given, so what it may hold is kept when it is
+// outgrown, until the workspace is released.
+struct Buffer {
+    void *p = nullptr;
+    size_t bytes = 0;
+    bool in_graph = false;
+    std::vector<std::pair<void *, size_t>> outgrown;
+
+    template <class T>
+    T *as() const {
+        return static_cast<T *>(p);
+    }
+};
+
 struct Workspace {
-    float *partials = nullptr;
-    size_t partial_bytes = 0;
-    int *counters = nullptr;
-    size_t counter_count = 0;
-    float *pack = nullptr;  // aligned copies of unaligned operands
-    size_t pack_bytes = 0;
-    float *split = nullptr;  // 3xTF32 hi / lo operand copies
-    size_t split_bytes = 0;
-    void *ops = nullptr;  // intermediates of the feed-forward operators
-    size_t ops_bytes = 0;
+    Buffer partials, counters;
+    Buffer pack;   // aligned copies of unaligned operands
+    Buffer split;  // 3xTF32 hi / lo operand copies
+    Buffer ops;    // intermediates of the feed-forward operators
 };
 
 struct HostBuffers {
@@ -125,38 +135,50 @@ sgemm_status_t device_state(DeviceState **out) {
     return SGEMM_OK;
 }
 
-sgemm_status_t ensure_workspace(DeviceState &d, cudaStream_t stream, size_t partial_bytes,
-                                size_t counters, Workspace **out) {
-    Workspace &w = d.ws[stream];
-    if (w.partial_bytes < partial_bytes) {
-        if (w.partials) cudaFree(w.partials);
-        w.partials = nullptr;
-        w.partial_bytes = 0;
-        if (cudaMalloc(&w.partials, partial_bytes) != cudaSuccess) return SGEMM_ERR_ALLOC;
-        w.partial_bytes = partial_bytes;
+// Makes `b` hold at least `bytes` for a call on `stream`; `grown` says whether it is new.
+sgemm_status_t grow(Buffer &b, size_t bytes, cudaStream_t stream, bool *grown = nullptr) {
+    if (grown) *grown = false;
+    if (bytes == 0) return SGEMM_OK;
+    if (b.bytes < bytes) {
+        if (b.p && (b.in_graph || cudaFree(b.p) != cudaSuccess)) b.outgrown.emplace_back(b.p, b.bytes);
+        b.p = nullptr;
+        b.bytes = 0;
+        b.in_graph = false;
+        if (cudaMalloc(&b.p, bytes) != cudaSuccess) {
+            cudaGetLastError();
+            b.p = nullptr;
+            return SGEMM_ERR_ALLOC;
+        }
+        b.bytes = bytes;
+        if (grown) *grown = true;
     }
-    if (w.counter_count < counters) {
-        if (w.counters) cudaFree(w.counters);
-        w.counters = nullptr;
-        w.counter_count = 0;
-        if (cudaMalloc(&w.counters, counters * sizeof(int)) != cudaSuccess) return SGEMM_ERR_ALLOC;
-        if (cudaMemset(w.counters, 0, counters * sizeof(int)) != cudaSuccess) return SGEMM_ERR_ALLOC;
-        w.counter_count = counters;
-    }
-    *out = &w;
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess)
+        cudaGetLastError();  // the default stream beside a capture: the launches will say so
+    else if (cap != cudaStreamCaptureStatusNone)
+        b.in_graph = true;
     return SGEMM_OK;
 }
 
-sgemm_status_t ensure_pack(DeviceState &d, cudaStream_t stream, size_t bytes, float **out) {
+void release(Buffer &b) {
+    if (b.p) cudaFree(b.p);
+    for (auto &o : b.outgrown) cudaFree(o.first);
+    b = Buffer();
+}
+
+sgemm_status_t ensure_workspace(DeviceState &d, cudaStream_t stream, size_t partial_bytes,
+                                size_t counters, Workspace **out) {
     Workspace &w = d.ws[stream];
-    if (w.pack_bytes < bytes) {
-        if (w.pack) cudaFree(w.pack);
-        w.pack = nullptr;
-        w.pack_bytes = 0;
-        if (cudaMalloc(&w.pack, bytes) != cudaSuccess) return SGEMM_ERR_ALLOC;
-        w.pack_bytes = bytes;
+    sgemm_status_t s = grow(w.partials, partial_bytes, stream);
+    if (s != SGEMM_OK) return s;
+    bool grown = false;
+    s = grow(w.counters, counters * sizeof(int), stream, &grown);
+    if (s != SGEMM_OK) return s;
+    if (grown && cudaMemset(w.counters.p, 0, w.counters.bytes) != cudaSuccess) {
+        w.counters.bytes = 0;  // the next call makes new ones
+        return SGEMM_ERR_ALLOC;
     }
-    *out = w.pack;
+    *out = &w;
     return SGEMM_OK;
 }
 
@@ -198,11 +220,11 @@ size_t skinny_partial_bytes(const Plan &pl) {
 }
 
 // The skinny kernel on the plan `pl` (A and B 16-byte aligned, M <= 32), with
-// the workspace `w` (at least skinny_partial_bytes(pl) and pl.slabs counters).
+// at least skinny_partial_bytes(pl) of `partials` and pl.slabs `counters`.
 sgemm_status_t run_skinny(DeviceState &d, const Plan &pl, int64_t M, int64_t N, int64_t K,
                           float alpha, const float *A, int64_t lda, const float *B, int64_t ldb,
-                          float beta, float *C, int64_t ldc, const Epilogue &epi, Workspace *w,
-                          cudaStream_t stream) {
+                          float beta, float *C, int64_t ldc, const Epilogue &epi, float *partials,
+                          int *counters, cudaStream_t stream) {
     const unsigned bit = 1u << (24 + pl.m_tile / 8);  // m_tile 8, 16, 32: bits 25, 26, 28
     if (!(d.configured & bit)) {
         if (skinny_configure(pl.m_tile) != cudaSuccess) return SGEMM_ERR_LAUNCH;
@@ -225,8 +247,8 @@ sgemm_status_t run_skinny(DeviceState &d, const Plan &pl, int64_t M, int64_t N, 
     const unsigned long long to = g_timeout_ns.load();
     sp.timeout_ns = to ? to : kDefaultTimeoutNs;
     sp.skip_loads_from = g_skip_loads_from.load();
-    sp.partials = w->partials;
-    sp.counters = w->counters;
+    sp.partials = partials;
+    sp.counters = counters;
     return status_from(launch_skinny(pl.m_tile, mapA, mapB, sp, pl.grid, stream));
 }
 
@@ -293,9 +315,10 @@ sgemm_status_t run_locked(int64_t M, int64_t N, int64_t K, float alpha, const fl
                 const size_t a_floats = pl.pack_a ? (size_t)M * pl.lda_packed : 0;
                 const size_t a_span = (a_floats + 63) / 64 * 64;  // keeps B's copy 256-byte aligned
                 const size_t b_floats = pl.pack_b ? (size_t)K * pl.ldb_packed : 0;
-                float *buf = nullptr;
-                sgemm_status_t s = ensure_pack(d, stream, (a_span + b_floats) * sizeof(float), &buf);
+                Buffer &pack = d.ws[stream].pack;
+                sgemm_status_t s = grow(pack, (a_span + b_floats) * sizeof(float), stream);
                 if (s != SGEMM_OK) return s;
+                float *buf = pack.as<float>();
                 PackJob jobs[2];
                 int n = 0;
                 if (pl.pack_a) {
@@ -360,8 +383,8 @@ sgemm_status_t run_locked(int64_t M, int64_t N, int64_t K, float alpha, const fl
                 s = ensure_workspace(d, stream, pbytes, counters, &w);
                 if (s != SGEMM_OK) return s;
                 if (pl.sk_tiles > 0) {
-                    tp.partials = w->partials;
-                    tp.counters = w->counters;
+                    tp.partials = w->partials.as<float>();
+                    tp.counters = w->counters.as<int>();
                 }
             }
             // The edges go to a second stream forked after the copies, so
@@ -403,12 +426,10 @@ sgemm_status_t run_locked(int64_t M, int64_t N, int64_t K, float alpha, const fl
                                Buse + N0, ldb_use, beta, C + N0, ldc, eepi, es);
             }
             if (s == SGEMM_OK && pl.edge_m > 0) {
-                Workspace ew = *w;
-                ew.partials = reinterpret_cast<float *>(reinterpret_cast<char *>(w->partials) +
-                                                        tile_pbytes);
-                ew.counters = w->counters + tile_counters;
                 s = run_skinny(d, edge_plan, pl.edge_m, N0, K, alpha, Ause + M0 * lda_use, lda_use,
-                               Buse, ldb_use, beta, C + M0 * ldc, ldc, epi, &ew, es);
+                               Buse, ldb_use, beta, C + M0 * ldc, ldc, epi,
+                               w->partials.as<float>() + tile_pbytes / sizeof(float),
+                               w->counters.as<int>() + tile_counters, es);
             }
             if (es != stream) {
                 // Join even after a failed launch, so the caller's stream
@@ -441,8 +462,8 @@ sgemm_status_t run_locked(int64_t M, int64_t N, int64_t K, float alpha, const fl
                 const size_t pbytes = (size_t)2 * pl.grid * pl.mid_bm * kMidBN * sizeof(float);
                 const sgemm_status_t s = ensure_workspace(d, stream, pbytes, (size_t)pl.sk_tiles, &w);
                 if (s != SGEMM_OK) return s;
-                mp.partials = w->partials;
-                mp.counters = w->counters;
+                mp.partials = w->partials.as<float>();
+                mp.counters = w->counters.as<int>();
             }
             return status_from(launch_mid(pl.mid_bm, pl.b_vec, mp, pl.grid, stream));
         }
@@ -486,7 +507,8 @@ sgemm_status_t run_locked(int64_t M, int64_t N, int64_t K, float alpha, const fl
             const sgemm_status_t s =
                 ensure_workspace(d, stream, skinny_partial_bytes(pl), (size_t)pl.slabs, &w);
             if (s != SGEMM_OK) return s;
-            return run_skinny(d, pl, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, epi, w, stream);
+            return run_skinny(d, pl, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, epi,
+                              w->partials.as<float>(), w->counters.as<int>(), stream);
         }
         case kVarNarrow:
             return run_narrow(d, pl.narrow_nn, pl.a_vec, pl.grid, pl.narrow_rows, M, N, K, alpha, A,
@@ -559,19 +581,10 @@ sgemm_status_t op_workspace(cudaStream_t stream, size_t bytes, void **out) {
     DeviceState *d = nullptr;
     const sgemm_status_t s = device_state(&d);
     if (s != SGEMM_OK) return s;
-    Workspace &w = d->ws[stream];
-    if (w.ops_bytes < bytes) {
-        if (w.ops) cudaFree(w.ops);
-        w.ops = nullptr;
-        w.ops_bytes = 0;
-        if (cudaMalloc(&w.ops, bytes) != cudaSuccess) {
-            cudaGetLastError();
-            return SGEMM_ERR_ALLOC;
-        }
-        w.ops_bytes = bytes;
-    }
-    *out = w.ops;
-    return SGEMM_OK;
+    Buffer &ops = d->ws[stream].ops;
+    const sgemm_status_t g = grow(ops, bytes, stream);
+    *out = ops.p;
+    return g;
 }
 
 sgemm_status_t op_counters(cudaStream_t stream, size_t count, int **out) {
@@ -579,13 +592,13 @@ sgemm_status_t op_counters(cudaStream_t stream, size_t count, int **out) {
     sgemm_status_t s = device_state(&d);
     if (s != SGEMM_OK) return s;
     Workspace *w = nullptr;
-    const bool grow = d->ws[stream].counter_count < count;
+    const bool grown = d->ws[stream].counters.bytes < count * sizeof(int);
     s = ensure_workspace(*d, stream, 0, count, &w);
     if (s != SGEMM_OK) return s;
     // New counters are cleared on the default stream, which `stream` need not
     // wait for.
-    if (grow && cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) return SGEMM_ERR_LAUNCH;
-    *out = w->counters;
+    if (grown && cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+    *out = w->counters.as<int>();
     return SGEMM_OK;
 }
 
@@ -685,17 +698,11 @@ sgemm_status_t sgemm_run_3xtf32_epilogue(int64_t M, int64_t N, int64_t K, float 
     const size_t a_floats = a_raw ? 0 : (size_t)(2 * Mp * Kp), b_floats = (size_t)(2 * Np * Kp);
     const size_t p_floats = a_pack ? (size_t)((M * ld_pack + 63) / 64 * 64) : 0;
     const size_t r_floats = splits > 1 ? (size_t)(splits * Mp * Np) : 0;
-    Workspace &w = d->ws[st];
-    const size_t bytes = (a_floats + b_floats + p_floats + r_floats) * sizeof(float);
-    if (w.split_bytes < bytes) {
-        if (w.split) cudaFree(w.split);
-        w.split = nullptr;
-        w.split_bytes = 0;
-        if (cudaMalloc(&w.split, bytes) != cudaSuccess) return SGEMM_ERR_ALLOC;
-        w.split_bytes = bytes;
-    }
+    Buffer &split = d->ws[st].split;
+    s = grow(split, (a_floats + b_floats + p_floats + r_floats) * sizeof(float), st);
+    if (s != SGEMM_OK) return s;
     // a_floats and b_floats are multiples of 64 floats (256 bytes)
-    float *sa = w.split, *sb = w.split + a_floats, *pa = sb + b_floats, *pr = pa + p_floats;
+    float *sa = split.as<float>(), *sb = sa + a_floats, *pa = sb + b_floats, *pr = pa + p_floats;
     const float *a_map = A;
     int64_t lda_map = lda;
     if (a_pack) {
@@ -910,10 +917,12 @@ sgemm_status_t sgemm_device_status(void *stream) {
     // A kernel gave up: clear the word and every arrival counter, so the
     // stream-K tickets of the abandoned call do not leak into the next one.
     if (cudaMemset(d->err, 0, sizeof(int)) != cudaSuccess) return SGEMM_ERR_LAUNCH;
-    for (auto &kv : d->ws)
-        if (kv.second.counters &&
-            cudaMemset(kv.second.counters, 0, kv.second.counter_count * sizeof(int)) != cudaSuccess)
-            return SGEMM_ERR_LAUNCH;
+    for (auto &kv : d->ws) {
+        const Buffer &c = kv.second.counters;
+        if (c.p && cudaMemset(c.p, 0, c.bytes) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+        for (auto &o : c.outgrown)
+            if (cudaMemset(o.first, 0, o.second) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+    }
     if (cudaDeviceSynchronize() != cudaSuccess) return SGEMM_ERR_LAUNCH;
     return SGEMM_ERR_DEVICE_TIMEOUT;
 }
@@ -1009,11 +1018,9 @@ sgemm_status_t sgemm_release_workspace(void) {
         cudaSetDevice(kv.first);
         cudaDeviceSynchronize();
         for (auto &w : d.ws) {
-            if (w.second.partials) cudaFree(w.second.partials);
-            if (w.second.counters) cudaFree(w.second.counters);
-            if (w.second.pack) cudaFree(w.second.pack);
-            if (w.second.split) cudaFree(w.second.split);
-            if (w.second.ops) cudaFree(w.second.ops);
+            for (Buffer *b : {&w.second.partials, &w.second.counters, &w.second.pack, &w.second.split,
+                              &w.second.ops})
+                release(*b);
         }
         d.ws.clear();
         if (d.side) cudaStreamDestroy(d.side);

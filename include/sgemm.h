@@ -71,6 +71,10 @@ enum {
  *   the library on first use per (device, stream) and kept until
  *   sgemm_release_workspace().  Concurrent calls on one stream are ordered by
  *   the stream; calls on different streams use different workspaces.
+ *   It grows with the calls.  What a captured CUDA graph may hold of it stays
+ *   allocated when it is outgrown, so a graph can be replayed after larger calls
+ *   on its stream, but not after sgemm_release_workspace(), and not at the same
+ *   time as other work of the stream that it was captured on.
  * Returns SGEMM_ERR_INVALID_ARG if M, N or K < 0, a leading dimension is below
  *   its minimum, or a pointer the operation must dereference is NULL or not
  *   4-byte aligned; SGEMM_ERR_LAUNCH if a launch fails.  A bounded device wait

@@ -9,8 +9,8 @@
  * Conventions are those of sgemm.h: row-major matrices with a leading
  * dimension in elements, device pointers owned by the caller, work queued on
  * `stream` without host synchronisation, workspace kept per (device, stream)
- * until sgemm_release_workspace(), errors returned before any work is
- * queued, a bounded device wait that gave up reported by
+ * until sgemm_release_workspace() (what a captured graph holds of it too, when
+ * a larger call outgrows it), errors returned before any work is queued, a bounded device wait that gave up reported by
  * sgemm_device_status().  A pointer has to be aligned to its element's size;
  * 16-byte aligned pointers whose rows lie a multiple of 16 bytes apart take
  * the fastest path.  For given sizes, leading dimensions and alignment the

@@ -1,6 +1,7 @@
 """Memory and order where the feed-forward operators run on another stream than
 the current one: outputs made by a call come from the memory of the stream that
-writes them, and an optimizer's states are zero before the first step on any.
+writes them, an optimizer's states are zero before the first step on any, and the
+workspace that a captured graph holds outlives larger calls.
 """
 import contextlib
 
@@ -173,3 +174,73 @@ def test_states_wait_for_their_fill(monkeypatch):
         m.setattr(torch.cuda, "current_stream", lambda device=None: Stream())
         ffn.AdamW([OnDevice(300)], [OnDevice(300)], state_bits=8)
     assert log == ["fill"] * 4 + ["wait"]
+
+
+def ffn_case(T, D=64, F=500):
+    gen = torch.Generator("cuda").manual_seed(T)
+    x, wg, wu, wd = (torch.randn(a, b, generator=gen, device="cuda").bfloat16()
+                     for a, b in ((T, D), (D, F), (D, F), (F, D)))
+    y = torch.empty_like(x)
+    return lambda: sg.ffn_forward(x, wg, wu, wd, y=y), y
+
+
+def product_case(run, M, N, K):
+    gen = torch.Generator("cuda").manual_seed(M)
+    a, b = (torch.randn(n, m, generator=gen, device="cuda") for n, m in ((M, K), (K, N)))
+    c = torch.empty(M, N, device="cuda")
+    return lambda: run(a, b, c), c
+
+
+# A small call, a larger one of the same kind on the same stream, and the megabytes of
+# the small one's workspace: the block's partial tiles (152 of 256 KB and more), stream-K
+# tiles (two 128 KB slots a CTA), split operands of the 3xTF32 form (2 of 4 bytes each way).
+GROWING = {
+    "block": (lambda: ffn_case(150), lambda: ffn_case(3000), 40),
+    "stream-K": (lambda: product_case(sg.run, 2048, 1024, 1024),
+                 lambda: product_case(sg.run, 2048, 2048, 2048), 30),
+    "counters": (lambda: product_case(sg.run, 2048, 1024, 1024),
+                 lambda: product_case(sg.run, 20, 200_000, 500), 0),
+    "3xTF32": (lambda: product_case(sg.run_3xtf32, 1024, 1024, 2048),
+               lambda: product_case(sg.run_3xtf32, 2048, 2048, 2048), 16),
+}
+
+
+@gpu
+@pytest.mark.parametrize("name", GROWING)
+def test_a_graph_outlives_a_larger_call_on_its_stream(device, name):
+    small, large, megabytes = GROWING[name]
+    sg.release_workspace()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    call, y = small()
+    other, z = large()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.synchronize()
+    want = y.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    with torch.cuda.stream(side):
+        other()
+    torch.cuda.synchronize()
+    first = z.clone()
+    # The larger workspace came beside the one that the graph holds.
+    assert free - torch.cuda.mem_get_info()[0] >= megabytes * 1_000_000
+    for _ in range(2):
+        y.zero_()
+        z.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            other()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(z, first)
+    assert sg.device_status(side) == 0
+    del graph
+    before = torch.cuda.mem_get_info()[0]
+    sg.release_workspace()
+    assert torch.cuda.mem_get_info()[0] - before >= 2 * megabytes * 1_000_000
