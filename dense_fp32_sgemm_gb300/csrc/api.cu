@@ -174,7 +174,10 @@ sgemm_status_t ensure_workspace(DeviceState &d, cudaStream_t stream, size_t part
     bool grown = false;
     s = grow(w.counters, counters * sizeof(int), stream, &grown);
     if (s != SGEMM_OK) return s;
-    if (grown && cudaMemset(w.counters.p, 0, w.counters.bytes) != cudaSuccess) {
+    // New counters are cleared on the default stream, which `stream` need not wait
+    // for and which may be busy: the host waits, once for each growth.
+    if (grown && (cudaMemset(w.counters.p, 0, w.counters.bytes) != cudaSuccess ||
+                  cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess)) {
         w.counters.bytes = 0;  // the next call makes new ones
         return SGEMM_ERR_ALLOC;
     }
@@ -592,12 +595,8 @@ sgemm_status_t op_counters(cudaStream_t stream, size_t count, int **out) {
     sgemm_status_t s = device_state(&d);
     if (s != SGEMM_OK) return s;
     Workspace *w = nullptr;
-    const bool grown = d->ws[stream].counters.bytes < count * sizeof(int);
     s = ensure_workspace(*d, stream, 0, count, &w);
     if (s != SGEMM_OK) return s;
-    // New counters are cleared on the default stream, which `stream` need not
-    // wait for.
-    if (grown && cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) return SGEMM_ERR_LAUNCH;
     *out = w->counters.as<int>();
     return SGEMM_OK;
 }

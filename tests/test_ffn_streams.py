@@ -244,3 +244,25 @@ def test_a_graph_outlives_a_larger_call_on_its_stream(device, name):
     before = torch.cuda.mem_get_info()[0]
     sg.release_workspace()
     assert torch.cuda.mem_get_info()[0] - before >= 2 * megabytes * 1_000_000
+
+
+@gpu
+@pytest.mark.parametrize("name", ["block", "stream-K"])
+def test_the_first_call_on_a_stream_while_the_default_one_is_busy(device, name):
+    # The call's new counters have to be zero, whatever stands in the default stream.
+    # Memory that held ones is freed first, so that new counters are not zero by chance.
+    call, y = GROWING[name][0]()
+    call()
+    torch.cuda.synchronize()
+    want = y.clone()
+    dirty = torch.full((1 << 24,), -1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    sg.release_workspace()
+    del dirty
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    sg.probe_hold(20_000_000)  # on the default stream
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and sg.device_status(side) == 0
