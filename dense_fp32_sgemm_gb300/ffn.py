@@ -10,9 +10,11 @@ for ``stream`` and tell the allocator by ``record_stream``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 import dense_fp32_sgemm_gb300 as _sg
 
@@ -113,13 +115,49 @@ def ffn_forward(x, w_gate, w_up, w_down, y=None, activation: int = 0, saved=None
     w_down: F x D; rows may lie apart, columns not.  ``activation`` is
     GATE_SILU, GATE_GELU or GATE_RELU.  ``saved``: a buffer from ffn_saved()
     for ffn_backward().  Returns y (allocated when not given).
+
+    Where one of the matrices requires a gradient, y is part of the graph: its
+    gradient goes through ffn_backward(), with ``saved`` if given (one for each
+    forward pass that waits for its gradient), else from the inputs anew.  A given
+    y is refused then.
     """
+    if torch.is_grad_enabled() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad
+                                    or w_down.requires_grad):
+        if y is not None:
+            raise ValueError("a given y has no gradient, and x or a weight requires one: "
+                             "leave y out, or call under torch.no_grad()")
+        # (the gradient runs on the stream that is current here)
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            return _Block.apply(x, w_gate, w_up, w_down, int(activation), saved)
     T, D, F, kind, args = _block(x, w_gate, w_up, w_down)
     if y is None:
         y = _empty(T, D, x.dtype, x.device, stream)
     _call(_sg.library().sgemm_ffn_forward, x.device, stream, T, D, F, kind, int(activation), *args,
           *_matrix(y, "y", T, D, x.dtype, x.device), _saved_address(saved, T, F, kind, x.device))
+    if saved is not None:
+        torch.autograd.graph.increment_version(saved)  # graphs that hold it will know
     return y
+
+
+class _Block(torch.autograd.Function):
+    """ffn_forward as a node of the graph."""
+
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up, w_down, activation, saved):
+        y = ffn_forward(x, w_gate, w_up, w_down, activation=activation, saved=saved)
+        ctx.save_for_backward(x, w_gate, w_up, w_down, saved)
+        ctx.activation = activation
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, w_gate, w_up, w_down, saved = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        # (a sum's gradient comes with rows or columns that share memory)
+        grads = ffn_backward(dy.contiguous(), x, w_gate, w_up, w_down, activation=ctx.activation,
+                             saved=saved, need_dx=need[0], need_dw=any(need[1:4]))
+        return (*grads, None, None)
 
 
 def ffn_backward(dy, x, w_gate, w_up, w_down, dx=None, dw_gate=None, dw_up=None, dw_down=None,
@@ -184,7 +222,15 @@ class W4Matrix:
 
     def matvec(self, x, y=None, stream=None):
         """y = x @ W for M x K rows x (M is meant to be small: the weights are
-        read once per 16 rows, 8 with float32).  Returns y (allocated when not given)."""
+        read once per 16 rows, 8 with float32).  Returns y (allocated when not given).
+        No gradient goes through it: where x requires one, a backward pass through y
+        raises NotImplementedError, and a given y is refused."""
+        if x.requires_grad and torch.is_grad_enabled():
+            if y is not None:
+                raise ValueError("a given y has no gradient, and x requires one: "
+                                 "leave y out, or call under torch.no_grad()")
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                return _Matvec.apply(x, self)
         M = x.shape[0]
         if y is None:
             y = _empty(M, self.N, self.dtype, self.device, stream)
@@ -199,6 +245,18 @@ class W4Matrix:
         _call(self._fn, self.device, stream, M, self.N, self.K, self.group, self.type, xa, ldx,
               *self._weights, ya, ldy)
         return y
+
+
+class _Matvec(torch.autograd.Function):
+    """W4Matrix.matvec as a node of the graph that has no gradient, and says so."""
+
+    @staticmethod
+    def forward(ctx, x, matrix):
+        return matrix.matvec(x)
+
+    @staticmethod
+    def backward(ctx, dy):
+        raise NotImplementedError("products with 4-bit weights have no gradient")
 
 
 def w4_quantize(w, group: int = 128, zeros: bool = True, stream=None) -> W4Matrix:
