@@ -114,7 +114,9 @@ def ffn_forward(x, w_gate, w_up, w_down, y=None, activation: int = 0, saved=None
     x: T x D, w_gate and w_up: D x F (they may be halves of one matrix),
     w_down: F x D; rows may lie apart, columns not.  ``activation`` is
     GATE_SILU, GATE_GELU or GATE_RELU.  ``saved``: a buffer from ffn_saved()
-    for ffn_backward().  Returns y (allocated when not given).
+    for ffn_backward().  Returns y (allocated when not given).  With 16-bit types h is
+    rounded to the type between the products, but for a few rows without ``saved``: an
+    FP16 h above 65504 becomes infinite.
 
     Where one of the matrices requires a gradient, y is part of the graph: its
     gradient goes through ffn_backward(), with ``saved`` if given (one for each
@@ -168,7 +170,8 @@ def ffn_backward(dy, x, w_gate, w_up, w_down, dx=None, dw_gate=None, dw_up=None,
     ``saved``: the buffer the forward pass filled, or None to compute its
     contents again.  Outputs not given are allocated; ``need_dx`` and
     ``need_dw`` leave out the input's or the weights' gradients (None is
-    returned in their place).
+    returned in their place).  With FP16 the gradients inside the block are FP16 too:
+    scale a small dy up by a power of two, and the results (or AdamW's grad_scale) down.
     """
     T, D, F, kind, args = _block(x, w_gate, w_up, w_down)
     dev, dtype = x.device, x.dtype

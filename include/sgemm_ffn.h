@@ -50,9 +50,12 @@ enum {
  * x: T x D (ldx >= D); Wg, Wu: D x F (ldg, ldu >= F; they may be the halves of
  * one D x 2F matrix); Wd: F x D (ldd >= D); y: T x D (ldy >= D), not
  * overlapping any input.  All matrices are of `type` (SGEMM_TYPE_*); sums are
- * held in 32 bits.  With 16-bit types h is rounded to the type between the two
- * products (except in the form for few rows, T <= 8), with FP32 nothing is rounded below
- * 24 bits.
+ * held in 32 bits.  With FP32 nothing is rounded below 24 bits.  With 16-bit
+ * types h is rounded to the type between the two products, as the second one's
+ * operand: an FP16 h above 65504 becomes infinite there, and its row of y with it.
+ * Only the form for few rows keeps h in 32 bits; calls without `saved` take it
+ * up to T = 24 with FP32, and with 16-bit types up to T = 4 where D F > 6 * 2^20
+ * and the three weights lie in 16-byte aligned rows, else up to T = 8.
  * saved: NULL, or a device buffer (16-byte aligned) of sgemm_ffn_saved_floats(T, F,
  * type) floats for sgemm_ffn_backward: it receives u act'(g) and act(g) in 32
  * bits and h, in a layout of the library's own.
@@ -81,8 +84,11 @@ SGEMM_API int64_t sgemm_ffn_saved_floats(int64_t T, int64_t F, int type);
  * are computed again.  dx: T x D, dWg and dWu: D x F, dWd: F x D, written whole.
  * dx may be NULL (no gradient of the input), and so may dWg, dWu and dWd, all
  * three together (frozen weights).  With 16-bit types h, dg and du are
- * rounded to the type before they enter the products.  T == 0: the weight
- * gradients are zero.  Errors as for the forward call.
+ * rounded to the type before they enter the products.  In FP16 they are infinite
+ * above 65504, lose bits below 2^-14 and are zero below 2^-25, whatever the sizes
+ * of the gradients that they add up to: with small dy, scale dy up by a power of
+ * two and the gradients down again (loss scaling; the AdamW step's grad_scale).
+ * T == 0: the weight gradients are zero.  Errors as for the forward call.
  */
 SGEMM_API sgemm_status_t sgemm_ffn_backward(int64_t T, int64_t D, int64_t F, int type,
                                             int activation, const void *x, int64_t ldx,

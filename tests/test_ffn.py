@@ -292,6 +292,40 @@ def test_infinities_and_nan_stay_in_their_rows(device):
 
 
 @gpu
+def test_the_range_of_fp16_between_the_products(device):
+    # h of some 10^5 in row 1 (times weights of 10^-3): a number in the form for few
+    # rows, infinite where it is held in FP16; no other row minds.
+    for T, saved in ((8, None), (9, None), (3, "kept")):
+        m = make(T, 64, 96, "fp16")
+        m["wd"] *= 2.0 ** -10
+        m["x"][1] *= 500
+        w = (m["wg"], m["wu"], m["wd"])
+        want = formula(m["x"], *w, "relu")["y"]
+        assert float((formula(m["x"], m["wg"], m["wu"], torch.eye(96, device="cuda"), "relu")["y"][1]).max()) > 7e4
+        slack = bounds(m["x"], *w, "relu", TYPES["fp16"][1], TINY["fp16"])["y"]
+        keep = sg.ffn_saved(T, 96, dtype=torch.float16) if saved else None
+        y = sg.ffn_forward(m["x"], *w, activation=ACTS["relu"], saved=keep)
+        rows = [t for t in range(T) if t != 1 or (T <= 8 and not saved)]
+        assert_close(y[rows], want[rows], slack[rows], TYPES["fp16"][1], TINY["fp16"], f"{T} rows")
+        if 1 not in rows:
+            assert not torch.isfinite(y[1]).any()
+
+
+@gpu
+def test_small_fp16_gradients_by_scaling(device):
+    # dy of 10^-6, whose products are FP16 subnormals: scaled by 2^14 and back, all
+    # gradients have h, dg, du and their own rounding: 3 roundings of 2^-11 at most.
+    m = make(300, 96, 160, "fp16")
+    w = (m["wg"], m["wu"], m["wd"])
+    dy = (m["dy"].double() * 1e-6 * 2.0 ** 14).half()
+    want = formula(m["x"], *w, "silu", dy.double() * 2.0 ** -14)
+    got = sg.ffn_backward(dy, m["x"], *w)
+    for k, v in zip(("dx", "dwg", "dwu", "dwd"), got):
+        v = v.double() * 2.0 ** -14
+        assert float((v - want[k]).norm()) <= 3 * 2.0 ** -11 * float(want[k].norm()), k
+
+
+@gpu
 def test_offsets_beyond_32_bits(device):
     # h and the kept values have 2^32 elements.
     T, D, F = 131072, 16, 32768
