@@ -60,7 +60,8 @@ __device__ __forceinline__ float bf16_rest(float x, float part) {
 }
 // x as the sum of three bf16 values (its 24 significant bits in parts of 8),
 // each the rounded rest of those before it; an infinity or NaN is its first part
-// alone.
+// alone.  (In a product with another value's parts an infinity meets zero parts, so
+// the sum it enters is NaN.)
 __device__ __forceinline__ void split3(float x, float (&part)[3]) {
     part[0] = bf16_part(x);
     const float r = bf16_rest(x, part[0]);

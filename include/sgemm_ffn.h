@@ -56,6 +56,10 @@ enum {
  * Only the form for few rows keeps h in 32 bits; calls without `saved` take it
  * up to T = 24 with FP32, and with 16-bit types up to T = 4 where D F > 6 * 2^20
  * and the three weights lie in 16-byte aligned rows, else up to T = 8.
+ * Infinities and NaN in x reach their own rows of y alone.  With FP32 on the tensor
+ * cores (above T = 24, with `saved`, and in the backward pass) an infinite element
+ * is NaN in every sum that it enters: values are taken in parts there, and
+ * infinity times the zero part of another value is NaN.
  * saved: NULL, or a device buffer (16-byte aligned) of sgemm_ffn_saved_floats(T, F,
  * type) floats for sgemm_ffn_backward: it receives u act'(g) and act(g) in 32
  * bits and h, in a layout of the library's own.

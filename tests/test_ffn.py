@@ -292,6 +292,37 @@ def test_infinities_and_nan_stay_in_their_rows(device):
 
 
 @gpu
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("T,saved", [(4, None), (4, "kept"), (40, None), (140, "kept")])
+def test_infinities_and_nan_in_every_form(device, T, saved, kind):
+    # Where the formula has no finite value there is none (an infinity may come out as
+    # NaN), and everything else keeps its bits: x in rows, weights and dy by what they
+    # enter.
+    act = "silu"
+    m = make(T, 64, 72, kind)
+    keep = sg.ffn_saved(T, 72, dtype=m["x"].dtype) if saved else None
+
+    def run(m):
+        w = (m["wg"], m["wu"], m["wd"])
+        y = sg.ffn_forward(m["x"], *w, activation=ACTS[act], saved=keep)
+        return dict(zip(("y", "dx", "dwg", "dwu", "dwd"),
+                        (y, *sg.ffn_backward(m["dy"], m["x"], *w, activation=ACTS[act], saved=keep))))
+
+    clean = run(m)
+    for name, at in (("x", (1, 5)), ("wd", (7, 3)), ("dy", (2, 9))):
+        for value in (float("nan"), float("inf"), -float("inf")):
+            bad = {k: v.clone() for k, v in m.items()}
+            bad[name][at] = value
+            want = formula(bad["x"], bad["wg"], bad["wu"], bad["wd"], act, bad["dy"])
+            for k, v in run(bad).items():
+                fine = torch.isfinite(want[k])
+                assert torch.equal(torch.isfinite(v), fine), (name, value, k)
+                untouched = fine & (want[k] == formula(m["x"], m["wg"], m["wu"], m["wd"], act, m["dy"])[k])
+                assert torch.equal(v[untouched], clean[k][untouched]), (name, value, k)
+    assert sg.device_status(torch.cuda.current_stream()) == 0
+
+
+@gpu
 def test_the_range_of_fp16_between_the_products(device):
     # h of some 10^5 in row 1 (times weights of 10^-3): a number in the form for few
     # rows, infinite where it is held in FP16; no other row minds.
