@@ -43,8 +43,11 @@ __device__ __forceinline__ void gate_act_slope(float g, int act, float &a, float
     } else if (act == kGateGelu) {
         const float s = gate_sigmoid<ACCURATE>(2.0f * kGeluC * fmaf(kGeluK * g * g, g, g));
         a = g * s;
-        // d/dg [g s(w)] = s + g s (1 - s) w',  w' = 2 c (1 + 3 k g^2)
-        slope = fmaf(a * (1.0f - s), 2.0f * kGeluC * fmaf(3.0f * kGeluK * g, g, 1.0f), s);
+        // d/dg [g s(w)] = s + g s (1 - s) w',  w' = 2 c (1 + 3 k g^2).  From |g| = 16 on
+        // s (1 - s) is zero in FP32; there w' is held at a finite value, which g^2 is
+        // not above 10^19 (and zero times infinity is NaN, where the slope is 0 or 1).
+        const float t = fminf(fabsf(g), 64.0f);
+        slope = fmaf(a * (1.0f - s), 2.0f * kGeluC * fmaf(3.0f * kGeluK * t, t, 1.0f), s);
     } else {
         a = g > 0.0f ? g : (g != g ? g : 0.0f);
         slope = g > 0.0f ? 1.0f : 0.0f;

@@ -292,6 +292,21 @@ def test_infinities_and_nan_stay_in_their_rows(device):
 
 
 @gpu
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("act", ACTS)
+def test_slopes_of_huge_gates(device, act, kind):
+    # Gates of 10^20, whose square is beyond FP32: slope 0 or 1, and finite gradients.
+    T, dtype = 30, TYPES[kind][0]
+    m = make(T, 1, 6, kind)
+    m["x"].fill_(1)
+    m["dy"].fill_(1)
+    m["wg"][0] = torch.tensor([1e20, -1e20, 1e10, -1e10, 70.0, -70.0], device="cuda", dtype=dtype)
+    m["wu"].fill_(1)
+    m["wd"][:, 0] = torch.tensor([1e-20, 1e-20, 1e-10, 1e-10, 1.0, 1.0], device="cuda", dtype=dtype)
+    check(m, kind, act, "kept")
+
+
+@gpu
 @pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("T,saved", [(4, None), (4, "kept"), (40, None), (140, "kept")])
 def test_infinities_and_nan_in_every_form(device, T, saved, kind):
