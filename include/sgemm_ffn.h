@@ -113,9 +113,13 @@ SGEMM_API sgemm_status_t sgemm_ffn_backward(int64_t T, int64_t D, int64_t F, int
  * are q[8 r + i][n]; what the last row of words holds beyond K is ignored.
  * zeros: NULL (every z is 8), or ceil(K / group) x N bytes of which the low
  * four bits are read (ldz >= N).  group: a multiple of 32.
- * q - z enters the products exactly, x with all its bits, sums are held in 32
- * bits, and each group's sum is scaled in 32 bits.  Weights are read once per
- * 16 rows of x (8 with FP32).
+ * x enters with all its bits; sums are held in 32 bits, and each group's sum is
+ * scaled in 32 bits.  With FP32 x the products are those of x and q - z.  With
+ * 16-bit x they are those of x and q (FP16) or 128 + q (BF16), and the offset's
+ * part comes off at the end of a group: at most two (FP16) or five (BF16) of the
+ * 24 bits of a group's sum go with it, an infinity in x gives NaN where its
+ * q - z would give an infinity, and in BF16 143 times the group's sum of |x| has
+ * to stay within FP32.  Weights are read once per 16 rows of x (8 with FP32).
  * M == 0 or N == 0: nothing is done.  K == 0: y = 0.
  * Returns SGEMM_ERR_INVALID_ARG for a negative size, a group that is not a
  * positive multiple of 32, a leading dimension below its row length, a NULL or

@@ -148,6 +148,29 @@ def test_rows_are_independent(device):
 
 
 @gpu
+@pytest.mark.parametrize("kind", TYPES)
+def test_the_range_of_x(device, kind):
+    # The largest x that the stated ranges allow, against the same bound; an infinity
+    # is an infinity or NaN with FP32 as q - z has it, else not finite.
+    K, N, G = 256, 80, 64
+    x, q, s, z = make(2, K, N, G, kind, True)
+    s.fill_(2.0 ** -20)
+    x = (x / x.abs().max() * {"fp32": 2.0 ** 113, "fp16": 65504.0, "bf16": 2.0 ** 113}[kind]).to(x.dtype)
+    check(x, q, s, z, G, kind)
+    w = sg.W4Matrix(q, s, K, G, zeros=z)
+    x = torch.zeros_like(x)
+    x[0, 70], x[1, 3] = float("inf"), 1.0
+    y = w.matvec(x)
+    step = nibbles(q, K)[70].long() - z[70 // G].long()
+    if kind == "fp32":
+        assert torch.equal(torch.isnan(y[0]), step == 0)
+        assert torch.equal(y[0][step != 0], step[step != 0] * float("inf"))
+    else:
+        assert not torch.isfinite(y[0]).any()
+    assert torch.isfinite(y[1]).all()
+
+
+@gpu
 def test_same_bits_every_time_and_on_any_stream(device):
     x, q, s, z = make(1, 8192, 96, 64, "bf16", True)
     w = sg.W4Matrix(q, s, 8192, 64, zeros=z)
