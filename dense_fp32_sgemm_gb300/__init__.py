@@ -179,8 +179,16 @@ def _matrix_args(t, name):
     rows, cols = t.shape
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have unit column stride (row-major)")
-    ld = t.stride(0) if rows > 1 else max(1, cols)
-    return t.data_ptr(), max(ld, cols, 1)
+    return t.data_ptr(), _leading(name, rows, cols, t.stride(0))
+
+
+def _leading(name, rows, cols, step):
+    """The leading dimension of a matrix whose rows lie `step` elements apart.  Rows that
+    share memory (an expanded tensor's) or run backwards have none."""
+    if rows > 1 and step < cols:
+        raise ValueError(f"{name} has overlapping rows ({step} elements apart, {cols} long): "
+                         "pass a contiguous copy")
+    return max(step if rows > 1 else cols, cols, 1)
 
 
 def run(A, B, C, alpha: float = 1.0, beta: float = 0.0, stream=None, bias=None,
@@ -282,8 +290,9 @@ def run_host(A, B, C, alpha: float = 1.0, beta: float = 0.0, stream=None):
             raise TypeError(f"{name} must be a 2-D float32 array")
         if arr.shape[1] > 1 and arr.strides[1] != 4:
             raise ValueError(f"{name} must have unit column stride")
-        ld = arr.strides[0] // 4 if arr.shape[0] > 1 else max(1, arr.shape[1])
-        return arr.ctypes.data, max(ld, arr.shape[1], 1), arr.shape
+        if arr.shape[0] > 1 and arr.strides[0] % 4:
+            raise ValueError(f"{name} must have rows a whole number of elements apart")
+        return arr.ctypes.data, _leading(name, *arr.shape, arr.strides[0] // 4), arr.shape
 
     a, lda, (M, K) = host_args(A, "A")
     b, ldb, (K2, N) = host_args(B, "B")

@@ -33,12 +33,7 @@ def _matrix(t, name, rows, cols, dtype, device):
     step, unit = t.stride()
     if cols > 1 and unit != 1:
         raise ValueError(f"{name} must have unit column stride (row-major)")
-    # Rows that share memory (an expanded tensor's) have no leading dimension:
-    # read as rows of their full length, they would end outside the tensor.
-    if rows > 1 and step < cols:
-        raise ValueError(f"{name} has overlapping rows ({step} elements apart, {cols} long): "
-                         "pass a contiguous copy")
-    return t.data_ptr(), max(step if rows > 1 else cols, cols, 1)
+    return t.data_ptr(), _sg._leading(name, rows, cols, step)
 
 
 def _empty(rows, cols, dtype, device, stream):
