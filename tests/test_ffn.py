@@ -392,6 +392,24 @@ def test_offsets_beyond_32_bits(device):
 
 
 @gpu
+@pytest.mark.parametrize("kind,offset", [("bf16", 0), ("bf16", 1), ("fp32", 0), ("fp32", 1)])
+def test_rows_beyond_32_bits(device, kind, offset):
+    # All matrices are columns of one buffer whose 300 rows lie 2^24 elements apart:
+    # their last rows start behind 2^32 elements. Few rows, and the tensor cores.
+    D, F, ld, dtype = 296, 288, 2 ** 24, TYPES[kind][0]
+    wide = torch.zeros(300 * ld, device="cuda", dtype=dtype)[: 300 * ld].view(300, ld)
+    for T in (3, 40):
+        small = make(T, D, F, kind)
+        m, at = {}, offset
+        for k, v in small.items():
+            m[k] = wide[300 - v.shape[0]:, at:at + v.shape[1]]
+            m[k].copy_(v)
+            at += 512
+        assert m["wg"].storage_offset() + (D - 1) * ld > 2 ** 32
+        check(m, kind, "silu", None if T == 3 else "kept", need=T > 3)
+
+
+@gpu
 def test_graph_capture(device):
     m = make(150, 64, 500, "bf16")
     side = torch.cuda.Stream()

@@ -4,6 +4,7 @@ writes them, an optimizer's states are zero before the first step on any, and th
 workspace that a captured graph holds outlives larger calls.
 """
 import contextlib
+import threading
 
 import pytest
 
@@ -266,3 +267,86 @@ def test_the_first_call_on_a_stream_while_the_default_one_is_busy(device, name):
         call()
     torch.cuda.synchronize()
     assert torch.equal(y, want) and sg.device_status(side) == 0
+
+
+def work(seed):
+    """Calls of every kind on tensors of their own, and what they leave (each call writes
+    the same again, but for the parameters)."""
+    gen = torch.Generator("cuda").manual_seed(seed)
+    T, D, F = 130 + seed, 72, 3000
+    x, wg, wu, wd, dy = ((torch.randn(a, b, generator=gen, device="cuda") * b ** -0.5).bfloat16()
+                         for a, b in ((T, D), (D, F), (D, F), (F, D), (T, D)))
+    y, few = torch.empty_like(x), torch.empty_like(x[:3])
+    grads = [torch.empty_like(t) for t in (x, wg, wu, wd)]
+    packed = sg.w4_quantize(wd, 64)
+    tokens = torch.randn(2, F, generator=gen, device="cuda").bfloat16()
+    out = torch.empty(2, D, device="cuda", dtype=torch.bfloat16)
+    master = wg.float()
+    opt = sg.AdamW([master], grads[1:2], state_bits=8)
+
+    def run():
+        sg.ffn_forward(x, wg, wu, wd, y=y)
+        sg.ffn_forward(x[:3], wg, wu, wd, y=few)
+        sg.ffn_backward(dy, x, wg, wu, wd, *grads)
+        packed.matvec(tokens, out)
+        opt.step()
+
+    return run, [y, few, *grads, out, master, opt.m[0].view(torch.uint8)]
+
+
+ROUNDS = 12
+
+
+def alone(seed):
+    run, left = work(seed)
+    for _ in range(ROUNDS):
+        run()
+    torch.cuda.synchronize()
+    return [t.clone() for t in left]
+
+
+@gpu
+def test_two_streams_at_once(device):
+    want = [alone(seed) for seed in (0, 1)]
+    both = [work(seed) for seed in (0, 1)]
+    streams = [torch.cuda.Stream() for _ in both]
+    torch.cuda.synchronize()
+    for _ in range(ROUNDS):
+        for (run, _), stream in zip(both, streams):
+            with torch.cuda.stream(stream):
+                run()
+    torch.cuda.synchronize()
+    for (_, left), expected in zip(both, want):
+        assert all(torch.equal(a, b) for a, b in zip(left, expected))
+    assert all(sg.device_status(s) == 0 for s in streams)
+
+
+@gpu
+@pytest.mark.parametrize("shared", [False, True])
+def test_two_host_threads(device, shared):
+    # On streams of their own, and on one stream: a call's launches stay together.
+    want = [alone(seed) for seed in (0, 1)]
+    both = [work(seed) for seed in (0, 1)]
+    one = torch.cuda.Stream()
+    streams = [one, one] if shared else [torch.cuda.Stream() for _ in both]
+    torch.cuda.synchronize()
+    failed = []
+
+    def thread(run, stream):
+        try:
+            with torch.cuda.stream(stream):
+                for _ in range(ROUNDS):
+                    run()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=thread, args=(run, s)) for (run, _), s in zip(both, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for (_, left), expected in zip(both, want):
+        assert all(torch.equal(a, b) for a, b in zip(left, expected))
+    assert all(sg.device_status(s) == 0 for s in streams)
