@@ -658,12 +658,17 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const W4QuantParams p)
     const long long k0 = (long long)gi * p.group;
     const int count = (int)min((long long)p.group, p.K - k0);
     float lo = 0.0f, hi = 0.0f;
+    // Four bits have no infinity or NaN (which a minimum passes over): the scale says it.
+    bool finite = true;
     for (int k = 0; k < count; ++k) {
         const float w = load_as_float(p.W, p.type, (k0 + k) * p.ldw + n);
         lo = fminf(lo, w);
         hi = fmaxf(hi, w);
+        finite = finite && fabsf(w) < INFINITY;
     }
-    const float span = p.zeros ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.0f;
+    const float span = !finite  ? __int_as_float(0x7FC00000)
+                       : p.zeros ? (hi - lo) / 15.0f
+                                 : fmaxf(hi, -lo) / 7.0f;
     store_from_float(p.scales, p.type, (long long)gi * p.lds + n, span);
     const float scale = load_as_float(p.scales, p.type, (long long)gi * p.lds + n);
     const float zero = !p.zeros ? 8.0f

@@ -141,6 +141,7 @@ SGEMM_API sgemm_status_t sgemm_w4_matvec(int64_t M, int64_t N, int64_t K, int64_
  * zeros == NULL: scale = max |w| / 7, q = clamp(round(w / scale) + 8, 0, 15).
  * The scale is rounded to `type` before it divides.  A group of zeros has
  * scale 0 and q = z (8 without zeros).  round() is to nearest, ties to even.
+ * An infinity or NaN in a group makes its scale NaN, and so its weights.
  * Arguments and errors as for sgemm_w4_matvec.
  */
 SGEMM_API sgemm_status_t sgemm_w4_quantize(int64_t N, int64_t K, int64_t group, int type,
@@ -179,7 +180,7 @@ typedef struct {
  * scales are the block's largest |m| and sqrt(v), at least 2^-96; codes are
  * rounded to nearest even, and a sqrt(v) above zero takes at least the
  * smallest code above zero.  The update uses the values before rounding.
- * All-zero codes with any scale are the initial state.  A block that meets an
+ * All-zero codes with any finite scale are the initial state.  A block that meets an
  * infinity or NaN keeps NaN in its state.
  * Returns SGEMM_ERR_INVALID_ARG for a negative count or numel, a NULL or
  * misaligned pointer, an unknown type, state_bits other than 8 or 32,

@@ -244,6 +244,24 @@ def test_quantize(device, K, N, G, zeros, kind):
     assert bool(((back - w.float()).abs() <= 1.01 * scale.repeat_interleave(G, 0)[:K] + 1e-30).all())
 
 
+@gpu
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("zeros", [False, True])
+def test_quantize_does_not_hide_infinities_and_nan(device, zeros, kind):
+    gen = torch.Generator("cuda").manual_seed(10)
+    w = torch.randn(96, 40, generator=gen, device="cuda").to(TYPES[kind][0])
+    clean = sg.w4_quantize(w, 32, zeros=zeros)
+    w[40, 3], w[41, 5], w[70, 3], w[71, 9] = float("nan"), float("inf"), -float("inf"), float("nan")
+    got = sg.w4_quantize(w, 32, zeros=zeros)
+    spoilt = torch.zeros(3, 40, dtype=torch.bool, device="cuda")
+    for g, n in ((1, 3), (1, 5), (2, 3), (2, 9)):
+        spoilt[g, n] = True
+    assert torch.equal(~torch.isfinite(got.scales), spoilt)
+    assert torch.equal(got.scales[~spoilt], clean.scales[~spoilt])
+    y = got.matvec(torch.ones(2, 96, device="cuda", dtype=w.dtype))
+    assert torch.equal(torch.isnan(y).any(0), spoilt.any(0))
+
+
 # ---- refusals (no device needed) ------------------------------------------------
 
 def call(**over):
