@@ -426,13 +426,20 @@ sgemm_status_t sgemm_ffn_forward(int64_t T, int64_t D, int64_t F, int type, int 
     s = op_device(&dev);
     if (s != SGEMM_OK) return s;
     if (F == 0) return zero_matrix(y, ldy, T, D, type, st);
-    // Few rows: passes over the weights on the FP32 pipe, one for every eight.
-    // From five rows of 16-bit weights on that is the slower way (8 x 4096 x 12288:
-    // 94 us, the tensor cores 72; 8 x 2048 x 8192: 53 and 39), unless the products
-    // are small (8 x 1024 x 4096: 22 us, the tensor cores 29) or the weights would
-    // have to be copied to aligned rows (8 x 2047 x 5461: 49 us, 67 and more that
-    // way); with FP32 weights, which the tensor cores need split in three first, from
-    // 25 (2048 x 5464: 24 rows 100 us, 32 rows on the tensor cores 144).
+    // Few rows: passes over the weights on the FP32 pipe, one for every eight, cheaper
+    // than the tensor cores as long as these would wait for more.  Microseconds of
+    // this form and of the tensor cores, weights cold (D x F):
+    //   16 bits in place, 4 rows: 1024 x 2048 15, 20; 1280 x 5120 24.5, 23.6; 2048 x
+    //     8192 30, 33; 4096 x 12288 59, 69.  8 rows: 512 x 2048 14, 18; 1024 x 4096
+    //     20.6, 21.7; 1024 x 6144 26, 24; 1536 x 6144 32, 27; 4096 x 12288 93, 69.
+    //   Off 16 bytes (the tensor cores have the weights copied first), 8 rows: 1023 x
+    //     4095 27, 33; 2047 x 5461 48, 40; 4095 x 12287 150, 191.  9 rows: 43, 33; 74,
+    //     40; 214, 190.
+    //   FP32 (split in three first), 24 rows: 1024 x 4096 60, 69; 2048 x 8192 149, 169;
+    //     4096 x 12288 308, 438.  25 rows: 72, 69; 186, 168; 403, 439.  Off 16 bytes, 16
+    //     rows: 54, 70; 144, 169; 280, 441.  24 rows: 80, 70; 212, 169; 419, 441.
+    // So each limit lies where the two cross for some sizes and within a quarter of the
+    // faster form for the others.
     const bool in_place = type != kTypeF32 && aligned(Wg, 16) && aligned(Wu, 16) &&
                           aligned(Wd, 16) && ldg % 8 == 0 && ldu % 8 == 0 && ldd % 8 == 0;
     const bool small = D * F <= 6 << 20;

@@ -31,10 +31,12 @@
 // columns; the first CTA's thread issues for both.  A launch may start while the
 // one before it on the stream drains (programmatic dependent launch).
 // Bound: the tensor pipe where tiles are many (85 to 95 % busy, then the card's
-// power), shared memory in single CTAs and FP32.  Measured per call: 4096 x 4096 x
-// 12288 bf16 619-643 us (1.9-2.0 PFLOP/s), the training step 8192 x 2048 x 8192 bf16
-// 1345-1394 us (1.8), 2048 x 2048 x 8192 FP32 2130 us (290 TFLOP/s, 1.7 PFLOP/s of
-// plane products), 333 x 2000 x 5336 fp16 47-53 us.
+// power), shared memory in single CTAs and FP32.  Measured in a long run, which sits at
+// the power limit, and for calls apart from one another: 4096 x 4096 x 12288 bf16
+// 729-744 us (1.7 PFLOP/s), apart 619-648; the training step 8192 x 2048 x 8192 bf16
+// 1569-1618 us (1.5), apart 1345-1461; the step 2048 x 2048 x 8192 FP32 2364 us (262
+// TFLOP/s, 1.6 PFLOP/s of plane products), apart 2130-2178; 333 x 2000 x 5336 fp16
+// 47-53 us either way.
 // Every wait is bounded; a role that gives up flags the error word, the others
 // run out in turn, and the CTA lets its copies land before it leaves.
 #include <algorithm>

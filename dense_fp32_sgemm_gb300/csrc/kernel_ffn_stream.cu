@@ -14,8 +14,9 @@
 // anywhere are brought in by the aligned 16-byte pieces that cover them (element by
 // element FP32 1 x 2047 x 5461 took 53 us, so 35; BF16 4 x 2047 x 5461 57 and 37).
 //
-// Measured: 1 x 4096 x 12288 bf16 53-57 us (5.3-5.6 TB/s), 4 x 4096 x 12288 59 us,
-// 8 x 2048 x 5464 FP32 35 us (3.8 TB/s), 5 x 2047 x 5461 45-47 us.
+// Measured: 1 x 4096 x 12288 bf16 53-57 us (5.3-5.6 TB/s), 4 x 4096 x 12288 58 us,
+// 4 x 2047 x 5461 34-37 us (rows off 16 bytes), 8 x 2048 x 5464 FP32 34 us (4.0 TB/s),
+// 5 x 2047 x 5461 45-47 us, 24 x 2048 x 8192 150 us (three passes).
 //
 // Split.  A CTA owns a stretch of columns and a range of K; its lanes' rows go
 // round robin over warps (and over parts of a warp, where the stretch is narrower

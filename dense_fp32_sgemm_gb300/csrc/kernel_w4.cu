@@ -38,7 +38,13 @@
 // clocks for each.
 //
 // Measured: 1 x 4096 x 12288 bf16 9.5 us (2.7 TB/s; 10.3 as a call), 16 x 12288 x
-// 4096 16 us, 1 x 16384 x 24576 49 us (4.2 TB/s), 3 x 8191 x 8191 FP32 31 us.
+// 4096 16 us (18.3 as a call), 3 x 8191 x 8191 FP32 31 us (32.4); as calls also 1 x
+// 16384 x 24576 49-53 us (4.0-4.2 TB/s) and 8 x 4096 x 12288 14.3 us.  More rows take a
+// launch for every 16, each of which reads q again: 300 x 4096 x 4096 195 us, 4096 rows
+// 2635 us (52 TFLOP/s).
+// What bounds the larger ones is the latency of a warp's chain (shared read, expansion,
+// matrix instructions, group scaling): shared memory leaves an SM two or three CTAs of
+// four warps, which keep the issue slots 30-38 % and HBM 14-26 % busy.
 //
 // Split.  A CTA's four warps stand side by side on 64 columns each
 // or behind one another along K (taking every n-th unit), or both: few rows of
@@ -647,8 +653,10 @@ cudaError_t launch_nt(const CUtensorMap &map, const W4Params &p, bool vec, int c
 
 // ---------------------------------------------------------------------------
 // Quantisation: one thread per column of a group, so a warp reads and writes
-// along rows.  Bound by HBM (W is read twice, the second time from L2 where a
-// group's rows fit there); it runs once per matrix.
+// along rows.  W is read twice, the second time from L2 where a group's rows fit
+// there.  4096 x 12288 in groups of 128: 106 us from BF16 (its bytes once: 19), 143 us
+// from FP32 (34); bound by a thread's chain of loads, one group of a column after the
+// other.  It runs once per matrix.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) w4_quantize_kernel(const W4QuantParams p) {
     const int col_blocks = (p.N + 255) / 256;
