@@ -218,7 +218,14 @@ def _gate_plain(s, case):
         a = g / (1 + torch.exp(-2 * z))  # = g/2 (1 + tanh z)
     else:
         a = torch.where(g > 0, g, 0.0)
-    q, top = _codes(a * u)
+    v = a * u
+    q, top = _codes(v)
+    if case["act"] != "relu":
+        # An element whose gate is that of the row's largest may lie exactly between two
+        # codes (127 times the quotient of two u); the gate's rounding must not decide.
+        at = v.abs().argmax(dim=1, keepdim=True)
+        t = (u * 127 / u.gather(1, at).abs()) * (a / a.gather(1, at).abs())
+        q = torch.where(top > TINY, torch.round(t).to(torch.int8), q)
     return {"q": q, "scales": (top / 127).float().view(-1)}
 
 
@@ -298,6 +305,10 @@ def _exact_gate(case, seed):
     else:
         a = g.clamp(min=0)
     q, scales = _exact_codes(a * u)
+    if case["act"] != "relu":  # (ties exactly: a factor that both have is not rounded twice)
+        best = (a * u).abs().max(dim=1, keepdim=True).indices
+        ratio = (127 * u / u.gather(1, best).abs()) * (a / a.gather(1, best).abs())
+        q = torch.where((scales * 127 > TINY)[:, None], ratio.round().to(torch.int8), q)
     return {"q": q, "scales": scales}
 
 
