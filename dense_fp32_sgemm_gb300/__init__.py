@@ -5,7 +5,8 @@ library's CUDA kernels.  The functions mirror the C ABI in include/sgemm.h
 and include/sgemm_probe.h; ``run`` and ``run_host`` add the conversion from
 torch tensors / numpy arrays to pointers and leading dimensions.  The
 feed-forward operators (include/sgemm_ffn.h: the gated block and its gradients,
-products with 4-bit weights, the AdamW step) take torch tensors: ffn.py.
+products with 4-bit weights, the AdamW step) take torch tensors: ffn.py; so do
+those around them (include/sgemm_q8.h: the norm, serving in 8 bits): q8.py.
 
 There is no fallback: if the library has not been built, or no sm_103 GPU is
 present, calls raise.
@@ -28,6 +29,7 @@ __all__ = [
     "VARIANT_SKINNY", "VARIANT_MID", "VARIANT_MID64", "VARIANT_KSPLIT", "VARIANT_NARROW", "VARIANT_KSPLIT64", "VARIANT_SMALL",
     "STATUS",
     "ffn_forward", "ffn_saved", "ffn_backward", "W4Matrix", "w4_quantize", "AdamW",
+    "rms_norm", "rms_norm_backward", "rms_norm_q8", "gate_q8", "rows_q8", "Q8Matrix", "q8_quantize",
     "GATE_SILU", "GATE_GELU", "GATE_RELU", "TYPE_F32", "TYPE_F16", "TYPE_BF16",
 ]
 
@@ -86,6 +88,16 @@ _SIGNATURES = {
                                  _i64, _vp]),
     "sgemm_adamw_step": (_int, [_vp, _i64, _int, _int, _int, _int, _f64, _f64, _f64, _f64, _f64,
                                 _i64, _f64, _vp]),
+    "sgemm_rms_norm": (_int, [_i64, _i64, _int, _vp, _i64, _vp, _i64, _vp, _int, _f64, _vp, _i64,
+                              _vp, _i64, _vp]),
+    "sgemm_rms_norm_q8": (_int, [_i64, _i64, _int, _vp, _i64, _vp, _i64, _vp, _int, _f64, _vp, _i64,
+                                 _vp, _i64, _vp, _vp]),
+    "sgemm_rms_norm_backward": (_int, [_i64, _i64, _int, _vp, _i64, _vp, _i64, _vp, _int, _f64, _vp,
+                                       _i64, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "sgemm_q8_gate": (_int, [_i64, _i64, _int, _int, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "sgemm_q8_quantize": (_int, [_i64, _i64, _int, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "sgemm_q8_matmul": (_int, [_i64, _i64, _i64, _int, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64,
+                               _vp]),
 }
 EXPORTED_SYMBOLS = tuple(_SIGNATURES)
 
@@ -392,14 +404,17 @@ def probe_hold(ns: int, stream=None) -> None:
     _check(library().sgemm_probe_hold(int(ns), s), "sgemm_probe_hold")
 
 
-# The feed-forward operators work on torch tensors: their module is imported
-# with the first of its names that is used, so that the rest needs no torch.
+# The feed-forward operators work on torch tensors: their modules are imported
+# with the first of their names that is used, so that the rest needs no torch.
 _FFN_NAMES = ("ffn_forward", "ffn_saved", "ffn_backward", "W4Matrix", "w4_quantize", "AdamW")
+_Q8_NAMES = ("rms_norm", "rms_norm_backward", "rms_norm_q8", "gate_q8", "rows_q8", "Q8Matrix",
+             "q8_quantize")
 
 
 def __getattr__(name):
-    if name in _FFN_NAMES:
-        from . import ffn
-        value = globals()[name] = getattr(ffn, name)
+    if name in _FFN_NAMES or name in _Q8_NAMES:
+        import importlib
+        module = importlib.import_module(".ffn" if name in _FFN_NAMES else ".q8", __name__)
+        value = globals()[name] = getattr(module, name)
         return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -624,6 +624,21 @@ sgemm_status_t op_encode_words(CUtensorMap *map, const uint32_t *base, int64_t r
                      CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+sgemm_status_t op_encode_bytes(CUtensorMap *map, const void *base, int64_t rows, int64_t cols,
+                               int64_t ld, int box_rows) {
+    if (!g_encode) return SGEMM_ERR_TMA;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    // (one row: its stride is not used, but has to be valid)
+    const cuuint64_t strides[1] = {rows > 1 ? (cuuint64_t)ld : ((cuuint64_t)cols + 15) / 16 * 16};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r =
+        g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
+                 estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SGEMM_OK : SGEMM_ERR_TMA;
+}
+
 }  // namespace sgemm
 
 using namespace sgemm;

@@ -1,0 +1,324 @@
+// C ABI of the norm and of the operators in 8 bits (declared in
+// include/sgemm_q8.h): argument checks, workspace and launches.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <initializer_list>
+
+#include "../../include/sgemm_ffn.h"
+#include "../../include/sgemm_q8.h"
+#include "kernels_q8.h"
+#include "ops_internal.h"
+
+namespace sgemm {
+namespace {
+
+constexpr int64_t kMaxRows = INT32_MAX, kMaxSize = int64_t(1) << 26, kMaxQ8K = 131071;
+
+bool aligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+bool type_ok(int type) {
+    return type == SGEMM_TYPE_F32 || type == SGEMM_TYPE_F16 || type == SGEMM_TYPE_BF16;
+}
+bool present(const void *p, int type) { return p && aligned(p, type_bytes(type)); }
+int64_t at_least_one(int64_t v) { return v > 1 ? v : 1; }
+sgemm_status_t status(cudaError_t e) { return e == cudaSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH; }
+int64_t up(int64_t v, int64_t unit) { return (v + unit - 1) / unit * unit; }
+
+// A matrix whose rows all start on 16 bytes (or that is not there).
+bool rows16(const void *p, int64_t ld, int64_t rows, int type) {
+    return !p || (aligned(p, 16) && (rows <= 1 || ld * type_bytes(type) % 16 == 0));
+}
+// A matrix of codes whose rows all start where a thread's piece is stored at once.
+bool codes_vec(const int8_t *q, int64_t ld, int64_t rows, int type) {
+    const int64_t piece = type == kTypeF32 ? 4 : 8;
+    return aligned(q, piece) && (rows <= 1 || ld % piece == 0);
+}
+
+struct NormArgs {
+    int64_t T, D;
+    int type;
+    const void *x;
+    int64_t ldx;
+    const void *residual;
+    int64_t ldr;
+    const void *weight;
+    int weight_type;
+    double eps;
+    void *h;
+    int64_t ldh;
+};
+
+sgemm_status_t check_norm(const NormArgs &a) {
+    if (a.T < 0 || a.D < 0 || !type_ok(a.type) || !(a.eps >= 0.0) ||
+        (a.weight_type != a.type && a.weight_type != SGEMM_TYPE_F32))
+        return SGEMM_ERR_INVALID_ARG;
+    const int64_t least = at_least_one(a.D);
+    if (a.ldx < least || (a.residual && a.ldr < least) || (a.h && a.ldh < least))
+        return SGEMM_ERR_INVALID_ARG;
+    if (a.T > kMaxRows || a.D > kMaxSize) return SGEMM_ERR_UNSUPPORTED;
+    if (a.D > 0 && (!present(a.weight, a.weight_type) ||
+                    (a.T > 0 && (!present(a.x, a.type) || !aligned(a.residual, type_bytes(a.type)) ||
+                                 !aligned(a.h, type_bytes(a.type))))))
+        return SGEMM_ERR_INVALID_ARG;
+    return SGEMM_OK;
+}
+
+RowParams row_params(const NormArgs &a) {
+    RowParams p = {};
+    p.rows = a.T;
+    p.cols = (int)a.D;
+    p.a = a.x; p.lda = a.ldx;
+    p.b = a.residual; p.ldb = a.ldr;
+    p.w = a.weight;
+    p.w_f32 = a.weight_type == SGEMM_TYPE_F32;
+    p.eps = (float)a.eps;
+    p.h = a.h; p.ldh = a.ldh;
+    return p;
+}
+bool norm_vec(const NormArgs &a) {
+    return rows16(a.x, a.ldx, a.T, a.type) && rows16(a.residual, a.ldr, a.T, a.type) &&
+           rows16(a.h, a.ldh, a.T, a.type) && aligned(a.weight, 16);
+}
+
+}  // namespace
+}  // namespace sgemm
+
+using namespace sgemm;
+
+extern "C" {
+
+sgemm_status_t sgemm_rms_norm(int64_t T, int64_t D, int type, const void *x, int64_t ldx,
+                              const void *residual, int64_t ldr, const void *weight, int weight_type,
+                              double eps, void *h, int64_t ldh, void *y, int64_t ldy, void *stream) {
+    const NormArgs a{T, D, type, x, ldx, residual, ldr, weight, weight_type, eps, h, ldh};
+    sgemm_status_t s = check_norm(a);
+    if (s != SGEMM_OK) return s;
+    if (ldy < at_least_one(D)) return SGEMM_ERR_INVALID_ARG;
+    if (T == 0 || D == 0) return SGEMM_OK;
+    if (!present(y, type)) return SGEMM_ERR_INVALID_ARG;
+    std::lock_guard<std::mutex> lock(api_mutex());
+    OpDevice dev;
+    s = op_device(&dev);
+    if (s != SGEMM_OK) return s;
+    RowParams p = row_params(a);
+    p.y = y; p.ldy = ldy;
+    return status(launch_rows(p, type, kRowNorm, norm_vec(a) && rows16(y, ldy, T, type), dev.num_sms,
+                              static_cast<cudaStream_t>(stream)));
+}
+
+sgemm_status_t sgemm_rms_norm_q8(int64_t T, int64_t D, int type, const void *x, int64_t ldx,
+                                 const void *residual, int64_t ldr, const void *weight,
+                                 int weight_type, double eps, void *h, int64_t ldh, int8_t *q,
+                                 int64_t ldq, float *scales, void *stream) {
+    const NormArgs a{T, D, type, x, ldx, residual, ldr, weight, weight_type, eps, h, ldh};
+    sgemm_status_t s = check_norm(a);
+    if (s != SGEMM_OK) return s;
+    if (ldq < at_least_one(D)) return SGEMM_ERR_INVALID_ARG;
+    if (T == 0 || D == 0) return SGEMM_OK;
+    if (!q || !scales || !aligned(scales, 4)) return SGEMM_ERR_INVALID_ARG;
+    std::lock_guard<std::mutex> lock(api_mutex());
+    OpDevice dev;
+    s = op_device(&dev);
+    if (s != SGEMM_OK) return s;
+    RowParams p = row_params(a);
+    p.h_last = h && (h == x || h == residual);
+    p.q = q; p.ldq = ldq;
+    p.q_vec = codes_vec(q, ldq, T, type);
+    p.scales = scales;
+    return status(launch_rows(p, type, kRowNormQ8, norm_vec(a) && p.q_vec,
+                              dev.num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+sgemm_status_t sgemm_rms_norm_backward(int64_t T, int64_t D, int type, const void *x, int64_t ldx,
+                                       const void *residual, int64_t ldr, const void *weight, int weight_type, double eps,
+                                       const void *dy, int64_t lddy, const void *dh, int64_t lddh,
+                                       void *dx, int64_t lddx, void *dweight, void *stream) {
+    const NormArgs a{T, D, type, x, ldx, residual, ldr, weight, weight_type, eps, nullptr, 0};
+    sgemm_status_t s = check_norm(a);
+    if (s != SGEMM_OK) return s;
+    const int64_t least = at_least_one(D);
+    const int e = type_bytes(type), we = type_bytes(weight_type);
+    if (lddy < least || (dh && lddh < least) || (dx && lddx < least) || !aligned(dh, e) ||
+        !aligned(dx, e) || !aligned(dweight, we))
+        return SGEMM_ERR_INVALID_ARG;
+    if (D == 0 || (!dx && !dweight)) return SGEMM_OK;
+    if (T > 0 && !present(dy, type)) return SGEMM_ERR_INVALID_ARG;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    std::lock_guard<std::mutex> lock(api_mutex());
+    OpDevice dev;
+    s = op_device(&dev);
+    if (s != SGEMM_OK) return s;
+    if (T == 0)
+        return dweight ? status(cudaMemsetAsync(dweight, 0, (size_t)D * we, st)) : SGEMM_OK;
+    const bool vec = norm_vec(a) && rows16(dy, lddy, T, type) && rows16(dh, lddh, T, type) &&
+                     rows16(dx, lddx, T, type);
+    NormGradParams p = {};
+    p.rows = T;
+    p.cols = (int)D;
+    p.x = x; p.ldx = ldx;
+    p.r = residual; p.ldr = ldr;
+    p.dy = dy; p.lddy = lddy;
+    p.dh = dh; p.lddh = lddh;
+    p.w = weight;
+    p.w_f32 = weight_type == SGEMM_TYPE_F32;
+    p.eps = (float)eps;
+    p.dx = dx; p.lddx = lddx;
+    p.dw = dweight;
+    p.parts = norm_grad_parts(T, (int)D, type, vec, dev.num_sms);
+    void *w = nullptr;
+    const size_t stats = up(T * (int64_t)sizeof(float2), 256);
+    s = op_workspace(st, stats + (size_t)p.parts * D * sizeof(float), &w);
+    if (s != SGEMM_OK) return s;
+    p.stats = static_cast<float2 *>(w);
+    p.partials = reinterpret_cast<float *>(static_cast<char *>(w) + stats);
+    return status(launch_norm_grad(p, type, vec, dev.num_sms, st));
+}
+
+sgemm_status_t sgemm_q8_gate(int64_t T, int64_t F, int type, int activation, const void *g,
+                             int64_t ldg, const void *u, int64_t ldu, int8_t *q, int64_t ldq,
+                             float *scales, void *stream) {
+    if (T < 0 || F < 0 || !type_ok(type)) return SGEMM_ERR_INVALID_ARG;
+    if (u && activation != SGEMM_GATE_SILU && activation != SGEMM_GATE_GELU &&
+        activation != SGEMM_GATE_RELU)
+        return SGEMM_ERR_INVALID_ARG;
+    const int64_t least = at_least_one(F);
+    if (ldg < least || (u && ldu < least) || ldq < least) return SGEMM_ERR_INVALID_ARG;
+    if (T > kMaxRows || F > kMaxSize) return SGEMM_ERR_UNSUPPORTED;
+    if (T == 0) return SGEMM_OK;
+    if (!scales || !aligned(scales, 4)) return SGEMM_ERR_INVALID_ARG;
+    if (F > 0 && (!present(g, type) || !aligned(u, type_bytes(type)) || !q)) return SGEMM_ERR_INVALID_ARG;
+    std::lock_guard<std::mutex> lock(api_mutex());
+    OpDevice dev;
+    const sgemm_status_t s = op_device(&dev);
+    if (s != SGEMM_OK) return s;
+    RowParams p = {};
+    p.rows = T;
+    p.cols = (int)F;
+    p.a = g; p.lda = ldg;
+    p.b = u; p.ldb = ldu;
+    p.act = activation;
+    p.q = q; p.ldq = ldq;
+    p.q_vec = codes_vec(q, ldq, T, type);
+    p.scales = scales;
+    const bool vec = rows16(g, ldg, T, type) && rows16(u, ldu, T, type) && p.q_vec;
+    return status(launch_rows(p, type, kRowGateQ8, vec, dev.num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+sgemm_status_t sgemm_q8_quantize(int64_t N, int64_t K, int type, const void *W, int64_t ldw, int8_t *q,
+                                 int64_t ldq, float *scales, void *stream) {
+    if (N < 0 || K < 0 || !type_ok(type)) return SGEMM_ERR_INVALID_ARG;
+    if (ldw < at_least_one(N) || ldq < at_least_one(K)) return SGEMM_ERR_INVALID_ARG;
+    if (N > kMaxSize || K > kMaxSize) return SGEMM_ERR_UNSUPPORTED;
+    if (N == 0) return SGEMM_OK;
+    if (!scales || !aligned(scales, 4) || (K > 0 && (!present(W, type) || !q))) return SGEMM_ERR_INVALID_ARG;
+    std::lock_guard<std::mutex> lock(api_mutex());
+    OpDevice dev;
+    const sgemm_status_t s = op_device(&dev);
+    if (s != SGEMM_OK) return s;
+    Q8QuantParams p;
+    p.N = (int)N; p.K = (int)K;
+    p.type = type;
+    p.W = W; p.ldw = ldw;
+    p.q = q; p.ldq = ldq;
+    p.scales = scales;
+    return status(launch_q8_quantize(p, static_cast<cudaStream_t>(stream)));
+}
+
+sgemm_status_t sgemm_q8_matmul(int64_t M, int64_t N, int64_t K, int type, const int8_t *x, int64_t ldx,
+                               const float *x_scales, const int8_t *w, int64_t ldw,
+                               const float *w_scales, void *y, int64_t ldy, void *stream) {
+    if (M < 0 || N < 0 || K < 0 || !type_ok(type)) return SGEMM_ERR_INVALID_ARG;
+    if (ldx < at_least_one(K) || ldw < at_least_one(K) || ldy < at_least_one(N)) return SGEMM_ERR_INVALID_ARG;
+    if (M > kMaxSize || N > kMaxSize || K > kMaxQ8K) return SGEMM_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0) return SGEMM_OK;
+    if (!present(y, type)) return SGEMM_ERR_INVALID_ARG;
+    if (K > 0 && (!x || !w || !present(x_scales, kTypeF32) || !present(w_scales, kTypeF32)))
+        return SGEMM_ERR_INVALID_ARG;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    std::lock_guard<std::mutex> lock(api_mutex());
+    OpDevice dev;
+    sgemm_status_t s = op_device(&dev);
+    if (s != SGEMM_OK) return s;
+    if (K == 0) {
+        const size_t e = type_bytes(type);
+        return status(cudaMemset2DAsync(y, ldy * e, 0, N * e, M, st));
+    }
+    const bool stream_form = M <= kQ8StreamRows;
+    const bool in_place = aligned(w, 16) && (N == 1 || ldw % 16 == 0);
+
+    // Workspace: aligned weights, x in FP16, partial tiles.
+    size_t bytes = 0;
+    auto take = [&](size_t n) {
+        const size_t at = bytes;
+        bytes += (n + 255) / 256 * 256;
+        return at;
+    };
+    const int64_t ld_w = in_place ? ldw : up(K, 16), ld_x = up(K, 8);
+    const size_t w_at = in_place ? 0 : take((size_t)(N * ld_w));
+    const size_t x_at = stream_form ? 0 : take((size_t)(M * ld_x) * 2);
+    const size_t part_at = stream_form ? 0 : take((size_t)2 * dev.num_sms * q8_slot_ints() * sizeof(int));
+    char *base = nullptr;
+    if (bytes) {
+        void *p = nullptr;
+        s = op_workspace(st, bytes, &p);
+        if (s != SGEMM_OK) return s;
+        base = static_cast<char *>(p);
+    }
+    if (!in_place) {
+        int8_t *copy = reinterpret_cast<int8_t *>(base + w_at);
+        if (launch_q8_align(w, ldw, (int)N, (int)K, copy, ld_w, dev.num_sms, st) != cudaSuccess)
+            return SGEMM_ERR_LAUNCH;
+        w = copy;
+    }
+    if (stream_form) {
+        Q8StreamParams p = {};
+        p.M = (int)M; p.N = (int)N; p.K = (int)K;
+        p.x = x; p.ldx = ldx;
+        p.x_scales = x_scales;
+        p.w = w; p.ldw = ld_w;
+        p.w_scales = w_scales;
+        p.y = y; p.ldy = ldy;
+        p.x_vec = aligned(x, 16) && (M == 1 || ldx % 16 == 0);
+        return status(launch_q8_stream(p, type, dev.num_sms, st));
+    }
+
+    const bool pair = M > kQ8Tokens;
+    const int64_t most = kQ8Tokens * (pair ? 2 : 1), channels = kQ8Channels * (pair ? 2 : 1);
+    const int64_t tiles_m = (M + most - 1) / most, tiles_n = (N + channels - 1) / channels;
+    if (tiles_m * tiles_n > INT32_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
+    Q8GemmParams p = {};
+    p.M = (int)M; p.N = (int)N; p.K = (int)K;
+    p.tokens = (int)up((M + tiles_m - 1) / tiles_m, 32);
+    p.tiles_m = (int)((M + p.tokens - 1) / p.tokens);
+    p.tiles_n = (int)tiles_n;
+    p.stages_k = (int)((K + kQ8StageK - 1) / kQ8StageK);
+    p.workers = dev.num_sms / (pair ? 2 : 1);
+    const int tiles = p.tiles_m * p.tiles_n;
+    p.full_tiles = tiles / p.workers;
+    p.tail_tiles = tiles % p.workers;
+    if (p.tail_tiles) {
+        const int64_t share = std::max<int64_t>(1, std::min<int64_t>(4, p.stages_k));
+        const int64_t n = std::min<int64_t>(p.workers, (int64_t)p.tail_tiles * p.stages_k / share);
+        p.tail_workers = n > p.tail_tiles ? (int)n : 0;
+    }
+    s = op_counters(st, (size_t)dev.num_sms * 8, &p.counters);
+    if (s != SGEMM_OK) return s;
+    uint16_t *wide = reinterpret_cast<uint16_t *>(base + x_at);
+    p.partials = reinterpret_cast<int *>(base + part_at);
+    p.x_scales = x_scales;
+    p.w_scales = w_scales;
+    p.y = y; p.ldy = ldy;
+    p.device = dev.index;
+    p.err = dev.err;
+    p.timeout_ns = dev.timeout_ns;
+    p.skip_loads_from = dev.skip_loads_from;
+    CUtensorMap map_w, map_x;
+    s = op_encode_bytes(&map_w, w, N, K, ld_w, kQ8Channels);
+    if (s == SGEMM_OK) s = op_encode_16(&map_x, false, wide, M, K, ld_x, 1, M * ld_x, p.tokens / (pair ? 2 : 1));
+    if (s != SGEMM_OK) return s;
+    if (launch_q8_widen(x, ldx, (int)M, (int)K, wide, ld_x, dev.num_sms, st) != cudaSuccess)
+        return SGEMM_ERR_LAUNCH;
+    return status(launch_q8_gemm(map_w, map_x, p, type, pair, st));
+}
+
+}  // extern "C"

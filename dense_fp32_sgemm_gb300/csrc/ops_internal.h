@@ -1,4 +1,4 @@
-// What api.cu lends the translation units of the feed-forward operators: its
+// What api.cu lends the translation units of the operators around it: its
 // lock, the per-device state, a workspace per (device, stream) and the TMA
 // descriptor encoder.  Host-visible only.
 #pragma once
@@ -46,5 +46,10 @@ sgemm_status_t op_encode_16(CUtensorMap *map, bool bf16, const void *base, int64
 // box_rows x box_cols, 128-byte swizzle, zero outside.
 sgemm_status_t op_encode_words(CUtensorMap *map, const uint32_t *base, int64_t rows, int64_t cols,
                                int64_t ld, int box_cols, int box_rows);
+
+// Row-major rows x cols matrix of bytes, rows ld bytes apart (a multiple of 16);
+// boxes of box_rows x 128, 128-byte swizzle, zero outside.
+sgemm_status_t op_encode_bytes(CUtensorMap *map, const void *base, int64_t rows, int64_t cols,
+                               int64_t ld, int box_rows);
 
 }  // namespace sgemm

@@ -1,0 +1,161 @@
+// Pieces of a row: V consecutive elements (16 bytes) of a matrix, in FP32.
+//
+// Rows that do not start on 16 bytes are read through the two aligned pieces that
+// cover a piece, shifted into place, and written through shared memory, a warp's 512
+// bytes at a time: aligned pieces of the destination, and its ends element by
+// element.  (One element per lane and instruction took 145 us for the norm of 8192 x 8191
+// FP16, where the whole traffic takes 40.)
+#pragma once
+
+#include "ops_common.cuh"
+
+namespace sgemm {
+
+// Elements of a 16-byte piece.
+constexpr int piece_elements(int type) { return type == kTypeF32 ? 4 : 8; }
+
+// The memory of a rows x cols matrix, from which aligned pieces may be read.
+struct Matrix {
+    const char *begin, *end;
+    long long ld;  // bytes
+};
+__device__ __forceinline__ Matrix matrix(const void *p, long long rows, int cols, long long ld, int bytes) {
+    const char *b = static_cast<const char *>(p);
+    return {b, b + ((rows - 1) * ld + cols) * bytes, ld * bytes};
+}
+
+// w >> (8 * shift) over eight words, the first four of it; shift in 0 .. 15, even.
+__device__ __forceinline__ uint4 shift_pieces(uint4 a, uint4 b, int shift) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t u[7], t[5], o[4];
+#pragma unroll
+    for (int k = 0; k < 7; ++k) u[k] = shift & 4 ? w[k + 1] : w[k];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) t[k] = shift & 8 ? u[k + 2] : u[k];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = __funnelshift_r(t[k], t[k + 1], (shift & 2) * 8);
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int TYPE>
+__device__ __forceinline__ void unpack_piece(uint4 f, float (&v)[piece_elements(TYPE)]) {
+    const uint32_t w[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (TYPE == kTypeF32) {
+            v[j] = __uint_as_float(w[j]);
+        } else {
+            const float2 e = unpack16<TYPE>(w[j]);
+            v[2 * j] = e.x;
+            v[2 * j + 1] = e.y;
+        }
+    }
+}
+template <int TYPE>
+__device__ __forceinline__ uint4 pack_piece(const float (&v)[piece_elements(TYPE)]) {
+    if constexpr (TYPE == kTypeF32)
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                          __float_as_uint(v[3]));
+    else
+        return make_uint4(pack16<TYPE>(v[0], v[1]), pack16<TYPE>(v[2], v[3]), pack16<TYPE>(v[4], v[5]),
+                          pack16<TYPE>(v[6], v[7]));
+}
+
+// n (at least 1) elements from p on, as they lie in memory, zeros for the others up to
+// a piece.  ALIGNED: p is on 16 bytes.
+template <int TYPE, bool ALIGNED>
+__device__ __forceinline__ uint4 load_piece(const char *p, int n, const Matrix &m) {
+    constexpr int V = piece_elements(TYPE), E = 16 / V;
+    const int shift = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15);
+    const char *first = p - shift;
+    if (n >= V && (ALIGNED || (first >= m.begin && first + 32 <= m.end))) {
+        const uint4 a = *reinterpret_cast<const uint4 *>(first);
+        if constexpr (ALIGNED) return a;
+        return shift_pieces(a, *reinterpret_cast<const uint4 *>(first + 16), shift);
+    }
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        if (j < n) {
+            if constexpr (E == 4)
+                w[j] = *reinterpret_cast<const uint32_t *>(p + 4 * j);
+            else
+                w[j / 2] |= (uint32_t)*reinterpret_cast<const uint16_t *>(p + 2 * j) << (16 * (j % 2));
+        }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <int TYPE, bool ALIGNED>
+__device__ __forceinline__ void load_values(const char *p, int n, const Matrix &m,
+                                            float (&v)[piece_elements(TYPE)]) {
+    unpack_piece<TYPE>(load_piece<TYPE, ALIGNED>(p, n, m), v);
+}
+
+// n (at least 1) elements of the norm's weight from c on; its type is TYPE or FP32.
+template <int TYPE, bool ALIGNED>
+__device__ __forceinline__ void load_weight(const Matrix &m, bool f32, int c, int n,
+                                            float (&v)[piece_elements(TYPE)]) {
+    if constexpr (TYPE == kTypeF32) {
+        load_values<TYPE, ALIGNED>(m.begin + 4LL * c, n, m, v);
+    } else if (!f32) {
+        load_values<TYPE, ALIGNED>(m.begin + 2LL * c, n, m, v);
+    } else {
+        float a[4], b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        load_values<kTypeF32, ALIGNED>(m.begin + 4LL * c, n, m, a);
+        if (n > 4) load_values<kTypeF32, ALIGNED>(m.begin + 4LL * c + 16, n - 4, m, b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = a[j];
+            v[4 + j] = b[j];
+        }
+    }
+}
+
+// Shared memory of a warp for store_piece().
+constexpr int kStageWords = 33 * 4;  // 32 pieces, and one that a read may reach into
+
+// A whole warp's pieces, lane by lane from `p` on (the address of lane 0's): n
+// elements of each lane's exist (none where n < 1).  Every lane calls it.
+template <int TYPE, bool ALIGNED>
+__device__ __forceinline__ void store_piece(char *p, int n, uint4 w, uint32_t *stage) {
+    constexpr int V = piece_elements(TYPE), E = 16 / V;
+    const int lane = threadIdx.x & 31;
+    const int shift = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15);
+    if (ALIGNED || shift == 0) {
+        char *to = p + 16 * lane;
+        if (n >= V) {
+            *reinterpret_cast<uint4 *>(to) = w;
+        } else {
+            const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (j < n) {
+                    if constexpr (E == 4)
+                        reinterpret_cast<uint32_t *>(to)[j] = e[j];
+                    else
+                        reinterpret_cast<uint16_t *>(to)[j] = (uint16_t)(e[j / 2] >> (16 * (j % 2)));
+                }
+        }
+        return;
+    }
+    __syncwarp();
+    reinterpret_cast<uint4 *>(stage)[lane] = w;
+    __syncwarp();
+    const int bytes = __reduce_add_sync(0xffffffffu, max(0, min(n, V))) * E;
+    const int head = 16 - shift;  // bytes before the destination's first aligned piece
+    const int at = head + 16 * lane;
+    if (at + 16 <= bytes) {
+        const uint4 *from = reinterpret_cast<const uint4 *>(stage) + lane;
+        *reinterpret_cast<uint4 *>(p + at) = shift_pieces(from[0], from[1], head);
+    }
+    // The ends: before `head`, and behind the last whole piece.
+    const int tail = bytes > head ? head + (bytes - head) / 16 * 16 : bytes;
+    const int i = (lane & 15) * E, off = lane < 16 ? i : tail + i;
+    if (lane < 16 ? i < min(head, bytes) : off < bytes) {
+        if constexpr (E == 4)
+            *reinterpret_cast<uint32_t *>(p + off) = stage[off / 4];
+        else
+            *reinterpret_cast<uint16_t *>(p + off) = reinterpret_cast<const uint16_t *>(stage)[off / 2];
+    }
+}
+
+}  // namespace sgemm
