@@ -252,7 +252,7 @@ def _own(s, case):
     out = dict(zip(("y", "h"), got)) if case["residual"] else {"y": got}
     if case["op"] == "train":
         out["dx"], out["dweight"] = sg.rms_norm_backward(
-            s["dy"], out.get("h", s["x"]), s["weight"],
+            s["dy"], s["x"], s["weight"], residual=residual,
             dh=s["dh"] if case["residual"] else None, eps=EPS)
     return out
 
