@@ -8,18 +8,20 @@
 // and neither the tiles nor the way that K is shared out changes a bit of it.
 //
 // y^T = w x^T: a tile is 128 channels (256 by a pair of CTAs) by up to 96 (192)
-// tokens.  The weights stay 8 bits wide up to the SM: they are widened by four
+// tokens.  The weights stay 8 bits wide up to the SM: they are widened by eight
 // warps from shared memory into tensor memory, from where the tensor core reads its
 // first operand, so that shared memory carries them once in 8 bits and not again in
 // 16.  x, read by every channel tile, is widened by a kernel of its own first.
 //
-// 448 threads a CTA, one CTA per SM:
-//   warps 0-3    widen: 64 k of a row per thread from a stage (128-byte swizzle) to a
-//                slot of 32 tensor-memory columns
-//   warps 4-11   epilogue: accumulators to integers, scales, stores
-//   warp 12      TMA loads: w 16 KB and x up to 24 KB per stage of 128 k
-//   warp 13      tcgen05.mma, one elected thread; allocates tensor memory
-// Tensor memory: two accumulators of 192 columns, four slots of 32.
+// 640 threads a CTA, one CTA per SM, registers moved to where the sums are
+// (setmaxnreg; the launch has 96 a thread):
+//   warp 0       TMA loads: w 16 KB and x up to 24 KB per stage of 128 k
+//   warp 1       tcgen05.mma, one elected thread
+//   warp 2       allocates tensor memory
+//   warps 4-11   widen: a warp 64 k of 32 rows of a stage (128-byte swizzle), into 32 of
+//                the 64 tensor-memory columns of a slot
+//   warps 12-19  epilogue: accumulators to integers, scales, stores
+// Tensor memory: two accumulators of 192 columns, two slots of 64.
 // Every wait is bounded; a role that gives up flags the error word, the others
 // run out in turn, and the CTA lets its copies land before it leaves.
 #include <algorithm>
@@ -32,16 +34,20 @@
 namespace sgemm {
 namespace {
 
-constexpr int kThreads = 448;
-constexpr int kStages = 5, kSlots = 4;
+constexpr int kThreads = 640;
+constexpr int kRegsRoles = 40, kRegsWiden = 80, kRegsEpilogue = 136;
+static_assert(128 * kRegsRoles + 256 * (kRegsWiden + kRegsEpilogue) <= 96 * kThreads, "");
+constexpr int kStages = 5, kSlots = 2;
 constexpr uint32_t kWBytes = kQ8Channels * kQ8StageK;
 constexpr uint32_t kXBoxBytes = kQ8Tokens * 128;
 constexpr uint32_t kStageBytes = kWBytes + 2 * kXBoxBytes;
 constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024;
 constexpr int kAccCols = 2 * kQ8Tokens, kSlotCol = 2 * kAccCols;  // tensor-memory columns
 constexpr int kTmemCols = 512;
-static_assert(kSlotCol + kSlots * (kQ8SlotK / 2) == kTmemCols, "");
-constexpr int kEpiWarps = 8;
+constexpr int kSlotCols = kQ8StageK / 2;
+static_assert(kSlotCol + kSlots * kSlotCols == kTmemCols, "");
+constexpr int kWidenWarps = 8, kEpiWarps = 8;
+constexpr int kFirstWiden = 4, kFirstEpi = 12;
 constexpr int kParts = kQ8Tokens / 16;                // of 16 columns, an epilogue warp's
 constexpr int kChunk = kQ8ExactK / kQ8StageK;         // stages of an accumulator
 constexpr int kMaxDevices = 64;
@@ -176,6 +182,16 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
             : "memory");
 }
 
+// A whole warpgroup gives registers back, or takes what others gave back.
+template <int N>
+__device__ __forceinline__ void set_fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 template <int TYPE, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
     q8_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
@@ -197,12 +213,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&w_full[s], 1);
-            mbar_init(&w_empty[s], 4);
+            mbar_init(&w_empty[s], kWidenWarps);
             mbar_init(&x_full[s], 1);
             mbar_init(&x_empty[s], 1);
         }
         for (int j = 0; j < kSlots; ++j) {
-            mbar_init(&a_full[j], 4 * CG);
+            mbar_init(&a_full[j], kWidenWarps * CG);
             mbar_init(&a_empty[j], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -213,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_barrier_init();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (warp == 13) tc_alloc<CG, kTmemCols>(&tmem_slot);
+    if (warp == 2) tc_alloc<CG, kTmemCols>(&tmem_slot);
     tc_fence_before_sync();
     __syncthreads();
     if constexpr (CG == 2) cluster_barrier();
@@ -232,141 +248,137 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     Unit unit;
 
-    if (warp == 12) {
-        const int tokens = p.tokens / CG;  // that this CTA brings in
-        const uint32_t x_bytes = (uint32_t)tokens * 256 * CG;
-        const uint32_t x_bar0 = CG == 2 ? cluster_addr(&x_full[0], 0) : smem_addr(&x_full[0]);
-        int it = 0, s = 0;
-        uint32_t parity = 1;
-        for (int u = 0; ok && unit_at(p, worker, u, unit); ++u) {
-            const int n0 = (unit.n * CG + (int)rank) * kQ8Channels;
-            const int m0 = unit.m * p.tokens + (int)rank * tokens;
-            for (int st = unit.s0; st < unit.s1; ++st, ++it) {
-                if (p.skip_loads_from >= 0 && it >= p.skip_loads_from) {
-                    ok = false;
-                    break;
-                }
-                ok = tc_wait_warp(&w_empty[s], parity, p.timeout_ns) &&
-                     tc_wait_warp(&x_empty[s], parity, p.timeout_ns);
-                if (!ok) {
-                    give_up(kErrWaitTimeout);
-                    break;
-                }
-                if (tc_elect()) {
-                    const uint32_t w = sbase + s * kStageBytes, x = w + kWBytes;
-                    const int k = st * kQ8StageK;
-                    mbar_arrive_expect_tx(&w_full[s], kWBytes);
-                    // The pair's tokens all complete on the first CTA's barrier.
-                    if (rank == 0) mbar_arrive_expect_tx(&x_full[s], x_bytes);
-                    tma_load_2d(smem + s * kStageBytes, &map_w, &w_full[s], k, n0);
-                    tc_load_3d<CG>(x, &map_x, x_bar0 + s * 8, k, m0, 0);
-                    tc_load_3d<CG>(x + kXBoxBytes, &map_x, x_bar0 + s * 8, k + 64, m0, 0);
-                }
-                __syncwarp();
-                if (++s == kStages) {
-                    s = 0;
-                    parity ^= 1;
-                }
-            }
-        }
-        // The last releases of the stages have to arrive before the CTA leaves.
-        for (int i = max(0, it - kStages); ok && i < it; ++i) {
-            ok = tc_wait_warp(&x_empty[i % kStages], (i / kStages) & 1, p.timeout_ns) &&
-                 tc_wait_warp(&w_empty[i % kStages], (i / kStages) & 1, p.timeout_ns);
-            if (!ok) give_up(kErrDrainTimeout);
-        }
-        __syncwarp();
-    } else if (warp == 13) {
-        if (rank == 0) {
-            const uint64_t desc = tc_desc(sbase + kWBytes, 0);
-            const uint32_t idesc = tc_idesc(kQ8Channels * CG, p.tokens, false, false, false);
-            int s = 0, slot = 0, buf = 0;
-            uint32_t parity = 0, slot_parity = 0, acc_parity = 1;
+    if (warp < kFirstWiden) {
+        set_fewer_registers<kRegsRoles>();
+        if (warp == 0) {
+            const int tokens = p.tokens / CG;  // that this CTA brings in
+            const uint32_t x_bytes = (uint32_t)tokens * 256 * CG;
+            const uint32_t x_bar0 = CG == 2 ? cluster_addr(&x_full[0], 0) : smem_addr(&x_full[0]);
+            int it = 0, s = 0;
+            uint32_t parity = 1;
             for (int u = 0; ok && unit_at(p, worker, u, unit); ++u) {
-                for (int st = unit.s0; ok && st < unit.s1; ++st) {
-                    const int at = (st - unit.s0) % kChunk;
-                    if (at == 0) ok = tc_wait_warp(&acc_empty[buf], acc_parity, p.timeout_ns);
-                    ok = ok && tc_wait_warp(&x_full[s], parity, p.timeout_ns);
-                    const bool last = at == kChunk - 1 || st + 1 == unit.s1;
-#pragma unroll 1
-                    for (int half = 0; ok && half < 2; ++half) {
-                        ok = tc_wait_warp(&a_full[slot], slot_parity, p.timeout_ns);
-                        if (!ok) break;
-                        tc_fence_after_sync();
-                        if (tc_elect()) {
-                            const uint64_t b = desc + ((s * kStageBytes + half * kXBoxBytes) >> 4);
-                            const uint32_t a = tmem + kSlotCol + slot * (kQ8SlotK / 2);
-#pragma unroll
-                            for (int kk = 0; kk < kQ8SlotK / 16; ++kk)
-                                tc_mma_ts<CG>(tmem + buf * kAccCols, a + kk * 8, b + kk * 2, idesc,
-                                              at != 0 || half != 0 || kk != 0);
-                            tc_commit<CG>(&a_empty[slot]);
-                            if (half == 1) {
-                                tc_commit<CG>(&x_empty[s]);
-                                if (last) tc_commit<CG>(&acc_full[buf]);
-                            }
-                        }
-                        __syncwarp();
-                        if (++slot == kSlots) {
-                            slot = 0;
-                            slot_parity ^= 1;
-                        }
+                const int n0 = (unit.n * CG + (int)rank) * kQ8Channels;
+                const int m0 = unit.m * p.tokens + (int)rank * tokens;
+                for (int st = unit.s0; st < unit.s1; ++st, ++it) {
+                    if (p.skip_loads_from >= 0 && it >= p.skip_loads_from) {
+                        ok = false;
+                        break;
                     }
-                    if (last) {
-                        buf ^= 1;
-                        acc_parity ^= buf ^ 1;
+                    ok = tc_wait_warp(&w_empty[s], parity, p.timeout_ns) &&
+                         tc_wait_warp(&x_empty[s], parity, p.timeout_ns);
+                    if (!ok) {
+                        give_up(kErrWaitTimeout);
+                        break;
                     }
+                    if (tc_elect()) {
+                        const uint32_t w = sbase + s * kStageBytes, x = w + kWBytes;
+                        const int k = st * kQ8StageK;
+                        mbar_arrive_expect_tx(&w_full[s], kWBytes);
+                        // The pair's tokens all complete on the first CTA's barrier.
+                        if (rank == 0) mbar_arrive_expect_tx(&x_full[s], x_bytes);
+                        tma_load_2d(smem + s * kStageBytes, &map_w, &w_full[s], k, n0);
+                        tc_load_3d<CG>(x, &map_x, x_bar0 + s * 8, k, m0, 0);
+                        tc_load_3d<CG>(x + kXBoxBytes, &map_x, x_bar0 + s * 8, k + 64, m0, 0);
+                    }
+                    __syncwarp();
                     if (++s == kStages) {
                         s = 0;
                         parity ^= 1;
                     }
                 }
             }
-            if (!ok) give_up(kErrWaitTimeout);
+            // The last releases of the stages have to arrive before the CTA leaves.
+            for (int i = max(0, it - kStages); ok && i < it; ++i) {
+                ok = tc_wait_warp(&x_empty[i % kStages], (i / kStages) & 1, p.timeout_ns) &&
+                     tc_wait_warp(&w_empty[i % kStages], (i / kStages) & 1, p.timeout_ns);
+                if (!ok) give_up(kErrDrainTimeout);
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            if (rank == 0) {
+                const uint64_t desc = tc_desc(sbase + kWBytes, 0);
+                const uint32_t idesc = tc_idesc(kQ8Channels * CG, p.tokens, false, false, false);
+                int s = 0, slot = 0, buf = 0;
+                uint32_t parity = 0, slot_parity = 0, acc_parity = 1;
+                for (int u = 0; ok && unit_at(p, worker, u, unit); ++u) {
+                    for (int st = unit.s0; st < unit.s1; ++st) {
+                        const int at = (st - unit.s0) % kChunk;
+                        const bool last = at == kChunk - 1 || st + 1 == unit.s1;
+                        ok = (at != 0 || tc_wait_warp(&acc_empty[buf], acc_parity, p.timeout_ns)) &&
+                             tc_wait_warp(&x_full[s], parity, p.timeout_ns) &&
+                             tc_wait_warp(&a_full[slot], slot_parity, p.timeout_ns);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        if (tc_elect()) {
+                            const uint64_t b = desc + ((s * kStageBytes) >> 4);
+                            const uint32_t a = tmem + kSlotCol + slot * kSlotCols, d = tmem + buf * kAccCols;
+#pragma unroll
+                            for (int kk = 0; kk < kQ8StageK / 16; ++kk)
+                                tc_mma_ts<CG>(d, a + kk * 8,
+                                              b + (kk / 4) * (kXBoxBytes >> 4) + (kk % 4) * 2, idesc,
+                                              at != 0 || kk != 0);
+                            tc_commit<CG>(&a_empty[slot]);
+                            tc_commit<CG>(&x_empty[s]);
+                            if (last) tc_commit<CG>(&acc_full[buf]);
+                        }
+                        __syncwarp();
+                        if (last) {
+                            buf ^= 1;
+                            acc_parity ^= buf ^ 1;
+                        }
+                        if (++slot == kSlots) {
+                            slot = 0;
+                            slot_parity ^= 1;
+                        }
+                        if (++s == kStages) {
+                            s = 0;
+                            parity ^= 1;
+                        }
+                    }
+                }
+                if (!ok) give_up(kErrWaitTimeout);
+            }
+            __syncwarp();
         }
-        __syncwarp();
-    } else if (warp < 4) {
-        const int row = warp * 32 + lane;
-        const uint32_t t_lane = tmem + kSlotCol + ((uint32_t)(warp * 32) << 16);
-        const uint32_t bar0 = CG == 2 ? cluster_addr(&a_full[0], 0) : smem_addr(&a_full[0]);
+    } else if (warp < kFirstEpi) {
+        set_fewer_registers<kRegsWiden>();
+        const int quad = warp & 3, half = (warp - kFirstWiden) >> 2;
+        const int row = quad * 32 + lane;
+        const uint32_t t_lane = tmem + kSlotCol + half * (kQ8SlotK / 2) + ((uint32_t)(quad * 32) << 16);
+        const uint32_t bar0 = cluster_addr(&a_full[0], 0);
         int s = 0, slot = 0, done = 0;
         uint32_t parity = 0, slot_parity = 1;
         for (int u = 0; ok && unit_at(p, worker, u, unit); ++u) {
-            for (int st = unit.s0; ok && st < unit.s1; ++st) {
+            for (int st = unit.s0; st < unit.s1; ++st) {
                 ok = tc_wait_warp(&w_full[s], parity, p.timeout_ns);
+                if (!ok) break;
                 const unsigned char *from = smem + s * kStageBytes + row * 128;
-#pragma unroll 1
-                for (int half = 0; ok && half < 2; ++half) {
-                    uint32_t r[32];
+                uint4 w[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint4 w =
-                            *reinterpret_cast<const uint4 *>(from + (((half * 4 + c) ^ (row & 7)) << 4));
-                        widen(w.x, r[8 * c], r[8 * c + 1]);
-                        widen(w.y, r[8 * c + 2], r[8 * c + 3]);
-                        widen(w.z, r[8 * c + 4], r[8 * c + 5]);
-                        widen(w.w, r[8 * c + 6], r[8 * c + 7]);
-                    }
-                    if (half == 1) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&w_empty[s]);
-                    }
-                    ok = tc_wait_warp(&a_empty[slot], slot_parity, p.timeout_ns);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    tc_st32(t_lane + slot * (kQ8SlotK / 2), r);
-                    tc_wait_st();
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0)
-                        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                                         bar0 + slot * 8)
-                                     : "memory");
-                    ++done;
-                    if (++slot == kSlots) {
-                        slot = 0;
-                        slot_parity ^= 1;
-                    }
+                for (int c = 0; c < 4; ++c)
+                    w[c] = *reinterpret_cast<const uint4 *>(from + (((half * 4 + c) ^ (row & 7)) << 4));
+                uint32_t r[32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    widen(w[c].x, r[8 * c], r[8 * c + 1]);
+                    widen(w[c].y, r[8 * c + 2], r[8 * c + 3]);
+                    widen(w[c].z, r[8 * c + 4], r[8 * c + 5]);
+                    widen(w[c].w, r[8 * c + 6], r[8 * c + 7]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&w_empty[s]);
+                ok = tc_wait_warp(&a_empty[slot], slot_parity, p.timeout_ns);
+                if (!ok) break;
+                tc_fence_after_sync();
+                tc_st32(t_lane + slot * kSlotCols, r);
+                tc_wait_st();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) cluster_arrive(bar0 + slot * 8);
+                ++done;
+                if (++slot == kSlots) {
+                    slot = 0;
+                    slot_parity ^= 1;
                 }
                 if (++s == kStages) {
                     s = 0;
@@ -381,13 +393,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) give_up(kErrDrainTimeout);
         }
     } else {
-        const int quad = warp & 3, half = (warp - 4) >> 2;
+        set_more_registers<kRegsEpilogue>();
+        const int quad = warp & 3, half = (warp - kFirstEpi) >> 2;
         const int mine = p.tokens / 2;  // columns of this warp's half
         const int parts = (mine + 15) / 16;
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16) + half * mine;
         int buf = 0;
         uint32_t parity = 0;
         for (int u = 0; ok && unit_at(p, worker, u, unit); ++u) {
+            const int n = (unit.n * CG + (int)rank) * kQ8Channels + quad * 32 + lane;
+            const int m0 = unit.m * p.tokens + half * mine;
+            const int left = min(mine, p.M - m0);
+            // The tile's scales, before they are waited for: of 96 tokens, three a lane.
+            float xs[kQ8Tokens / 32];
+#pragma unroll
+            for (int j = 0; j < kQ8Tokens / 32; ++j)
+                xs[j] = j * 32 + lane < left ? __ldg(p.x_scales + m0 + j * 32 + lane) : 0.0f;
+            const float ws = n < p.N ? __ldg(p.w_scales + n) : 0.0f;
             int sum[kParts][16];
 #pragma unroll
             for (int j = 0; j < kParts; ++j)
@@ -413,13 +435,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 parity ^= buf ^ 1;
             }
             if (!ok) break;
-            const int n = (unit.n * CG + (int)rank) * kQ8Channels + quad * 32 + lane;
-            const int m0 = unit.m * p.tokens + half * mine;
             bool emit = true;
             if (unit.pieces > 1) {
                 auto slot = [&](int q) {
                     return p.partials +
-                           ((size_t)(piece_slot(unit, q) * CG + (int)rank) * kEpiWarps + (warp - 4)) *
+                           ((size_t)(piece_slot(unit, q) * CG + (int)rank) * kEpiWarps + (warp - kFirstEpi)) *
                                (kParts * 16 * 32) + lane;
                 };
                 int *to = slot(unit.piece);
@@ -431,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 __threadfence();
                 __syncwarp();
-                int *counter = p.counters + (unit.tail * CG + (int)rank) * kEpiWarps + (warp - 4);
+                int *counter = p.counters + (unit.tail * CG + (int)rank) * kEpiWarps + (warp - kFirstEpi);
                 int arrived = 0;
                 if (lane == 0) {
                     arrived = atomicAdd(counter, 1);
@@ -452,17 +472,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                     }
             }
-            if (emit && n < p.N) {
-                const float ws = __ldg(p.w_scales + n);
-                const int left = min(mine, p.M - m0);
+            if (emit) {
+                const long long at = (long long)m0 * p.ldy + n;
 #pragma unroll
                 for (int j = 0; j < kParts; ++j)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int t = j * 16 + i;
-                        if (t < left)
-                            store_from_float(p.y, TYPE, (long long)(m0 + t) * p.ldy + n,
-                                             (float)sum[j][i] * __ldg(p.x_scales + m0 + t) * ws);
+                        const float v =
+                            (float)sum[j][i] * __shfl_sync(0xffffffffu, xs[t / 32], t % 32) * ws;
+                        if (t < left && n < p.N) store_from_float(p.y, TYPE, at + t * p.ldy, v);
                     }
             }
         }
@@ -482,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // No CTA of a pair leaves, or frees its tensor memory, while the other's
     // loads and products may still reach it.
     if constexpr (CG == 2) cluster_barrier();
-    if (warp == 13) {
+    if (warp == 2) {
         tc_fence_after_sync();
         tc_dealloc<CG, kTmemCols>(tmem);
     }
