@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     q8_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                    const Q8GemmParams p) {
     extern __shared__ unsigned char q8_smem_raw[];
-    __shared__ uint64_t w_full[kStages], w_empty[kStages], x_full[kStages], x_empty[kStages];
+    __shared__ uint64_t full[kStages], empty[kStages];
     __shared__ uint64_t a_full[kSlots], a_empty[kSlots], acc_full[2], acc_empty[2];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int s_abort;
@@ -212,10 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&w_full[s], 1);
-            mbar_init(&w_empty[s], kWidenWarps);
-            mbar_init(&x_full[s], 1);
-            mbar_init(&x_empty[s], 1);
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
         }
         for (int j = 0; j < kSlots; ++j) {
             mbar_init(&a_full[j], kWidenWarps * CG);
@@ -252,8 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         set_fewer_registers<kRegsRoles>();
         if (warp == 0) {
             const int tokens = p.tokens / CG;  // that this CTA brings in
-            const uint32_t x_bytes = (uint32_t)tokens * 256 * CG;
-            const uint32_t x_bar0 = CG == 2 ? cluster_addr(&x_full[0], 0) : smem_addr(&x_full[0]);
+            const uint32_t bytes = kWBytes + (uint32_t)tokens * 256;
             int it = 0, s = 0;
             uint32_t parity = 1;
             for (int u = 0; ok && unit_at(p, worker, u, unit); ++u) {
@@ -264,8 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    ok = tc_wait_warp(&w_empty[s], parity, p.timeout_ns) &&
-                         tc_wait_warp(&x_empty[s], parity, p.timeout_ns);
+                    // (products done: the weights were widened before them)
+                    ok = tc_wait_warp(&empty[s], parity, p.timeout_ns);
                     if (!ok) {
                         give_up(kErrWaitTimeout);
                         break;
@@ -273,12 +270,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (tc_elect()) {
                         const uint32_t w = sbase + s * kStageBytes, x = w + kWBytes;
                         const int k = st * kQ8StageK;
-                        mbar_arrive_expect_tx(&w_full[s], kWBytes);
-                        // The pair's tokens all complete on the first CTA's barrier.
-                        if (rank == 0) mbar_arrive_expect_tx(&x_full[s], x_bytes);
-                        tma_load_2d(smem + s * kStageBytes, &map_w, &w_full[s], k, n0);
-                        tc_load_3d<CG>(x, &map_x, x_bar0 + s * 8, k, m0, 0);
-                        tc_load_3d<CG>(x + kXBoxBytes, &map_x, x_bar0 + s * 8, k + 64, m0, 0);
+                        const uint32_t bar = smem_addr(&full[s]);
+                        mbar_arrive_expect_tx(&full[s], bytes);
+                        tma_load_2d(smem + s * kStageBytes, &map_w, &full[s], k, n0);
+                        tc_load_3d<1>(x, &map_x, bar, k, m0, 0);
+                        tc_load_3d<1>(x + kXBoxBytes, &map_x, bar, k + 64, m0, 0);
                     }
                     __syncwarp();
                     if (++s == kStages) {
@@ -289,8 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // The last releases of the stages have to arrive before the CTA leaves.
             for (int i = max(0, it - kStages); ok && i < it; ++i) {
-                ok = tc_wait_warp(&x_empty[i % kStages], (i / kStages) & 1, p.timeout_ns) &&
-                     tc_wait_warp(&w_empty[i % kStages], (i / kStages) & 1, p.timeout_ns);
+                ok = tc_wait_warp(&empty[i % kStages], (i / kStages) & 1, p.timeout_ns);
                 if (!ok) give_up(kErrDrainTimeout);
             }
             __syncwarp();
@@ -299,13 +294,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t desc = tc_desc(sbase + kWBytes, 0);
                 const uint32_t idesc = tc_idesc(kQ8Channels * CG, p.tokens, false, false, false);
                 int s = 0, slot = 0, buf = 0;
-                uint32_t parity = 0, slot_parity = 0, acc_parity = 1;
+                uint32_t slot_parity = 0, acc_parity = 1;
                 for (int u = 0; ok && unit_at(p, worker, u, unit); ++u) {
                     for (int st = unit.s0; st < unit.s1; ++st) {
                         const int at = (st - unit.s0) % kChunk;
                         const bool last = at == kChunk - 1 || st + 1 == unit.s1;
+                        // The slots' warps, of both CTAs, waited for the tokens too.
                         ok = (at != 0 || tc_wait_warp(&acc_empty[buf], acc_parity, p.timeout_ns)) &&
-                             tc_wait_warp(&x_full[s], parity, p.timeout_ns) &&
                              tc_wait_warp(&a_full[slot], slot_parity, p.timeout_ns);
                         if (!ok) break;
                         tc_fence_after_sync();
@@ -318,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                               b + (kk / 4) * (kXBoxBytes >> 4) + (kk % 4) * 2, idesc,
                                               at != 0 || kk != 0);
                             tc_commit<CG>(&a_empty[slot]);
-                            tc_commit<CG>(&x_empty[s]);
+                            tc_commit<CG>(&empty[s]);
                             if (last) tc_commit<CG>(&acc_full[buf]);
                         }
                         __syncwarp();
@@ -330,10 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             slot = 0;
                             slot_parity ^= 1;
                         }
-                        if (++s == kStages) {
-                            s = 0;
-                            parity ^= 1;
-                        }
+                        if (++s == kStages) s = 0;
                     }
                 }
                 if (!ok) give_up(kErrWaitTimeout);
@@ -350,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t parity = 0, slot_parity = 1;
         for (int u = 0; ok && unit_at(p, worker, u, unit); ++u) {
             for (int st = unit.s0; st < unit.s1; ++st) {
-                ok = tc_wait_warp(&w_full[s], parity, p.timeout_ns);
+                ok = tc_wait_warp(&full[s], parity, p.timeout_ns);
                 if (!ok) break;
                 const unsigned char *from = smem + s * kStageBytes + row * 128;
                 uint4 w[4];
@@ -365,8 +357,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     widen(w[c].z, r[8 * c + 4], r[8 * c + 5]);
                     widen(w[c].w, r[8 * c + 6], r[8 * c + 7]);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&w_empty[s]);
                 ok = tc_wait_warp(&a_empty[slot], slot_parity, p.timeout_ns);
                 if (!ok) break;
                 tc_fence_after_sync();
