@@ -603,11 +603,11 @@ sgemm_status_t op_counters(cudaStream_t stream, size_t count, int **out) {
 
 sgemm_status_t op_encode_16(CUtensorMap *map, bool bf16, const void *base, int64_t rows,
                             int64_t cols, int64_t ld, int64_t planes, int64_t plane_stride,
-                            int box_rows) {
+                            int box_rows, int box_planes) {
     if (!g_encode) return SGEMM_ERR_TMA;
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
     const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)plane_stride * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_planes};
     const cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = g_encode(
         map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,

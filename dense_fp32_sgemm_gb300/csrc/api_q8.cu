@@ -253,7 +253,7 @@ sgemm_status_t sgemm_q8_matmul(int64_t M, int64_t N, int64_t K, int type, const 
         bytes += (n + 255) / 256 * 256;
         return at;
     };
-    const int64_t ld_w = in_place ? ldw : up(K, 16), ld_x = up(K, 8);
+    const int64_t ld_w = in_place ? ldw : up(K, 16), ld_x = up(K, 64);
     const size_t w_at = in_place ? 0 : take((size_t)(N * ld_w));
     const size_t x_at = stream_form ? 0 : take((size_t)(M * ld_x) * 2);
     const size_t part_at = stream_form ? 0 : take((size_t)2 * dev.num_sms * q8_slot_ints() * sizeof(int));
@@ -314,7 +314,9 @@ sgemm_status_t sgemm_q8_matmul(int64_t M, int64_t N, int64_t K, int type, const 
     p.skip_loads_from = dev.skip_loads_from;
     CUtensorMap map_w, map_x;
     s = op_encode_bytes(&map_w, w, N, K, ld_w, kQ8Channels);
-    if (s == SGEMM_OK) s = op_encode_16(&map_x, false, wide, M, K, ld_x, 1, M * ld_x, p.tokens / (pair ? 2 : 1));
+    // x as its stretches of 64 k, two of which are a stage's.
+    if (s == SGEMM_OK)
+        s = op_encode_16(&map_x, false, wide, M, 64, ld_x, ld_x / 64, 64, p.tokens / (pair ? 2 : 1), 2);
     if (s != SGEMM_OK) return s;
     if (launch_q8_widen(x, ldx, (int)M, (int)K, wide, ld_x, dev.num_sms, st) != cudaSuccess)
         return SGEMM_ERR_LAUNCH;

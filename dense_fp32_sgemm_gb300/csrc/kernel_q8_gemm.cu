@@ -15,7 +15,7 @@
 //
 // 640 threads a CTA, one CTA per SM, registers moved to where the sums are
 // (setmaxnreg; the launch has 96 a thread):
-//   warp 0       TMA loads: w 16 KB and x up to 24 KB per stage of 128 k
+//   warps 0, 3   TMA loads: w 16 KB and x up to 24 KB per stage of 128 k
 //   warp 1       tcgen05.mma, one elected thread
 //   warp 2       allocates tensor memory
 //   warps 4-11   widen: a warp 64 k of 32 rows of a stage (128-byte swizzle), into 32 of
@@ -39,8 +39,7 @@ constexpr int kRegsRoles = 40, kRegsWiden = 80, kRegsEpilogue = 136;
 static_assert(128 * kRegsRoles + 256 * (kRegsWiden + kRegsEpilogue) <= 96 * kThreads, "");
 constexpr int kStages = 5, kSlots = 2;
 constexpr uint32_t kWBytes = kQ8Channels * kQ8StageK;
-constexpr uint32_t kXBoxBytes = kQ8Tokens * 128;
-constexpr uint32_t kStageBytes = kWBytes + 2 * kXBoxBytes;
+constexpr uint32_t kStageBytes = kWBytes + kQ8Tokens * kQ8StageK * 2;
 constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024;
 constexpr int kAccCols = 2 * kQ8Tokens, kSlotCol = 2 * kAccCols;  // tensor-memory columns
 constexpr int kTmemCols = 512;
@@ -212,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 2);
             mbar_init(&empty[s], 1);
         }
         for (int j = 0; j < kSlots; ++j) {
@@ -248,9 +247,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kFirstWiden) {
         set_fewer_registers<kRegsRoles>();
-        if (warp == 0) {
+        if (warp == 0 || warp == 3) {
+            // One warp brings the weights, the other the tokens: a stage's loads take one
+            // some 600 clocks to issue.
             const int tokens = p.tokens / CG;  // that this CTA brings in
-            const uint32_t bytes = kWBytes + (uint32_t)tokens * 256;
+            const uint32_t bytes = warp == 0 ? kWBytes : (uint32_t)tokens * 256;
             int it = 0, s = 0;
             uint32_t parity = 1;
             for (int u = 0; ok && unit_at(p, worker, u, unit); ++u) {
@@ -268,13 +269,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     if (tc_elect()) {
-                        const uint32_t w = sbase + s * kStageBytes, x = w + kWBytes;
-                        const int k = st * kQ8StageK;
-                        const uint32_t bar = smem_addr(&full[s]);
                         mbar_arrive_expect_tx(&full[s], bytes);
-                        tma_load_2d(smem + s * kStageBytes, &map_w, &full[s], k, n0);
-                        tc_load_3d<1>(x, &map_x, bar, k, m0, 0);
-                        tc_load_3d<1>(x + kXBoxBytes, &map_x, bar, k + 64, m0, 0);
+                        if (warp == 0)
+                            tma_load_2d(smem + s * kStageBytes, &map_w, &full[s], st * kQ8StageK, n0);
+                        else
+                            tc_load_3d<1>(sbase + s * kStageBytes + kWBytes, &map_x, smem_addr(&full[s]), 0,
+                                          m0, st * 2);
                     }
                     __syncwarp();
                     if (++s == kStages) {
@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == 1) {
             if (rank == 0) {
                 const uint64_t desc = tc_desc(sbase + kWBytes, 0);
+                const uint32_t second = (uint32_t)(p.tokens / CG) * 128 >> 4;  // from 64 k to the next
                 const uint32_t idesc = tc_idesc(kQ8Channels * CG, p.tokens, false, false, false);
                 int s = 0, slot = 0, buf = 0;
                 uint32_t slot_parity = 0, acc_parity = 1;
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int kk = 0; kk < kQ8StageK / 16; ++kk)
                                 tc_mma_ts<CG>(d, a + kk * 8,
-                                              b + (kk / 4) * (kXBoxBytes >> 4) + (kk % 4) * 2, idesc,
+                                              b + (kk / 4) * second + (kk % 4) * 2, idesc,
                                               at != 0 || kk != 0);
                             tc_commit<CG>(&a_empty[slot]);
                             tc_commit<CG>(&empty[s]);
@@ -340,40 +341,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t bar0 = cluster_addr(&a_full[0], 0);
         int s = 0, slot = 0, done = 0;
         uint32_t parity = 0, slot_parity = 1;
-        for (int u = 0; ok && unit_at(p, worker, u, unit); ++u) {
-            for (int st = unit.s0; st < unit.s1; ++st) {
-                ok = tc_wait_warp(&full[s], parity, p.timeout_ns);
-                if (!ok) break;
-                const unsigned char *from = smem + s * kStageBytes + row * 128;
-                uint4 w[4];
+        int total = 0;
+        for (int u = 0; unit_at(p, worker, u, unit); ++u) total += unit.s1 - unit.s0;
+        uint4 w[4];
+        auto bring = [&]() {
+            ok = tc_wait_warp(&full[s], parity, p.timeout_ns);
+            const unsigned char *from = smem + s * kStageBytes + row * 128;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    w[c] = *reinterpret_cast<const uint4 *>(from + (((half * 4 + c) ^ (row & 7)) << 4));
-                uint32_t r[32];
+            for (int c = 0; c < 4; ++c)
+                w[c] = *reinterpret_cast<const uint4 *>(from + (((half * 4 + c) ^ (row & 7)) << 4));
+            if (++s == kStages) {
+                s = 0;
+                parity ^= 1;
+            }
+        };
+        if (total) bring();
+        for (int left = total; ok && left > 0; --left) {
+            uint32_t r[32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    widen(w[c].x, r[8 * c], r[8 * c + 1]);
-                    widen(w[c].y, r[8 * c + 2], r[8 * c + 3]);
-                    widen(w[c].z, r[8 * c + 4], r[8 * c + 5]);
-                    widen(w[c].w, r[8 * c + 6], r[8 * c + 7]);
-                }
-                ok = tc_wait_warp(&a_empty[slot], slot_parity, p.timeout_ns);
-                if (!ok) break;
-                tc_fence_after_sync();
-                tc_st32(t_lane + slot * kSlotCols, r);
-                tc_wait_st();
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) cluster_arrive(bar0 + slot * 8);
-                ++done;
-                if (++slot == kSlots) {
-                    slot = 0;
-                    slot_parity ^= 1;
-                }
-                if (++s == kStages) {
-                    s = 0;
-                    parity ^= 1;
-                }
+            for (int c = 0; c < 4; ++c) {
+                widen(w[c].x, r[8 * c], r[8 * c + 1]);
+                widen(w[c].y, r[8 * c + 2], r[8 * c + 3]);
+                widen(w[c].z, r[8 * c + 4], r[8 * c + 5]);
+                widen(w[c].w, r[8 * c + 6], r[8 * c + 7]);
+            }
+            if (left > 1) bring();
+            if (!ok) break;
+            ok = tc_wait_warp(&a_empty[slot], slot_parity, p.timeout_ns);
+            if (!ok) break;
+            tc_fence_after_sync();
+            tc_st32(t_lane + slot * kSlotCols, r);
+            tc_wait_st();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) cluster_arrive(bar0 + slot * 8);
+            ++done;
+            if (++slot == kSlots) {
+                slot = 0;
+                slot_parity ^= 1;
             }
         }
         if (!ok) give_up(kErrWaitTimeout);

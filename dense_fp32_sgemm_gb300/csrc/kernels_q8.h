@@ -120,8 +120,8 @@ struct Q8GemmParams {
     int skip_loads_from;
 };
 inline int q8_slot_ints() { return kQ8Channels * kQ8Tokens * 2; }
-// w: boxes of 128 channels x 128 bytes; x: fp16, boxes of tokens x 64 (128-byte
-// swizzles).
+// w: boxes of 128 channels x 128 bytes; x: fp16, boxes of two stretches of tokens x 64
+// (128-byte swizzles).
 cudaError_t launch_q8_gemm(const CUtensorMap &w, const CUtensorMap &x, const Q8GemmParams &p,
                            int type, bool pair, cudaStream_t stream);
 

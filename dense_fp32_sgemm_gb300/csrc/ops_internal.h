@@ -36,11 +36,11 @@ sgemm_status_t op_workspace(cudaStream_t stream, size_t bytes, void **out);
 sgemm_status_t op_counters(cudaStream_t stream, size_t count, int **out);
 
 // `planes` row-major rows x cols matrices of 16-bit elements (bf16 or fp16),
-// rows ld and planes plane_stride elements apart; boxes of one plane,
-// box_rows x 64, 128-byte swizzle, zero outside.
+// rows ld and planes plane_stride elements apart; boxes of box_planes planes,
+// box_rows x 64 of each, 128-byte swizzle, zero outside.
 sgemm_status_t op_encode_16(CUtensorMap *map, bool bf16, const void *base, int64_t rows,
                             int64_t cols, int64_t ld, int64_t planes, int64_t plane_stride,
-                            int box_rows);
+                            int box_rows, int box_planes = 1);
 
 // Row-major rows x cols matrix of 32-bit words, rows ld words apart; boxes of
 // box_rows x box_cols, 128-byte swizzle, zero outside.
