@@ -308,6 +308,7 @@ sgemm_status_t sgemm_q8_matmul(int64_t M, int64_t N, int64_t K, int type, const 
     p.x_scales = x_scales;
     p.w_scales = w_scales;
     p.y = y; p.ldy = ldy;
+    p.y_vec = rows16(y, ldy, M, type);
     p.device = dev.index;
     p.err = dev.err;
     p.timeout_ns = dev.timeout_ns;

@@ -40,12 +40,14 @@ static_assert(128 * kRegsRoles + 256 * (kRegsWiden + kRegsEpilogue) <= 96 * kThr
 constexpr int kStages = 5, kSlots = 2;
 constexpr uint32_t kWBytes = kQ8Channels * kQ8StageK;
 constexpr uint32_t kStageBytes = kWBytes + kQ8Tokens * kQ8StageK * 2;
-constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024;
+constexpr int kEpiWarps = 8;
+constexpr uint32_t kEpiBytes = 16 * 32 * 4;  // an epilogue warp's staging: 16 tokens of 32 channels
+constexpr size_t kSmem = (size_t)kStages * kStageBytes + kEpiWarps * kEpiBytes + 1024;
 constexpr int kAccCols = 2 * kQ8Tokens, kSlotCol = 2 * kAccCols;  // tensor-memory columns
 constexpr int kTmemCols = 512;
 constexpr int kSlotCols = kQ8StageK / 2;
 static_assert(kSlotCol + kSlots * kSlotCols == kTmemCols, "");
-constexpr int kWidenWarps = 8, kEpiWarps = 8;
+constexpr int kWidenWarps = 8;
 constexpr int kFirstWiden = 4, kFirstEpi = 12;
 constexpr int kParts = kQ8Tokens / 16;                // of 16 columns, an epilogue warp's
 constexpr int kChunk = kQ8ExactK / kQ8StageK;         // stages of an accumulator
@@ -393,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int mine = p.tokens / 2;  // columns of this warp's half
         const int parts = (mine + 15) / 16;
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16) + half * mine;
+        unsigned char *stage = smem + kStages * kStageBytes + (warp - kFirstEpi) * kEpiBytes;
         int buf = 0;
         uint32_t parity = 0;
         for (int u = 0; ok && unit_at(p, worker, u, unit); ++u) {
@@ -468,15 +471,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
             }
             if (emit) {
-                const long long at = (long long)m0 * p.ldy + n;
+                // 16 tokens at a time through shared memory, from a lane a channel to 16 bytes
+                // of a token a lane.  (Stored as they lie in registers, 2 bytes a lane, a
+                // tile took 16000 clocks, more than half of its products.)
+                const int channels = p.N - (n - lane);  // of the warp's 32 that exist
 #pragma unroll
                 for (int j = 0; j < kParts; ++j)
+                    if (j * 16 < left) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int t = j * 16 + i;
-                        const float v =
-                            (float)sum[j][i] * __shfl_sync(0xffffffffu, xs[t / 32], t % 32) * ws;
-                        if (t < left && n < p.N) store_from_float(p.y, TYPE, at + t * p.ldy, v);
+                        for (int i = 0; i < 16; ++i) {
+                            const int t = j * 16 + i;
+                            const float v =
+                                (float)sum[j][i] * __shfl_sync(0xffffffffu, xs[t / 32], t % 32) * ws;
+                            store_from_float(stage, TYPE, i * 32 + lane, v);
+                        }
+                        __syncwarp();
+                        constexpr int kElem = TYPE == kTypeF32 ? 4 : 2, kPer = 16 / kElem;
+                        constexpr int kRow = 32 / kPer;  // lanes of a token
+                        unsigned char *out = static_cast<unsigned char *>(p.y) +
+                                             ((m0 + j * 16) * p.ldy + (n - lane)) * kElem;
+                        const int tokens = min(16, left - j * 16);
+                        if (p.y_vec && channels >= 32) {
+                            const int c = lane % kRow * 16;
+#pragma unroll
+                            for (int token = lane / kRow; token < 16; token += 32 / kRow)
+                                if (token < tokens)
+                                    *reinterpret_cast<uint4 *>(out + token * p.ldy * kElem + c) =
+                                        *reinterpret_cast<const uint4 *>(stage + token * 32 * kElem + c);
+                        } else if (lane < channels) {
+#pragma unroll 4
+                            for (int token = 0; token < tokens; ++token) {
+                                unsigned char *to = out + (token * p.ldy + lane) * kElem;
+                                const unsigned char *from = stage + (token * 32 + lane) * kElem;
+                                if constexpr (kElem == 4)
+                                    *reinterpret_cast<uint32_t *>(to) = *reinterpret_cast<const uint32_t *>(from);
+                                else
+                                    *reinterpret_cast<uint16_t *>(to) = *reinterpret_cast<const uint16_t *>(from);
+                            }
+                        }
+                        __syncwarp();
                     }
             }
         }

@@ -114,6 +114,7 @@ struct Q8GemmParams {
     const float *x_scales, *w_scales;
     void *y;
     long long ldy;
+    int y_vec;                        // its rows start on 16 bytes
     int device;
     int *err;
     unsigned long long timeout_ns;
