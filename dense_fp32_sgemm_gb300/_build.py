@@ -23,10 +23,10 @@ LIB_PATH = os.path.join(BUILD, LIB_NAME)
 SOURCES = ["api.cu", "plan.cpp", "kernel_tile.cu", "kernel_skinny.cu", "kernel_generic.cu", "kernel_mid.cu",
            "kernel_ksplit.cu", "kernel_narrow.cu", "kernel_small.cu", "probes.cu", "noalloc.cu", "kernel_3xtf32.cu",
            "api_ffn.cu", "kernel_ffn.cu", "kernel_ffn_stream.cu", "kernel_w4.cu", "kernel_adamw.cu",
-           "api_q8.cu", "kernel_rows.cu", "kernel_norm_grad.cu", "kernel_q8_gemm.cu", "kernel_q8_stream.cu"]
+           "api_q8.cu", "kernel_rows.cu", "kernel_gate_q8.cu", "kernel_norm_grad.cu", "kernel_q8_gemm.cu", "kernel_q8_stream.cu"]
 HEADERS = ["device_common.cuh", "kernels.h", "kernels_3xtf32.h", "plan.h",
            "kernels_ffn.h", "ops_internal.h", "ops_common.cuh",
-           "tc_common.cuh", "ffn_gate.cuh", "kernels_q8.h", "row_codes.cuh", "row_io.cuh"]
+           "tc_common.cuh", "ffn_gate.cuh", "kernels_q8.h", "row_codes.cuh", "row_io.cuh", "row_kernel.cuh"]
 PUBLIC_HEADERS = ["sgemm.h", "sgemm_probe.h", "sgemm_ffn.h", "sgemm_q8.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -102,7 +102,7 @@ sgemm_status_t sgemm_rms_norm(int64_t T, int64_t D, int type, const void *x, int
     if (s != SGEMM_OK) return s;
     RowParams p = row_params(a);
     p.y = y; p.ldy = ldy;
-    return status(launch_rows(p, type, kRowNorm, norm_vec(a) && rows16(y, ldy, T, type), dev.num_sms,
+    return status(launch_norm(p, type, false, norm_vec(a) && rows16(y, ldy, T, type), dev.num_sms,
                               static_cast<cudaStream_t>(stream)));
 }
 
@@ -125,7 +125,7 @@ sgemm_status_t sgemm_rms_norm_q8(int64_t T, int64_t D, int type, const void *x, 
     p.q = q; p.ldq = ldq;
     p.q_vec = codes_vec(q, ldq, T, type);
     p.scales = scales;
-    return status(launch_rows(p, type, kRowNormQ8, norm_vec(a) && p.q_vec,
+    return status(launch_norm(p, type, true, norm_vec(a) && p.q_vec,
                               dev.num_sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -201,7 +201,7 @@ sgemm_status_t sgemm_q8_gate(int64_t T, int64_t F, int type, int activation, con
     p.q_vec = codes_vec(q, ldq, T, type);
     p.scales = scales;
     const bool vec = rows16(g, ldg, T, type) && rows16(u, ldu, T, type) && p.q_vec;
-    return status(launch_rows(p, type, kRowGateQ8, vec, dev.num_sms, static_cast<cudaStream_t>(stream)));
+    return status(launch_gate_q8(p, type, vec, dev.num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 sgemm_status_t sgemm_q8_quantize(int64_t N, int64_t K, int type, const void *W, int64_t ldw, int8_t *q,

@@ -43,32 +43,21 @@ __device__ __forceinline__ float2 row_stats(float2 sums, int cols, float eps) {
     return make_float2(r, r * r * r * (sums.y / (float)cols));
 }
 
-// A row's matrices.
-struct Inputs {
-    Matrix x, r, dy, dh, w;
-    bool two, more;  // r, dh are there
-};
-template <int E>
-__device__ __forceinline__ Inputs inputs(const NormGradParams &p) {
-    return {matrix(p.x, p.rows, p.cols, p.ldx, E),   matrix(p.r, p.rows, p.cols, p.ldr, E),
-            matrix(p.dy, p.rows, p.cols, p.lddy, E), matrix(p.dh, p.rows, p.cols, p.lddh, E),
-            matrix(p.w, 1, p.cols, 0, p.w_f32 ? 4 : E), p.r != nullptr, p.dh != nullptr};
-}
 // A piece of a row as it comes from memory; zeros where it has no elements.
 struct Raw {
     uint4 x, r, dy, dh;
 };
 template <int TYPE, bool ALIGNED>
-__device__ __forceinline__ Raw fetch(const Inputs &m, long long row, int c, int n, bool with_dh) {
+__device__ __forceinline__ Raw fetch(const NormGradParams &p, long long row, int c, int n, bool with_dh) {
     constexpr int E = 16 / piece_elements(TYPE);
     Raw v;
     v.x = v.r = v.dy = v.dh = make_uint4(0, 0, 0, 0);
     if (n <= 0) return v;
-    const long long at = (long long)c * E;
-    v.x = load_piece<TYPE, ALIGNED>(m.x.begin + row * m.x.ld + at, n, m.x);
-    v.dy = load_piece<TYPE, ALIGNED>(m.dy.begin + row * m.dy.ld + at, n, m.dy);
-    if (m.two) v.r = load_piece<TYPE, ALIGNED>(m.r.begin + row * m.r.ld + at, n, m.r);
-    if (with_dh) v.dh = load_piece<TYPE, ALIGNED>(m.dh.begin + row * m.dh.ld + at, n, m.dh);
+    const bool inside = row > 0 && row + 1 < p.rows;
+    v.x = load_piece<TYPE, ALIGNED>(row_source(p.x, row, p.cols, p.ldx, E, inside), c * E, n);
+    v.dy = load_piece<TYPE, ALIGNED>(row_source(p.dy, row, p.cols, p.lddy, E, inside), c * E, n);
+    if (p.r) v.r = load_piece<TYPE, ALIGNED>(row_source(p.r, row, p.cols, p.ldr, E, inside), c * E, n);
+    if (with_dh) v.dh = load_piece<TYPE, ALIGNED>(row_source(p.dh, row, p.cols, p.lddh, E, inside), c * E, n);
     return v;
 }
 // h: the sum of its parts in FP32.
@@ -105,7 +94,7 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_kernel(const NormGr
     const int warps = blockDim.x >> 5, step = blockDim.x * V;
     uint32_t *stage = reinterpret_cast<uint32_t *>(s_stage) +
                       (ALIGNED ? 0 : (group * warps + (tid >> 5)) * kStageWords);
-    const Inputs m = inputs<E>(p);
+    const RowSource W = row_source(p.w, 0, p.cols, 0, p.w_f32 ? 4 : E, false);
     asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
     float dw[NP][V];
 #pragma unroll
@@ -118,7 +107,7 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_kernel(const NormGr
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int c = tid * V + i * step;
-            raw[i] = fetch<TYPE, ALIGNED>(m, row, c, row < p.rows ? p.cols - c : 0, m.more && kAhead);
+            raw[i] = fetch<TYPE, ALIGNED>(p, row, c, row < p.rows ? p.cols - c : 0, p.dh && kAhead);
         }
     };
     const long long first = (long long)blockIdx.x * groups + group, stride = (long long)gridDim.x * groups;
@@ -133,12 +122,12 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_kernel(const NormGr
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int c = tid * V + i * step;
-            sum_h<TYPE>(raw[i], m.two, h[i]);
+            sum_h<TYPE>(raw[i], p.r, h[i]);
             dy_raw[i] = raw[i].dy;
             dh_raw[i] = raw[i].dh;
             if (c < p.cols) {
                 float w[V], dy[V];
-                load_weight<TYPE, ALIGNED>(m.w, p.w_f32, c, p.cols - c, w);
+                load_weight<TYPE, ALIGNED>(W, p.w_f32, c, p.cols - c, w);
                 unpack_piece<TYPE>(dy_raw[i], dy);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
@@ -159,9 +148,10 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_kernel(const NormGr
             if (p.dx && live && c - lane * V < p.cols) {  // (the whole warp)
                 float w[V];
                 if (n > 0) {
-                    load_weight<TYPE, ALIGNED>(m.w, p.w_f32, c, n, w);
-                    if (!kAhead && m.more)
-                        dh_raw[i] = load_piece<TYPE, ALIGNED>(m.dh.begin + row * m.dh.ld + (long long)c * E, n, m.dh);
+                    load_weight<TYPE, ALIGNED>(W, p.w_f32, c, n, w);
+                    if (!kAhead && p.dh)
+                        dh_raw[i] = load_piece<TYPE, ALIGNED>(
+                            row_source(p.dh, row, p.cols, p.lddh, E, row > 0 && row + 1 < p.rows), c * E, n);
                 }
                 store_piece<TYPE, ALIGNED>(static_cast<char *>(p.dx) + (row * p.lddx + c - lane * V) * E, n,
                                            make_dx<TYPE>(h[i], w, dy_raw[i], dh_raw[i], st), stage);
@@ -189,15 +179,15 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_wide_kernel(const N
     const int tid = threadIdx.x, lane = tid & 31, step = blockDim.x * V;
     uint32_t *stage = reinterpret_cast<uint32_t *>(s_stage) + (ALIGNED ? 0 : (tid >> 5) * kStageWords);
     const long long row = blockIdx.x;
-    const Inputs m = inputs<E>(p);
+    const RowSource W = row_source(p.w, 0, p.cols, 0, p.w_f32 ? 4 : E, false);
     asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
     float2 sums = make_float2(0.0f, 0.0f);
     float h[V], dy[V], w[V];
     for (int c = tid * V; c < p.cols; c += step) {
-        const Raw raw = fetch<TYPE, ALIGNED>(m, row, c, p.cols - c, false);
-        sum_h<TYPE>(raw, m.two, h);
+        const Raw raw = fetch<TYPE, ALIGNED>(p, row, c, p.cols - c, false);
+        sum_h<TYPE>(raw, p.r, h);
         unpack_piece<TYPE>(raw.dy, dy);
-        load_weight<TYPE, ALIGNED>(m.w, p.w_f32, c, p.cols - c, w);
+        load_weight<TYPE, ALIGNED>(W, p.w_f32, c, p.cols - c, w);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             sums.x = fmaf(h[j], h[j], sums.x);
@@ -209,9 +199,9 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_wide_kernel(const N
     if (!p.dx) return;
     for (int c = tid * V; c - lane * V < p.cols; c += step) {
         const int n = p.cols - c;
-        const Raw raw = fetch<TYPE, ALIGNED>(m, row, c, n, m.more);
-        sum_h<TYPE>(raw, m.two, h);
-        if (n > 0) load_weight<TYPE, ALIGNED>(m.w, p.w_f32, c, n, w);
+        const Raw raw = fetch<TYPE, ALIGNED>(p, row, c, n, p.dh);
+        sum_h<TYPE>(raw, p.r, h);
+        if (n > 0) load_weight<TYPE, ALIGNED>(W, p.w_f32, c, n, w);
         store_piece<TYPE, ALIGNED>(static_cast<char *>(p.dx) + (row * p.lddx + c - lane * V) * E, n,
                                    make_dx<TYPE>(h, w, raw.dy, raw.dh, st), stage);
     }
@@ -234,24 +224,30 @@ __global__ void __launch_bounds__(256) norm_grad_columns_kernel(const NormGradPa
     p.partials[(long long)blockIdx.y * p.cols + c] = sum;
 }
 
-// dw: the partial rows added up, 32 columns a CTA.
+// dw: the partial rows added up, eight columns a CTA (a thread adds few of them, so
+// that its loads are under way at once).
 __global__ void __launch_bounds__(1024) norm_grad_reduce_kernel(const NormGradParams p, int type) {
-    __shared__ float s[32][33];
-    const int c = blockIdx.x * 32 + threadIdx.x;
+    __shared__ float s[32][9];
+    const int c = blockIdx.x * 8 + threadIdx.x, y = threadIdx.y;
     asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
     float sum = 0.0f;
     if (c < p.cols) {
 #pragma unroll 8
-        for (int q = threadIdx.y; q < p.parts; q += 32)
-            sum += __ldcg(p.partials + (long long)q * p.cols + c);
+        for (int q = y; q < p.parts; q += 128) sum += __ldcg(p.partials + (long long)q * p.cols + c);
     }
-    s[threadIdx.y][threadIdx.x] = sum;
+    // A warp has four values of each column.
+    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+    if (y % 4 == 0) s[y / 4][threadIdx.x] = sum;
     __syncthreads();
-    sum = s[threadIdx.x][threadIdx.y];
+    if (y >= 32) return;
+    // Eight warps, a column each.
+    const int lane = (y * 8 + threadIdx.x) & 31, column = (y * 8 + threadIdx.x) >> 5;
+    sum = s[lane][column];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const int out = blockIdx.x * 32 + threadIdx.y;
-    if (threadIdx.x == 0 && out < p.cols) store_from_float(p.dw, p.w_f32 ? kTypeF32 : type, out, sum);
+    const int out = blockIdx.x * 8 + column;
+    if (lane == 0 && out < p.cols) store_from_float(p.dw, p.w_f32 ? kTypeF32 : type, out, sum);
 }
 
 // How a row lies over threads: pieces of a thread (0: too many for registers),
@@ -312,7 +308,7 @@ cudaError_t launch_form(const NormGradParams &p, int num_sms, cudaStream_t strea
             e = launch(norm_grad_wide_kernel<TYPE, ALIGNED>, dim3((unsigned)p.rows), dim3(kMostThreads), stream, p);
     }
     if (e != cudaSuccess || !p.dw) return e;
-    return launch(norm_grad_reduce_kernel, dim3((p.cols + 31) / 32), dim3(32, 32), stream, p, TYPE);
+    return launch(norm_grad_reduce_kernel, dim3((p.cols + 7) / 8), dim3(8, 128), stream, p, TYPE);
 }
 
 }  // namespace

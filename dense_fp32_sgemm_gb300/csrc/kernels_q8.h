@@ -13,11 +13,6 @@ namespace sgemm {
 // ---------------------------------------------------------------------------
 // Rows in one pass: the norm, and rows that leave in 8 bits.
 // ---------------------------------------------------------------------------
-enum : int {
-    kRowNorm = 0,    // y = norm(a + b) * w
-    kRowNormQ8 = 1,  // its codes
-    kRowGateQ8 = 2,  // codes of act(a) * b, or of a where b is null
-};
 
 struct RowParams {
     long long rows;
@@ -38,9 +33,11 @@ struct RowParams {
     int q_vec;               // its rows start on 8 bytes (FP32: 4)
     float *scales;
 };
-// vec: rows of every matrix (and the weight) start on 16 bytes, those of q as above.
-cudaError_t launch_rows(const RowParams &p, int type, int op, bool vec, int num_sms,
+// y = norm(a + b) * w, or with q8 its codes; codes of act(a) * b, or of a where b is
+// null.  vec: rows of every matrix (and the weight) start on 16 bytes, those of q as above.
+cudaError_t launch_norm(const RowParams &p, int type, bool q8, bool vec, int num_sms,
                         cudaStream_t stream);
+cudaError_t launch_gate_q8(const RowParams &p, int type, bool vec, int num_sms, cudaStream_t stream);
 
 struct NormGradParams {
     long long rows;

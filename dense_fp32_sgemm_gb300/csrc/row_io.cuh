@@ -14,14 +14,16 @@ namespace sgemm {
 // Elements of a 16-byte piece.
 constexpr int piece_elements(int type) { return type == kTypeF32 ? 4 : 8; }
 
-// The memory of a rows x cols matrix, from which aligned pieces may be read.
-struct Matrix {
-    const char *begin, *end;
-    long long ld;  // bytes
+// A row to read.  inside: there are rows before it and after it, so that aligned pieces
+// which reach over its ends (by less than 16 bytes) stay inside the matrix.
+struct RowSource {
+    const char *row;
+    int bytes;  // of the row
+    bool inside;
 };
-__device__ __forceinline__ Matrix matrix(const void *p, long long rows, int cols, long long ld, int bytes) {
-    const char *b = static_cast<const char *>(p);
-    return {b, b + ((rows - 1) * ld + cols) * bytes, ld * bytes};
+__device__ __forceinline__ RowSource row_source(const void *p, long long row, int cols, long long ld,
+                                                int element, bool inside) {
+    return {static_cast<const char *>(p) + row * ld * element, cols * element, inside};
 }
 
 // w >> (8 * shift) over eight words, the first four of it; shift in 0 .. 15, even.
@@ -61,17 +63,19 @@ __device__ __forceinline__ uint4 pack_piece(const float (&v)[piece_elements(TYPE
                           pack16<TYPE>(v[6], v[7]));
 }
 
-// n (at least 1) elements from p on, as they lie in memory, zeros for the others up to
-// a piece.  ALIGNED: p is on 16 bytes.
+// n (at least 1) elements of a row from byte `at` (a multiple of 16) on, as they lie in
+// memory, zeros for the others up to a piece.  ALIGNED: the row is on 16 bytes.
 template <int TYPE, bool ALIGNED>
-__device__ __forceinline__ uint4 load_piece(const char *p, int n, const Matrix &m) {
+__device__ __forceinline__ uint4 load_piece(const RowSource &m, int at, int n) {
     constexpr int V = piece_elements(TYPE), E = 16 / V;
-    const int shift = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15);
-    const char *first = p - shift;
-    if (n >= V && (ALIGNED || (first >= m.begin && first + 32 <= m.end))) {
-        const uint4 a = *reinterpret_cast<const uint4 *>(first);
-        if constexpr (ALIGNED) return a;
-        return shift_pieces(a, *reinterpret_cast<const uint4 *>(first + 16), shift);
+    const char *p = m.row + at;
+    const int shift = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(m.row) & 15);
+    if (n >= V) {
+        if (ALIGNED || shift == 0) return *reinterpret_cast<const uint4 *>(p);
+        if (m.inside || (at >= shift && at - shift + 32 <= m.bytes)) {
+            const uint4 *first = reinterpret_cast<const uint4 *>(p - shift);
+            return shift_pieces(first[0], first[1], shift);
+        }
     }
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -85,23 +89,23 @@ __device__ __forceinline__ uint4 load_piece(const char *p, int n, const Matrix &
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 template <int TYPE, bool ALIGNED>
-__device__ __forceinline__ void load_values(const char *p, int n, const Matrix &m,
+__device__ __forceinline__ void load_values(const RowSource &m, int at, int n,
                                             float (&v)[piece_elements(TYPE)]) {
-    unpack_piece<TYPE>(load_piece<TYPE, ALIGNED>(p, n, m), v);
+    unpack_piece<TYPE>(load_piece<TYPE, ALIGNED>(m, at, n), v);
 }
 
 // n (at least 1) elements of the norm's weight from c on; its type is TYPE or FP32.
 template <int TYPE, bool ALIGNED>
-__device__ __forceinline__ void load_weight(const Matrix &m, bool f32, int c, int n,
+__device__ __forceinline__ void load_weight(const RowSource &m, bool f32, int c, int n,
                                             float (&v)[piece_elements(TYPE)]) {
     if constexpr (TYPE == kTypeF32) {
-        load_values<TYPE, ALIGNED>(m.begin + 4LL * c, n, m, v);
+        load_values<TYPE, ALIGNED>(m, 4 * c, n, v);
     } else if (!f32) {
-        load_values<TYPE, ALIGNED>(m.begin + 2LL * c, n, m, v);
+        load_values<TYPE, ALIGNED>(m, 2 * c, n, v);
     } else {
         float a[4], b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        load_values<kTypeF32, ALIGNED>(m.begin + 4LL * c, n, m, a);
-        if (n > 4) load_values<kTypeF32, ALIGNED>(m.begin + 4LL * c + 16, n - 4, m, b);
+        load_values<kTypeF32, ALIGNED>(m, 4 * c, n, a);
+        if (n > 4) load_values<kTypeF32, ALIGNED>(m, 4 * c + 16, n - 4, b);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             v[j] = a[j];
