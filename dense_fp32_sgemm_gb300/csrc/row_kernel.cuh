@@ -77,8 +77,8 @@ __device__ __noinline__ double gate_exact(float g, float u) {
 
 enum : int { kRowNorm, kRowNormQ8, kRowGateQ8 };  // what a row becomes
 
-constexpr int kRowThreads = 512;  // most of a row
-constexpr int kRowPieces = 4;     // most of a thread
+constexpr int kRowThreads = 1024;  // most of a row
+constexpr int kRowPieces = 2;      // most of a thread (with four the registers leave too few warps)
 
 // The larger; NaN where one is NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_kernel(const RowParams p) 
         if constexpr (kStores) {
             sum = lane < warps ? s_sum[slot + lane] : 0.0f;
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
         if constexpr (OP != kRowNorm)
             most = __reduce_max_sync(0xffffffffu, lane < warps ? s_max[slot + lane] : 0u);
@@ -394,7 +394,7 @@ template <int TYPE, int OP, int ACT, bool ALIGNED>
 cudaError_t launch_op(const RowParams &p, int num_sms, cudaStream_t stream) {
     constexpr int V = piece_elements(TYPE), kDeep = kRowPieces;
     // Threads of a row: with few rows as many as leave each one piece, else as many as
-    // hold the row in four pieces each.
+    // hold the row in two pieces each.
     const long long most = (p.cols + V - 1) / V;  // pieces
     const bool few = p.rows <= 2 * num_sms && most <= kRowThreads;
     const long long want = few ? most : (most + kDeep - 1) / kDeep;
