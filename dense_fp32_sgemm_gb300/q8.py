@@ -16,7 +16,7 @@ from torch.autograd.function import once_differentiable
 
 import dense_fp32_sgemm_gb300 as _sg
 
-from .ffn import _TYPES, _call, _empty, _matrix, _type_of
+from .ffn import _TYPES, _call, _empty, _matrix, _raw_stream, _type_of
 
 _Q8_MOST_K = 131071
 
@@ -32,18 +32,59 @@ def _vector(t, name, n, dtype, device):
     return t.data_ptr()
 
 
-def _empty_vector(n, device, stream):
-    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
-        return torch.empty(n, dtype=torch.float32, device=device)
+def _empty_vector(n, dtype, device, stream):
+    if stream is None:
+        return torch.empty(n, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=dtype, device=device)
 
 
 def _empty_codes(rows, cols, device, stream):
     """A new matrix of codes whose rows start on 16 bytes."""
-    return _empty(rows, -(-cols // 16) * 16, torch.int8, device, stream)[:, :cols]
+    shape, strides = (rows, cols), (max(-(-cols // 16) * 16, 1), 1)
+    if stream is None:
+        return torch.empty_strided(shape, strides, dtype=torch.int8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty_strided(shape, strides, dtype=torch.int8, device=device)
+
+
+# A call takes a few microseconds on the device and its checks several times as long on
+# the host (Grace, one by one: 20 us for the norm of one row, 8 without them).  So the usual
+# call, contiguous matrices of one type on the current device and its current stream, goes
+# to the library at once; all others, and all refusals, go through _matrix() and _vector().
+
+_current_device = torch._C._cuda_getDevice
+
+
+def _usual(index, dtype, shape, *tensors):
+    """Whether these (or None) are contiguous, of this type and shape, on this device."""
+    for t in tensors:
+        if t is not None and not (t.dtype is dtype and t.get_device() == index
+                                  and t.shape == shape and t.is_contiguous()):
+            return False
+    return True
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(fn, index, *args):
+    status = fn(*args, _raw_stream(index))
+    if status != 0:
+        raise _sg.SgemmError(status, fn.__name__)
+
+
+def _address(t, name, rows, cols, dtype, device):
+    """Address and leading dimension, of None too."""
+    return (None, max(cols, 1)) if t is None else _matrix(t, name, rows, cols, dtype, device)
 
 
 def _graph(*tensors):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            return torch.is_grad_enabled()
+    return False
 
 
 def _no_gradient(what, *tensors):
@@ -61,14 +102,12 @@ def _norm_args(x, weight, residual, eps, h, stream, want_h, h_name="h"):
     kind, dev = _type_of(x, "x"), x.device
     if weight.dtype is not x.dtype and weight.dtype is not torch.float32:
         raise TypeError(f"weight must be {x.dtype} or torch.float32")
-    args = (T, D, kind, *_matrix(x, "x", T, D, x.dtype, dev),
-            *((None, max(D, 1)) if residual is None
-              else _matrix(residual, "residual", T, D, x.dtype, dev)),
+    args = (T, D, kind, *_address(x, "x", T, D, x.dtype, dev),
+            *_address(residual, "residual", T, D, x.dtype, dev),
             _vector(weight, "weight", D, weight.dtype, dev), _TYPES[weight.dtype], float(eps))
     if h is None and want_h:
         h = _empty(T, D, x.dtype, dev, stream)
-    return T, D, dev, args, h, ((None, max(D, 1)) if h is None
-                                else _matrix(h, h_name, T, D, x.dtype, dev))
+    return T, D, dev, args, h, _address(h, h_name, T, D, x.dtype, dev)
 
 
 def rms_norm(x, weight, residual=None, eps: float = 1e-6, y=None, h=None, stream=None):
@@ -91,10 +130,26 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, y=None, h=None, stream
         # (the gradient runs on the stream that is current here)
         with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
             return _Norm.apply(x, weight, residual, float(eps))
+    index, dtype, shape = x.get_device(), x.dtype, x.shape
+    if (stream is None and index >= 0 and len(shape) == 2 and dtype in _TYPES
+            and _usual(index, dtype, shape, x, residual, y, h) and index == _current_device()
+            and _usual(index, weight.dtype, shape[1:], weight)
+            and (weight.dtype is dtype or weight.dtype is torch.float32)
+            and (y is None or h is None or y.data_ptr() != h.data_ptr())):
+        if y is None:
+            y = torch.empty_like(x)
+        if h is None and residual is not None:
+            h = torch.empty_like(x)
+        T, D = shape
+        ld = D or 1
+        _launch(_sg.library().sgemm_rms_norm, index, T, D, _TYPES[dtype], x.data_ptr(), ld,
+                _at(residual), ld, weight.data_ptr(), _TYPES[weight.dtype], float(eps), _at(h), ld,
+                y.data_ptr(), ld)
+        return y if residual is None else (y, h)
     T, D, dev, args, h, ha = _norm_args(x, weight, residual, eps, h, stream, residual is not None)
     if y is None:
         y = _empty(T, D, x.dtype, dev, stream)
-    ya = _matrix(y, "y", T, D, x.dtype, dev)
+    ya = _address(y, "y", T, D, x.dtype, dev)
     if h is not None and T and D and ya[0] == ha[0]:
         raise ValueError("y and h must not be the same tensor")
     _call(_sg.library().sgemm_rms_norm, dev, stream, *args, *ha, *ya)
@@ -141,20 +196,33 @@ def rms_norm_backward(dy, x, weight, residual=None, dh=None, eps: float = 1e-6, 
     and of the residual alike.  Outputs not given are allocated (dx may be dy or dh
     itself); ``need_dx`` and ``need_dw`` leave one out (None is returned in its place).
     """
+    index, dtype, shape = x.get_device(), x.dtype, x.shape
+    if (stream is None and index >= 0 and len(shape) == 2 and dtype in _TYPES
+            and _usual(index, dtype, shape, x, residual, dy, dh, dx) and index == _current_device()
+            and _usual(index, weight.dtype, shape[1:], weight, dweight)
+            and (weight.dtype is dtype or weight.dtype is torch.float32)):
+        dx = (torch.empty_like(x) if dx is None else dx) if need_dx else None
+        dweight = (torch.empty_like(weight) if dweight is None else dweight) if need_dw else None
+        T, D = shape
+        ld = D or 1
+        _launch(_sg.library().sgemm_rms_norm_backward, index, T, D, _TYPES[dtype], x.data_ptr(), ld,
+                _at(residual), ld, weight.data_ptr(), _TYPES[weight.dtype], float(eps), dy.data_ptr(), ld,
+                _at(dh), ld, _at(dx), ld, _at(dweight))
+        return dx, dweight
     T, D, dev, args, _, dha = _norm_args(x, weight, residual, eps, dh, stream, False, "dh")
-    dya = _matrix(dy, "dy", T, D, x.dtype, dev)
+    dya = _address(dy, "dy", T, D, x.dtype, dev)
     dxa, dwa = (None, max(D, 1)), None
     if not need_dx:
         dx = None
     else:
         if dx is None:
             dx = _empty(T, D, x.dtype, dev, stream)
-        dxa = _matrix(dx, "dx", T, D, x.dtype, dev)
+        dxa = _address(dx, "dx", T, D, x.dtype, dev)
     if not need_dw:
         dweight = None
     else:
         if dweight is None:
-            dweight = _empty(1, D, weight.dtype, dev, stream).view(D)
+            dweight = _empty_vector(D, weight.dtype, dev, stream)
         dwa = _vector(dweight, "dweight", D, weight.dtype, dev)
     _call(_sg.library().sgemm_rms_norm_backward, dev, stream, *args, *dya, *dha, *dxa, dwa)
     return dx, dweight
@@ -165,8 +233,8 @@ def _codes(q, scales, T, D, dev, stream):
     if q is None:
         q = _empty_codes(T, D, dev, stream)
     if scales is None:
-        scales = _empty_vector(T, dev, stream)
-    return q, scales, (*_matrix(q, "q", T, D, torch.int8, dev),
+        scales = _empty_vector(T, torch.float32, dev, stream)
+    return q, scales, (*_address(q, "q", T, D, torch.int8, dev),
                        _vector(scales, "scales", T, torch.float32, dev))
 
 
@@ -180,6 +248,21 @@ def rms_norm_q8(x, weight, residual=None, eps: float = 1e-6, h=None, q=None, sca
     through it: inputs that require one are refused.
     """
     _no_gradient("rms_norm_q8", x, weight, residual)
+    index, dtype, shape = x.get_device(), x.dtype, x.shape
+    if (stream is None and q is None and scales is None and index >= 0 and len(shape) == 2
+            and dtype in _TYPES and _usual(index, dtype, shape, x, residual, h)
+            and index == _current_device() and _usual(index, weight.dtype, shape[1:], weight)
+            and (weight.dtype is dtype or weight.dtype is torch.float32)):
+        T, D = shape
+        q, scales = _empty_codes(T, D, x.device, None), torch.empty(T, device=x.device,
+                                                                   dtype=torch.float32)
+        if h is None and residual is not None:
+            h = torch.empty_like(x)
+        ld = D or 1
+        _launch(_sg.library().sgemm_rms_norm_q8, index, T, D, _TYPES[dtype], x.data_ptr(), ld,
+                _at(residual), ld, weight.data_ptr(), _TYPES[weight.dtype], float(eps), _at(h), ld,
+                q.data_ptr(), -(-D // 16) * 16 or 1, scales.data_ptr())
+        return (q, scales) if residual is None else (q, scales, h)
     T, D, dev, args, h, ha = _norm_args(x, weight, residual, eps, h, stream, residual is not None)
     q, scales, qa = _codes(q, scales, T, D, dev, stream)
     _call(_sg.library().sgemm_rms_norm_q8, dev, stream, *args, *ha, *qa)
@@ -195,10 +278,22 @@ def gate_q8(g, u, activation: int = 0, q=None, scales=None, stream=None):
     _no_gradient("gate_q8", g, u)
     if g.dim() != 2:
         raise ValueError("g must be 2-D")
+    index, dtype, shape = g.get_device(), g.dtype, g.shape
+    if (stream is None and q is None and scales is None and index >= 0 and dtype in _TYPES
+            and u.dtype is dtype and u.get_device() == index == _current_device()
+            and u.shape == shape and g.stride(0) >= shape[1] <= u.stride(0) and shape[1] > 1
+            and g.stride(1) == 1 == u.stride(1)):
+        (T, F), ldg, ldu = shape, g.stride(0), u.stride(0)
+        q, scales = _empty_codes(T, F, g.device, None), torch.empty(T, device=g.device,
+                                                                   dtype=torch.float32)
+        _launch(_sg.library().sgemm_q8_gate, index, T, F, _TYPES[dtype], int(activation),
+                g.data_ptr(), ldg, u.data_ptr(), ldu, q.data_ptr(), -(-F // 16) * 16,
+                scales.data_ptr())
+        return q, scales
     T, F = g.shape
     dev = g.device
     kind = _type_of(g, "g")
-    ga = _matrix(g, "g", T, F, g.dtype, dev)
+    ga = _address(g, "g", T, F, g.dtype, dev)
     ua = _matrix(u, "u", T, F, g.dtype, dev)
     q, scales, qa = _codes(q, scales, T, F, dev, stream)
     _call(_sg.library().sgemm_q8_gate, dev, stream, T, F, kind, int(activation), *ga, *ua, *qa)
@@ -213,7 +308,7 @@ def rows_q8(x, q=None, scales=None, stream=None):
     T, D = x.shape
     dev = x.device
     kind = _type_of(x, "x")
-    xa = _matrix(x, "x", T, D, x.dtype, dev)
+    xa = _address(x, "x", T, D, x.dtype, dev)
     q, scales, qa = _codes(q, scales, T, D, dev, stream)
     _call(_sg.library().sgemm_q8_gate, dev, stream, T, D, kind, 0, *xa, None, max(D, 1), *qa)
     return q, scales
@@ -255,25 +350,21 @@ class Q8Matrix:
         rms_norm_q8, gate_q8 and rows_q8 return them.  The sums are exact.  Returns y
         (allocated when not given).  No gradient goes through it."""
         _no_gradient("Q8Matrix.matmul", x_scales, y)
-        M = x.shape[0]
+        M, N, K, index = x.shape[0], self.N, self.K, self._index
         if y is None:
-            y = _empty(M, self.N, self.dtype, self.device, stream)
-        if (x.shape == (M, self.K) and y.shape == (M, self.N) and x_scales.shape == (M,)
-                and x.dtype is torch.int8 and y.dtype is self.dtype
-                and x_scales.dtype is torch.float32
-                and x.get_device() == y.get_device() == x_scales.get_device() == self._index
-                and x.is_contiguous() and y.is_contiguous() and x_scales.is_contiguous()):
-            # The usual call, a few microseconds long on the device.
-            xa, ldx, sa = x.data_ptr(), max(self.K, 1), x_scales.data_ptr()
-            ya, ldy = y.data_ptr(), max(self.N, 1)
-        else:
-            if x.dim() != 2:
-                raise ValueError("x must be 2-D")
-            xa, ldx = _matrix(x, "x", M, self.K, torch.int8, self.device)
-            sa = _vector(x_scales, "x_scales", M, torch.float32, self.device)
-            ya, ldy = _matrix(y, "y", M, self.N, self.dtype, self.device)
-        _call(self._fn, self.device, stream, M, self.N, self.K, self.type, xa, ldx, sa,
-              *self._weights, ya, ldy)
+            y = _empty(M, N, self.dtype, self.device, stream)
+        if (stream is None and _usual(index, torch.int8, (M, K), x)
+                and _usual(index, self.dtype, (M, N), y)
+                and _usual(index, torch.float32, (M,), x_scales) and index == _current_device()):
+            _launch(self._fn, index, M, N, K, self.type, x.data_ptr(), K or 1, x_scales.data_ptr(),
+                    *self._weights, y.data_ptr(), N or 1)
+            return y
+        if x.dim() != 2:
+            raise ValueError("x must be 2-D")
+        xa = _address(x, "x", M, self.K, torch.int8, self.device)
+        sa = _vector(x_scales, "x_scales", M, torch.float32, self.device)
+        _call(self._fn, self.device, stream, M, self.N, self.K, self.type, *xa, sa, *self._weights,
+              *_address(y, "y", M, self.N, self.dtype, self.device))
         return y
 
 
@@ -288,7 +379,7 @@ def q8_quantize(w, stream=None) -> Q8Matrix:
     kind, dev = _type_of(w, "w"), w.device
     a = _matrix(w, "w", K, N, w.dtype, dev)
     q = _empty_codes(N, K, dev, stream)
-    scales = _empty_vector(N, dev, stream)
+    scales = _empty_vector(N, torch.float32, dev, stream)
     _call(_sg.library().sgemm_q8_quantize, dev, stream, N, K, kind, *a, q.data_ptr(),
           max(q.stride(0), K, 1), scales.data_ptr())
     return Q8Matrix(q, scales, dtype=w.dtype)
