@@ -72,6 +72,7 @@ RowParams row_params(const NormArgs &a) {
     p.w = a.weight;
     p.w_f32 = a.weight_type == SGEMM_TYPE_F32;
     p.eps = (float)a.eps;
+    p.inv_cols = 1.0f / (float)a.D;
     p.h = a.h; p.ldh = a.ldh;
     return p;
 }
@@ -101,6 +102,7 @@ sgemm_status_t sgemm_rms_norm(int64_t T, int64_t D, int type, const void *x, int
     s = op_device(&dev);
     if (s != SGEMM_OK) return s;
     RowParams p = row_params(a);
+    p.device = dev.index;
     p.y = y; p.ldy = ldy;
     return status(launch_norm(p, type, false, norm_vec(a) && rows16(y, ldy, T, type), dev.num_sms,
                               static_cast<cudaStream_t>(stream)));
@@ -121,6 +123,7 @@ sgemm_status_t sgemm_rms_norm_q8(int64_t T, int64_t D, int type, const void *x, 
     s = op_device(&dev);
     if (s != SGEMM_OK) return s;
     RowParams p = row_params(a);
+    p.device = dev.index;
     p.h_last = h && (h == x || h == residual);
     p.q = q; p.ldq = ldq;
     p.q_vec = codes_vec(q, ldq, T, type);
@@ -197,6 +200,7 @@ sgemm_status_t sgemm_q8_gate(int64_t T, int64_t F, int type, int activation, con
     p.a = g; p.lda = ldg;
     p.b = u; p.ldb = ldu;
     p.act = activation;
+    p.device = dev.index;
     p.q = q; p.ldq = ldq;
     p.q_vec = codes_vec(q, ldq, T, type);
     p.scales = scales;

@@ -53,11 +53,10 @@ __device__ __forceinline__ Raw fetch(const NormGradParams &p, long long row, int
     Raw v;
     v.x = v.r = v.dy = v.dh = make_uint4(0, 0, 0, 0);
     if (n <= 0) return v;
-    const bool inside = row > 0 && row + 1 < p.rows;
-    v.x = load_piece<TYPE, ALIGNED>(row_source(p.x, row, p.cols, p.ldx, E, inside), c * E, n);
-    v.dy = load_piece<TYPE, ALIGNED>(row_source(p.dy, row, p.cols, p.lddy, E, inside), c * E, n);
-    if (p.r) v.r = load_piece<TYPE, ALIGNED>(row_source(p.r, row, p.cols, p.ldr, E, inside), c * E, n);
-    if (with_dh) v.dh = load_piece<TYPE, ALIGNED>(row_source(p.dh, row, p.cols, p.lddh, E, inside), c * E, n);
+    v.x = load_piece<TYPE, ALIGNED>(row_source(p.x, row, p.cols, p.ldx, E, p.rows), c * E, n);
+    v.dy = load_piece<TYPE, ALIGNED>(row_source(p.dy, row, p.cols, p.lddy, E, p.rows), c * E, n);
+    if (p.r) v.r = load_piece<TYPE, ALIGNED>(row_source(p.r, row, p.cols, p.ldr, E, p.rows), c * E, n);
+    if (with_dh) v.dh = load_piece<TYPE, ALIGNED>(row_source(p.dh, row, p.cols, p.lddh, E, p.rows), c * E, n);
     return v;
 }
 // h: the sum of its parts in FP32.
@@ -94,7 +93,7 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_kernel(const NormGr
     const int warps = blockDim.x >> 5, step = blockDim.x * V;
     uint32_t *stage = reinterpret_cast<uint32_t *>(s_stage) +
                       (ALIGNED ? 0 : (group * warps + (tid >> 5)) * kStageWords);
-    const RowSource W = row_source(p.w, 0, p.cols, 0, p.w_f32 ? 4 : E, false);
+    const RowSource W = row_source(p.w, 0, p.cols, 0, p.w_f32 ? 4 : E, 1);
     asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
     float dw[NP][V];
 #pragma unroll
@@ -151,7 +150,7 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_kernel(const NormGr
                     load_weight<TYPE, ALIGNED>(W, p.w_f32, c, n, w);
                     if (!kAhead && p.dh)
                         dh_raw[i] = load_piece<TYPE, ALIGNED>(
-                            row_source(p.dh, row, p.cols, p.lddh, E, row > 0 && row + 1 < p.rows), c * E, n);
+                            row_source(p.dh, row, p.cols, p.lddh, E, p.rows), c * E, n);
                 }
                 store_piece<TYPE, ALIGNED>(static_cast<char *>(p.dx) + (row * p.lddx + c - lane * V) * E, n,
                                            make_dx<TYPE>(h[i], w, dy_raw[i], dh_raw[i], st), stage);
@@ -179,7 +178,7 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_wide_kernel(const N
     const int tid = threadIdx.x, lane = tid & 31, step = blockDim.x * V;
     uint32_t *stage = reinterpret_cast<uint32_t *>(s_stage) + (ALIGNED ? 0 : (tid >> 5) * kStageWords);
     const long long row = blockIdx.x;
-    const RowSource W = row_source(p.w, 0, p.cols, 0, p.w_f32 ? 4 : E, false);
+    const RowSource W = row_source(p.w, 0, p.cols, 0, p.w_f32 ? 4 : E, 1);
     asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
     float2 sums = make_float2(0.0f, 0.0f);
     float h[V], dy[V], w[V];

@@ -21,7 +21,7 @@ struct RowParams {
     long long lda, ldb;
     const void *w;           // the norm's weight
     int w_f32;               // it is FP32 whatever the type
-    float eps;
+    float eps, inv_cols;
     int act;
     void *h;                 // null, or receives a + b
     long long ldh;
@@ -32,6 +32,8 @@ struct RowParams {
     long long ldq;
     int q_vec;               // its rows start on 8 bytes (FP32: 4)
     float *scales;
+    int device;
+    int stages;              // (set by the launch) rows on their way
 };
 // y = norm(a + b) * w, or with q8 its codes; codes of act(a) * b, or of a where b is
 // null.  vec: rows of every matrix (and the weight) start on 16 bytes, those of q as above.

@@ -7,6 +7,7 @@
 // FP16, where the whole traffic takes 40.)
 #pragma once
 
+#include "device_common.cuh"
 #include "ops_common.cuh"
 
 namespace sgemm {
@@ -19,11 +20,12 @@ constexpr int piece_elements(int type) { return type == kTypeF32 ? 4 : 8; }
 struct RowSource {
     const char *row;
     int bytes;  // of the row
-    bool inside;
+    bool first, inside;
 };
 __device__ __forceinline__ RowSource row_source(const void *p, long long row, int cols, long long ld,
-                                                int element, bool inside) {
-    return {static_cast<const char *>(p) + row * ld * element, cols * element, inside};
+                                                int element, long long rows) {
+    return {static_cast<const char *>(p) + row * ld * element, cols * element, row == 0,
+            row > 0 && row + 1 < rows};
 }
 
 // w >> (8 * shift) over eight words, the first four of it; shift in 0 .. 15, even.
@@ -88,6 +90,37 @@ __device__ __forceinline__ uint4 load_piece(const RowSource &m, int at, int n) {
         }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
+// Bytes of shared memory for a piece on its way: the aligned pieces that cover it.
+constexpr int piece_slots(bool aligned) { return aligned ? 1 : 2; }
+
+// Starts copying what covers a row's piece (from byte `at` on, a multiple of 16 below the
+// row's length) into `slot` and, for rows off 16 bytes, slot[pitch]; zeros behind the row's
+// end.  Only the matrix's first piece cannot be had this way, when the row before
+// it is not there: take_piece() loads it.
+template <bool ALIGNED>
+__device__ __forceinline__ void start_piece(uint4 *slot, int pitch, const RowSource &m, int at) {
+    const int shift = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(m.row) & 15);
+    const int left = m.bytes - at + shift;
+    const char *first = m.row + at - shift;
+    if (!ALIGNED && m.first && at < shift) return;
+    cp_async16(reinterpret_cast<float *>(slot), reinterpret_cast<const float *>(first), min(16, left));
+    if (!ALIGNED && shift)
+        cp_async16(reinterpret_cast<float *>(slot + pitch),
+                   reinterpret_cast<const float *>(left > 16 ? first + 16 : first),
+                   max(0, min(16, left - 16)));
+}
+template <int TYPE, bool ALIGNED>
+__device__ __forceinline__ uint4 take_piece(const uint4 *slot, int pitch, const RowSource &m, int at) {
+    if constexpr (ALIGNED) {
+        return *slot;
+    } else {
+        const int shift = (int)(reinterpret_cast<uintptr_t>(m.row) & 15);
+        if (shift == 0) return *slot;
+        if (m.first && at < shift) return load_piece<TYPE, false>(m, at, (m.bytes - at) / (16 / piece_elements(TYPE)));
+        return shift_pieces(slot[0], slot[pitch], shift);
+    }
+}
+
 template <int TYPE, bool ALIGNED>
 __device__ __forceinline__ void load_values(const RowSource &m, int at, int n,
                                             float (&v)[piece_elements(TYPE)]) {

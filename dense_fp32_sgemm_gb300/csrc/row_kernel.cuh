@@ -8,6 +8,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 
 #include "kernels_q8.h"
 #include "row_codes.cuh"
@@ -23,22 +24,22 @@ constexpr double kGeluC2 = 2.0 * 0.79788456080286535588;  // 2 sqrt(2 / pi)
 // What gate_value() gathers over a thread's elements.
 struct GateSpread {
     float mass = 0.0f;             // of the exponent's rounding (GELU)
-    float lowest = 0.0f;           // z
-    float largest = 0.0f;          // |g u|
-    // Beyond z = -80 the exponential leaves FP32.  An element there matters from |g u| =
-    // 100 on: below, its magnitude is under 2^-108 and its code zero whatever it is.
-    __device__ __forceinline__ bool far() const { return lowest < -80.0f && largest >= 100.0f; }
+    float lowest = 0.0f;           // z; beyond -80 the exponential leaves FP32
 };
 
 // act(g) u with act(g) = g / (1 + exp(-z)), off by at most 2^-20.5 of itself and 2^-21 of
 // `mass` (GELU's z is a rounded value: what it is off by counts as far as the
 // exponential does).
 template <int ACT>
+__device__ __forceinline__ float gate_z(float g) {
+    return ACT == kGateSilu ? g : (float)kGeluC2 * fmaf(0.044715f * g * g, g, g);
+}
+template <int ACT>
 __device__ __forceinline__ float gate_value(float g, float u, GateSpread &s) {
     if constexpr (ACT == kGateRelu) return (g > 0.0f ? g : (g != g ? g : 0.0f)) * u;
     const float gu = g * u;
-    const float z = ACT == kGateSilu ? g : (float)kGeluC2 * fmaf(0.044715f * g * g, g, g);
-    const float x = fminf(fmaxf(z, -80.0f), 100.0f);
+    const float z = gate_z<ACT>(g);
+    const float x = fmaxf(z, -80.0f);  // (infinite g: a is not finite either way)
     // exp(-x) = 2^t 2^c: c is what t lost in rounding.
     constexpr float kL = 1.4426950408889634f;
     constexpr float kLRest = (float)(1.4426950408889634074 - (double)kL);
@@ -50,7 +51,6 @@ __device__ __forceinline__ float gate_value(float g, float u, GateSpread &s) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     const float a = gu * r;
     s.lowest = fminf(s.lowest, z);
-    s.largest = fmaxf(s.largest, fabsf(gu));
     if constexpr (ACT == kGateGelu) s.mass = fmaxf(s.mass, fabsf(a * x) * (e * r));
     return a;
 }
@@ -77,8 +77,17 @@ __device__ __noinline__ double gate_exact(float g, float u) {
 
 enum : int { kRowNorm, kRowNormQ8, kRowGateQ8 };  // what a row becomes
 
-constexpr int kRowThreads = 1024;  // most of a row
-constexpr int kRowPieces = 2;      // most of a thread (with four the registers leave too few warps)
+// A thread's pieces of a row and its registers.  The norm takes two pieces (of 8192 x 8191
+// FP16 108 us, with four 135: fewer warps); what leaves in 8 bits, whose threads have more to
+// do for every row, four (the gate of 4096 x 12288 96 us, with two, which leave one CTA of
+// 768 threads an SM, 132).
+constexpr int row_pieces(int op) { return op == kRowNorm ? 2 : 4; }
+constexpr int row_threads(int op) { return op == kRowNorm ? 1024 : 512; }  // most of a row
+constexpr int row_regs(int op, int act, bool aligned) {
+    return op == kRowNorm ? 64 : act >= 0 && !aligned ? 88 : 80;
+}
+constexpr int kMaxDevices = 64;
+constexpr int kRingBytes = 192 * 1024;  // of an SM, for rows on their way
 
 // The larger; NaN where one is NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -86,61 +95,61 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
-// A positive double of FP32's range, cut to FP32 (a conversion would go through the
-// FP64 pipe, for every thread).
-__device__ __forceinline__ float cut_to_float(unsigned long long bits) {
-    return __uint_as_float((unsigned)(bits >> 29) - ((1023u - 127u) << 23));
-}
-
 // NP: pieces of a thread, a row in registers.  KEEP false: a row has more than
 // that, and is read again.  ACT: the gate's, or -1: plain rows.
 template <int TYPE, int OP, int ACT, int NP, bool KEEP, bool ALIGNED>
-__global__ void __launch_bounds__(kRowThreads, 1) row_kernel(const RowParams p) {
+__global__ void __maxnreg__(row_regs(OP, ACT, ALIGNED)) row_kernel(const RowParams p) {
     constexpr int V = piece_elements(TYPE), E = 16 / V;
     constexpr bool kGate = OP == kRowGateQ8 && ACT >= 0, kPlain = OP == kRowGateQ8 && ACT < 0;
     constexpr bool kStores = OP != kRowGateQ8;  // matrices of TYPE
-    __shared__ float s_sum[kRowThreads / 32];
-    __shared__ unsigned s_max[kRowThreads / 32];
-    __shared__ unsigned long long s_top[kRowThreads / 32];
-    __shared__ uint4 s_stage[ALIGNED || !kStores ? 1 : kRowThreads / 32 * kStageWords / 4];
+    // Alternating from row to row, so that a row's readers are done when they are written again.
+    constexpr int kWarps = row_threads(OP) / 32;
+    __shared__ float s_sum[2][kWarps];
+    __shared__ unsigned s_max[2][kWarps], s_mass[2][kWarps];
+    __shared__ unsigned long long s_top[3][kWarps];
+    __shared__ float s_scale[3][kWarps];
+    __shared__ uint4 s_stage[ALIGNED || !kStores ? 1 : kWarps * kStageWords / 4];
     const int tid = threadIdx.x, lane = tid & 31;
     const int group = threadIdx.y, warps = blockDim.x >> 5;
     uint32_t *stage = reinterpret_cast<uint32_t *>(s_stage) +
                       (ALIGNED || !kStores ? 0 : (group * warps + (tid >> 5)) * kStageWords);
-    const long long row = (long long)blockIdx.x * blockDim.y + group;
-    const bool live = row < p.rows;
-    const int step = blockDim.x * V, cols = live ? p.cols : 0;
+    const int step = blockDim.x * V;
     const bool two = kGate || (!kPlain && p.b != nullptr);
-    // Rows that are neither the first nor the last may be read in pieces that reach
-    // over their ends.
-    const bool inside = row > 0 && row + 1 < p.rows;
-    const RowSource A = row_source(p.a, row, p.cols, p.lda, E, inside);
-    const RowSource B = row_source(p.b, row, p.cols, p.ldb, E, inside);
-    const RowSource W = row_source(p.w, 0, p.cols, 0, p.w_f32 ? 4 : E, false);
+    const RowSource W = row_source(p.w, 0, p.cols, 0, p.w_f32 ? 4 : E, 1);
+    const unsigned rows = (unsigned)p.rows, stride = gridDim.x * blockDim.y;
+    unsigned row = blockIdx.x * blockDim.y + group;  // at work on
+    int cols = 0;  // of it: none behind the last row
+    // (made anew where they are used: they would hold registers all along)
+    auto A = [&](unsigned r) { return row_source(p.a, r, p.cols, p.lda, E, p.rows); };
+    auto B = [&](unsigned r) { return row_source(p.b, r, p.cols, p.ldb, E, p.rows); };
 
-    if (tid == 0) s_top[group] = 0;
+    if (tid == 0) s_top[0][group] = s_top[1][group] = 0;
     asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
 
     // Of the thread's elements: h of the norm; what is coded.
     float keep[NP][V];
-    float sum = 0.0f, largest = 0.0f;  // of squares; |what is coded|, NaN where one is
+    float sum, largest;  // of squares; |what is coded|, NaN where one is
     GateSpread spread;
 
+    auto go_to = [&](unsigned r) {
+        row = r;
+        cols = r < rows ? p.cols : 0;
+    };
     auto exact = [&](int c) -> double {
-        const float a = load_as_float(A.row, TYPE, c);
+        const float a = load_as_float(A(row).row, TYPE, c);
         if constexpr (kPlain) {
             return a;
         } else if constexpr (kGate) {
-            return gate_exact<ACT>(a, load_as_float(B.row, TYPE, c));
+            return gate_exact<ACT>(a, load_as_float(B(row).row, TYPE, c));
         } else {
-            const double h = two ? (double)a + (double)load_as_float(B.row, TYPE, c) : (double)a;
+            const double h = two ? (double)a + (double)load_as_float(B(row).row, TYPE, c) : (double)a;
             return h * (double)load_as_float(p.w, p.w_f32 ? kTypeF32 : TYPE, c);
         }
     };
     // A piece (n > 0 elements from c on) as it comes from memory; what of it is kept.
     auto fetch = [&](int c, int n, uint4 &x, uint4 &y) {
-        x = load_piece<TYPE, ALIGNED>(A, c * E, n);
-        if (two) y = load_piece<TYPE, ALIGNED>(B, c * E, n);
+        x = load_piece<TYPE, ALIGNED>(A(row), c * E, n);
+        if (two) y = load_piece<TYPE, ALIGNED>(B(row), c * E, n);
     };
     auto take = [&](uint4 x, uint4 y, float (&v)[V]) {
         unpack_piece<TYPE>(x, v);
@@ -173,26 +182,91 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_kernel(const RowParams p) 
     };
     auto put = [&](void *to, long long ld, int c, int n, const float (&v)[V]) {
         // The address of lane 0's piece.
-        char *at = static_cast<char *>(to) + (row * ld + c - lane * V) * E;
+        char *at = static_cast<char *>(to) + ((long long)row * ld + c - lane * V) * E;
         store_piece<TYPE, ALIGNED>(at, n, pack_piece<TYPE>(v), stage);
     };
     // h over x or the residual would take from exact() what it reads: then it is stored last.
-    const bool early = KEEP && !p.h_last;
+    const bool early = KEEP && (OP == kRowNorm || !p.h_last);
 
-    if constexpr (KEEP) {
-        uint4 x[NP], y[NP];
-        // All loads before the first use.
+    // In registers: the pieces of the next rows are on their way, a thread's own into its own
+    // places of a ring, so that nobody has to wait for another's.
+    extern __shared__ uint4 s_ring[];
+    constexpr int kSlots = piece_slots(ALIGNED);
+    const int pitch = blockDim.x * blockDim.y, arrays = two ? 2 : 1;
+    auto slot = [&](int stage_of, int array, int i) {
+        return s_ring + (((stage_of * arrays + array) * NP + i) * kSlots) * pitch + group * blockDim.x + tid;
+    };
+    auto start = [&](unsigned r, int stage_of) {
+        if (r < rows) {
+            const RowSource a = A(r), b = B(r);
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int c = tid * V + i * step, n = cols - c;
-            x[i] = y[i] = make_uint4(0, 0, 0, 0);
-            if (n > 0) fetch(c, n, x[i], y[i]);
+            for (int i = 0; i < NP; ++i) {
+                const int c = tid * V + i * step;
+                if (c < p.cols) {
+                    start_piece<ALIGNED>(slot(stage_of, 0, i), pitch, a, c * E);
+                    if (two) start_piece<ALIGNED>(slot(stage_of, 1, i), pitch, b, c * E);
+                }
+            }
         }
+        cp_async_commit();
+    };
+    const unsigned first = row;
+    int ring = 0;
+    if constexpr (KEEP)
+        for (int s = 0; s < p.stages; ++s) start(first + s * stride, s);
+    static_assert(NP * V <= 32, "");
+    // The column of the thread's i-th element in registers.
+    auto element = [&](int i) { return tid * V + i / V * step + i % V; };
+    // Calls f(c) for each of the thread's elements.
+    auto each = [&](auto &&f) {
+        for (int c = tid * V; c < cols; c += step)
+            for (int j = 0; j < min(V, cols - c); ++j) f(c + j);
+    };
+    // What is left to do for a row whose codes are stored: those in doubt (of the thread's
+    // elements in registers; `all`: every element) and the scale.
+    unsigned doubt = 0;
+    bool all = false;
+    auto decide = [&](int c, int turn_of) {
+        const double top = fmax(__longlong_as_double((long long)s_top[turn_of][group]), (double)kRowTiny);
+        p.q[(long long)row * p.ldq + c] = (int8_t)row_code_exact(exact(c), top, 127.0f / (float)top);
+    };
+    auto finish = [&](unsigned r, int turn_of) {
+        if (doubt || all || tid == 0) {
+            const unsigned now = row;
+            const int cols_now = cols;
+            go_to(r);
+            for (; doubt; doubt &= doubt - 1) decide(element(__ffs(doubt) - 1), turn_of);
+            if (all) each([&](int c) { decide(c, turn_of); });
+            all = false;
+            if (tid == 0 && r < rows)
+                p.scales[r] = fmaxf((float)__longlong_as_double((long long)s_top[turn_of][group]), kRowTiny) *
+                              s_scale[turn_of][group];
+            row = now;
+            cols = cols_now;
+        }
+    };
+    int turn = 0;
+    bool flip = false, begun = false;
+    unsigned at = first;
+    for (; at - group < rows; at += stride, flip = !flip) {
+    go_to(at);
+    sum = largest = 0.0f;
+    spread = GateSpread();
+    if constexpr (KEEP) {
+        // All but the last stages - 1 rows' copies have landed.
+        if (p.stages == 1) cp_async_wait<0>();
+        else if (p.stages == 2) cp_async_wait<1>();
+        else cp_async_wait<2>();
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int c = tid * V + i * step, n = cols - c;
             if (c - lane * V < cols) {  // (the whole warp, for put())
-                take(x[i], y[i], keep[i]);
+                uint4 x = make_uint4(0, 0, 0, 0), y = x;
+                if (n > 0) {
+                    x = take_piece<TYPE, ALIGNED>(slot(ring, 0, i), pitch, A(row), c * E);
+                    if (two) y = take_piece<TYPE, ALIGNED>(slot(ring, 1, i), pitch, B(row), c * E);
+                }
+                take(x, y, keep[i]);
                 if constexpr (kStores) {
                     square(keep[i]);
                     if (p.h && early) put(p.h, p.ldh, c, n, keep[i]);
@@ -204,6 +278,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_kernel(const RowParams p) 
                 for (int j = 0; j < V; ++j) keep[i][j] = 0.0f;
             }
         }
+        start(at + p.stages * stride, ring);
+        if (++ring == p.stages) ring = 0;
     } else {
         for (int c = tid * V; c < cols; c += step) {
             uint4 x, y = make_uint4(0, 0, 0, 0);
@@ -214,19 +290,19 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_kernel(const RowParams p) 
             if constexpr (OP != kRowNorm) compare(keep[0]);
         }
     }
-    static_assert(NP * V <= 32, "");
-    // The column of the thread's i-th element in registers.
-    auto element = [&](int i) { return tid * V + i / V * step + i % V; };
-    // Calls f(c) for each of the thread's elements.
-    auto each = [&](auto &&f) {
-        for (int c = tid * V; c < cols; c += step)
-            for (int j = 0; j < min(V, cols - c); ++j) f(c + j);
-    };
-    const bool far = kGate && spread.far();
+    bool far = false;
     if constexpr (kGate) {
-        if (far && largest == largest) {
-            largest = 0.0f;
-            each([&](int c) { largest = max_nan(largest, (float)fabs(exact(c))); });
+        // An element beyond z = -80 matters from |g u| = 100 on: below, its magnitude is under
+        // 2^-108 and its code zero whatever it is.
+        if (ACT != kGateRelu && spread.lowest < -80.0f && largest == largest) {
+            each([&](int c) {
+                const float g = load_as_float(A(row).row, TYPE, c), u = load_as_float(B(row).row, TYPE, c);
+                far = far || (gate_z<ACT>(g) < -80.0f && !(fabsf(g * u) < 100.0f));
+            });
+            if (far) {
+                largest = 0.0f;
+                each([&](int c) { largest = max_nan(largest, (float)fabs(exact(c))); });
+            }
         }
     }
 
@@ -237,23 +313,27 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_kernel(const RowParams p) 
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
     if constexpr (OP != kRowNorm) most = __reduce_max_sync(0xffffffffu, most);
+    unsigned mass = __float_as_uint(spread.mass);
+    if constexpr (ACT == kGateGelu) mass = __reduce_max_sync(0xffffffffu, mass);
     if (OP != kRowNorm || warps > 1) {
         const int slot = group * warps;
         if (lane == 0) {
-            s_sum[slot + (tid >> 5)] = sum;
-            s_max[slot + (tid >> 5)] = most;
+            s_sum[flip][slot + (tid >> 5)] = sum;
+            s_max[flip][slot + (tid >> 5)] = most;
+            if constexpr (ACT == kGateGelu) s_mass[flip][slot + (tid >> 5)] = mass;
         }
         __syncthreads();
         if constexpr (kStores) {
-            sum = lane < warps ? s_sum[slot + lane] : 0.0f;
+            sum = lane < warps ? s_sum[flip][slot + lane] : 0.0f;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
         if constexpr (OP != kRowNorm)
-            most = __reduce_max_sync(0xffffffffu, lane < warps ? s_max[slot + lane] : 0u);
+            most = __reduce_max_sync(0xffffffffu, lane < warps ? s_max[flip][slot + lane] : 0u);
+        if constexpr (ACT == kGateGelu)
+            mass = __reduce_max_sync(0xffffffffu, lane < warps ? s_mass[flip][slot + lane] : 0u);
     }
-    if constexpr (kStores) sum = __shfl_sync(0xffffffffu, sum, 0);
-    const float rstd = kStores ? 1.0f / sqrtf(sum / (float)p.cols + p.eps) : 1.0f;
+    const float rstd = kStores ? rsqrtf(fmaf(sum, p.inv_cols, p.eps)) : 1.0f;
 
     // Calls f(c, n, values, number) for each piece of the row, with the whole warp.
     auto pieces = [&](auto &&f) {
@@ -280,59 +360,61 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_kernel(const RowParams p) 
             if (n > 0) load_weight<TYPE, ALIGNED>(W, p.w_f32, c, n, w);
 #pragma unroll
             for (int j = 0; j < V; ++j) y[j] = n > 0 ? v[j] * rstd * w[j] : 0.0f;
-            if (p.h && !early) put(p.h, p.ldh, c, n, v);
+            if (!KEEP && p.h) put(p.h, p.ldh, c, n, v);
             put(p.y, p.ldy, c, n, y);
         });
     } else {
+        // Nobody reads what the row before the last one left any more.
+        const int next_turn = turn == 2 ? 0 : turn + 1;
+        if (tid == 0) s_top[next_turn][group] = 0;
+        const bool later = KEEP && !p.h_last;  // what is left of a row is done with the next one
+        if (later && begun) finish(at - stride, turn == 0 ? 2 : turn - 1);
+        begun = true;
         const bool bad = most >= 0x7F800000u;
-        const float top32 = fmaxf(__uint_as_float(most), kRowTiny);
-        // The largest magnitude in more bits, among those that FP32 cannot tell
-        // from it (plain rows are exact as they are).
-        float top = top32;
-        if constexpr (!kPlain) {
-            const float limit = top32 * (1.0f - 0x1p-12f);
-            if (!bad && largest >= limit) {
-                auto raise = [&](int c) {
-                    atomicMax(&s_top[group], (unsigned long long)__double_as_longlong(fabs(exact(c))));
-                };
-                if (far) {
-                    each(raise);
-                } else if constexpr (KEEP) {
-                    unsigned mask = 0;
+        const float top = fmaxf(__uint_as_float(most), kRowTiny);
+        const float inv = bad ? 0.0f : 127.0f / top;
+        all = far && !bad;
+        if (tid == 0) s_scale[turn][group] = bad ? __int_as_float(0x7FC00000) : rstd / 127.0f;
+        // The largest magnitude in more bits, among those that FP32 cannot tell from it.
+        const float limit = top * (1.0f - 0x1p-12f);
+        auto refine = [&]() {
+            if (bad || !(largest >= limit)) return;
+            auto raise = [&](int c) {
+                atomicMax(&s_top[turn][group],
+                          (unsigned long long)__double_as_longlong(fabs(exact(c))));
+            };
+            if (far) {
+                each(raise);
+            } else if constexpr (KEEP) {
+                unsigned mask = 0;
 #pragma unroll
-                    for (int i = 0; i < NP; ++i)
+                for (int i = 0; i < NP; ++i)
 #pragma unroll
-                        for (int j = 0; j < V; ++j)
-                            mask |= (unsigned)(fabsf(keep[i][j]) >= limit) << (i * V + j);
-                    for (; mask; mask &= mask - 1) raise(element(__ffs(mask) - 1));
-                } else {
-                    for (int c = tid * V; c < cols; c += step) {
-                        uint4 x, y = make_uint4(0, 0, 0, 0);
-                        fetch(c, cols - c, x, y);
-                        take(x, y, keep[0]);
-                        if constexpr (OP == kRowNormQ8) weigh(c, cols - c, keep[0]);
+                    for (int j = 0; j < V; ++j)
+                        mask |= (unsigned)(fabsf(keep[i][j]) >= limit) << (i * V + j);
+                for (; mask; mask &= mask - 1) raise(element(__ffs(mask) - 1));
+            } else {
+                for (int c = tid * V; c < cols; c += step) {
+                    uint4 x, y = make_uint4(0, 0, 0, 0);
+                    fetch(c, cols - c, x, y);
+                    take(x, y, keep[0]);
+                    if constexpr (OP == kRowNormQ8) weigh(c, cols - c, keep[0]);
 #pragma unroll
-                        for (int j = 0; j < V; ++j)
-                            if (fabsf(keep[0][j]) >= limit) raise(c + j);
-                    }
+                    for (int j = 0; j < V; ++j)
+                        if (fabsf(keep[0][j]) >= limit) raise(c + j);
                 }
             }
+        };
+        if constexpr (!KEEP) {
+            refine();
             __syncthreads();
-            const unsigned long long bits = s_top[group];
-            if (bits > (unsigned long long)(1023 - 96) << 52) top = cut_to_float(bits);
         }
-        auto exact_top = [&]() {
-            return kPlain ? (double)top
-                          : fmax(__longlong_as_double((long long)s_top[group]), (double)kRowTiny);
-        };
-        const float inv = bad ? 0.0f : 127.0f / top;
-        // Nearer than this to the middle between two codes FP32 does not decide.
-        float border = 0.5f - 127.0f * 0x1p-20f;
-        if constexpr (kGate) border -= fminf(spread.mass * inv, 1e4f) * 0x1p-21f;
-        unsigned doubt = 0;  // of the thread's elements
-        auto decide = [&](int c) {
-            p.q[row * p.ldq + c] = (int8_t)row_code_exact(exact(c), exact_top(), inv);
-        };
+        // What FP32 does not decide: a quotient nearer to the middle between two codes than it
+        // is off itself, kOff of it for a and top (in the gate 2^-20.5 each, two roundings
+        // each in the norm) and, in GELU, twice what the exponents are off.
+        constexpr float kOff = kGate ? 0x1p-19f : 0x1p-21f;
+        float border = 0.5f - 0x1p-19f;
+        if constexpr (ACT == kGateGelu) border -= fminf(__uint_as_float(mass) * inv, 1e4f) * 0x1p-20f;
         pieces([&](int c, int n, float (&v)[V], int number) {
             if (n <= 0) return;
             // v inv + 1.5 2^23 is rounded to a whole number, ties to even, whose low byte is
@@ -340,18 +422,19 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_kernel(const RowParams p) 
             constexpr float kWhole = 12582912.0f;
             uint32_t r[V], word[V / 4];
             float widest = 0.0f;
+            auto doubt_of = [&](int j, uint32_t &bits) {
+                const float q = fmaf(v[j], inv, kWhole), k = kWhole - q;
+                bits = __float_as_uint(q);
+                return fmaf(fabsf(k), kOff, fabsf(fmaf(v[j], inv, k)));
+            };
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float q = fmaf(v[j], inv, kWhole);
-                r[j] = __float_as_uint(q);
-                widest = fmaxf(widest, fabsf(fmaf(v[j], inv, kWhole - q)));
-            }
+            for (int j = 0; j < V; ++j) widest = fmaxf(widest, doubt_of(j, r[j]));
 #pragma unroll
             for (int k = 0; k < V / 4; ++k)
                 word[k] = bad ? 0u
                               : __byte_perm(__byte_perm(r[4 * k], r[4 * k + 1], 0x0040),
                                             __byte_perm(r[4 * k + 2], r[4 * k + 3], 0x0040), 0x5410);
-            int8_t *out = p.q + row * p.ldq + c;
+            int8_t *out = p.q + (long long)row * p.ldq + c;
             if (n >= V && (ALIGNED || p.q_vec)) {
                 if constexpr (V == 8)
                     *reinterpret_cast<uint2 *>(out) = make_uint2(word[0], word[V / 4 - 1]);
@@ -366,45 +449,56 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_kernel(const RowParams p) 
                 unsigned mask = 0;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float q = fmaf(v[j], inv, kWhole);
-                    mask |= (unsigned)(j < n && fabsf(fmaf(v[j], inv, kWhole - q)) > border) << j;
+                    uint32_t bits;
+                    mask |= (unsigned)(j < n && doubt_of(j, bits) > border) << j;
                 }
                 if constexpr (KEEP)
                     doubt |= mask << (number * V);
                 else
-                    for (; mask; mask &= mask - 1) decide(c + __ffs(mask) - 1);
+                    for (; mask; mask &= mask - 1) decide(c + __ffs(mask) - 1, turn);
             }
         });
-        for (; doubt; doubt &= doubt - 1) decide(element(__ffs(doubt) - 1));
-        if (far && !bad) each([&](int c) { decide(c); });
-        if (OP == kRowNormQ8 && p.h && !early)
-            for (int c = tid * V; c - lane * V < cols; c += step) {
-                uint4 x = make_uint4(0, 0, 0, 0), y = x;
-                float v[V];
-                if (c < cols) fetch(c, cols - c, x, y);
-                take(x, y, v);
-                put(p.h, p.ldh, c, cols - c, v);
-            }
-        if (tid == 0 && live)
-            p.scales[row] = bad ? __int_as_float(0x7FC00000) : (float)exact_top() * rstd / 127.0f;
+        if constexpr (KEEP) refine();
+        // Decided when all of the row's threads have refined its largest magnitude: after the
+        // next row's barrier, or (h over what decide() reads) one of its own.
+        if (!later) {
+            if constexpr (KEEP) __syncthreads();
+            finish(at, turn);
+            if (OP == kRowNormQ8 && p.h)
+                for (int c = tid * V; c - lane * V < cols; c += step) {
+                    uint4 x = make_uint4(0, 0, 0, 0), y = x;
+                    float v[V];
+                    if (c < cols) fetch(c, cols - c, x, y);
+                    take(x, y, v);
+                    put(p.h, p.ldh, c, cols - c, v);
+                }
+        }
+        turn = next_turn;
+    }
+    }
+    if (OP != kRowNorm && KEEP && !p.h_last) {
+        __syncthreads();
+        if (begun) finish(at - stride, turn == 0 ? 2 : turn - 1);
     }
 }
 
 template <int TYPE, int OP, int ACT, bool ALIGNED>
 cudaError_t launch_op(const RowParams &p, int num_sms, cudaStream_t stream) {
-    constexpr int V = piece_elements(TYPE), kDeep = kRowPieces;
+    constexpr int V = piece_elements(TYPE), kDeep = row_pieces(OP);
     // Threads of a row: with few rows as many as leave each one piece, else as many as
-    // hold the row in two pieces each.
+    // hold the row in registers.
     const long long most = (p.cols + V - 1) / V;  // pieces
-    const bool few = p.rows <= 2 * num_sms && most <= kRowThreads;
+    const bool few = p.rows <= 2 * num_sms && most <= row_threads(OP);
     const long long want = few ? most : (most + kDeep - 1) / kDeep;
     int threads = 32;
     while (threads < want && threads < 128) threads *= 2;
-    if (threads < want) threads = (int)std::min<long long>((want + 31) / 32 * 32, kRowThreads);
+    if (threads < want) threads = (int)std::min<long long>((want + 31) / 32 * 32, row_threads(OP));
     const int groups = threads >= 128 ? 1 : 128 / threads;
     const bool fits = (long long)threads * (few ? 1 : kDeep) >= most;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.rows + groups - 1) / groups));
+    // As many CTAs as the SMs hold at once, each taking rows in turn.
+    const int per_sm = std::max(1, 65536 / row_regs(OP, ACT, ALIGNED) / (threads * groups));
+    cfg.gridDim = dim3((unsigned)std::min<long long>((p.rows + groups - 1) / groups, (long long)num_sms * per_sm));
     cfg.blockDim = dim3(threads, groups);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -412,9 +506,23 @@ cudaError_t launch_op(const RowParams &p, int num_sms, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (!fits) return cudaLaunchKernelEx(&cfg, row_kernel<TYPE, OP, ACT, 1, false, ALIGNED>, p);
-    if (few) return cudaLaunchKernelEx(&cfg, row_kernel<TYPE, OP, ACT, 1, true, ALIGNED>, p);
-    return cudaLaunchKernelEx(&cfg, row_kernel<TYPE, OP, ACT, kDeep, true, ALIGNED>, p);
+    // A ring of up to three rows' pieces in what shared memory the SM has for so many threads.
+    RowParams q = p;
+    const int bytes = (OP == kRowGateQ8 ? (ACT >= 0 ? 2 : 1) : p.b ? 2 : 1) * (few ? 1 : kDeep) *
+                      piece_slots(ALIGNED) * 16 * threads * groups;
+    q.stages = std::max(1, std::min(3, kRingBytes / (bytes * per_sm)));
+    if (!fits) return cudaLaunchKernelEx(&cfg, row_kernel<TYPE, OP, ACT, 1, false, ALIGNED>, q);
+    cfg.dynamicSmemBytes = (size_t)bytes * q.stages;
+    const auto kernel = few ? row_kernel<TYPE, OP, ACT, 1, true, ALIGNED> : row_kernel<TYPE, OP, ACT, kDeep, true, ALIGNED>;
+    static std::atomic<bool> configured[kMaxDevices][2];
+    if (p.device >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!configured[p.device][few].load()) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+        if (e != cudaSuccess) return e;
+        configured[p.device][few].store(true);
+    }
+    return cudaLaunchKernelEx(&cfg, kernel, q);
 }
 
 // For one of the library's types and alignments.

@@ -50,23 +50,45 @@ def _empty_codes(rows, cols, device, stream):
 
 # A call takes a few microseconds on the device and its checks several times as long on
 # the host (Grace, one by one: 20 us for the norm of one row, 8 without them).  So the usual
-# call, contiguous matrices of one type on the current device and its current stream, goes
-# to the library at once; all others, and all refusals, go through _matrix() and _vector().
+# call, matrices of one type on the current device and its current stream, goes to the
+# library at once; all others, and all refusals, go through _matrix() and _vector().
 
 _current_device = torch._C._cuda_getDevice
 
 
-def _usual(index, dtype, shape, *tensors):
-    """Whether these (or None) are contiguous, of this type and shape, on this device."""
+def _rows(index, dtype, shape, *tensors):
+    """Addresses and leading dimensions of matrices (or None) of this type and shape on this
+    device; None where one of them is not."""
+    args = []
+    D = shape[1]
     for t in tensors:
-        if t is not None and not (t.dtype is dtype and t.get_device() == index
-                                  and t.shape == shape and t.is_contiguous()):
-            return False
-    return True
+        if t is None:
+            args += (None, D or 1)
+            continue
+        if t.dtype is not dtype or t.get_device() != index or t.shape != shape:
+            return None
+        if t.is_contiguous():
+            args += (t.data_ptr(), D or 1)
+        else:
+            step, unit = t.stride()
+            if unit != 1 or step < D or D < 2 or shape[0] < 2:
+                return None
+            args += (t.data_ptr(), step)
+    return args
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
+def _plain(index, dtype, n, t):
+    """Whether t is a contiguous vector of n elements of this type on this device."""
+    return (t.dtype is dtype and t.get_device() == index and t.dim() == 1 and t.numel() == n
+            and t.is_contiguous())
+
+
+def _norm_usual(x, weight, stream):
+    """Whether a norm of x can take the short way, as far as these say."""
+    index, shape = x.get_device(), x.shape
+    return (stream is None and index >= 0 and len(shape) == 2 and x.dtype in _TYPES
+            and index == _current_device() and _plain(index, weight.dtype, shape[1], weight)
+            and (weight.dtype is x.dtype or weight.dtype is torch.float32))
 
 
 def _launch(fn, index, *args):
@@ -130,22 +152,17 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, y=None, h=None, stream
         # (the gradient runs on the stream that is current here)
         with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
             return _Norm.apply(x, weight, residual, float(eps))
-    index, dtype, shape = x.get_device(), x.dtype, x.shape
-    if (stream is None and index >= 0 and len(shape) == 2 and dtype in _TYPES
-            and _usual(index, dtype, shape, x, residual, y, h) and index == _current_device()
-            and _usual(index, weight.dtype, shape[1:], weight)
-            and (weight.dtype is dtype or weight.dtype is torch.float32)
-            and (y is None or h is None or y.data_ptr() != h.data_ptr())):
+    if _norm_usual(x, weight, stream):
+        index, dtype, shape = x.get_device(), x.dtype, x.shape
         if y is None:
-            y = torch.empty_like(x)
+            y = torch.empty(shape, dtype=dtype, device=x.device)
         if h is None and residual is not None:
-            h = torch.empty_like(x)
-        T, D = shape
-        ld = D or 1
-        _launch(_sg.library().sgemm_rms_norm, index, T, D, _TYPES[dtype], x.data_ptr(), ld,
-                _at(residual), ld, weight.data_ptr(), _TYPES[weight.dtype], float(eps), _at(h), ld,
-                y.data_ptr(), ld)
-        return y if residual is None else (y, h)
+            h = torch.empty(shape, dtype=dtype, device=x.device)
+        a = _rows(index, dtype, shape, x, residual, h, y)
+        if a is not None and a[4] != a[6]:
+            _launch(_sg.library().sgemm_rms_norm, index, *shape, _TYPES[dtype], *a[:4],
+                    weight.data_ptr(), _TYPES[weight.dtype], float(eps), *a[4:])
+            return y if residual is None else (y, h)
     T, D, dev, args, h, ha = _norm_args(x, weight, residual, eps, h, stream, residual is not None)
     if y is None:
         y = _empty(T, D, x.dtype, dev, stream)
@@ -196,19 +213,23 @@ def rms_norm_backward(dy, x, weight, residual=None, dh=None, eps: float = 1e-6, 
     and of the residual alike.  Outputs not given are allocated (dx may be dy or dh
     itself); ``need_dx`` and ``need_dw`` leave one out (None is returned in its place).
     """
-    index, dtype, shape = x.get_device(), x.dtype, x.shape
-    if (stream is None and index >= 0 and len(shape) == 2 and dtype in _TYPES
-            and _usual(index, dtype, shape, x, residual, dy, dh, dx) and index == _current_device()
-            and _usual(index, weight.dtype, shape[1:], weight, dweight)
-            and (weight.dtype is dtype or weight.dtype is torch.float32)):
-        dx = (torch.empty_like(x) if dx is None else dx) if need_dx else None
-        dweight = (torch.empty_like(weight) if dweight is None else dweight) if need_dw else None
-        T, D = shape
-        ld = D or 1
-        _launch(_sg.library().sgemm_rms_norm_backward, index, T, D, _TYPES[dtype], x.data_ptr(), ld,
-                _at(residual), ld, weight.data_ptr(), _TYPES[weight.dtype], float(eps), dy.data_ptr(), ld,
-                _at(dh), ld, _at(dx), ld, _at(dweight))
-        return dx, dweight
+    if _norm_usual(x, weight, stream):
+        index, dtype, shape = x.get_device(), x.dtype, x.shape
+        if not need_dx:
+            dx = None
+        elif dx is None:
+            dx = torch.empty(shape, dtype=dtype, device=x.device)
+        if not need_dw:
+            dweight = None
+        elif dweight is None:
+            dweight = torch.empty_like(weight)
+        a = _rows(index, dtype, shape, x, residual, dy, dh, dx)
+        if a is not None and (dweight is None
+                              or _plain(index, weight.dtype, shape[1], dweight)):
+            _launch(_sg.library().sgemm_rms_norm_backward, index, *shape, _TYPES[dtype], *a[:4],
+                    weight.data_ptr(), _TYPES[weight.dtype], float(eps), *a[4:],
+                    None if dweight is None else dweight.data_ptr())
+            return dx, dweight
     T, D, dev, args, _, dha = _norm_args(x, weight, residual, eps, dh, stream, False, "dh")
     dya = _address(dy, "dy", T, D, x.dtype, dev)
     dxa, dwa = (None, max(D, 1)), None
@@ -248,21 +269,18 @@ def rms_norm_q8(x, weight, residual=None, eps: float = 1e-6, h=None, q=None, sca
     through it: inputs that require one are refused.
     """
     _no_gradient("rms_norm_q8", x, weight, residual)
-    index, dtype, shape = x.get_device(), x.dtype, x.shape
-    if (stream is None and q is None and scales is None and index >= 0 and len(shape) == 2
-            and dtype in _TYPES and _usual(index, dtype, shape, x, residual, h)
-            and index == _current_device() and _usual(index, weight.dtype, shape[1:], weight)
-            and (weight.dtype is dtype or weight.dtype is torch.float32)):
-        T, D = shape
-        q, scales = _empty_codes(T, D, x.device, None), torch.empty(T, device=x.device,
-                                                                   dtype=torch.float32)
+    if q is None and scales is None and _norm_usual(x, weight, stream):
+        index, dtype, (T, D) = x.get_device(), x.dtype, x.shape
         if h is None and residual is not None:
-            h = torch.empty_like(x)
-        ld = D or 1
-        _launch(_sg.library().sgemm_rms_norm_q8, index, T, D, _TYPES[dtype], x.data_ptr(), ld,
-                _at(residual), ld, weight.data_ptr(), _TYPES[weight.dtype], float(eps), _at(h), ld,
-                q.data_ptr(), -(-D // 16) * 16 or 1, scales.data_ptr())
-        return (q, scales) if residual is None else (q, scales, h)
+            h = torch.empty(T, D, dtype=dtype, device=x.device)
+        a = _rows(index, dtype, x.shape, x, residual, h)
+        if a is not None:
+            q = _empty_codes(T, D, x.device, None)
+            scales = torch.empty(T, dtype=torch.float32, device=x.device)
+            _launch(_sg.library().sgemm_rms_norm_q8, index, T, D, _TYPES[dtype], *a[:4],
+                    weight.data_ptr(), _TYPES[weight.dtype], float(eps), *a[4:], q.data_ptr(),
+                    -(-D // 16) * 16 or 1, scales.data_ptr())
+            return (q, scales) if residual is None else (q, scales, h)
     T, D, dev, args, h, ha = _norm_args(x, weight, residual, eps, h, stream, residual is not None)
     q, scales, qa = _codes(q, scales, T, D, dev, stream)
     _call(_sg.library().sgemm_rms_norm_q8, dev, stream, *args, *ha, *qa)
@@ -280,16 +298,15 @@ def gate_q8(g, u, activation: int = 0, q=None, scales=None, stream=None):
         raise ValueError("g must be 2-D")
     index, dtype, shape = g.get_device(), g.dtype, g.shape
     if (stream is None and q is None and scales is None and index >= 0 and dtype in _TYPES
-            and u.dtype is dtype and u.get_device() == index == _current_device()
-            and u.shape == shape and g.stride(0) >= shape[1] <= u.stride(0) and shape[1] > 1
-            and g.stride(1) == 1 == u.stride(1)):
-        (T, F), ldg, ldu = shape, g.stride(0), u.stride(0)
-        q, scales = _empty_codes(T, F, g.device, None), torch.empty(T, device=g.device,
-                                                                   dtype=torch.float32)
-        _launch(_sg.library().sgemm_q8_gate, index, T, F, _TYPES[dtype], int(activation),
-                g.data_ptr(), ldg, u.data_ptr(), ldu, q.data_ptr(), -(-F // 16) * 16,
-                scales.data_ptr())
-        return q, scales
+            and index == _current_device()):
+        a = _rows(index, dtype, shape, g, u)
+        if a is not None:
+            T, F = shape
+            q = _empty_codes(T, F, g.device, None)
+            scales = torch.empty(T, dtype=torch.float32, device=g.device)
+            _launch(_sg.library().sgemm_q8_gate, index, T, F, _TYPES[dtype], int(activation), *a,
+                    q.data_ptr(), -(-F // 16) * 16 or 1, scales.data_ptr())
+            return q, scales
     T, F = g.shape
     dev = g.device
     kind = _type_of(g, "g")
@@ -353,12 +370,12 @@ class Q8Matrix:
         M, N, K, index = x.shape[0], self.N, self.K, self._index
         if y is None:
             y = _empty(M, N, self.dtype, self.device, stream)
-        if (stream is None and _usual(index, torch.int8, (M, K), x)
-                and _usual(index, self.dtype, (M, N), y)
-                and _usual(index, torch.float32, (M,), x_scales) and index == _current_device()):
-            _launch(self._fn, index, M, N, K, self.type, x.data_ptr(), K or 1, x_scales.data_ptr(),
-                    *self._weights, y.data_ptr(), N or 1)
-            return y
+        if stream is None and index == _current_device() and _plain(index, torch.float32, M, x_scales):
+            a, b = _rows(index, torch.int8, (M, K), x), _rows(index, self.dtype, (M, N), y)
+            if a is not None and b is not None:
+                _launch(self._fn, index, M, N, K, self.type, *a, x_scales.data_ptr(),
+                        *self._weights, *b)
+                return y
         if x.dim() != 2:
             raise ValueError("x must be 2-D")
         xa = _address(x, "x", M, self.K, torch.int8, self.device)
