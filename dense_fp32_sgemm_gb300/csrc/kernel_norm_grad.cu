@@ -3,13 +3,14 @@
 //   r = 1 / sqrt(mean(h^2) + eps), n = dy w
 //   dx = r (n - h r^2 mean(n h)) + dh,  dw = sum over rows of dy h r
 //
-// A group of threads holds a row of h and dy in registers, reduces both sums at
-// once, and writes dx; it owns the same columns in every row that it takes, so the
-// weight's gradient gathers in its registers and leaves once, as one of `parts` partial
-// rows, which a second kernel adds up in order.  Every input is read once and
+// A group of threads holds a row of h and dy in registers (its next rows are on their way to
+// shared memory), reduces both sums at once, and writes dx; it owns the same columns in every
+// row that it takes, so the weight's gradient gathers in its registers and leaves once, a
+// CTA's groups added up, as one of `parts` partial rows, which a second kernel adds up in order.  Every input is read once and
 // every output written once (plus the partial rows).  Rows that are too long for
 // registers are read again (norm_grad_wide_kernel).
 #include <algorithm>
+#include <atomic>
 
 #include "kernels_q8.h"
 #include "row_io.cuh"
@@ -18,6 +19,8 @@ namespace sgemm {
 namespace {
 
 constexpr int kMostThreads = 512;
+constexpr int kMaxDevices = 64;
+constexpr int kRingBytes = 192 * 1024;  // of an SM, for rows on their way
 
 __device__ __forceinline__ float2 warp_sum2(float2 v) {
 #pragma unroll
@@ -27,19 +30,20 @@ __device__ __forceinline__ float2 warp_sum2(float2 v) {
     }
     return v;
 }
-// Over the `warps` warps of each group; `buf` alternates, so that one barrier is enough.
+// Over the `warps` warps of each group, which wait for one another alone; `buf` alternates,
+// so that one barrier is enough.
 __device__ __forceinline__ float2 group_sum2(float2 v, float2 (*buf)[32], int group, int warps) {
     v = warp_sum2(v);
     if (warps == 1) return v;
     const int tid = threadIdx.x, lane = tid & 31;
     if (lane == 0) (*buf)[group * warps + (tid >> 5)] = v;
-    __syncthreads();
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"((int)blockDim.x) : "memory");
     v = lane < warps ? (*buf)[group * warps + lane] : make_float2(0.0f, 0.0f);
     return warp_sum2(v);
 }
 // r, and r^3 mean(n h), from the sums of h^2 and n h.
 __device__ __forceinline__ float2 row_stats(float2 sums, int cols, float eps) {
-    const float r = 1.0f / sqrtf(sums.x / (float)cols + eps);
+    const float r = rsqrtf(sums.x / (float)cols + eps);
     return make_float2(r, r * r * r * (sums.y / (float)cols));
 }
 
@@ -70,62 +74,92 @@ __device__ __forceinline__ void sum_h(const Raw &v, bool two, float (&h)[piece_e
         for (int j = 0; j < piece_elements(TYPE); ++j) h[j] += r[j];
     }
 }
+// dx of a piece from dy r.
 template <int TYPE>
 __device__ __forceinline__ uint4 make_dx(const float (&h)[piece_elements(TYPE)], const float (&w)[piece_elements(TYPE)],
-                                         uint4 dy_raw, uint4 dh_raw, float2 st) {
+                                         const float (&dyr)[piece_elements(TYPE)], uint4 dh_raw, float c) {
     constexpr int V = piece_elements(TYPE);
-    float dy[V], dh[V], dx[V];
-    unpack_piece<TYPE>(dy_raw, dy);
-    unpack_piece<TYPE>(dh_raw, dh);
+    float dx[V];
+    unpack_piece<TYPE>(dh_raw, dx);
 #pragma unroll
-    for (int j = 0; j < V; ++j) dx[j] = fmaf(-h[j], st.y, dy[j] * w[j] * st.x) + dh[j];
+    for (int j = 0; j < V; ++j) dx[j] = fmaf(-h[j], c, fmaf(dyr[j], w[j], dx[j]));
     return pack_piece<TYPE>(dx);
 }
 
-// NP: pieces of a thread.  With up to two, the next row is under way while one is worked on.
+// NP: pieces of a thread.
 template <int TYPE, int NP, bool ALIGNED>
 __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_kernel(const NormGradParams p) {
-    constexpr int V = piece_elements(TYPE), E = 16 / V;
-    constexpr bool kAhead = NP <= 2;
+    constexpr int V = piece_elements(TYPE), E = 16 / V, kSlots = piece_slots(ALIGNED);
     __shared__ float2 s_sum[2][32];
     __shared__ uint4 s_stage[ALIGNED ? 1 : kMostThreads / 32 * kStageWords / 4];
+    extern __shared__ uint4 s_ring[];  // pieces of the next rows, a thread's own in its own places
     const int tid = threadIdx.x, lane = tid & 31, group = threadIdx.y, groups = blockDim.y;
-    const int warps = blockDim.x >> 5, step = blockDim.x * V;
+    const int warps = blockDim.x >> 5, step = blockDim.x * V, pitch = blockDim.x * groups;
     uint32_t *stage = reinterpret_cast<uint32_t *>(s_stage) +
                       (ALIGNED ? 0 : (group * warps + (tid >> 5)) * kStageWords);
     const RowSource W = row_source(p.w, 0, p.cols, 0, p.w_f32 ? 4 : E, 1);
-    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+    // (with more than two pieces dh is loaded where it is used: it would not fit the registers)
+    constexpr bool kAhead = NP <= 2;
+    const int arrays = 2 + (p.r != nullptr) + (kAhead && p.dh);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float dw[NP][V];
 #pragma unroll
     for (int i = 0; i < NP; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) dw[i][j] = 0.0f;
 
-    Raw raw[NP];
-    auto load = [&](long long row) {
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int c = tid * V + i * step;
-            raw[i] = fetch<TYPE, ALIGNED>(p, row, c, row < p.rows ? p.cols - c : 0, p.dh && kAhead);
-        }
+    auto slot = [&](int ring, int array, int i) {
+        return s_ring + (((ring * arrays + array) * NP + i) * kSlots) * pitch + group * blockDim.x + tid;
     };
-    const long long first = (long long)blockIdx.x * groups + group, stride = (long long)gridDim.x * groups;
-    if (kAhead) load(first);
-    int flip = 0;
-    for (long long row = first; row - group < p.rows; row += stride, flip ^= 1) {
-        const bool live = row < p.rows;
-        if (!kAhead) load(row);
+    // In this order in a stage: x, dy, r, dh.
+    auto source = [&](int array, unsigned row) {
+        if (array == 2 && !p.r) array = 3;
+        return array == 0   ? row_source(p.x, row, p.cols, p.ldx, E, p.rows)
+               : array == 1 ? row_source(p.dy, row, p.cols, p.lddy, E, p.rows)
+               : array == 2 ? row_source(p.r, row, p.cols, p.ldr, E, p.rows)
+                            : row_source(p.dh, row, p.cols, p.lddh, E, p.rows);
+    };
+    auto start = [&](unsigned row, int ring) {
+        if (row < p.rows) {
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+                if (a < arrays) {
+                    const RowSource m = source(a, row);
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+                        if (tid * V + i * step < p.cols)
+                            start_piece<ALIGNED>(slot(ring, a, i), pitch, m, (tid * V + i * step) * E);
+                }
+        }
+        cp_async_commit();
+    };
+    auto take = [&](int ring, int array, int i, unsigned row) {
+        return take_piece<TYPE, ALIGNED>(slot(ring, array, i), pitch, source(array, row), (tid * V + i * step) * E);
+    };
+    const unsigned first = blockIdx.x * groups + group, stride = gridDim.x * groups;
+    for (int s = 0; s < p.stages; ++s) start(first + s * stride, s);
+    int flip = 0, ring = 0;
+    for (unsigned row = first; row < p.rows; row += stride, flip ^= 1) {
+        // All but the last stages - 1 rows' copies have landed.
+        if (p.stages == 1) cp_async_wait<0>();
+        else if (p.stages == 2) cp_async_wait<1>();
+        else cp_async_wait<2>();
         float h[NP][V];
         uint4 dy_raw[NP], dh_raw[NP];
         float2 sums = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int c = tid * V + i * step;
-            sum_h<TYPE>(raw[i], p.r, h[i]);
-            dy_raw[i] = raw[i].dy;
-            dh_raw[i] = raw[i].dh;
             if (c < p.cols) {
                 float w[V], dy[V];
+                unpack_piece<TYPE>(take(ring, 0, i, row), h[i]);
+                if (p.r) {
+                    unpack_piece<TYPE>(take(ring, 2, i, row), w);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) h[i][j] += w[j];
+                }
+                dy_raw[i] = take(ring, 1, i, row);
+                if (kAhead) dh_raw[i] = p.dh ? take(ring, arrays - 1, i, row) : make_uint4(0, 0, 0, 0);
                 load_weight<TYPE, ALIGNED>(W, p.w_f32, c, p.cols - c, w);
                 unpack_piece<TYPE>(dy_raw[i], dy);
 #pragma unroll
@@ -135,36 +169,50 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_kernel(const NormGr
                 }
             }
         }
-        if (kAhead) load(row + stride);
+        start(row + p.stages * stride, ring);
+        if (++ring == p.stages) ring = 0;
         const float2 st = row_stats(group_sum2(sums, &s_sum[flip], group, warps), p.cols, p.eps);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const int c = tid * V + i * step, n = live ? p.cols - c : 0;
-            float dy[V];
-            unpack_piece<TYPE>(dy_raw[i], dy);  // (zeros where there are no elements)
+            const int c = tid * V + i * step, n = p.cols - c;
+            float dyr[V];
+            if (n > 0) {
+                unpack_piece<TYPE>(dy_raw[i], dyr);
 #pragma unroll
-            for (int j = 0; j < V; ++j) dw[i][j] = fmaf(dy[j] * st.x, h[i][j], dw[i][j]);
-            if (p.dx && live && c - lane * V < p.cols) {  // (the whole warp)
+                for (int j = 0; j < V; ++j) {
+                    dyr[j] *= st.x;
+                    dw[i][j] = fmaf(dyr[j], h[i][j], dw[i][j]);
+                }
+            }
+            if (p.dx && c - lane * V < p.cols) {  // (the whole warp)
                 float w[V];
                 if (n > 0) {
                     load_weight<TYPE, ALIGNED>(W, p.w_f32, c, n, w);
-                    if (!kAhead && p.dh)
-                        dh_raw[i] = load_piece<TYPE, ALIGNED>(
-                            row_source(p.dh, row, p.cols, p.lddh, E, p.rows), c * E, n);
+                    if (!kAhead)
+                        dh_raw[i] = p.dh ? load_piece<TYPE, ALIGNED>(source(3, row), c * E, n) : make_uint4(0, 0, 0, 0);
                 }
-                store_piece<TYPE, ALIGNED>(static_cast<char *>(p.dx) + (row * p.lddx + c - lane * V) * E, n,
-                                           make_dx<TYPE>(h[i], w, dy_raw[i], dh_raw[i], st), stage);
+                store_piece<TYPE, ALIGNED>(static_cast<char *>(p.dx) + ((long long)row * p.lddx + c - lane * V) * E, n,
+                                           make_dx<TYPE>(h[i], w, dyr, dh_raw[i], st.y), stage);
             }
         }
     }
     if (!p.dw) return;
-    float *part = p.partials + ((long long)blockIdx.x * groups + group) * p.cols;
+    // The groups' sums, added up in order: one partial row of a CTA.
+    cp_async_wait<0>();
+    __syncthreads();
+    float *all = reinterpret_cast<float *>(s_ring);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const int c = tid * V + i * step;
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            if (c + j < p.cols) __stcg(part + c + j, dw[i][j]);
+            if (c + j < p.cols) all[group * p.cols + c + j] = dw[i][j];
+    }
+    __syncthreads();
+    for (int c = group * blockDim.x + tid; c < p.cols; c += pitch) {
+        float sum = all[c];
+        for (int g = 1; g < groups; ++g) sum += all[g * p.cols + c];
+        __stcg(p.partials + (long long)blockIdx.x * p.cols + c, sum);
     }
 }
 
@@ -179,7 +227,7 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_wide_kernel(const N
     uint32_t *stage = reinterpret_cast<uint32_t *>(s_stage) + (ALIGNED ? 0 : (tid >> 5) * kStageWords);
     const long long row = blockIdx.x;
     const RowSource W = row_source(p.w, 0, p.cols, 0, p.w_f32 ? 4 : E, 1);
-    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float2 sums = make_float2(0.0f, 0.0f);
     float h[V], dy[V], w[V];
     for (int c = tid * V; c < p.cols; c += step) {
@@ -200,9 +248,12 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_wide_kernel(const N
         const int n = p.cols - c;
         const Raw raw = fetch<TYPE, ALIGNED>(p, row, c, n, p.dh);
         sum_h<TYPE>(raw, p.r, h);
+        unpack_piece<TYPE>(raw.dy, dy);
+#pragma unroll
+        for (int j = 0; j < V; ++j) dy[j] *= st.x;
         if (n > 0) load_weight<TYPE, ALIGNED>(W, p.w_f32, c, n, w);
         store_piece<TYPE, ALIGNED>(static_cast<char *>(p.dx) + (row * p.lddx + c - lane * V) * E, n,
-                                   make_dx<TYPE>(h, w, raw.dy, raw.dh, st), stage);
+                                   make_dx<TYPE>(h, w, dy, raw.dh, st.y), stage);
     }
 }
 
@@ -211,7 +262,7 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_wide_kernel(const N
 template <int TYPE>
 __global__ void __launch_bounds__(256) norm_grad_columns_kernel(const NormGradParams p) {
     const int c = blockIdx.x * blockDim.x + threadIdx.x;
-    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (c >= p.cols) return;
     float sum = 0.0f;
 #pragma unroll 4
@@ -228,7 +279,7 @@ __global__ void __launch_bounds__(256) norm_grad_columns_kernel(const NormGradPa
 __global__ void __launch_bounds__(1024) norm_grad_reduce_kernel(const NormGradParams p, int type) {
     __shared__ float s[32][9];
     const int c = blockIdx.x * 8 + threadIdx.x, y = threadIdx.y;
-    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float sum = 0.0f;
     if (c < p.cols) {
 #pragma unroll 8
@@ -249,31 +300,36 @@ __global__ void __launch_bounds__(1024) norm_grad_reduce_kernel(const NormGradPa
     if (lane == 0 && out < p.cols) store_from_float(p.dw, p.w_f32 ? kTypeF32 : type, out, sum);
 }
 
+// Most pieces of a thread that fit its registers.
+constexpr int grad_depth(int type, bool aligned) { return type != kTypeF32 ? 2 : aligned ? 4 : 3; }
+
 // How a row lies over threads: pieces of a thread (0: too many for registers),
-// threads of a row, rows that a CTA has at once, CTAs.
+// threads of a row, rows that a CTA has at once, CTAs (one on an SM).
 struct Shape {
     int depth, threads, groups, ctas;
 };
 Shape shape(long long rows, int cols, int type, bool vec, int num_sms) {
-    const int most = vec ? 4 : 3;  // (shifting takes registers)
+    const int most = grad_depth(type, vec);
     Shape s;
     const int pieces = (cols + piece_elements(type) - 1) / piece_elements(type);
     s.depth = pieces <= kMostThreads && rows <= num_sms ? 1 : pieces <= 2 * kMostThreads ? 2
               : pieces <= most * kMostThreads ? most : 0;
     if (s.depth == 0) return s;
     s.threads = std::max(1, (pieces + 32 * s.depth - 1) / (32 * s.depth)) * 32;
-    s.groups = s.threads >= 128 ? 1 : 128 / s.threads;
-    const int per_sm = std::max(1, kMostThreads / (s.threads * s.groups));
-    s.ctas = (int)std::min<long long>((rows + s.groups - 1) / s.groups, (long long)num_sms * per_sm);
+    // Few rows are spread over the SMs first.
+    s.groups = (int)std::max<long long>(1, std::min<long long>({kMostThreads / s.threads, 15, rows / num_sms}));
+    s.ctas = (int)std::min<long long>((rows + s.groups - 1) / s.groups, num_sms);
     return s;
 }
 constexpr int kWideParts = 64;
 
 template <class... Params, class... Args>
-cudaError_t launch(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t stream, Args... args) {
+cudaError_t launch(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                   Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -283,38 +339,56 @@ cudaError_t launch(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+template <int TYPE, int NP, bool ALIGNED>
+cudaError_t launch_depth(const NormGradParams &p, const Shape &s, cudaStream_t stream) {
+    const auto kernel = norm_grad_kernel<TYPE, NP, ALIGNED>;
+    static std::atomic<bool> configured[kMaxDevices];
+    if (p.device >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!configured[p.device].load()) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+        if (e != cudaSuccess) return e;
+        configured[p.device].store(true);
+    }
+    NormGradParams q = p;
+    const int bytes = (2 + (p.r != nullptr) + (NP <= 2 && p.dh)) * NP * piece_slots(ALIGNED) * 16 *
+                      s.threads * s.groups;
+    q.stages = std::max(1, std::min(3, kRingBytes / bytes));
+    const size_t smem = std::max<size_t>((size_t)bytes * q.stages, (size_t)s.groups * p.cols * sizeof(float));
+    return launch(kernel, dim3(s.ctas), dim3(s.threads, s.groups), smem, stream, q);
+}
+
 template <int TYPE, bool ALIGNED>
 cudaError_t launch_form(const NormGradParams &p, int num_sms, cudaStream_t stream) {
     const Shape s = shape(p.rows, p.cols, TYPE, ALIGNED, num_sms);
     cudaError_t e;
     if (s.depth) {
-        const auto kernel = s.depth == 1   ? norm_grad_kernel<TYPE, 1, ALIGNED>
-                            : s.depth == 2 ? norm_grad_kernel<TYPE, 2, ALIGNED>
-                                           : norm_grad_kernel<TYPE, ALIGNED ? 4 : 3, ALIGNED>;
-        e = launch(kernel, dim3(s.ctas), dim3(s.threads, s.groups), stream, p);
+        e = s.depth == 1   ? launch_depth<TYPE, 1, ALIGNED>(p, s, stream)
+            : s.depth == 2 ? launch_depth<TYPE, 2, ALIGNED>(p, s, stream)
+                           : launch_depth<TYPE, grad_depth(TYPE, ALIGNED), ALIGNED>(p, s, stream);
     } else {
         // dx may lie over dy: the statistics first, then dw, then dx.
         NormGradParams q = p;
         e = cudaSuccess;
         if (p.dw) {
             q.dx = nullptr;
-            e = launch(norm_grad_wide_kernel<TYPE, ALIGNED>, dim3((unsigned)p.rows), dim3(kMostThreads), stream, q);
+            e = launch(norm_grad_wide_kernel<TYPE, ALIGNED>, dim3((unsigned)p.rows), dim3(kMostThreads), 0, stream, q);
             if (e == cudaSuccess)
-                e = launch(norm_grad_columns_kernel<TYPE>, dim3((p.cols + 255) / 256, p.parts), dim3(256),
+                e = launch(norm_grad_columns_kernel<TYPE>, dim3((p.cols + 255) / 256, p.parts), dim3(256), 0,
                            stream, p);
         }
         if (e == cudaSuccess && p.dx)
-            e = launch(norm_grad_wide_kernel<TYPE, ALIGNED>, dim3((unsigned)p.rows), dim3(kMostThreads), stream, p);
+            e = launch(norm_grad_wide_kernel<TYPE, ALIGNED>, dim3((unsigned)p.rows), dim3(kMostThreads), 0, stream, p);
     }
     if (e != cudaSuccess || !p.dw) return e;
-    return launch(norm_grad_reduce_kernel, dim3((p.cols + 7) / 8), dim3(8, 128), stream, p, TYPE);
+    return launch(norm_grad_reduce_kernel, dim3((p.cols + 7) / 8), dim3(8, 128), 0, stream, p, TYPE);
 }
 
 }  // namespace
 
 int norm_grad_parts(long long rows, int cols, int type, bool vec, int num_sms) {
     const Shape s = shape(rows, cols, type, vec, num_sms);
-    return s.depth ? s.ctas * s.groups : (int)std::min<long long>(rows, kWideParts);
+    return s.depth ? s.ctas : (int)std::min<long long>(rows, kWideParts);
 }
 
 cudaError_t launch_norm_grad(const NormGradParams &p, int type, bool vec, int num_sms,

@@ -4,8 +4,8 @@
 // channels by 512 k that its warps share out evenly; a lane multiplies 16 bytes of each
 // of the four by the same 16 of every row of x (four at a time, summed into 32 bits).
 // Sums are integers, so neither the sharing out nor the order of the additions
-// changes them.  x lies in shared memory, zeros from K on.  The loads of the next
-// item are under way while one is multiplied.  Bound: HBM.
+// changes them.  x lies in shared memory, zeros from K on.  The loads of three
+// items are under way at a time.  Bound: HBM.
 #include <algorithm>
 #include <atomic>
 
@@ -19,6 +19,7 @@ namespace {
 constexpr int kWarps = 16;
 constexpr int kChannels = 4;       // of an item
 constexpr int kItemK = 512;
+constexpr int kAhead = 3;          // items on their way
 constexpr int kCtaChannels = 256;  // most of a CTA
 constexpr int kMaxDevices = 64;
 
@@ -46,25 +47,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
     for (int k0 = 0; k0 < p.K; k0 += stage_k) {
         const int len = min(stage_k, p.K - k0), chunks = (len + kItemK - 1) / kItemK;
-        if (k0) __syncthreads();
-        for (int i = tid; i < p.M * chunks * (kItemK / 16); i += kWarps * 32) {
-            const int m = i / (chunks * (kItemK / 16)), k = (i - m * (chunks * (kItemK / 16))) * 16;
-            const int8_t *from = p.x + m * p.ldx + k0 + k;
-            int w[4] = {0, 0, 0, 0};
-            if (p.x_vec && k + 16 <= len) {
-                const int4 v = __ldg(reinterpret_cast<const int4 *>(from));
-                w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (k + j < len) w[j / 4] |= (int)(uint8_t)__ldg(from + j) << (8 * (j % 4));
-            }
-            *reinterpret_cast<int4 *>(s_x + m * stage_k + k) = make_int4(w[0], w[1], w[2], w[3]);
-        }
-        for (int i = p.M * stage_k + tid * 16; i < ROWS * stage_k; i += kWarps * 32 * 16)
-            *reinterpret_cast<int4 *>(s_x + i) = make_int4(0, 0, 0, 0);
-        __syncthreads();
-
         const int items = groups * chunks;
         const int first = (int)((long long)warp * items / kWarps), end = (int)((warp + 1LL) * items / kWarps);
         int acc[kChannels][ROWS];
@@ -90,7 +72,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             for (int c = 0; c < kChannels; ++c) {
                 const int n = g * kChannels + c;
                 w[c] = make_int4(0, 0, 0, 0);
-                if (n < count && k < len) {
+                if (it < end && n < count && k < len) {
                     const int8_t *from = p.w + (long long)(n0 + n) * p.ldw + k0 + k;
                     if (k + 16 <= len || n0 + n + 1 < p.N) {
                         w[c] = load_weights(from);
@@ -105,29 +87,55 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 }
             }
         };
+        // The first weights are on their way while x is brought in.
+        int4 ahead[kAhead][kChannels];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) fetch(first + a, ahead[a]);
+
+        if (k0) __syncthreads();
+        for (int i = tid; i < p.M * chunks * (kItemK / 16); i += kWarps * 32) {
+            const int m = i / (chunks * (kItemK / 16)), k = (i - m * (chunks * (kItemK / 16))) * 16;
+            const int8_t *from = p.x + m * p.ldx + k0 + k;
+            int w[4] = {0, 0, 0, 0};
+            if (p.x_vec && k + 16 <= len) {
+                const int4 v = __ldg(reinterpret_cast<const int4 *>(from));
+                w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (k + j < len) w[j / 4] |= (int)(uint8_t)__ldg(from + j) << (8 * (j % 4));
+            }
+            *reinterpret_cast<int4 *>(s_x + m * stage_k + k) = make_int4(w[0], w[1], w[2], w[3]);
+        }
+        for (int i = p.M * stage_k + tid * 16; i < ROWS * stage_k; i += kWarps * 32 * 16)
+            *reinterpret_cast<int4 *>(s_x + i) = make_int4(0, 0, 0, 0);
+        __syncthreads();
+
         clear();
-        int4 now[kChannels], next[kChannels];
-        if (first < end) fetch(first, now);
-        for (int it = first; it < end; ++it) {
-            if (it + 1 < end) fetch(it + 1, next);
-            const int g = it / chunks, k = (it - g * chunks) * kItemK + lane * 16;
+#pragma unroll 1
+        for (int it0 = first; it0 < end; it0 += kAhead) {
 #pragma unroll
-            for (int m = 0; m < ROWS; ++m) {
-                const int4 x = *reinterpret_cast<const int4 *>(s_x + m * stage_k + k);
+            for (int a = 0; a < kAhead; ++a) {
+                const int it = it0 + a;
+                if (it >= end) break;
+                const int g = it / chunks, k = (it - g * chunks) * kItemK + lane * 16;
 #pragma unroll
-                for (int c = 0; c < kChannels; ++c) {
-                    acc[c][m] = __dp4a(now[c].x, x.x, acc[c][m]);
-                    acc[c][m] = __dp4a(now[c].y, x.y, acc[c][m]);
-                    acc[c][m] = __dp4a(now[c].z, x.z, acc[c][m]);
-                    acc[c][m] = __dp4a(now[c].w, x.w, acc[c][m]);
+                for (int m = 0; m < ROWS; ++m) {
+                    const int4 x = *reinterpret_cast<const int4 *>(s_x + m * stage_k + k);
+#pragma unroll
+                    for (int c = 0; c < kChannels; ++c) {
+                        acc[c][m] = __dp4a(ahead[a][c].x, x.x, acc[c][m]);
+                        acc[c][m] = __dp4a(ahead[a][c].y, x.y, acc[c][m]);
+                        acc[c][m] = __dp4a(ahead[a][c].z, x.z, acc[c][m]);
+                        acc[c][m] = __dp4a(ahead[a][c].w, x.w, acc[c][m]);
+                    }
+                }
+                fetch(it + kAhead, ahead[a]);
+                if (it + 1 == end || (it + 1) / chunks != g) {
+                    flush(g);
+                    clear();
                 }
             }
-            if (it + 1 == end || (it + 1) / chunks != g) {
-                flush(g);
-                clear();
-            }
-#pragma unroll
-            for (int c = 0; c < kChannels; ++c) now[c] = next[c];
         }
     }
     __syncthreads();

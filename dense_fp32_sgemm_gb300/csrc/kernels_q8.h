@@ -55,6 +55,8 @@ struct NormGradParams {
     float *partials;          // parts x cols, sums of some rows each
     float2 *stats;            // rows: r and r^3 mean(n h), where rows do not fit registers
     int parts;
+    int device;
+    int stages;               // (set by the launch) rows on their way
 };
 // Partial rows of the weight's gradient.
 int norm_grad_parts(long long rows, int cols, int type, bool vec, int num_sms);

@@ -124,7 +124,9 @@ __global__ void __maxnreg__(row_regs(OP, ACT, ALIGNED)) row_kernel(const RowPara
     auto B = [&](unsigned r) { return row_source(p.b, r, p.cols, p.ldb, E, p.rows); };
 
     if (tid == 0) s_top[0][group] = s_top[1][group] = 0;
-    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+    // (The kernel behind this one may start when this one's CTAs end: its own, started earlier, took
+    // their places from rows still to be done, 85 us for a training step that takes 73.)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // Of the thread's elements: h of the norm; what is coded.
     float keep[NP][V];
