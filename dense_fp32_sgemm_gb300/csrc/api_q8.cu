@@ -81,6 +81,50 @@ bool norm_vec(const NormArgs &a) {
            rows16(a.h, a.ldh, a.T, a.type) && aligned(a.weight, 16);
 }
 
+// Single CTAs or pairs, tokens of a tile, and how the tiles left over after whole rounds
+// are cut along k: the least of a model of SM clocks, fitted to GB300 times.  A stage (128 k)
+// takes 4 for each token of a pair's tile (single CTAs 4 too: half the products, but
+// operands that pass through shared memory twice as often), at least 700, which its
+// weights take to be widened and to come from HBM.  A tile takes 3000 more for its results, one
+// cut in n pieces 5000 and 1200 n for those to meet.  (Even shares of the tail for
+// all workers, as the gated block has them, touch two tiles each and meet twice:
+// 96 x 4096 x 4096 26 us.)
+bool q8_plan(Q8GemmParams &p, bool &pair, int num_sms) {
+    double least = -1.0;
+    p.stages_k = (p.K + kQ8StageK - 1) / kQ8StageK;
+    for (int two = 0; two < 2; ++two) {
+        const int64_t most = kQ8Tokens * (two + 1), channels = kQ8Channels * (two + 1);
+        const int64_t tiles_n = (p.N + channels - 1) / channels, rows = (p.M + most - 1) / most;
+        const int workers = num_sms / (two + 1);
+        for (int64_t m = rows; m < rows + 4; ++m) {
+            const int tokens = (int)up((p.M + m - 1) / m, 32);
+            const int64_t tiles_m = (p.M + tokens - 1) / tokens, tiles = tiles_m * tiles_n;
+            if (tiles > INT32_MAX / 2) continue;
+            const double stage = std::max(700.0, 4.0 * tokens);
+            const int full = (int)(tiles / workers), tail = (int)(tiles % workers);
+            const double whole = full * (p.stages_k * stage + 3000.0);
+            for (int n = 1; n == 1 || (n * tail <= workers && n <= p.stages_k); ++n) {
+                const int per_piece = (p.stages_k + n - 1) / n;
+                const double cost = whole + (tail ? per_piece * stage + 3000.0 : 0.0) +
+                                    (n > 1 ? 5000.0 + 1200.0 * n * tokens / most : 0.0);
+                if (least < 0.0 || cost < least) {
+                    least = cost;
+                    pair = two != 0;
+                    p.tokens = tokens;
+                    p.tiles_m = (int)tiles_m;
+                    p.tiles_n = (int)tiles_n;
+                    p.workers = workers;
+                    p.full_tiles = full;
+                    p.tail_tiles = tail;
+                    p.tail_workers = n > 1 ? tail * n : 0;
+                }
+                if (tail == 0) break;
+            }
+        }
+    }
+    return least >= 0.0;
+}
+
 }  // namespace
 }  // namespace sgemm
 
@@ -287,25 +331,10 @@ sgemm_status_t sgemm_q8_matmul(int64_t M, int64_t N, int64_t K, int type, const 
         return status(launch_q8_stream(p, type, dev.num_sms, st));
     }
 
-    const bool pair = M > kQ8Tokens;
-    const int64_t most = kQ8Tokens * (pair ? 2 : 1), channels = kQ8Channels * (pair ? 2 : 1);
-    const int64_t tiles_m = (M + most - 1) / most, tiles_n = (N + channels - 1) / channels;
-    if (tiles_m * tiles_n > INT32_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
     Q8GemmParams p = {};
     p.M = (int)M; p.N = (int)N; p.K = (int)K;
-    p.tokens = (int)up((M + tiles_m - 1) / tiles_m, 32);
-    p.tiles_m = (int)((M + p.tokens - 1) / p.tokens);
-    p.tiles_n = (int)tiles_n;
-    p.stages_k = (int)((K + kQ8StageK - 1) / kQ8StageK);
-    p.workers = dev.num_sms / (pair ? 2 : 1);
-    const int tiles = p.tiles_m * p.tiles_n;
-    p.full_tiles = tiles / p.workers;
-    p.tail_tiles = tiles % p.workers;
-    if (p.tail_tiles) {
-        const int64_t share = std::max<int64_t>(1, std::min<int64_t>(4, p.stages_k));
-        const int64_t n = std::min<int64_t>(p.workers, (int64_t)p.tail_tiles * p.stages_k / share);
-        p.tail_workers = n > p.tail_tiles ? (int)n : 0;
-    }
+    bool pair = false;
+    if (!q8_plan(p, pair, dev.num_sms)) return SGEMM_ERR_UNSUPPORTED;
     s = op_counters(st, (size_t)dev.num_sms * 8, &p.counters);
     if (s != SGEMM_OK) return s;
     uint16_t *wide = reinterpret_cast<uint16_t *>(base + x_at);

@@ -435,17 +435,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             bool emit = true;
             if (unit.pieces > 1) {
+                // 16 bytes a lane, a part's four one after the other.
                 auto slot = [&](int q) {
-                    return p.partials +
-                           ((size_t)(piece_slot(unit, q) * CG + (int)rank) * kEpiWarps + (warp - kFirstEpi)) *
-                               (kParts * 16 * 32) + lane;
+                    return reinterpret_cast<int4 *>(
+                               p.partials + ((size_t)(piece_slot(unit, q) * CG + (int)rank) * kEpiWarps +
+                                             (warp - kFirstEpi)) * (kParts * 16 * 32)) + lane;
                 };
-                int *to = slot(unit.piece);
+                int4 *to = slot(unit.piece);
 #pragma unroll
                 for (int j = 0; j < kParts; ++j)
                     if (j < parts) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) __stcg(to + (j * 16 + i) * 32, sum[j][i]);
+                        for (int i = 0; i < 4; ++i)
+                            __stcg(to + (j * 4 + i) * 32, make_int4(sum[j][4 * i], sum[j][4 * i + 1],
+                                                                    sum[j][4 * i + 2], sum[j][4 * i + 3]));
                     }
                 __threadfence();
                 __syncwarp();
@@ -461,12 +464,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (emit)
                     for (int q = 0; q < unit.pieces; ++q) {
                         if (q == unit.piece) continue;
-                        const int *from = slot(q);
+                        const int4 *from = slot(q);
 #pragma unroll
                         for (int j = 0; j < kParts; ++j)
                             if (j < parts) {
+                                int4 v[4];
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) sum[j][i] += __ldcg(from + (j * 16 + i) * 32);
+                                for (int i = 0; i < 4; ++i) v[i] = __ldcg(from + (j * 4 + i) * 32);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    sum[j][4 * i] += v[i].x;
+                                    sum[j][4 * i + 1] += v[i].y;
+                                    sum[j][4 * i + 2] += v[i].z;
+                                    sum[j][4 * i + 3] += v[i].w;
+                                }
                             }
                     }
             }
