@@ -55,7 +55,7 @@ __device__ __forceinline__ float gate_value(float g, float u, GateSpread &s) {
     return a;
 }
 template <int ACT>
-__device__ __noinline__ double gate_exact(float g, float u) {
+__device__ __forceinline__ double gate_exact(float g, float u) {
     if (ACT == kGateRelu) return g > 0.0f ? (double)g * u : 0.0;
     Two z = {g, 0.0f};
     if (ACT == kGateGelu) {
@@ -133,10 +133,6 @@ __global__ void __maxnreg__(row_regs(OP, ACT, ALIGNED)) row_kernel(const RowPara
     float sum, largest;  // of squares; |what is coded|, NaN where one is
     GateSpread spread;
 
-    auto go_to = [&](unsigned r) {
-        row = r;
-        cols = r < rows ? p.cols : 0;
-    };
     auto exact = [&](int c) -> double {
         const float a = load_as_float(A(row).row, TYPE, c);
         if constexpr (kPlain) {
@@ -184,8 +180,8 @@ __global__ void __maxnreg__(row_regs(OP, ACT, ALIGNED)) row_kernel(const RowPara
     };
     auto put = [&](void *to, long long ld, int c, int n, const float (&v)[V]) {
         // The address of lane 0's piece.
-        char *at = static_cast<char *>(to) + ((long long)row * ld + c - lane * V) * E;
-        store_piece<TYPE, ALIGNED>(at, n, pack_piece<TYPE>(v), stage);
+        char *first = static_cast<char *>(to) + ((long long)row * ld + c - lane * V) * E;
+        store_piece<TYPE, ALIGNED>(first, n, pack_piece<TYPE>(v), stage);
     };
     // h over x or the residual would take from exact() what it reads: then it is stored last.
     const bool early = KEEP && (OP == kRowNorm || !p.h_last);
@@ -212,17 +208,16 @@ __global__ void __maxnreg__(row_regs(OP, ACT, ALIGNED)) row_kernel(const RowPara
         }
         cp_async_commit();
     };
-    const unsigned first = row;
     int ring = 0;
     if constexpr (KEEP)
-        for (int s = 0; s < p.stages; ++s) start(first + s * stride, s);
+        for (int s = 0; s < p.stages; ++s) start(row + s * stride, s);
     static_assert(NP * V <= 32, "");
     // The column of the thread's i-th element in registers.
     auto element = [&](int i) { return tid * V + i / V * step + i % V; };
     // Calls f(c) for each of the thread's elements.
     auto each = [&](auto &&f) {
-        for (int c = tid * V; c < cols; c += step)
-            for (int j = 0; j < min(V, cols - c); ++j) f(c + j);
+        for (int c = tid * V; c < p.cols; c += step)
+            for (int j = 0; j < min(V, p.cols - c); ++j) f(c + j);
     };
     // What is left to do for a row whose codes are stored: those in doubt (of the thread's
     // elements in registers; `all`: every element) and the scale.
@@ -232,26 +227,25 @@ __global__ void __maxnreg__(row_regs(OP, ACT, ALIGNED)) row_kernel(const RowPara
         const double top = fmax(__longlong_as_double((long long)s_top[turn_of][group]), (double)kRowTiny);
         p.q[(long long)row * p.ldq + c] = (int8_t)row_code_exact(exact(c), top, 127.0f / (float)top);
     };
-    auto finish = [&](unsigned r, int turn_of) {
+    auto finish = [&](int turn_of) {  // of `row`
+        for (; doubt; doubt &= doubt - 1) decide(element(__ffs(doubt) - 1), turn_of);
+        if (all) each([&](int c) { decide(c, turn_of); });
+        all = false;
+        if (tid == 0 && row < rows)
+            p.scales[row] = fmaxf((float)__longlong_as_double((long long)s_top[turn_of][group]), kRowTiny) *
+                            s_scale[turn_of][group];
+    };
+    auto finish_last = [&](int turn_of) {  // of the row before
         if (doubt || all || tid == 0) {
-            const unsigned now = row;
-            const int cols_now = cols;
-            go_to(r);
-            for (; doubt; doubt &= doubt - 1) decide(element(__ffs(doubt) - 1), turn_of);
-            if (all) each([&](int c) { decide(c, turn_of); });
-            all = false;
-            if (tid == 0 && r < rows)
-                p.scales[r] = fmaxf((float)__longlong_as_double((long long)s_top[turn_of][group]), kRowTiny) *
-                              s_scale[turn_of][group];
-            row = now;
-            cols = cols_now;
+            row -= stride;
+            finish(turn_of);
+            row += stride;
         }
     };
     int turn = 0;
     bool flip = false, begun = false;
-    unsigned at = first;
-    for (; at - group < rows; at += stride, flip = !flip) {
-    go_to(at);
+    for (; row - group < rows; row += stride, flip = !flip) {
+    cols = row < rows ? p.cols : 0;
     sum = largest = 0.0f;
     spread = GateSpread();
     if constexpr (KEEP) {
@@ -280,7 +274,7 @@ __global__ void __maxnreg__(row_regs(OP, ACT, ALIGNED)) row_kernel(const RowPara
                 for (int j = 0; j < V; ++j) keep[i][j] = 0.0f;
             }
         }
-        start(at + p.stages * stride, ring);
+        start(row + p.stages * stride, ring);
         if (++ring == p.stages) ring = 0;
     } else {
         for (int c = tid * V; c < cols; c += step) {
@@ -370,7 +364,7 @@ __global__ void __maxnreg__(row_regs(OP, ACT, ALIGNED)) row_kernel(const RowPara
         const int next_turn = turn == 2 ? 0 : turn + 1;
         if (tid == 0) s_top[next_turn][group] = 0;
         const bool later = KEEP && !p.h_last;  // what is left of a row is done with the next one
-        if (later && begun) finish(at - stride, turn == 0 ? 2 : turn - 1);
+        if (later && begun) finish_last(turn == 0 ? 2 : turn - 1);
         begun = true;
         const bool bad = most >= 0x7F800000u;
         const float top = fmaxf(__uint_as_float(most), kRowTiny);
@@ -465,7 +459,7 @@ __global__ void __maxnreg__(row_regs(OP, ACT, ALIGNED)) row_kernel(const RowPara
         // next row's barrier, or (h over what decide() reads) one of its own.
         if (!later) {
             if constexpr (KEEP) __syncthreads();
-            finish(at, turn);
+            finish(turn);
             if (OP == kRowNormQ8 && p.h)
                 for (int c = tid * V; c - lane * V < cols; c += step) {
                     uint4 x = make_uint4(0, 0, 0, 0), y = x;
@@ -480,7 +474,7 @@ __global__ void __maxnreg__(row_regs(OP, ACT, ALIGNED)) row_kernel(const RowPara
     }
     if (OP != kRowNorm && KEEP && !p.h_last) {
         __syncthreads();
-        if (begun) finish(at - stride, turn == 0 ? 2 : turn - 1);
+        if (begun) finish_last(turn == 0 ? 2 : turn - 1);
     }
 }
 
