@@ -108,11 +108,14 @@ __global__ void __maxnreg__(row_regs(OP, ACT, ALIGNED)) row_kernel(const RowPara
     __shared__ unsigned s_max[2][kWarps], s_mass[2][kWarps];
     __shared__ unsigned long long s_top[3][kWarps];
     __shared__ float s_scale[3][kWarps];
-    __shared__ uint4 s_stage[ALIGNED || !kStores ? 1 : kWarps * kStageWords / 4];
     const int tid = threadIdx.x, lane = tid & 31;
     const int group = threadIdx.y, warps = blockDim.x >> 5;
-    uint32_t *stage = reinterpret_cast<uint32_t *>(s_stage) +
-                      (ALIGNED || !kStores ? 0 : (group * warps + (tid >> 5)) * kStageWords);
+    // The ring below, and before it what store_piece() needs of each warp.
+    extern __shared__ uint4 s_dynamic[];
+    constexpr int kStage = kStores && !ALIGNED ? kStageWords / 4 : 0;
+    const int pitch = blockDim.x * blockDim.y;
+    uint32_t *stage = reinterpret_cast<uint32_t *>(s_dynamic + (group * warps + (tid >> 5)) * kStage);
+    uint4 *const s_ring = s_dynamic + (pitch >> 5) * kStage;
     const int step = blockDim.x * V;
     const bool two = kGate || (!kPlain && p.b != nullptr);
     const RowSource W = row_source(p.w, 0, p.cols, 0, p.w_f32 ? 4 : E, 1);
@@ -188,9 +191,8 @@ __global__ void __maxnreg__(row_regs(OP, ACT, ALIGNED)) row_kernel(const RowPara
 
     // In registers: the pieces of the next rows are on their way, a thread's own into its own
     // places of a ring, so that nobody has to wait for another's.
-    extern __shared__ uint4 s_ring[];
     constexpr int kSlots = piece_slots(ALIGNED);
-    const int pitch = blockDim.x * blockDim.y, arrays = two ? 2 : 1;
+    const int arrays = two ? 2 : 1;
     auto slot = [&](int stage_of, int array, int i) {
         return s_ring + (((stage_of * arrays + array) * NP + i) * kSlots) * pitch + group * blockDim.x + tid;
     };
@@ -507,14 +509,17 @@ cudaError_t launch_op(const RowParams &p, int num_sms, cudaStream_t stream) {
     const int bytes = (OP == kRowGateQ8 ? (ACT >= 0 ? 2 : 1) : p.b ? 2 : 1) * (few ? 1 : kDeep) *
                       piece_slots(ALIGNED) * 16 * threads * groups;
     q.stages = std::max(1, std::min(3, kRingBytes / (bytes * per_sm)));
+    constexpr int kStageBytes = OP != kRowGateQ8 && !ALIGNED ? kStageWords * 4 : 0;  // of a warp
+    cfg.dynamicSmemBytes = (size_t)threads * groups / 32 * kStageBytes;
     if (!fits) return cudaLaunchKernelEx(&cfg, row_kernel<TYPE, OP, ACT, 1, false, ALIGNED>, q);
-    cfg.dynamicSmemBytes = (size_t)bytes * q.stages;
+    cfg.dynamicSmemBytes += (size_t)bytes * q.stages;
     const auto kernel = few ? row_kernel<TYPE, OP, ACT, 1, true, ALIGNED> : row_kernel<TYPE, OP, ACT, kDeep, true, ALIGNED>;
     static std::atomic<bool> configured[kMaxDevices][2];
     if (p.device >= kMaxDevices) return cudaErrorInvalidDevice;
     if (!configured[p.device][few].load()) {
         const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kRingBytes + row_threads(OP) / 32 * kStageBytes);
         if (e != cudaSuccess) return e;
         configured[p.device][few].store(true);
     }

@@ -83,6 +83,13 @@ def _plain(index, dtype, n, t):
             and t.is_contiguous())
 
 
+def _written(*tensors):
+    """Graphs that hold a given output will know that it was overwritten."""
+    for t in tensors:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 def _norm_usual(x, weight, stream):
     """Whether a norm of x can take the short way, as far as these say."""
     index, shape = x.get_device(), x.shape
@@ -152,12 +159,14 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, y=None, h=None, stream
         # (the gradient runs on the stream that is current here)
         with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
             return _Norm.apply(x, weight, residual, float(eps))
+    if y is not None or h is not None:
+        _written(y, h)
     if _norm_usual(x, weight, stream):
         index, dtype, shape = x.get_device(), x.dtype, x.shape
         if y is None:
-            y = torch.empty(shape, dtype=dtype, device=x.device)
+            y = torch.empty_like(x)
         if h is None and residual is not None:
-            h = torch.empty(shape, dtype=dtype, device=x.device)
+            h = torch.empty_like(x)
         a = _rows(index, dtype, shape, x, residual, h, y)
         if a is not None and a[4] != a[6]:
             _launch(_sg.library().sgemm_rms_norm, index, *shape, _TYPES[dtype], *a[:4],
@@ -213,12 +222,14 @@ def rms_norm_backward(dy, x, weight, residual=None, dh=None, eps: float = 1e-6, 
     and of the residual alike.  Outputs not given are allocated (dx may be dy or dh
     itself); ``need_dx`` and ``need_dw`` leave one out (None is returned in its place).
     """
+    if dx is not None or dweight is not None:
+        _written(dx, dweight)
     if _norm_usual(x, weight, stream):
         index, dtype, shape = x.get_device(), x.dtype, x.shape
         if not need_dx:
             dx = None
         elif dx is None:
-            dx = torch.empty(shape, dtype=dtype, device=x.device)
+            dx = torch.empty_like(x)
         if not need_dw:
             dweight = None
         elif dweight is None:
@@ -269,10 +280,12 @@ def rms_norm_q8(x, weight, residual=None, eps: float = 1e-6, h=None, q=None, sca
     through it: inputs that require one are refused.
     """
     _no_gradient("rms_norm_q8", x, weight, residual)
+    if h is not None:
+        _written(h)
     if q is None and scales is None and _norm_usual(x, weight, stream):
         index, dtype, (T, D) = x.get_device(), x.dtype, x.shape
         if h is None and residual is not None:
-            h = torch.empty(T, D, dtype=dtype, device=x.device)
+            h = torch.empty_like(x)
         a = _rows(index, dtype, x.shape, x, residual, h)
         if a is not None:
             q = _empty_codes(T, D, x.device, None)
@@ -370,6 +383,8 @@ class Q8Matrix:
         M, N, K, index = x.shape[0], self.N, self.K, self._index
         if y is None:
             y = _empty(M, N, self.dtype, self.device, stream)
+        else:
+            _written(y)
         if stream is None and index == _current_device() and _plain(index, torch.float32, M, x_scales):
             a, b = _rows(index, torch.int8, (M, K), x), _rows(index, self.dtype, (M, N), y)
             if a is not None and b is not None:

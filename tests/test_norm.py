@@ -304,6 +304,18 @@ def test_frozen_inputs_get_no_gradient(device):
         sg.rms_norm(a, w, y=torch.empty_like(x))
 
 
+@gpu
+def test_a_tensor_overwritten_in_place_is_known_to_graphs_that_hold_it(device):
+    (x, r), w = make(6, 40, "fp32", "fp32", count=2)
+    a = x.clone().requires_grad_()
+    b = a * 2
+    loss = (b * b).sum()  # holds b
+    with torch.no_grad():
+        sg.rms_norm(r, w, residual=b, h=b)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
 # ---- refusals ---------------------------------------------------------------------
 
 def call(name, **change):
