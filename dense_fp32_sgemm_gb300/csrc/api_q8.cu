@@ -86,7 +86,7 @@ bool norm_vec(const NormArgs &a) {
 // takes 4 for each token of a pair's tile (single CTAs 4 too: half the products, but
 // operands that pass through shared memory twice as often), at least 700, which its
 // weights take to be widened and to come from HBM.  A tile takes 3000 more for its results, one
-// cut in n pieces 5000 and 1200 n for those to meet.  (Even shares of the tail for
+// cut in pieces 5000 for those to meet, and 600 for each.  (Even shares of the tail for
 // all workers, as the gated block has them, touch two tiles each and meet twice:
 // 96 x 4096 x 4096 26 us.)
 bool q8_plan(Q8GemmParams &p, bool &pair, int num_sms) {
@@ -106,7 +106,7 @@ bool q8_plan(Q8GemmParams &p, bool &pair, int num_sms) {
             for (int n = 1; n == 1 || (n * tail <= workers && n <= p.stages_k); ++n) {
                 const int per_piece = (p.stages_k + n - 1) / n;
                 const double cost = whole + (tail ? per_piece * stage + 3000.0 : 0.0) +
-                                    (n > 1 ? 5000.0 + 1200.0 * n * tokens / most : 0.0);
+                                    (n > 1 ? 5000.0 + 600.0 * n * tokens / most : 0.0);
                 if (least < 0.0 || cost < least) {
                     least = cost;
                     pair = two != 0;
@@ -116,7 +116,7 @@ bool q8_plan(Q8GemmParams &p, bool &pair, int num_sms) {
                     p.workers = workers;
                     p.full_tiles = full;
                     p.tail_tiles = tail;
-                    p.tail_workers = n > 1 ? tail * n : 0;
+                    p.pieces = n;
                 }
                 if (tail == 0) break;
             }
@@ -305,7 +305,6 @@ sgemm_status_t sgemm_q8_matmul(int64_t M, int64_t N, int64_t K, int type, const 
     const int64_t ld_w = in_place ? ldw : up(K, 16), ld_x = up(K, 64);
     const size_t w_at = in_place ? 0 : take((size_t)(N * ld_w));
     const size_t x_at = stream_form ? 0 : take((size_t)(M * ld_x) * 2);
-    const size_t part_at = stream_form ? 0 : take((size_t)2 * dev.num_sms * q8_slot_ints() * sizeof(int));
     char *base = nullptr;
     if (bytes) {
         void *p = nullptr;
@@ -335,10 +334,11 @@ sgemm_status_t sgemm_q8_matmul(int64_t M, int64_t N, int64_t K, int type, const 
     p.M = (int)M; p.N = (int)N; p.K = (int)K;
     bool pair = false;
     if (!q8_plan(p, pair, dev.num_sms)) return SGEMM_ERR_UNSUPPORTED;
-    s = op_counters(st, (size_t)dev.num_sms * 8, &p.counters);
+    // (15 MB whatever the sizes, so that the first call on a stream is the one that allocates)
+    s = op_counters(st, (size_t)dev.num_sms * (8 + q8_tile_ints()), &p.counters);
     if (s != SGEMM_OK) return s;
+    p.meet = p.counters + (size_t)dev.num_sms * 8;
     uint16_t *wide = reinterpret_cast<uint16_t *>(base + x_at);
-    p.partials = reinterpret_cast<int *>(base + part_at);
     p.x_scales = x_scales;
     p.w_scales = w_scales;
     p.y = y; p.ldy = ldy;

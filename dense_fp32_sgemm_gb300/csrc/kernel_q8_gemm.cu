@@ -57,8 +57,7 @@ constexpr int kMaxDevices = 64;
 struct Unit {
     int m, n;           // tile along the tokens, along the channels
     int s0, s1;         // stages [s0, s1)
-    int pieces, piece;  // the tile's stretches, and which this is
-    int first;          // the worker of piece 0
+    int pieces;         // the tile's stretches
     int tail;           // the tile's number in the tail
 };
 
@@ -74,49 +73,26 @@ __device__ __forceinline__ void locate(const Q8GemmParams &p, int t, Unit &u) {
     u.m = t / rows;
 }
 
-// The worker's i-th unit; false when there is none.  The tail's stages are shared
-// out evenly, so a worker's share touches at most two tiles when it is no longer
-// than a tile, which it never is (fewer tail tiles than workers).
+// The worker's i-th unit; false when there is none.  A tail tile's stages are shared out
+// evenly over as many workers as it has pieces.
 __device__ __forceinline__ bool unit_at(const Q8GemmParams &p, int worker, int i, Unit &u) {
-    if (i < p.full_tiles || p.tail_workers == 0) {
-        const int t = worker + i * p.workers;
-        if (t >= p.tiles_m * p.tiles_n) return false;
-        locate(p, t, u);
-        u.s0 = 0;
-        u.s1 = p.stages_k;
-        u.pieces = 1;
-        u.piece = u.tail = 0;
-        u.first = worker;
-        return true;
+    u.s0 = 0;
+    u.s1 = p.stages_k;
+    u.pieces = 1;
+    u.tail = 0;
+    int t = worker + i * p.workers;
+    if (i >= p.full_tiles && p.pieces > 1) {
+        if (i > p.full_tiles || worker >= p.tail_tiles * p.pieces) return false;
+        u.pieces = p.pieces;
+        u.tail = worker / p.pieces;
+        const int piece = worker - u.tail * p.pieces;
+        u.s0 = piece * p.stages_k / p.pieces;
+        u.s1 = (piece + 1) * p.stages_k / p.pieces;
+        t = p.full_tiles * p.workers + u.tail;
     }
-    if (worker >= p.tail_workers || i > p.full_tiles + 1) return false;
-    const long long steps = p.stages_k, all = p.tail_tiles * steps, n = p.tail_workers;
-    long long a = worker * all / n;
-    const long long e = (worker + 1) * all / n;
-    long long end = min(e, (a / steps + 1) * steps);
-    if (i > p.full_tiles) {
-        a = end;
-        end = e;
-    }
-    if (a >= end) return false;
-    const int t = (int)(a / steps);
-    // Worker w starts at floor(w all / n), so stage x is worker
-    // floor(((x + 1) n - 1) / all)'s.
-    const long long x0 = t * steps;
-    locate(p, p.full_tiles * p.workers + t, u);
-    u.tail = t;
-    u.s0 = (int)(a - x0);
-    u.s1 = (int)(end - x0);
-    u.first = (int)(((x0 + 1) * n - 1) / all);
-    u.pieces = (int)(((x0 + steps) * n - 1) / all) - u.first + 1;
-    u.piece = worker - u.first;
+    if (t >= p.tiles_m * p.tiles_n) return false;
+    locate(p, t, u);
     return true;
-}
-
-// Slot of piece q: a worker's first slot holds a piece that starts inside its
-// tile, the second one that starts with it.
-__device__ __forceinline__ int piece_slot(const Unit &u, int q) {
-    return 2 * (u.first + q) + (q == 0 ? 1 : 0);
 }
 
 // Four signed bytes to four FP16 values: with the sign bit flipped a byte is x +
@@ -435,20 +411,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             bool emit = true;
             if (unit.pieces > 1) {
-                // 16 bytes a lane, a part's four one after the other.
-                auto slot = [&](int q) {
-                    return reinterpret_cast<int4 *>(
-                               p.partials + ((size_t)(piece_slot(unit, q) * CG + (int)rank) * kEpiWarps +
-                                             (warp - kFirstEpi)) * (kParts * 16 * 32)) + lane;
-                };
-                int4 *to = slot(unit.piece);
+                // The pieces are added up in L2 (whole numbers: in any order), where all is zero
+                // before and, when the last to arrive has read it, again.
+                int *meet = p.meet + ((size_t)(unit.tail * CG + (int)rank) * kEpiWarps + (warp - kFirstEpi)) *
+                                         (kParts * 16 * 32) + lane;
 #pragma unroll
                 for (int j = 0; j < kParts; ++j)
                     if (j < parts) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            __stcg(to + (j * 4 + i) * 32, make_int4(sum[j][4 * i], sum[j][4 * i + 1],
-                                                                    sum[j][4 * i + 2], sum[j][4 * i + 3]));
+                        for (int i = 0; i < 16; ++i) atomicAdd(meet + (j * 16 + i) * 32, sum[j][i]);
                     }
                 __threadfence();
                 __syncwarp();
@@ -460,26 +431,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 emit = __shfl_sync(0xffffffffu, arrived, 0) == unit.pieces - 1;
                 __threadfence();
-                // The last to arrive adds the other pieces to its own.
-                if (emit)
-                    for (int q = 0; q < unit.pieces; ++q) {
-                        if (q == unit.piece) continue;
-                        const int4 *from = slot(q);
+                if (emit) {
 #pragma unroll
-                        for (int j = 0; j < kParts; ++j)
-                            if (j < parts) {
-                                int4 v[4];
+                    for (int j = 0; j < kParts; ++j)
+                        if (j < parts) {
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) v[i] = __ldcg(from + (j * 4 + i) * 32);
+                            for (int i = 0; i < 16; ++i) sum[j][i] = __ldcg(meet + (j * 16 + i) * 32);
+                        }
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    sum[j][4 * i] += v[i].x;
-                                    sum[j][4 * i + 1] += v[i].y;
-                                    sum[j][4 * i + 2] += v[i].z;
-                                    sum[j][4 * i + 3] += v[i].w;
-                                }
-                            }
-                    }
+                    for (int j = 0; j < kParts; ++j)
+                        if (j < parts) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) __stcg(meet + (j * 16 + i) * 32, 0);
+                        }
+                }
             }
             if (emit) {
                 // 16 tokens at a time through shared memory, from a lane a channel to 16 bytes
@@ -559,7 +524,7 @@ cudaError_t launch_one(const CUtensorMap &w, const CUtensorMap &x, const Q8GemmP
         configured[p.device].store(true);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(CG * (p.full_tiles > 0 ? p.workers : p.tail_workers ? p.tail_workers : p.tail_tiles));
+    cfg.gridDim = dim3(CG * (p.full_tiles > 0 ? p.workers : p.tail_tiles * p.pieces));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;

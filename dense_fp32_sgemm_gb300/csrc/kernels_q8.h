@@ -107,11 +107,11 @@ struct Q8GemmParams {
     int tokens;                       // of a tile
     int tiles_n, tiles_m;
     int stages_k;                     // ceil(K / kQ8StageK)
-    // Workers (CTAs or pairs) take full_tiles each, round-robin; the stages of the
-    // tail_tiles left over are shared out evenly over tail_workers (0: taken whole).
-    int workers, full_tiles, tail_tiles, tail_workers;
-    int *partials;                    // 2 slots per worker of q8_slot_ints() per CTA
-    int *counters;                    // tail_tiles x CTAs of a worker x 8, zero at rest
+    // Workers (CTAs or pairs) take full_tiles each, round-robin; the tail_tiles left over are
+    // cut along k into `pieces` of a worker each.
+    int workers, full_tiles, tail_tiles, pieces;
+    int *counters;                    // CTAs of the tail's tiles x 8, zero at rest
+    int *meet;                        // as many accumulators of q8_tile_ints(), zero at rest
     const float *x_scales, *w_scales;
     void *y;
     long long ldy;
@@ -121,7 +121,7 @@ struct Q8GemmParams {
     unsigned long long timeout_ns;
     int skip_loads_from;
 };
-inline int q8_slot_ints() { return kQ8Channels * kQ8Tokens * 2; }
+constexpr int q8_tile_ints() { return kQ8Channels * kQ8Tokens * 2; }  // of a CTA
 // w: boxes of 128 channels x 128 bytes; x: fp16, boxes of two stretches of tokens x 64
 // (128-byte swizzles).
 cudaError_t launch_q8_gemm(const CUtensorMap &w, const CUtensorMap &x, const Q8GemmParams &p,

@@ -374,9 +374,9 @@ def test_empty_products(device):
 @gpu
 @pytest.mark.parametrize("M", [40, 200])
 def test_a_wait_that_runs_out_is_reported(device, M):
-    # The loads stop after two stages: every role's wait ends, the call is flagged, and
-    # the next one is right again.
-    x, w = random_codes(M, 4096, 1), random_codes(512, 4096, 2)
+    # The loads stop after two stages (of 512, which at most 152 CTAs share): every role's
+    # wait ends, the call is flagged, and the next one is right again.
+    x, w = random_codes(M, 65536, 1), random_codes(512, 65536, 2)
     m = sg.Q8Matrix(w, scales(512, 4), dtype=torch.float32)
     xs = scales(M, 3)
     want = m.matmul(x, xs)
