@@ -4,7 +4,9 @@ A gated block with 16-bit weights learns to imitate another one: forward and
 backward pass (ffn_forward, ffn_backward), and an AdamW step (AdamW) with 8-bit
 states on FP32 master weights that writes the 16-bit weights back.  Then its
 weights are quantised to four bits (w4_quantize) and single tokens go through
-the quantised block (W4Matrix.matvec) and through the 16-bit one.
+the quantised block (W4Matrix.matvec) and through the 16-bit one.  Prompts go through the
+block in eight bits: the norm in front of it, whose residual it adds (rms_norm_q8), both
+halves' products in one (Q8Matrix.matmul), the gate (gate_q8) and the down product.
 
     python examples/feed_forward.py [steps]
 """
@@ -65,11 +67,33 @@ def serve(weights, tokens=4, group=64, seed=2):
     return (off / size) ** 0.5
 
 
+def serve_prompt(weights, rows=200, seed=3):
+    """A prompt through the norm and the block in 8 bits, and through both in 16; returns
+    the relative difference of their outputs."""
+    gen = torch.Generator("cuda").manual_seed(seed)
+    w_gate, w_up, w_down = weights
+    first = sg.q8_quantize(torch.cat([w_gate, w_up], dim=1))
+    down = sg.q8_quantize(w_down)
+    F = w_gate.shape[1]
+    x, stream = (torch.randn(rows, first.K, generator=gen, device="cuda").to(w_gate.dtype)
+                 for _ in range(2))
+    norm = torch.ones(first.K, device="cuda")
+    q, scales, h = sg.rms_norm_q8(x, norm, residual=stream)
+    both = first.matmul(q, scales)
+    q, scales = sg.gate_q8(both[:, :F], both[:, F:])
+    y = down.matmul(q, scales).float()
+    n, h16 = sg.rms_norm(x, norm, residual=stream)
+    assert torch.equal(h, h16)
+    want = sg.ffn_forward(n, *weights).float()
+    return float((y - want).norm() / want.norm())
+
+
 def main(steps=60):
     sg.build()
     weights, losses = train(steps)
     print(f"mean squared error: {losses[0]:.4f} at the first step, {losses[-1]:.4f} at step {steps}")
     print(f"4-bit weights: outputs {serve(weights):.3f} off the 16-bit block's")
+    print(f"8 bits: outputs {serve_prompt(weights):.4f} off the 16-bit block's")
 
 
 if __name__ == "__main__":
