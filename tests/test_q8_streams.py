@@ -26,15 +26,16 @@ EMPTY, EMPTY_STRIDED = torch.empty, torch.empty_strided
 class OnDevice:
     """What the wrappers read of a CUDA tensor, without one."""
 
+    end = 0
+
     def __init__(self, *shape, dtype=torch.float32, strides=None):
         t = EMPTY(*shape, dtype=dtype) if strides is None else \
             EMPTY_STRIDED(shape, strides, dtype=dtype)
         self.dtype, self.shape, self.device = dtype, t.shape, torch.device("cuda", 0)
         self.dim, self.stride, self.numel = t.dim, t.stride, t.numel
         self.is_contiguous, self.requires_grad = t.is_contiguous, False
-
-    def data_ptr(self):
-        return 4096
+        OnDevice.end += 4096
+        self.data_ptr = lambda at=OnDevice.end: at
 
     def get_device(self):
         return 0
