@@ -160,7 +160,9 @@ sgemm_status_t sgemm_rms_norm_q8(int64_t T, int64_t D, int type, const void *x, 
     sgemm_status_t s = check_norm(a);
     if (s != SGEMM_OK) return s;
     if (ldq < at_least_one(D)) return SGEMM_ERR_INVALID_ARG;
-    if (T == 0 || D == 0) return SGEMM_OK;
+    if (T == 0) return SGEMM_OK;
+    // (rows of nothing have the scale of rows of zeros)
+    if (D == 0) return sgemm_q8_gate(T, 0, type, 0, nullptr, 1, nullptr, 1, q, ldq, scales, stream);
     if (!q || !scales || !aligned(scales, 4)) return SGEMM_ERR_INVALID_ARG;
     std::lock_guard<std::mutex> lock(api_mutex());
     OpDevice dev;

@@ -55,6 +55,7 @@ SGEMM_API sgemm_status_t sgemm_rms_norm(int64_t T, int64_t D, int type, const vo
  * scales (T floats).  The row that is coded is a = h * weight, whose codes do
  * not depend on the norm; its scale is top / 127 / sqrt(mean(h^2) + eps).  h is
  * added in more bits where a code needs them.  q overlaps no other argument.
+ * D == 0: the scales are 2^-96 / 127.
  */
 SGEMM_API sgemm_status_t sgemm_rms_norm_q8(int64_t T, int64_t D, int type, const void *x,
                                            int64_t ldx, const void *residual, int64_t ldr,

@@ -369,6 +369,9 @@ def test_empty_products(device):
     q, s = sg.rows_q8(torch.empty(3, 0, device="cuda"))
     assert q.shape == (3, 0) and bool((s == ZERO).all())
     assert sg.rows_q8(torch.empty(0, 7, device="cuda"))[0].shape == (0, 7)
+    x, s = torch.empty(3, 0, device="cuda"), torch.full((3,), 5.0, device="cuda")
+    q, s = sg.rms_norm_q8(x, x[0], scales=s)
+    assert q.shape == (3, 0) and bool((s == ZERO).all())
 
 
 @gpu
