@@ -8,9 +8,12 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import hashlib
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -28,6 +31,11 @@ HEADERS = ["device_common.cuh", "kernels.h", "kernels_3xtf32.h", "plan.h",
            "kernels_ffn.h", "ops_internal.h", "ops_common.cuh",
            "tc_common.cuh", "ffn_gate.cuh", "kernels_q8.h", "row_codes.cuh", "row_io.cuh", "row_kernel.cuh"]
 PUBLIC_HEADERS = ["sgemm.h", "sgemm_probe.h", "sgemm_ffn.h", "sgemm_q8.h"]
+
+# The usual calls on torch tensors, a Python extension beside the library (not made where
+# there is no torch for CUDA).
+CALLS_SOURCE = "torch_calls.cpp"
+CALLS_PATH = os.path.join(BUILD, "_torch_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -48,14 +56,51 @@ def nvcc() -> str:
 
 def _digest() -> str:
     h = hashlib.sha256()
-    for name in SOURCES + HEADERS:
+    for name in SOURCES + HEADERS + [CALLS_SOURCE]:
         with open(os.path.join(CSRC, name), "rb") as f:
             h.update(name.encode() + b"\0" + f.read())
     for name in PUBLIC_HEADERS:
         with open(os.path.join(INCLUDE, name), "rb") as f:
             h.update(name.encode() + b"\0" + f.read())
-    h.update(" ".join(ARCH + NVCC_FLAGS).encode())
+    h.update(" ".join(ARCH + NVCC_FLAGS + _torch()[1:]).encode())
     return h.hexdigest()
+
+
+def _torch() -> list[str]:
+    """Where torch lies, its version and Python's; nothing where there is none for CUDA."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations or not os.path.exists(
+            os.path.join(spec.submodule_search_locations[0], "lib", "libc10_cuda.so")):
+        return []
+    return [spec.submodule_search_locations[0], importlib.metadata.version("torch"),
+            sysconfig.get_python_version()]
+
+
+def _compile_calls() -> str | None:
+    if not _torch():
+        return None
+    torch = _torch()[0]
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    obj = os.path.join(BUILD, "torch_calls.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           "-I", os.path.join(torch, "include"), "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(cuda, "include"), "-c", os.path.join(CSRC, CALLS_SOURCE), "-o", obj]
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError(f"g++ failed for {CALLS_SOURCE}:\n{proc.stdout}\n{proc.stderr}")
+    return obj
+
+
+def _link_calls(obj: str) -> None:
+    # (torch's libraries are in the process when it is imported)
+    tmp = CALLS_PATH + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + BUILD, "-l:" + LIB_NAME, "-Wl,-rpath,$ORIGIN",
+           "-L" + os.path.join(_torch()[0], "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
+           "-lc10_cuda"]
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError(f"link of {CALLS_SOURCE} failed:\n{proc.stdout}\n{proc.stderr}")
+    os.replace(tmp, CALLS_PATH)
 
 
 def _compile(src: str) -> tuple[str, str]:
@@ -76,8 +121,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if (not force and os.path.exists(LIB_PATH) and os.path.exists(stamp)
             and open(stamp).read().strip() == digest):
         return LIB_PATH
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
+        calls = pool.submit(_compile_calls)
         results = list(pool.map(_compile, SOURCES))
+        calls = calls.result()
     with open(os.path.join(BUILD, "ptxas.log"), "w") as log:
         for (obj, err), src in zip(results, SOURCES):
             log.write(f"== {src}\n{err}\n")
@@ -87,6 +134,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if proc.returncode != 0:
         raise RuntimeError(f"link failed:\n{proc.stdout}\n{proc.stderr}")
     os.replace(tmp, LIB_PATH)
+    if calls:
+        _link_calls(calls)
     with open(stamp, "w") as f:
         f.write(digest + "\n")
     if verbose:

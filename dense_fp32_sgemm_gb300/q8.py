@@ -10,13 +10,15 @@ ffn.py.
 from __future__ import annotations
 
 import contextlib
+import importlib.util
 
 import torch
 from torch.autograd.function import once_differentiable
 
 import dense_fp32_sgemm_gb300 as _sg
 
-from .ffn import _TYPES, _call, _empty, _matrix, _raw_stream, _type_of
+from . import _build
+from .ffn import _TYPES, _call, _empty, _matrix, _type_of
 
 _Q8_MOST_K = 131071
 
@@ -48,60 +50,36 @@ def _empty_codes(rows, cols, device, stream):
         return torch.empty_strided(shape, strides, dtype=torch.int8, device=device)
 
 
-# A call takes a few microseconds on the device and its checks several times as long on
-# the host (Grace, one by one: 20 us for the norm of one row, 8 without them).  So the usual
-# call, matrices of one type on the current device and its current stream, goes to the
-# library at once; all others, and all refusals, go through _matrix() and _vector().
-
-_current_device = torch._C._cuda_getDevice
-
-
-def _rows(index, dtype, shape, *tensors):
-    """Addresses and leading dimensions of matrices (or None) of this type and shape on this
-    device; None where one of them is not."""
-    args = []
-    D = shape[1]
-    for t in tensors:
-        if t is None:
-            args += (None, D or 1)
-            continue
-        if t.dtype is not dtype or t.get_device() != index or t.shape != shape:
-            return None
-        if t.is_contiguous():
-            args += (t.data_ptr(), D or 1)
-        else:
-            step, unit = t.stride()
-            if unit != 1 or step < D or D < 2 or shape[0] < 2:
-                return None
-            args += (t.data_ptr(), step)
-    return args
+# A call takes a few microseconds on the device and its checks several times as long here.
+# So the usual call, matrices of one type on the current device and its current stream, goes
+# through csrc/torch_calls.cpp, which answers None where there is more to it; all others,
+# and all refusals, go the way of this file.
+_calls = None
 
 
-def _plain(index, dtype, n, t):
-    """Whether t is a contiguous vector of n elements of this type on this device."""
-    return (t.dtype is dtype and t.get_device() == index and t.dim() == 1 and t.numel() == n
-            and t.is_contiguous())
+def _load_calls():
+    """The extension, once the library is there."""
+    global _calls
+    _sg.library()
+    spec = importlib.util.spec_from_file_location("_torch_calls", _build.CALLS_PATH)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    _calls = module
+    return module
+
+
+def _done(result, name):
+    """What a call returned, or the error that its status stands for."""
+    if type(result) is int:
+        raise _sg.SgemmError(result, name)
+    return result
 
 
 def _written(*tensors):
     """Graphs that hold a given output will know that it was overwritten."""
     for t in tensors:
-        if t is not None:
+        if t is not None and not t.is_inference():
             torch.autograd.graph.increment_version(t)
-
-
-def _norm_usual(x, weight, stream):
-    """Whether a norm of x can take the short way, as far as these say."""
-    index, shape = x.get_device(), x.shape
-    return (stream is None and index >= 0 and len(shape) == 2 and x.dtype in _TYPES
-            and index == _current_device() and _plain(index, weight.dtype, shape[1], weight)
-            and (weight.dtype is x.dtype or weight.dtype is torch.float32))
-
-
-def _launch(fn, index, *args):
-    status = fn(*args, _raw_stream(index))
-    if status != 0:
-        raise _sg.SgemmError(status, fn.__name__)
 
 
 def _address(t, name, rows, cols, dtype, device):
@@ -152,6 +130,10 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, y=None, h=None, stream
     their gradients go through rms_norm_backward() with h, which the graph keeps (the rounded
     sum alone, not x and the residual).  A given y or h is refused then.
     """
+    if stream is None:
+        got = (_calls or _load_calls()).rms_norm(x, weight, residual, eps, y, h)
+        if got is not None:
+            return _done(got, "sgemm_rms_norm")
     if _graph(x, weight, residual):
         if y is not None or h is not None:
             raise ValueError("a given y or h has no gradient, and an input requires one: "
@@ -159,19 +141,7 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, y=None, h=None, stream
         # (the gradient runs on the stream that is current here)
         with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
             return _Norm.apply(x, weight, residual, float(eps))
-    if y is not None or h is not None:
-        _written(y, h)
-    if _norm_usual(x, weight, stream):
-        index, dtype, shape = x.get_device(), x.dtype, x.shape
-        if y is None:
-            y = torch.empty_like(x)
-        if h is None and residual is not None:
-            h = torch.empty_like(x)
-        a = _rows(index, dtype, shape, x, residual, h, y)
-        if a is not None and a[4] != a[6]:
-            _launch(_sg.library().sgemm_rms_norm, index, *shape, _TYPES[dtype], *a[:4],
-                    weight.data_ptr(), _TYPES[weight.dtype], float(eps), *a[4:])
-            return y if residual is None else (y, h)
+    _written(y, h)
     T, D, dev, args, h, ha = _norm_args(x, weight, residual, eps, h, stream, residual is not None)
     if y is None:
         y = _empty(T, D, x.dtype, dev, stream)
@@ -222,25 +192,12 @@ def rms_norm_backward(dy, x, weight, residual=None, dh=None, eps: float = 1e-6, 
     and of the residual alike.  Outputs not given are allocated (dx may be dy or dh
     itself); ``need_dx`` and ``need_dw`` leave one out (None is returned in its place).
     """
-    if dx is not None or dweight is not None:
-        _written(dx, dweight)
-    if _norm_usual(x, weight, stream):
-        index, dtype, shape = x.get_device(), x.dtype, x.shape
-        if not need_dx:
-            dx = None
-        elif dx is None:
-            dx = torch.empty_like(x)
-        if not need_dw:
-            dweight = None
-        elif dweight is None:
-            dweight = torch.empty_like(weight)
-        a = _rows(index, dtype, shape, x, residual, dy, dh, dx)
-        if a is not None and (dweight is None
-                              or _plain(index, weight.dtype, shape[1], dweight)):
-            _launch(_sg.library().sgemm_rms_norm_backward, index, *shape, _TYPES[dtype], *a[:4],
-                    weight.data_ptr(), _TYPES[weight.dtype], float(eps), *a[4:],
-                    None if dweight is None else dweight.data_ptr())
-            return dx, dweight
+    if stream is None:
+        got = (_calls or _load_calls()).rms_norm_backward(x, weight, residual, eps, dy, dh, dx, dweight,
+                                                          need_dx, need_dw)
+        if got is not None:
+            return _done(got, "sgemm_rms_norm_backward")
+    _written(dx, dweight)
     T, D, dev, args, _, dha = _norm_args(x, weight, residual, eps, dh, stream, False, "dh")
     dya = _address(dy, "dy", T, D, x.dtype, dev)
     dxa, dwa = (None, max(D, 1)), None
@@ -279,21 +236,12 @@ def rms_norm_q8(x, weight, residual=None, eps: float = 1e-6, h=None, q=None, sca
     residual.  A row with an infinity or NaN has the scale NaN.  No gradient goes
     through it: inputs that require one are refused.
     """
+    if stream is None and q is None and scales is None:
+        got = (_calls or _load_calls()).rms_norm_q8(x, weight, residual, eps, h)
+        if got is not None:
+            return _done(got, "sgemm_rms_norm_q8")
     _no_gradient("rms_norm_q8", x, weight, residual)
-    if h is not None:
-        _written(h)
-    if q is None and scales is None and _norm_usual(x, weight, stream):
-        index, dtype, (T, D) = x.get_device(), x.dtype, x.shape
-        if h is None and residual is not None:
-            h = torch.empty_like(x)
-        a = _rows(index, dtype, x.shape, x, residual, h)
-        if a is not None:
-            q = _empty_codes(T, D, x.device, None)
-            scales = torch.empty(T, dtype=torch.float32, device=x.device)
-            _launch(_sg.library().sgemm_rms_norm_q8, index, T, D, _TYPES[dtype], *a[:4],
-                    weight.data_ptr(), _TYPES[weight.dtype], float(eps), *a[4:], q.data_ptr(),
-                    -(-D // 16) * 16 or 1, scales.data_ptr())
-            return (q, scales) if residual is None else (q, scales, h)
+    _written(h)
     T, D, dev, args, h, ha = _norm_args(x, weight, residual, eps, h, stream, residual is not None)
     q, scales, qa = _codes(q, scales, T, D, dev, stream)
     _call(_sg.library().sgemm_rms_norm_q8, dev, stream, *args, *ha, *qa)
@@ -306,20 +254,13 @@ def gate_q8(g, u, activation: int = 0, q=None, scales=None, stream=None):
     g, u: T x F of one type (they may be halves of one matrix).  ``activation`` is
     GATE_SILU, GATE_GELU or GATE_RELU.  Otherwise as rms_norm_q8.
     """
+    if stream is None and q is None and scales is None and u is not None:
+        got = (_calls or _load_calls()).gate_q8(g, u, activation)
+        if got is not None:
+            return _done(got, "sgemm_q8_gate")
     _no_gradient("gate_q8", g, u)
     if g.dim() != 2:
         raise ValueError("g must be 2-D")
-    index, dtype, shape = g.get_device(), g.dtype, g.shape
-    if (stream is None and q is None and scales is None and index >= 0 and dtype in _TYPES
-            and index == _current_device()):
-        a = _rows(index, dtype, shape, g, u)
-        if a is not None:
-            T, F = shape
-            q = _empty_codes(T, F, g.device, None)
-            scales = torch.empty(T, dtype=torch.float32, device=g.device)
-            _launch(_sg.library().sgemm_q8_gate, index, T, F, _TYPES[dtype], int(activation), *a,
-                    q.data_ptr(), -(-F // 16) * 16 or 1, scales.data_ptr())
-            return q, scales
     T, F = g.shape
     dev = g.device
     kind = _type_of(g, "g")
@@ -332,6 +273,10 @@ def gate_q8(g, u, activation: int = 0, q=None, scales=None, stream=None):
 
 def rows_q8(x, q=None, scales=None, stream=None):
     """The rows of x in 8 bits: (q, scales).  Otherwise as rms_norm_q8."""
+    if stream is None and q is None and scales is None:
+        got = (_calls or _load_calls()).gate_q8(x, None, 0)
+        if got is not None:
+            return _done(got, "sgemm_q8_gate")
     _no_gradient("rows_q8", x)
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
@@ -370,32 +315,28 @@ class Q8Matrix:
                 torch.cuda.current_stream(dev).synchronize()
             w, ldw = _matrix(qweight, "qweight", self.N, self.K, torch.int8, dev)
         self.qweight, self.scales, self.dtype, self.device = qweight, scales, dtype, dev
-        self.type = _TYPES[dtype]
-        self._weights = (w, ldw, s)
-        self._index = dev.index
-        self._fn = _sg.library().sgemm_q8_matmul
+        self._weights = (self.N, self.K, _TYPES[dtype], w, ldw, s, dev.index)
 
     def matmul(self, x, x_scales, y=None, stream=None):
         """y[m] = x_scales[m] * (x[m] @ W) for M x K codes x (int8) and M scales, as
         rms_norm_q8, gate_q8 and rows_q8 return them.  The sums are exact.  Returns y
         (allocated when not given).  No gradient goes through it."""
+        if stream is None:
+            got = (_calls or _load_calls()).q8_matmul(x, x_scales, y, self._weights)
+            if got is not None:
+                return _done(got, "sgemm_q8_matmul")
         _no_gradient("Q8Matrix.matmul", x_scales, y)
-        M, N, K, index = x.shape[0], self.N, self.K, self._index
-        if y is None:
-            y = _empty(M, N, self.dtype, self.device, stream)
-        else:
-            _written(y)
-        if stream is None and index == _current_device() and _plain(index, torch.float32, M, x_scales):
-            a, b = _rows(index, torch.int8, (M, K), x), _rows(index, self.dtype, (M, N), y)
-            if a is not None and b is not None:
-                _launch(self._fn, index, M, N, K, self.type, *a, x_scales.data_ptr(),
-                        *self._weights, *b)
-                return y
         if x.dim() != 2:
             raise ValueError("x must be 2-D")
+        M = x.shape[0]
+        if y is None:
+            y = _empty(M, self.N, self.dtype, self.device, stream)
+        else:
+            _written(y)
         xa = _address(x, "x", M, self.K, torch.int8, self.device)
         sa = _vector(x_scales, "x_scales", M, torch.float32, self.device)
-        _call(self._fn, self.device, stream, M, self.N, self.K, self.type, *xa, sa, *self._weights,
+        N, K, kind, *weights, _ = self._weights
+        _call(_sg.library().sgemm_q8_matmul, self.device, stream, M, N, K, kind, *xa, sa, *weights,
               *_address(y, "y", M, self.N, self.dtype, self.device))
         return y
 

@@ -85,7 +85,6 @@ def test_outputs_are_allocated_under_their_stream(monkeypatch, name):
     with monkeypatch.context() as m:
         m.setattr(torch.cuda, "stream", under)
         m.setattr(q8, "_call", lambda *a: None)
-        m.setattr(q8, "_current_device", lambda: 1)
         m.setattr(torch, "empty", empty)
         m.setattr(torch, "empty_like", lambda t: empty(*t.shape, dtype=t.dtype))
         m.setattr(torch, "empty_strided", empty_strided)
