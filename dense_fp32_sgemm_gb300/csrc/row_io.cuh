@@ -15,8 +15,8 @@ namespace sgemm {
 // Elements of a 16-byte piece.
 constexpr int piece_elements(int type) { return type == kTypeF32 ? 4 : 8; }
 
-// A row to read.  inside: there are rows before it and after it, so that aligned pieces
-// which reach over its ends (by less than 16 bytes) stay inside the matrix.
+// A row to read.  inside: aligned pieces which reach over its ends (by less than 16 bytes)
+// stay inside the matrix; first: those over its beginning do not.
 struct RowSource {
     const char *row;
     int bytes;  // of the row
@@ -24,8 +24,8 @@ struct RowSource {
 };
 __device__ __forceinline__ RowSource row_source(const void *p, long long row, int cols, long long ld,
                                                 int element, long long rows) {
-    return {static_cast<const char *>(p) + row * ld * element, cols * element, row == 0,
-            row > 0 && row + 1 < rows};
+    const long long before = row * ld * element, behind = (rows - 1 - row) * ld * element;
+    return {static_cast<const char *>(p) + before, cols * element, before < 16, before >= 16 && behind >= 16};
 }
 
 // w >> (8 * shift) over eight words, the first four of it; shift in 0 .. 15, even.
