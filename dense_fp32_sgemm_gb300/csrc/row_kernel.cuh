@@ -511,7 +511,10 @@ cudaError_t launch_op(const RowParams &p, int num_sms, cudaStream_t stream) {
     q.stages = std::max(1, std::min(3, kRingBytes / (bytes * per_sm)));
     constexpr int kStageBytes = OP != kRowGateQ8 && !ALIGNED ? kStageWords * 4 : 0;  // of a warp
     cfg.dynamicSmemBytes = (size_t)threads * groups / 32 * kStageBytes;
-    if (!fits) return cudaLaunchKernelEx(&cfg, row_kernel<TYPE, OP, ACT, 1, false, ALIGNED>, q);
+    // (the norm of rows off 16 bytes that fit has a kernel of its own)
+    if (OP == kRowNorm && !ALIGNED || !fits)
+        return cudaLaunchKernelEx(&cfg, row_kernel<TYPE, OP, ACT, 1, false, ALIGNED>, q);
+    if constexpr (OP != kRowNorm || ALIGNED) {
     cfg.dynamicSmemBytes += (size_t)bytes * q.stages;
     const auto kernel = few ? row_kernel<TYPE, OP, ACT, 1, true, ALIGNED> : row_kernel<TYPE, OP, ACT, kDeep, true, ALIGNED>;
     static std::atomic<bool> configured[kMaxDevices][2];
@@ -524,6 +527,7 @@ cudaError_t launch_op(const RowParams &p, int num_sms, cudaStream_t stream) {
         configured[p.device][few].store(true);
     }
     return cudaLaunchKernelEx(&cfg, kernel, q);
+    }
 }
 
 // For one of the library's types and alignments.

@@ -114,6 +114,28 @@ def test_strides_and_alignment(device, T, D, pad, offset, kind):
 
 @gpu
 @pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("pad,offset", [(0, 0), (1, 0), (3, 5), (4, 2)])
+@pytest.mark.parametrize("T,D", [(40, 1), (5, 3), (17, 7), (6, 127), (400, 129), (311, 257), (310, 4099),
+                                 (330, 12287), (310, 16383), (310, 16385)])
+def test_rows_off_16_bytes(device, T, D, pad, offset, kind):
+    # Outputs that start with either half of a word, h's not as y's.
+    (x, r), w = make(T, D, kind, kind, pad, offset, count=2)
+    y, h = forward(x, w, r, kind)
+    forward(x, w, None, kind)
+    for at_y, at_h in ((0, 1), (1, 1), (1, 0), (0, 8)):
+        out_y, out_h = (spread(torch.zeros_like(y), 1, at, 7.0) for at in (at_y, at_h))
+        sg.rms_norm(x, w, residual=r, eps=EPS, y=out_y, h=out_h)
+        hd = x.double() + r.double()
+        within(out_y, hd / (hd.square().mean(1, keepdim=True) + EPS).sqrt() * w.double(), slack_of(D))
+        assert torch.equal(out_h, h)
+        for out, at in ((out_y, at_y), (out_h, at_h)):
+            base = out._base
+            assert bool((base[:at] == 7.0).all()) and bool((base[at + T * (D + 1):] == 7.0).all())
+            assert bool((base[at:at + T * (D + 1)].view(T, D + 1)[:, D:] == 7.0).all())
+
+
+@gpu
+@pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("T,D", [(4, 520), (400, 257), (2, 40001)])
 def test_in_place(device, T, D, kind):
     (x, r, dy, dh), w = make(T, D, kind, kind)
