@@ -294,7 +294,11 @@ sgemm_status_t sgemm_q8_matmul(int64_t M, int64_t N, int64_t K, int type, const 
         const size_t e = type_bytes(type);
         return status(cudaMemset2DAsync(y, ldy * e, 0, N * e, M, st));
     }
-    const bool stream_form = M <= kQ8StreamRows;
+    // From five rows on a pass over a large matrix costs the streaming kernel more in
+    // multiplications than the tensor cores in their second launch (us, streaming and tensor
+    // cores, 5 to 8 rows: 4096 x 4096 14.5 and 14.6, 4096 x 8192 18.6 and 16.7,
+    // 12288 x 4096 22.9 and 18.6, 8192 x 28672 64 and 53; 3 rows of the last 48 and 53).
+    const bool stream_form = M <= 4 || (M <= kQ8StreamRows && N * K <= 24LL << 20);
     const bool in_place = aligned(w, 16) && (N == 1 || ldw % 16 == 0);
 
     // Workspace: aligned weights, x in FP16, partial tiles.

@@ -9,6 +9,10 @@
 // CTA's groups added up, as one of `parts` partial rows, which a second kernel adds up in order.  Every input is read once and
 // every output written once (plus the partial rows).  Rows that are too long for
 // registers are read again (norm_grad_wide_kernel).
+//
+// 8192 x 2048 BF16 with dh: 38 us and 5 for the partial rows (its bytes take 20).  Bound:
+// latency, one CTA of 512 threads an SM, which the weight's gradient leaves no registers beside.
+// Rows off 16 bytes: 1023 x 1025 FP32 11 and 5 us.
 #include <algorithm>
 #include <atomic>
 

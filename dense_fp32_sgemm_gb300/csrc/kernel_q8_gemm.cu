@@ -22,6 +22,13 @@
 //                the 64 tensor-memory columns of a slot
 //   warps 12-19  epilogue: accumulators to integers, scales, stores
 // Tensor memory: two accumulators of 192 columns, two slots of 64.
+// Widening takes a stage's warps some 700 clocks, the products of 192 tokens by a pair
+// 768: from there on the tensor pipe is the bound (90 % busy at 4096 x 4096 x 12288, 204 us,
+// 2.0 PFLOP/s; with the widening of x 12 us more; in a long run 233 to 242, at the power
+// limit).  With fewer tokens it is the weights' way (64 x 12288 x 4096, pieces of 64 tiles:
+// 20 us where HBM would take 7.7): widening, a pipeline of stages that fills once a tile, and
+// the pieces' meeting, 2 to 3 us.
+//
 // Every wait is bounded; a role that gives up flags the error word, the others
 // run out in turn, and the CTA lets its copies land before it leaves.
 #include <algorithm>

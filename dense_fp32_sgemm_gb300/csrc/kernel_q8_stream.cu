@@ -5,7 +5,9 @@
 // of the four by the same 16 of every row of x (four at a time, summed into 32 bits).
 // Sums are integers, so neither the sharing out nor the order of the additions
 // changes them.  x lies in shared memory, zeros from K on.  The loads of three
-// items are under way at a time.  Bound: HBM.
+// items are under way at a time.  Bound: HBM (1 x 4096 x 12288 11.4 us, 4.4 TB/s of the copy's
+// 6.7, of which a launch and its first loads are 3; 1 x 8192 x 28672 44 us, 5.4 TB/s); from five
+// rows on the multiplications (8 x 8192 x 8192 26 us, 2.5 TB/s).
 #include <algorithm>
 #include <atomic>
 

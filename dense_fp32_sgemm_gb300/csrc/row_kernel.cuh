@@ -1,10 +1,16 @@
 // Rows in one pass: the root-mean-square norm with the residual's addition, and
 // rows that leave in 8 bits (the norm, the gate act(g) u, plain rows).
 //
-// A group of threads takes a row into registers with one round of 16-byte loads,
-// reduces it (sum of squares and largest magnitude together), and writes it out:
-// every byte moves once.  Rows that are too long for registers are read a second
-// time.
+// A group of threads takes a row into registers, reduces it (sum of squares and
+// largest magnitude together), and writes it out: every byte moves once.  CTAs
+// stay and take rows in turn; the pieces of their next rows are on their way to shared
+// memory meanwhile.  Rows that are too long for registers are read a second time.
+//
+// Measured, and the time of the bytes: norm of 8192 x 2048 BF16 with its residual 24 us (20); in
+// 8 bits of 4096 x 4096 BF16 with its residual 31 us (17.6, 3.8 TB/s); gate of 4096 x 12288 BF16
+// 72 us (37.7, 3.5 TB/s).  Bound: instructions.  A code costs its element some 15 beside
+// the norm's or gate's own, and the issue slots are 65 to 70 % used with what registers leave
+// of warps (35 to 46 % of the SM's).
 #pragma once
 
 #include <algorithm>
@@ -247,232 +253,232 @@ __global__ void __maxnreg__(row_regs(OP, ACT, ALIGNED)) row_kernel(const RowPara
     int turn = 0;
     bool flip = false, begun = false;
     for (; row - group < rows; row += stride, flip = !flip) {
-    cols = row < rows ? p.cols : 0;
-    sum = largest = 0.0f;
-    spread = GateSpread();
-    if constexpr (KEEP) {
-        // All but the last stages - 1 rows' copies have landed.
-        if (p.stages == 1) cp_async_wait<0>();
-        else if (p.stages == 2) cp_async_wait<1>();
-        else cp_async_wait<2>();
+        cols = row < rows ? p.cols : 0;
+        sum = largest = 0.0f;
+        spread = GateSpread();
+        if constexpr (KEEP) {
+            // All but the last stages - 1 rows' copies have landed.
+            if (p.stages == 1) cp_async_wait<0>();
+            else if (p.stages == 2) cp_async_wait<1>();
+            else cp_async_wait<2>();
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int c = tid * V + i * step, n = cols - c;
-            if (c - lane * V < cols) {  // (the whole warp, for put())
-                uint4 x = make_uint4(0, 0, 0, 0), y = x;
-                if (n > 0) {
-                    x = take_piece<TYPE, ALIGNED>(slot(ring, 0, i), pitch, A(row), c * E);
-                    if (two) y = take_piece<TYPE, ALIGNED>(slot(ring, 1, i), pitch, B(row), c * E);
-                }
-                take(x, y, keep[i]);
-                if constexpr (kStores) {
-                    square(keep[i]);
-                    if (p.h && early) put(p.h, p.ldh, c, n, keep[i]);
-                }
-                if (OP == kRowNormQ8 && n > 0) weigh(c, n, keep[i]);
-                if constexpr (OP != kRowNorm) compare(keep[i]);
-            } else {
+            for (int i = 0; i < NP; ++i) {
+                const int c = tid * V + i * step, n = cols - c;
+                if (c - lane * V < cols) {  // (the whole warp, for put())
+                    uint4 x = make_uint4(0, 0, 0, 0), y = x;
+                    if (n > 0) {
+                        x = take_piece<TYPE, ALIGNED>(slot(ring, 0, i), pitch, A(row), c * E);
+                        if (two) y = take_piece<TYPE, ALIGNED>(slot(ring, 1, i), pitch, B(row), c * E);
+                    }
+                    take(x, y, keep[i]);
+                    if constexpr (kStores) {
+                        square(keep[i]);
+                        if (p.h && early) put(p.h, p.ldh, c, n, keep[i]);
+                    }
+                    if (OP == kRowNormQ8 && n > 0) weigh(c, n, keep[i]);
+                    if constexpr (OP != kRowNorm) compare(keep[i]);
+                } else {
 #pragma unroll
-                for (int j = 0; j < V; ++j) keep[i][j] = 0.0f;
+                    for (int j = 0; j < V; ++j) keep[i][j] = 0.0f;
+                }
+            }
+            start(row + p.stages * stride, ring);
+            if (++ring == p.stages) ring = 0;
+        } else {
+            for (int c = tid * V; c < cols; c += step) {
+                uint4 x, y = make_uint4(0, 0, 0, 0);
+                fetch(c, cols - c, x, y);
+                take(x, y, keep[0]);
+                if constexpr (kStores) square(keep[0]);
+                if constexpr (OP == kRowNormQ8) weigh(c, cols - c, keep[0]);
+                if constexpr (OP != kRowNorm) compare(keep[0]);
             }
         }
-        start(row + p.stages * stride, ring);
-        if (++ring == p.stages) ring = 0;
-    } else {
-        for (int c = tid * V; c < cols; c += step) {
-            uint4 x, y = make_uint4(0, 0, 0, 0);
-            fetch(c, cols - c, x, y);
-            take(x, y, keep[0]);
-            if constexpr (kStores) square(keep[0]);
-            if constexpr (OP == kRowNormQ8) weigh(c, cols - c, keep[0]);
-            if constexpr (OP != kRowNorm) compare(keep[0]);
-        }
-    }
-    bool far = false;
-    if constexpr (kGate) {
-        // An element beyond z = -80 matters from |g u| = 100 on: below, its magnitude is under
-        // 2^-108 and its code zero whatever it is.
-        if (ACT != kGateRelu && spread.lowest < -80.0f && largest == largest) {
-            each([&](int c) {
-                const float g = load_as_float(A(row).row, TYPE, c), u = load_as_float(B(row).row, TYPE, c);
-                far = far || (gate_z<ACT>(g) < -80.0f && !(fabsf(g * u) < 100.0f));
-            });
-            if (far) {
-                largest = 0.0f;
-                each([&](int c) { largest = max_nan(largest, (float)fabs(exact(c))); });
+        bool far = false;
+        if constexpr (kGate) {
+            // An element beyond z = -80 matters from |g u| = 100 on: below, its magnitude is under
+            // 2^-108 and its code zero whatever it is.
+            if (ACT != kGateRelu && spread.lowest < -80.0f && largest == largest) {
+                each([&](int c) {
+                    const float g = load_as_float(A(row).row, TYPE, c), u = load_as_float(B(row).row, TYPE, c);
+                    far = far || (gate_z<ACT>(g) < -80.0f && !(fabsf(g * u) < 100.0f));
+                });
+                if (far) {
+                    largest = 0.0f;
+                    each([&](int c) { largest = max_nan(largest, (float)fabs(exact(c))); });
+                }
             }
         }
-    }
 
-    // Over the row's threads.
-    unsigned most = __float_as_uint(largest);  // (above infinity's bits where it is NaN)
-    if constexpr (kStores) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
-    if constexpr (OP != kRowNorm) most = __reduce_max_sync(0xffffffffu, most);
-    unsigned mass = __float_as_uint(spread.mass);
-    if constexpr (ACT == kGateGelu) mass = __reduce_max_sync(0xffffffffu, mass);
-    if (OP != kRowNorm || warps > 1) {
-        const int slot = group * warps;
-        if (lane == 0) {
-            s_sum[flip][slot + (tid >> 5)] = sum;
-            s_max[flip][slot + (tid >> 5)] = most;
-            if constexpr (ACT == kGateGelu) s_mass[flip][slot + (tid >> 5)] = mass;
-        }
-        __syncthreads();
+        // Over the row's threads.
+        unsigned most = __float_as_uint(largest);  // (above infinity's bits where it is NaN)
         if constexpr (kStores) {
-            sum = lane < warps ? s_sum[flip][slot + lane] : 0.0f;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
-        if constexpr (OP != kRowNorm)
-            most = __reduce_max_sync(0xffffffffu, lane < warps ? s_max[flip][slot + lane] : 0u);
-        if constexpr (ACT == kGateGelu)
-            mass = __reduce_max_sync(0xffffffffu, lane < warps ? s_mass[flip][slot + lane] : 0u);
-    }
-    const float rstd = kStores ? rsqrtf(fmaf(sum, p.inv_cols, p.eps)) : 1.0f;
-
-    // Calls f(c, n, values, number) for each piece of the row, with the whole warp.
-    auto pieces = [&](auto &&f) {
-        if constexpr (KEEP) {
+        if constexpr (OP != kRowNorm) most = __reduce_max_sync(0xffffffffu, most);
+        unsigned mass = __float_as_uint(spread.mass);
+        if constexpr (ACT == kGateGelu) mass = __reduce_max_sync(0xffffffffu, mass);
+        if (OP != kRowNorm || warps > 1) {
+            const int slot = group * warps;
+            if (lane == 0) {
+                s_sum[flip][slot + (tid >> 5)] = sum;
+                s_max[flip][slot + (tid >> 5)] = most;
+                if constexpr (ACT == kGateGelu) s_mass[flip][slot + (tid >> 5)] = mass;
+            }
+            __syncthreads();
+            if constexpr (kStores) {
+                sum = lane < warps ? s_sum[flip][slot + lane] : 0.0f;
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                const int c = tid * V + i * step;
-                if (c - lane * V < cols) f(c, cols - c, keep[i], i);
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             }
-        } else {
-            for (int c = tid * V; c - lane * V < cols; c += step) {
-                uint4 x = make_uint4(0, 0, 0, 0), y = x;
-                if (c < cols) fetch(c, cols - c, x, y);
-                take(x, y, keep[0]);
-                if (OP == kRowNormQ8 && c < cols) weigh(c, cols - c, keep[0]);
-                f(c, cols - c, keep[0], 0);
-            }
+            if constexpr (OP != kRowNorm)
+                most = __reduce_max_sync(0xffffffffu, lane < warps ? s_max[flip][slot + lane] : 0u);
+            if constexpr (ACT == kGateGelu)
+                mass = __reduce_max_sync(0xffffffffu, lane < warps ? s_mass[flip][slot + lane] : 0u);
         }
-    };
+        const float rstd = kStores ? rsqrtf(fmaf(sum, p.inv_cols, p.eps)) : 1.0f;
 
-    if constexpr (OP == kRowNorm) {
-        pieces([&](int c, int n, float (&v)[V], int) {
-            float w[V], y[V];
-            if (n > 0) load_weight<TYPE, ALIGNED>(W, p.w_f32, c, n, w);
+        // Calls f(c, n, values, number) for each piece of the row, with the whole warp.
+        auto pieces = [&](auto &&f) {
+            if constexpr (KEEP) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) y[j] = n > 0 ? v[j] * rstd * w[j] : 0.0f;
-            if (!KEEP && p.h) put(p.h, p.ldh, c, n, v);
-            put(p.y, p.ldy, c, n, y);
-        });
-    } else {
-        // Nobody reads what the row before the last one left any more.
-        const int next_turn = turn == 2 ? 0 : turn + 1;
-        if (tid == 0) s_top[next_turn][group] = 0;
-        const bool later = KEEP && !p.h_last;  // what is left of a row is done with the next one
-        if (later && begun) finish_last(turn == 0 ? 2 : turn - 1);
-        begun = true;
-        const bool bad = most >= 0x7F800000u;
-        const float top = fmaxf(__uint_as_float(most), kRowTiny);
-        const float inv = bad ? 0.0f : 127.0f / top;
-        all = far && !bad;
-        if (tid == 0) s_scale[turn][group] = bad ? __int_as_float(0x7FC00000) : rstd / 127.0f;
-        // The largest magnitude in more bits, among those that FP32 cannot tell from it.
-        const float limit = top * (1.0f - 0x1p-12f);
-        auto refine = [&]() {
-            if (bad || !(largest >= limit)) return;
-            auto raise = [&](int c) {
-                atomicMax(&s_top[turn][group],
-                          (unsigned long long)__double_as_longlong(fabs(exact(c))));
-            };
-            if (far) {
-                each(raise);
-            } else if constexpr (KEEP) {
-                unsigned mask = 0;
-#pragma unroll
-                for (int i = 0; i < NP; ++i)
-#pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        mask |= (unsigned)(fabsf(keep[i][j]) >= limit) << (i * V + j);
-                for (; mask; mask &= mask - 1) raise(element(__ffs(mask) - 1));
+                for (int i = 0; i < NP; ++i) {
+                    const int c = tid * V + i * step;
+                    if (c - lane * V < cols) f(c, cols - c, keep[i], i);
+                }
             } else {
-                for (int c = tid * V; c < cols; c += step) {
-                    uint4 x, y = make_uint4(0, 0, 0, 0);
-                    fetch(c, cols - c, x, y);
+                for (int c = tid * V; c - lane * V < cols; c += step) {
+                    uint4 x = make_uint4(0, 0, 0, 0), y = x;
+                    if (c < cols) fetch(c, cols - c, x, y);
                     take(x, y, keep[0]);
-                    if constexpr (OP == kRowNormQ8) weigh(c, cols - c, keep[0]);
-#pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        if (fabsf(keep[0][j]) >= limit) raise(c + j);
+                    if (OP == kRowNormQ8 && c < cols) weigh(c, cols - c, keep[0]);
+                    f(c, cols - c, keep[0], 0);
                 }
             }
         };
-        if constexpr (!KEEP) {
-            refine();
-            __syncthreads();
-        }
-        // What FP32 does not decide: a quotient nearer to the middle between two codes than it
-        // is off itself, kOff of it for a and top (in the gate 2^-20.5 each, two roundings
-        // each in the norm) and, in GELU, twice what the exponents are off.
-        constexpr float kOff = kGate ? 0x1p-19f : 0x1p-21f;
-        float border = 0.5f - 0x1p-19f;
-        if constexpr (ACT == kGateGelu) border -= fminf(__uint_as_float(mass) * inv, 1e4f) * 0x1p-20f;
-        pieces([&](int c, int n, float (&v)[V], int number) {
-            if (n <= 0) return;
-            // v inv + 1.5 2^23 is rounded to a whole number, ties to even, whose low byte is
-            // the code's.
-            constexpr float kWhole = 12582912.0f;
-            uint32_t r[V], word[V / 4];
-            float widest = 0.0f;
-            auto doubt_of = [&](int j, uint32_t &bits) {
-                const float q = fmaf(v[j], inv, kWhole), k = kWhole - q;
-                bits = __float_as_uint(q);
-                return fmaf(fabsf(k), kOff, fabsf(fmaf(v[j], inv, k)));
+
+        if constexpr (OP == kRowNorm) {
+            pieces([&](int c, int n, float (&v)[V], int) {
+                float w[V], y[V];
+                if (n > 0) load_weight<TYPE, ALIGNED>(W, p.w_f32, c, n, w);
+#pragma unroll
+                for (int j = 0; j < V; ++j) y[j] = n > 0 ? v[j] * rstd * w[j] : 0.0f;
+                if (!KEEP && p.h) put(p.h, p.ldh, c, n, v);
+                put(p.y, p.ldy, c, n, y);
+            });
+        } else {
+            // Nobody reads what the row before the last one left any more.
+            const int next_turn = turn == 2 ? 0 : turn + 1;
+            if (tid == 0) s_top[next_turn][group] = 0;
+            const bool later = KEEP && !p.h_last;  // what is left of a row is done with the next one
+            if (later && begun) finish_last(turn == 0 ? 2 : turn - 1);
+            begun = true;
+            const bool bad = most >= 0x7F800000u;
+            const float top = fmaxf(__uint_as_float(most), kRowTiny);
+            const float inv = bad ? 0.0f : 127.0f / top;
+            all = far && !bad;
+            if (tid == 0) s_scale[turn][group] = bad ? __int_as_float(0x7FC00000) : rstd / 127.0f;
+            // The largest magnitude in more bits, among those that FP32 cannot tell from it.
+            const float limit = top * (1.0f - 0x1p-12f);
+            auto refine = [&]() {
+                if (bad || !(largest >= limit)) return;
+                auto raise = [&](int c) {
+                    atomicMax(&s_top[turn][group],
+                              (unsigned long long)__double_as_longlong(fabs(exact(c))));
+                };
+                if (far) {
+                    each(raise);
+                } else if constexpr (KEEP) {
+                    unsigned mask = 0;
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+#pragma unroll
+                        for (int j = 0; j < V; ++j)
+                            mask |= (unsigned)(fabsf(keep[i][j]) >= limit) << (i * V + j);
+                    for (; mask; mask &= mask - 1) raise(element(__ffs(mask) - 1));
+                } else {
+                    for (int c = tid * V; c < cols; c += step) {
+                        uint4 x, y = make_uint4(0, 0, 0, 0);
+                        fetch(c, cols - c, x, y);
+                        take(x, y, keep[0]);
+                        if constexpr (OP == kRowNormQ8) weigh(c, cols - c, keep[0]);
+#pragma unroll
+                        for (int j = 0; j < V; ++j)
+                            if (fabsf(keep[0][j]) >= limit) raise(c + j);
+                    }
+                }
             };
-#pragma unroll
-            for (int j = 0; j < V; ++j) widest = fmaxf(widest, doubt_of(j, r[j]));
-#pragma unroll
-            for (int k = 0; k < V / 4; ++k)
-                word[k] = bad ? 0u
-                              : __byte_perm(__byte_perm(r[4 * k], r[4 * k + 1], 0x0040),
-                                            __byte_perm(r[4 * k + 2], r[4 * k + 3], 0x0040), 0x5410);
-            int8_t *out = p.q + (long long)row * p.ldq + c;
-            if (n >= V && (ALIGNED || p.q_vec)) {
-                if constexpr (V == 8)
-                    *reinterpret_cast<uint2 *>(out) = make_uint2(word[0], word[V / 4 - 1]);
-                else
-                    *reinterpret_cast<uint32_t *>(out) = word[0];
-            } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (j < n) out[j] = (int8_t)(word[j / 4] >> (8 * (j % 4)));
+            if constexpr (!KEEP) {
+                refine();
+                __syncthreads();
             }
-            if (widest > border && !bad && !far) {
-                unsigned mask = 0;
+            // What FP32 does not decide: a quotient nearer to the middle between two codes than it
+            // is off itself, kOff of it for a and top (in the gate 2^-20.5 each, two roundings
+            // each in the norm) and, in GELU, twice what the exponents are off.
+            constexpr float kOff = kGate ? 0x1p-19f : 0x1p-21f;
+            float border = 0.5f - 0x1p-19f;
+            if constexpr (ACT == kGateGelu) border -= fminf(__uint_as_float(mass) * inv, 1e4f) * 0x1p-20f;
+            pieces([&](int c, int n, float (&v)[V], int number) {
+                if (n <= 0) return;
+                // v inv + 1.5 2^23 is rounded to a whole number, ties to even, whose low byte is
+                // the code's.
+                constexpr float kWhole = 12582912.0f;
+                uint32_t r[V], word[V / 4];
+                float widest = 0.0f;
+                auto doubt_of = [&](int j, uint32_t &bits) {
+                    const float q = fmaf(v[j], inv, kWhole), k = kWhole - q;
+                    bits = __float_as_uint(q);
+                    return fmaf(fabsf(k), kOff, fabsf(fmaf(v[j], inv, k)));
+                };
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    uint32_t bits;
-                    mask |= (unsigned)(j < n && doubt_of(j, bits) > border) << j;
+                for (int j = 0; j < V; ++j) widest = fmaxf(widest, doubt_of(j, r[j]));
+#pragma unroll
+                for (int k = 0; k < V / 4; ++k)
+                    word[k] = bad ? 0u
+                                  : __byte_perm(__byte_perm(r[4 * k], r[4 * k + 1], 0x0040),
+                                                __byte_perm(r[4 * k + 2], r[4 * k + 3], 0x0040), 0x5410);
+                int8_t *out = p.q + (long long)row * p.ldq + c;
+                if (n >= V && (ALIGNED || p.q_vec)) {
+                    if constexpr (V == 8)
+                        *reinterpret_cast<uint2 *>(out) = make_uint2(word[0], word[V / 4 - 1]);
+                    else
+                        *reinterpret_cast<uint32_t *>(out) = word[0];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        if (j < n) out[j] = (int8_t)(word[j / 4] >> (8 * (j % 4)));
                 }
-                if constexpr (KEEP)
-                    doubt |= mask << (number * V);
-                else
-                    for (; mask; mask &= mask - 1) decide(c + __ffs(mask) - 1, turn);
+                if (widest > border && !bad && !far) {
+                    unsigned mask = 0;
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        uint32_t bits;
+                        mask |= (unsigned)(j < n && doubt_of(j, bits) > border) << j;
+                    }
+                    if constexpr (KEEP)
+                        doubt |= mask << (number * V);
+                    else
+                        for (; mask; mask &= mask - 1) decide(c + __ffs(mask) - 1, turn);
+                }
+            });
+            if constexpr (KEEP) refine();
+            // Decided when all of the row's threads have refined its largest magnitude: after the
+            // next row's barrier, or (h over what decide() reads) one of its own.
+            if (!later) {
+                if constexpr (KEEP) __syncthreads();
+                finish(turn);
+                if (OP == kRowNormQ8 && p.h)
+                    for (int c = tid * V; c - lane * V < cols; c += step) {
+                        uint4 x = make_uint4(0, 0, 0, 0), y = x;
+                        float v[V];
+                        if (c < cols) fetch(c, cols - c, x, y);
+                        take(x, y, v);
+                        put(p.h, p.ldh, c, cols - c, v);
+                    }
             }
-        });
-        if constexpr (KEEP) refine();
-        // Decided when all of the row's threads have refined its largest magnitude: after the
-        // next row's barrier, or (h over what decide() reads) one of its own.
-        if (!later) {
-            if constexpr (KEEP) __syncthreads();
-            finish(turn);
-            if (OP == kRowNormQ8 && p.h)
-                for (int c = tid * V; c - lane * V < cols; c += step) {
-                    uint4 x = make_uint4(0, 0, 0, 0), y = x;
-                    float v[V];
-                    if (c < cols) fetch(c, cols - c, x, y);
-                    take(x, y, v);
-                    put(p.h, p.ldh, c, cols - c, v);
-                }
+            turn = next_turn;
         }
-        turn = next_turn;
-    }
     }
     if (OP != kRowNorm && KEEP && !p.h_last) {
         __syncthreads();

@@ -292,7 +292,8 @@ MANY = [(9, 128, 128), (9, 1, 1), (10, 17, 300), (16, 1000, 520), (33, 130, 257)
         (97, 64, 256), (97, 1025, 700), (192, 4096, 256), (193, 257, 1000), (333, 2047, 1365), (500, 3000, 130),
         (1000, 96, 3001), (700, 1500, 5000)]
 FEW = [(1, 1, 1), (1, 15, 3), (1, 16, 4), (1, 4096, 1025), (2, 513, 300), (3, 1000, 640), (4, 2047, 77),
-       (5, 2050, 260), (7, 64, 40000), (8, 12288, 96), (8, 30000, 24)]
+       (5, 2050, 260), (7, 64, 40000), (8, 12288, 96), (8, 30000, 24),
+       (4, 8192, 4096), (5, 5001, 5300), (8, 8192, 4096)]
 
 
 @gpu
