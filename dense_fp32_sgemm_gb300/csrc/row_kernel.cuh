@@ -8,9 +8,8 @@
 //
 // Measured, and the time of the bytes: norm of 8192 x 2048 BF16 with its residual 24 us (20); in
 // 8 bits of 4096 x 4096 BF16 with its residual 31 us (17.6, 3.8 TB/s); gate of 4096 x 12288 BF16
-// 72 us (37.7, 3.5 TB/s).  Bound: instructions.  A code costs its element some 15 beside
-// the norm's or gate's own, and the issue slots are 65 to 70 % used with what registers leave
-// of warps (35 to 46 % of the SM's).
+// 72 us (37.7, 3.5 TB/s).  Bound: instructions, 39 and 37 an element: the issue slots are 65
+// to 70 % used with what registers leave of warps (35 to 46 % of the SM's).
 #pragma once
 
 #include <algorithm>

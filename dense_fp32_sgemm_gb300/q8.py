@@ -5,7 +5,8 @@ of 8-bit integers).
 
 Argument checks and marshalling only; all arithmetic runs in the library's
 CUDA kernels (include/sgemm_q8.h).  Streams, new outputs and errors are as in
-ffn.py.
+ffn.py.  Graphs captured on one stream share that stream's workspace: they may be
+replayed one after the other, not at once.
 """
 from __future__ import annotations
 

@@ -4,8 +4,11 @@
  * integers for serving it with many rows, whose operands the norm, the gate and
  * the weights are brought into 8 bits for.
  *
- * Conventions are those of sgemm_ffn.h.  Element types and activations are the
- * constants declared there.  All results are bitwise reproducible.
+ * Conventions are those of sgemm_ffn.h, its workspace of a device and stream among them
+ * (of sgemm_rms_norm_backward and sgemm_q8_matmul here; a call's first use on a
+ * stream may allocate, so run it once before capturing it; graphs captured on one
+ * stream share its workspace and run one after the other, not at once).  Element types and
+ * activations are the constants declared there.  All results are bitwise reproducible.
  *
  * Rows in 8 bits: a row a[0..n) has one scale and n codes,
  *
@@ -76,7 +79,7 @@ SGEMM_API sgemm_status_t sgemm_rms_norm_q8(int64_t T, int64_t D, int type, const
  * residual stream's own).  dx: T x D of `type`, the gradient of x and of the
  * residual alike; it may be dy or dh itself (same address and leading dimension).  dweight: D elements
  * of weight_type.  One of dx and dweight may be NULL.  T == 0: dweight is zero.
- * Sums are held in 32 bits, in an order that depends on the sizes alone.
+ * Sums are held in 32 bits, in an order that depends on sizes and alignment alone.
  * Errors as for the forward call.
  */
 SGEMM_API sgemm_status_t sgemm_rms_norm_backward(int64_t T, int64_t D, int type, const void *x,
