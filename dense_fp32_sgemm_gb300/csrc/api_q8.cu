@@ -214,7 +214,7 @@ sgemm_status_t sgemm_rms_norm_backward(int64_t T, int64_t D, int type, const voi
     p.dx = dx; p.lddx = lddx;
     p.dw = dweight;
     p.device = dev.index;
-    p.parts = norm_grad_parts(T, (int)D, type, vec, dev.num_sms);
+    p.parts = norm_grad_parts(p, type, vec, dev.num_sms);
     void *w = nullptr;
     const size_t stats = up(T * (int64_t)sizeof(float2), 256);
     s = op_workspace(st, stats + (size_t)p.parts * D * sizeof(float), &w);

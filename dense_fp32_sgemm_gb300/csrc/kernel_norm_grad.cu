@@ -8,7 +8,10 @@
 // row that it takes, so the weight's gradient gathers in its registers and leaves once, a
 // CTA's groups added up, as one of `parts` partial rows, which a second kernel adds up in order.  Every input is read once and
 // every output written once (plus the partial rows).  Rows that are too long for
-// registers are read again (norm_grad_wide_kernel).
+// registers are read again (norm_grad_wide_kernel).  16-bit rows of more than 8192 columns
+// keep the weight's gradient in shared memory, and dy and dh stay there until they are used
+// (calls from Python with cold inputs and dh, and in two readings: 1388 x 10504 BF16 63 us, 88;
+// 2048 x 16384 101, 182; 1388 x 10504 off 16 bytes 89, 159).
 //
 // 8192 x 2048 BF16 with dh: 38 us and 5 for the partial rows (its bytes take 20).  Bound:
 // latency, one CTA of 512 threads an SM, which the weight's gradient leaves no registers beside.
@@ -25,6 +28,11 @@ namespace {
 constexpr int kMostThreads = 512;
 constexpr int kMaxDevices = 64;
 constexpr int kRingBytes = 192 * 1024;  // of an SM, for rows on their way
+constexpr int kLateBytes = 214 * 1024;  // and the weight's gradient beside them
+// Whether a thread of so many pieces has registers for a row's h alone.
+constexpr bool is_late(int type, int np) { return piece_elements(type) * np > 16; }
+// Matrices whose pieces are on their way, of those that there are.
+constexpr int ring_arrays(int type, int np, bool r, bool dh) { return 2 + r + (dh && (np <= 2 || is_late(type, np))); }
 
 __device__ __forceinline__ float2 warp_sum2(float2 v) {
 #pragma unroll
@@ -102,15 +110,19 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_kernel(const NormGr
     uint32_t *stage = reinterpret_cast<uint32_t *>(s_stage) +
                       (ALIGNED ? 0 : (group * warps + (tid >> 5)) * kStageWords);
     const RowSource W = row_source(p.w, 0, p.cols, 0, p.w_f32 ? 4 : E, 1);
-    // (with more than two pieces dh is loaded where it is used: it would not fit the registers)
-    constexpr bool kAhead = NP <= 2;
-    const int arrays = 2 + (p.r != nullptr) + (kAhead && p.dh);
+    // kLate: dy, dh and dw lie in shared memory.  Else (with three pieces or four) dh is loaded
+    // where it is used: it would not fit the registers.
+    constexpr bool kLate = is_late(TYPE, NP), kAhead = NP <= 2;
+    const int arrays = ring_arrays(TYPE, NP, p.r, p.dh);
+    float4 *const s_dw = reinterpret_cast<float4 *>(s_ring + p.stages * arrays * NP * kSlots * pitch) + tid;  // (kLate)
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    float dw[NP][V];
+    float dw[kLate ? 1 : NP][V];
 #pragma unroll
-    for (int i = 0; i < NP; ++i)
+    for (int i = 0; i < (kLate ? 1 : NP); ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) dw[i][j] = 0.0f;
+    if (kLate)
+        for (int i = 0; i < NP * V / 4; ++i) s_dw[i * pitch] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 
     auto slot = [&](int ring, int array, int i) {
         return s_ring + (((ring * arrays + array) * NP + i) * kSlots) * pitch + group * blockDim.x + tid;
@@ -149,7 +161,7 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_kernel(const NormGr
         else if (p.stages == 2) cp_async_wait<1>();
         else cp_async_wait<2>();
         float h[NP][V];
-        uint4 dy_raw[NP], dh_raw[NP];
+        uint4 dy_raw[kLate ? 1 : NP], dh_raw[kLate ? 1 : NP];
         float2 sums = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
@@ -162,10 +174,11 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_kernel(const NormGr
 #pragma unroll
                     for (int j = 0; j < V; ++j) h[i][j] += w[j];
                 }
-                dy_raw[i] = take(ring, 1, i, row);
+                const uint4 raw = take(ring, 1, i, row);
+                if (!kLate) dy_raw[i] = raw;
                 if (kAhead) dh_raw[i] = p.dh ? take(ring, arrays - 1, i, row) : make_uint4(0, 0, 0, 0);
                 load_weight<TYPE, ALIGNED>(W, p.w_f32, c, p.cols - c, w);
-                unpack_piece<TYPE>(dy_raw[i], dy);
+                unpack_piece<TYPE>(raw, dy);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     sums.x = fmaf(h[i][j], h[i][j], sums.x);
@@ -173,34 +186,63 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_kernel(const NormGr
                 }
             }
         }
-        start(row + p.stages * stride, ring);
-        if (++ring == p.stages) ring = 0;
+        if (!kLate) start(row + p.stages * stride, ring);
         const float2 st = row_stats(group_sum2(sums, &s_sum[flip], group, warps), p.cols, p.eps);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int c = tid * V + i * step, n = p.cols - c;
             float dyr[V];
+            uint4 dh = make_uint4(0, 0, 0, 0);
             if (n > 0) {
-                unpack_piece<TYPE>(dy_raw[i], dyr);
+                if constexpr (kLate) {
+                    unpack_piece<TYPE>(take(ring, 1, i, row), dyr);
+                    if (p.dh) dh = take(ring, arrays - 1, i, row);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    dyr[j] *= st.x;
-                    dw[i][j] = fmaf(dyr[j], h[i][j], dw[i][j]);
+                    for (int k = 0; k < V / 4; ++k) {
+                        float4 *at = s_dw + (i * (V / 4) + k) * pitch, d = *at;
+                        dyr[4 * k] *= st.x, dyr[4 * k + 1] *= st.x, dyr[4 * k + 2] *= st.x, dyr[4 * k + 3] *= st.x;
+                        d.x = fmaf(dyr[4 * k], h[i][4 * k], d.x);
+                        d.y = fmaf(dyr[4 * k + 1], h[i][4 * k + 1], d.y);
+                        d.z = fmaf(dyr[4 * k + 2], h[i][4 * k + 2], d.z);
+                        d.w = fmaf(dyr[4 * k + 3], h[i][4 * k + 3], d.w);
+                        *at = d;
+                    }
+                } else {
+                    unpack_piece<TYPE>(dy_raw[i], dyr);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        dyr[j] *= st.x;
+                        dw[i][j] = fmaf(dyr[j], h[i][j], dw[i][j]);
+                    }
+                    if (kAhead) dh = dh_raw[i];
                 }
             }
             if (p.dx && c - lane * V < p.cols) {  // (the whole warp)
                 float w[V];
                 if (n > 0) {
                     load_weight<TYPE, ALIGNED>(W, p.w_f32, c, n, w);
-                    if (!kAhead)
-                        dh_raw[i] = p.dh ? load_piece<TYPE, ALIGNED>(source(3, row), c * E, n) : make_uint4(0, 0, 0, 0);
+                    if (!kAhead && !kLate && p.dh) dh = load_piece<TYPE, ALIGNED>(source(3, row), c * E, n);
                 }
                 store_piece<TYPE, ALIGNED>(static_cast<char *>(p.dx) + ((long long)row * p.lddx + c - lane * V) * E, n,
-                                           make_dx<TYPE>(h[i], w, dyr, dh_raw[i], st.y), stage);
+                                           make_dx<TYPE>(h[i], w, dyr, dh, st.y), stage);
             }
         }
+        if (kLate) start(row + p.stages * stride, ring);
+        if (++ring == p.stages) ring = 0;
     }
     if (!p.dw) return;
+    if constexpr (kLate) {  // (one group)
+        for (int i = 0; i < NP * V / 4; ++i) {
+            const float4 d = s_dw[i * pitch];
+            const int c = tid * V + i / (V / 4) * step + i % (V / 4) * 4;
+            float *out = p.partials + (long long)blockIdx.x * p.cols + c;
+            if (c < p.cols) __stcg(out, d.x);
+            if (c + 1 < p.cols) __stcg(out + 1, d.y);
+            if (c + 2 < p.cols) __stcg(out + 2, d.z);
+            if (c + 3 < p.cols) __stcg(out + 3, d.w);
+        }
+        return;
+    }
     // The groups' sums, added up in order: one partial row of a CTA.
     cp_async_wait<0>();
     __syncthreads();
@@ -307,17 +349,35 @@ __global__ void __launch_bounds__(1024) norm_grad_reduce_kernel(const NormGradPa
 // Most pieces of a thread that fit its registers.
 constexpr int grad_depth(int type, bool aligned) { return type != kTypeF32 ? 2 : aligned ? 4 : 3; }
 
+// 16-bit rows of more columns: pieces of a thread, bytes of a stage of the ring, and of dw.
+constexpr int kLatePieces = 4;
+int stage_bytes(int type, int np, bool vec, bool r, bool dh, int threads) {
+    return ring_arrays(type, np, r, dh) * np * piece_slots(vec) * 16 * threads;
+}
+int late_bytes(int threads) { return kLatePieces * 8 * 4 * threads; }
+
 // How a row lies over threads: pieces of a thread (0: too many for registers),
 // threads of a row, rows that a CTA has at once, CTAs (one on an SM).
 struct Shape {
     int depth, threads, groups, ctas;
 };
-Shape shape(long long rows, int cols, int type, bool vec, int num_sms) {
+Shape shape(long long rows, int cols, int type, bool vec, bool r, int num_sms) {
     const int most = grad_depth(type, vec);
     Shape s;
     const int pieces = (cols + piece_elements(type) - 1) / piece_elements(type);
     s.depth = pieces <= kMostThreads && rows <= num_sms ? 1 : pieces <= 2 * kMostThreads ? 2
               : pieces <= most * kMostThreads ? most : 0;
+    if (s.depth == 0 && type != kTypeF32 && pieces <= kLatePieces * kMostThreads) {
+        // As many threads as there is shared memory for, with dh or without (dw's order is the same).
+        for (int each = (pieces + kMostThreads - 1) / kMostThreads; each <= kLatePieces && s.depth == 0; ++each) {
+            s.threads = (pieces + 32 * each - 1) / (32 * each) * 32;
+            if (stage_bytes(type, kLatePieces, vec, r, true, s.threads) + late_bytes(s.threads) > kLateBytes) continue;
+            s.depth = kLatePieces;
+            s.groups = 1;
+            s.ctas = (int)std::min<long long>(rows, num_sms);
+        }
+        return s;
+    }
     if (s.depth == 0) return s;
     s.threads = std::max(1, (pieces + 32 * s.depth - 1) / (32 * s.depth)) * 32;
     // Few rows are spread over the SMs first.
@@ -346,30 +406,33 @@ cudaError_t launch(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem
 template <int TYPE, int NP, bool ALIGNED>
 cudaError_t launch_depth(const NormGradParams &p, const Shape &s, cudaStream_t stream) {
     const auto kernel = norm_grad_kernel<TYPE, NP, ALIGNED>;
+    constexpr bool kLate = is_late(TYPE, NP);
     static std::atomic<bool> configured[kMaxDevices];
     if (p.device >= kMaxDevices) return cudaErrorInvalidDevice;
     if (!configured[p.device].load()) {
         const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLate ? kLateBytes : kRingBytes);
         if (e != cudaSuccess) return e;
         configured[p.device].store(true);
     }
     NormGradParams q = p;
-    const int bytes = (2 + (p.r != nullptr) + (NP <= 2 && p.dh)) * NP * piece_slots(ALIGNED) * 16 *
-                      s.threads * s.groups;
-    q.stages = std::max(1, std::min(3, kRingBytes / bytes));
-    const size_t smem = std::max<size_t>((size_t)bytes * q.stages, (size_t)s.groups * p.cols * sizeof(float));
+    const int bytes = stage_bytes(TYPE, NP, ALIGNED, p.r, p.dh, s.threads) * s.groups;
+    const int beside = kLate ? late_bytes(s.threads) : 0;
+    q.stages = std::max(1, std::min(3, ((kLate ? kLateBytes : kRingBytes) - beside) / bytes));
+    const size_t all = kLate ? 0 : (size_t)s.groups * p.cols * sizeof(float);  // the groups' sums
+    const size_t smem = std::max<size_t>((size_t)bytes * q.stages + beside, all);
     return launch(kernel, dim3(s.ctas), dim3(s.threads, s.groups), smem, stream, q);
 }
 
 template <int TYPE, bool ALIGNED>
 cudaError_t launch_form(const NormGradParams &p, int num_sms, cudaStream_t stream) {
-    const Shape s = shape(p.rows, p.cols, TYPE, ALIGNED, num_sms);
+    const Shape s = shape(p.rows, p.cols, TYPE, ALIGNED, p.r, num_sms);
     cudaError_t e;
     if (s.depth) {
+        constexpr int kMost = TYPE == kTypeF32 ? grad_depth(TYPE, ALIGNED) : kLatePieces;
         e = s.depth == 1   ? launch_depth<TYPE, 1, ALIGNED>(p, s, stream)
             : s.depth == 2 ? launch_depth<TYPE, 2, ALIGNED>(p, s, stream)
-                           : launch_depth<TYPE, grad_depth(TYPE, ALIGNED), ALIGNED>(p, s, stream);
+                           : launch_depth<TYPE, kMost, ALIGNED>(p, s, stream);
     } else {
         // dx may lie over dy: the statistics first, then dw, then dx.
         NormGradParams q = p;
@@ -390,9 +453,9 @@ cudaError_t launch_form(const NormGradParams &p, int num_sms, cudaStream_t strea
 
 }  // namespace
 
-int norm_grad_parts(long long rows, int cols, int type, bool vec, int num_sms) {
-    const Shape s = shape(rows, cols, type, vec, num_sms);
-    return s.depth ? s.ctas : (int)std::min<long long>(rows, kWideParts);
+int norm_grad_parts(const NormGradParams &p, int type, bool vec, int num_sms) {
+    const Shape s = shape(p.rows, p.cols, type, vec, p.r, num_sms);
+    return s.depth ? s.ctas : (int)std::min<long long>(p.rows, kWideParts);
 }
 
 cudaError_t launch_norm_grad(const NormGradParams &p, int type, bool vec, int num_sms,

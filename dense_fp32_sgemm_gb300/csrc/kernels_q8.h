@@ -59,7 +59,7 @@ struct NormGradParams {
     int stages;               // (set by the launch) rows on their way
 };
 // Partial rows of the weight's gradient.
-int norm_grad_parts(long long rows, int cols, int type, bool vec, int num_sms);
+int norm_grad_parts(const NormGradParams &p, int type, bool vec, int num_sms);
 cudaError_t launch_norm_grad(const NormGradParams &p, int type, bool vec, int num_sms,
                              cudaStream_t stream);
 

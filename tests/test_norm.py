@@ -205,7 +205,8 @@ def backward(h, dy, dh, w):
 @gpu
 @pytest.mark.parametrize("kind,wkind", [("fp32", "fp32"), ("fp16", "fp16"), ("bf16", "fp32"),
                                         ("bf16", "bf16")])
-@pytest.mark.parametrize("T,D", [*SIZES, (1500, 64), (3000, 33), (700, 12288), (100, 12296)])
+@pytest.mark.parametrize("T,D", [*SIZES, (1500, 64), (3000, 33), (700, 12288), (100, 12296), (310, 9001),
+                                 (200, 16384), (155, 16377)])
 def test_backward(device, T, D, kind, wkind):
     (h, dy, dh), w = make(T, D, kind, wkind, count=3)
     dx, dw = backward(h, dy, dh, w)
@@ -218,7 +219,7 @@ def test_backward(device, T, D, kind, wkind):
 
 @gpu
 @pytest.mark.parametrize("kind", TYPES)
-@pytest.mark.parametrize("T,D", [(3, 31), (300, 520), (50, 1025), (40, 8192), (3, 40001)])
+@pytest.mark.parametrize("T,D", [(3, 31), (300, 520), (50, 1025), (40, 8192), (320, 9001), (200, 10504), (3, 40001)])
 def test_backward_at_the_sum_in_32_bits(device, T, D, kind):
     (x, r, dy, dh), w = make(T, D, kind, "fp32")
     dx, dw = sg.rms_norm_backward(dy, x, w, residual=r, dh=dh, eps=EPS)
