@@ -80,7 +80,7 @@ def _compile_calls() -> str | None:
     if not _torch():
         return None
     torch = _torch()[0]
-    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     obj = os.path.join(BUILD, "torch_calls.o")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
            "-I", os.path.join(torch, "include"), "-I", sysconfig.get_paths()["include"],

@@ -129,7 +129,9 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, y=None, h=None, stream
 
     Where one of the inputs requires a gradient, y and h are part of the graph:
     their gradients go through rms_norm_backward() with h, which the graph keeps (the rounded
-    sum alone, not x and the residual).  A given y or h is refused then.
+    sum alone, not x and the residual).  A given y or h is refused then.  A backward pass may
+    be captured where no eager graph of the same leaves is alive: torch waits for
+    the stream of such a graph, which a capture cannot.
     """
     if stream is None:
         got = (_calls or _load_calls()).rms_norm(x, weight, residual, eps, y, h)

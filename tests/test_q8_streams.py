@@ -295,6 +295,15 @@ def test_rows_beyond_2_31_elements(device):
     assert torch.equal(q[part], one[0]) and torch.equal(s[part], one[1])
     y = sg.rms_norm(x, w)
     assert torch.equal(y[part], sg.rms_norm(x[part], w))
+    # (rows off 16 bytes: another order of the sum, off by 2^-18 at most, and half a step of BF16)
+    odd = sg.rms_norm(x[:, 1:], w[1:])
+    want = x[part, 1:].double()
+    want = want / (want.square().mean(1, keepdim=True) + 1e-6).sqrt() * w[1:].double()
+    assert bool(((odd[part].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -17) * want.abs()).all())
+    dx, dw = sg.rms_norm_backward(x[:, 1:], x[:, 1:], w[1:], dx=odd)
+    one = sg.rms_norm_backward(x[part, 1:], x[part, 1:], w[1:], need_dw=False)[0]
+    assert bool(((odd[part].double() - one.double()).abs() <= 2.0 ** -6 * one.double().abs() + 2.0 ** -10).all())
+    del odd, dx, want, one
     q, s, h = sg.rms_norm_q8(x, w, residual=y, h=y)
     assert torch.equal(h[part], (x[part].float() + sg.rms_norm(x[part], w).float()).bfloat16())
     del q, s, h
