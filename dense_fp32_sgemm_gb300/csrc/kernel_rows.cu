@@ -200,7 +200,10 @@ __global__ void __launch_bounds__(kWordThreads, 2) norm_words_kernel(const RowPa
     }
 }
 
-// Whether rows of p fit (with two CTAs an SM or one), and the launch.
+// Whether there are many rows of p and they fit (with two CTAs an SM or one), and the launch.  Few
+// are faster piece by piece, with nothing to lay out first (100 x 4097 BF16 4.4 us, 7.0 here; 300 x
+// 1025 FP32 4.9 and 6.9), many here (1817 x 2816 FP32 15.1 us and 12.6 here, 8000 x 1025 25.9 and
+// 17.7, 4000 x 4097 BF16 50.5 and 35.6; only short ones lose a little, 16000 x 233 13.9 and 15.1).
 template <int TYPE>
 bool launch_words(const RowParams &p, int num_sms, cudaStream_t stream, cudaError_t &e) {
     constexpr int PER = word_elements(TYPE), NW = most_words(TYPE);
@@ -209,7 +212,7 @@ bool launch_words(const RowParams &p, int num_sms, cudaStream_t stream, cudaErro
     const int target = p.rows <= 2 * num_sms ? 4 : NW;
     const int threads = std::min(((count + target - 1) / target + 31) / 32 * 32, kWordThreads);
     const int words = (count + threads - 1) / threads;
-    if (words > NW) return false;
+    if (words > NW || few_rows<TYPE, kRowNorm>(p, num_sms)) return false;
     int groups = kWordThreads / threads;
     if (p.rows <= 2 * num_sms) groups = 1;
     const size_t weight = 4 * ((size_t)(threads * words + 2) * PER + 4);

@@ -485,13 +485,20 @@ __global__ void __maxnreg__(row_regs(OP, ACT, ALIGNED)) row_kernel(const RowPara
     }
 }
 
+// So few rows that each thread has one piece of one.
+template <int TYPE, int OP>
+bool few_rows(const RowParams &p, int num_sms) {
+    constexpr int V = piece_elements(TYPE);
+    return p.rows <= 2 * num_sms && (p.cols + V - 1) / V <= row_threads(OP);
+}
+
 template <int TYPE, int OP, int ACT, bool ALIGNED>
 cudaError_t launch_op(const RowParams &p, int num_sms, cudaStream_t stream) {
     constexpr int V = piece_elements(TYPE), kDeep = row_pieces(OP);
     // Threads of a row: with few rows as many as leave each one piece, else as many as
     // hold the row in registers.
     const long long most = (p.cols + V - 1) / V;  // pieces
-    const bool few = p.rows <= 2 * num_sms && most <= row_threads(OP);
+    const bool few = few_rows<TYPE, OP>(p, num_sms);
     const long long want = few ? most : (most + kDeep - 1) / kDeep;
     int threads = 32;
     while (threads < want && threads < 128) threads *= 2;
@@ -516,12 +523,13 @@ cudaError_t launch_op(const RowParams &p, int num_sms, cudaStream_t stream) {
     q.stages = std::max(1, std::min(3, kRingBytes / (bytes * per_sm)));
     constexpr int kStageBytes = OP != kRowGateQ8 && !ALIGNED ? kStageWords * 4 : 0;  // of a warp
     cfg.dynamicSmemBytes = (size_t)threads * groups / 32 * kStageBytes;
-    // (the norm of rows off 16 bytes that fit has a kernel of its own)
-    if (OP == kRowNorm && !ALIGNED || !fits)
+    // (Many rows off 16 bytes have a kernel of their own in the norm.)
+    constexpr bool kFewOnly = OP == kRowNorm && !ALIGNED;
+    if (!fits || (kFewOnly && !few))
         return cudaLaunchKernelEx(&cfg, row_kernel<TYPE, OP, ACT, 1, false, ALIGNED>, q);
-    if constexpr (OP != kRowNorm || ALIGNED) {
     cfg.dynamicSmemBytes += (size_t)bytes * q.stages;
-    const auto kernel = few ? row_kernel<TYPE, OP, ACT, 1, true, ALIGNED> : row_kernel<TYPE, OP, ACT, kDeep, true, ALIGNED>;
+    const auto kernel = few ? row_kernel<TYPE, OP, ACT, 1, true, ALIGNED>
+                            : row_kernel<TYPE, OP, ACT, kFewOnly ? 1 : kDeep, true, ALIGNED>;
     static std::atomic<bool> configured[kMaxDevices][2];
     if (p.device >= kMaxDevices) return cudaErrorInvalidDevice;
     if (!configured[p.device][few].load()) {
@@ -532,7 +540,6 @@ cudaError_t launch_op(const RowParams &p, int num_sms, cudaStream_t stream) {
         configured[p.device][few].store(true);
     }
     return cudaLaunchKernelEx(&cfg, kernel, q);
-    }
 }
 
 // For one of the library's types and alignments.
