@@ -64,6 +64,9 @@ __device__ __forceinline__ double gate_exact(float g, float u) {
     if (ACT == kGateRelu) return g > 0.0f ? (double)g * u : 0.0;
     Two z = {g, 0.0f};
     if (ACT == kGateGelu) {
+        // (z is beyond +-70,000, its exponential 0 or beyond 64 bits; from 10^12 on two floats do
+        // not hold the cube)
+        if (fabsf(g) > 100.0f) return (g > 0.0f ? (double)g : (double)g * 0.0) * (double)u;
         constexpr double k = 0.044715;
         const Two g2 = two_prod(g, g);
         z = g2 * Two{(float)k, (float)(k - (float)k)} + Two{1.0f, 0.0f};
