@@ -34,7 +34,8 @@ struct GateSpread {
 
 // act(g) u with act(g) = g / (1 + exp(-z)), off by at most 2^-20.5 of itself and 2^-21 of
 // `mass` (GELU's z is a rounded value: what it is off by counts as far as the
-// exponential does).
+// exponential does).  Where FP32 does not hold g u, z or its multiple below, the result is not
+// finite, whatever act(g) u is; gate_exact() has it then.
 template <int ACT>
 __device__ __forceinline__ float gate_z(float g) {
     return ACT == kGateSilu ? g : (float)kGeluC2 * fmaf(0.044715f * g * g, g, g);
@@ -44,7 +45,7 @@ __device__ __forceinline__ float gate_value(float g, float u, GateSpread &s) {
     if constexpr (ACT == kGateRelu) return (g > 0.0f ? g : (g != g ? g : 0.0f)) * u;
     const float gu = g * u;
     const float z = gate_z<ACT>(g);
-    const float x = fmaxf(z, -80.0f);  // (infinite g: a is not finite either way)
+    const float x = fmaxf(z, -80.0f);
     // exp(-x) = 2^t 2^c: c is what t lost in rounding.
     constexpr float kL = 1.4426950408889634f;
     constexpr float kLRest = (float)(1.4426950408889634074 - (double)kL);
@@ -297,18 +298,18 @@ __global__ void __maxnreg__(row_regs(OP, ACT, ALIGNED)) row_kernel(const RowPara
             }
         }
         bool far = false;
-        if constexpr (kGate) {
+        if constexpr (kGate && ACT != kGateRelu) {
             // An element beyond z = -80 matters from |g u| = 100 on: below, its magnitude is under
-            // 2^-108 and its code zero whatever it is.
-            if (ACT != kGateRelu && spread.lowest < -80.0f && largest == largest) {
+            // 2^-108 and its code zero whatever it is.  One that is not finite in FP32 may be in 64 bits.
+            far = !(largest < __int_as_float(0x7F800000));
+            if (!far && spread.lowest < -80.0f)
                 each([&](int c) {
                     const float g = load_as_float(A(row).row, TYPE, c), u = load_as_float(B(row).row, TYPE, c);
                     far = far || (gate_z<ACT>(g) < -80.0f && !(fabsf(g * u) < 100.0f));
                 });
-                if (far) {
-                    largest = 0.0f;
-                    each([&](int c) { largest = max_nan(largest, (float)fabs(exact(c))); });
-                }
+            if (far) {
+                largest = 0.0f;
+                each([&](int c) { largest = max_nan(largest, (float)fabs(exact(c))); });
             }
         }
 
