@@ -14,6 +14,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <limits>
 
 #include "kernels_q8.h"
 #include "row_codes.cuh"
@@ -65,13 +66,13 @@ __device__ __forceinline__ double gate_exact(float g, float u) {
     if (ACT == kGateRelu) return g > 0.0f ? (double)g * u : 0.0;
     Two z = {g, 0.0f};
     if (ACT == kGateGelu) {
-        // (z is beyond +-70,000, its exponential 0 or beyond 64 bits; from 10^12 on two floats do
-        // not hold the cube)
-        if (fabsf(g) > 100.0f) return (g > 0.0f ? (double)g : (double)g * 0.0) * (double)u;
+        // (beyond +-100 the exponential is 0 or beyond 64 bits; two floats do not hold the cube of
+        // 10^13)
+        const float c = fminf(fmaxf(g, -100.0f), 100.0f);
         constexpr double k = 0.044715;
-        const Two g2 = two_prod(g, g);
+        const Two g2 = two_prod(c, c);
         z = g2 * Two{(float)k, (float)(k - (float)k)} + Two{1.0f, 0.0f};
-        z = z * Two{g, 0.0f} * Two{(float)kGeluC2, (float)(kGeluC2 - (float)kGeluC2)};
+        z = z * Two{c, 0.0f} * Two{(float)kGeluC2, (float)(kGeluC2 - (float)kGeluC2)};
     }
     const bool neg = z.hi < 0.0f;
     if (neg) z = Two{-z.hi, -z.lo};
@@ -301,15 +302,16 @@ __global__ void __maxnreg__(row_regs(OP, ACT, ALIGNED)) row_kernel(const RowPara
         if constexpr (kGate && ACT != kGateRelu) {
             // An element beyond z = -80 matters from |g u| = 100 on: below, its magnitude is under
             // 2^-108 and its code zero whatever it is.  One that is not finite in FP32 may be in 64 bits.
-            far = !(largest < __int_as_float(0x7F800000));
-            if (!far && spread.lowest < -80.0f)
+            constexpr float kInf = std::numeric_limits<float>::infinity();
+            if (spread.lowest < -80.0f || largest >= kInf || largest != largest) {
                 each([&](int c) {
                     const float g = load_as_float(A(row).row, TYPE, c), u = load_as_float(B(row).row, TYPE, c);
-                    far = far || (gate_z<ACT>(g) < -80.0f && !(fabsf(g * u) < 100.0f));
+                    far = far || (gate_z<ACT>(g) < -80.0f && !(fabsf(g * u) < 100.0f)) || !(largest < kInf);
                 });
-            if (far) {
-                largest = 0.0f;
-                each([&](int c) { largest = max_nan(largest, (float)fabs(exact(c))); });
+                if (far) {
+                    largest = 0.0f;
+                    each([&](int c) { largest = max_nan(largest, (float)fabs(exact(c))); });
+                }
             }
         }
 
