@@ -117,7 +117,7 @@ __global__ void __maxnreg__(row_regs(OP, ACT, ALIGNED)) row_kernel(const RowPara
     __shared__ float s_sum[2][kWarps];
     __shared__ unsigned s_max[2][kWarps], s_mass[2][kWarps];
     __shared__ unsigned long long s_top[3][kWarps];
-    __shared__ float s_scale[3][kWarps];
+    __shared__ float s_root[3][kWarps];  // what the scale is multiplied by
     const int tid = threadIdx.x, lane = tid & 31;
     const int group = threadIdx.y, warps = blockDim.x >> 5;
     // The ring below, and before it what store_piece() needs of each warp.
@@ -244,8 +244,8 @@ __global__ void __maxnreg__(row_regs(OP, ACT, ALIGNED)) row_kernel(const RowPara
         if (all) each([&](int c) { decide(c, turn_of); });
         all = false;
         if (tid == 0 && row < rows)
-            p.scales[row] = fmaxf((float)__longlong_as_double((long long)s_top[turn_of][group]), kRowTiny) *
-                            s_scale[turn_of][group];
+            p.scales[row] = fmaxf((float)__longlong_as_double((long long)s_top[turn_of][group]), kRowTiny) /
+                            127.0f * s_root[turn_of][group];
     };
     auto finish_last = [&](int turn_of) {  // of the row before
         if (doubt || all || tid == 0) {
@@ -383,7 +383,7 @@ __global__ void __maxnreg__(row_regs(OP, ACT, ALIGNED)) row_kernel(const RowPara
             const float top = fmaxf(__uint_as_float(most), kRowTiny);
             const float inv = bad ? 0.0f : 127.0f / top;
             all = far && !bad;
-            if (tid == 0) s_scale[turn][group] = bad ? __int_as_float(0x7FC00000) : rstd / 127.0f;
+            if (tid == 0) s_root[turn][group] = bad ? __int_as_float(0x7FC00000) : rstd;
             // The largest magnitude in more bits, among those that FP32 cannot tell from it.
             const float limit = top * (1.0f - 0x1p-12f);
             auto refine = [&]() {
