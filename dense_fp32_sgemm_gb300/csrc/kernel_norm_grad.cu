@@ -1,7 +1,7 @@
 // Gradients of the root-mean-square norm.
 //
 //   r = 1 / sqrt(mean(h^2) + eps), n = dy w
-//   dx = r (n - h r^2 mean(n h)) + dh,  dw = sum over rows of dy h r
+//   dx = r n - (h r) (r^2 mean(n h)) + dh,  dw = sum over rows of dy (h r)
 //
 // A group of threads holds a row of h and dy in registers (its next rows are on their way to
 // shared memory), reduces both sums at once, and writes dx; it owns the same columns in every
@@ -54,10 +54,11 @@ __device__ __forceinline__ float2 group_sum2(float2 v, float2 (*buf)[32], int gr
     v = lane < warps ? (*buf)[group * warps + lane] : make_float2(0.0f, 0.0f);
     return warp_sum2(v);
 }
-// r, and r^3 mean(n h), from the sums of h^2 and n h.
+// r, and r^2 mean(n h), from the sums of h^2 and n h.  (h r is of size one and this of dx's: a
+// factor r^3 would leave FP32 for rows of 10^13, and of 10^-13 without eps.)
 __device__ __forceinline__ float2 row_stats(float2 sums, int cols, float eps) {
     const float r = rsqrtf(sums.x / (float)cols + eps);
-    return make_float2(r, r * r * r * (sums.y / (float)cols));
+    return make_float2(r, sums.y / (float)cols * r * r);
 }
 
 // A piece of a row as it comes from memory; zeros where it has no elements.
@@ -87,15 +88,15 @@ __device__ __forceinline__ void sum_h(const Raw &v, bool two, float (&h)[piece_e
         for (int j = 0; j < piece_elements(TYPE); ++j) h[j] += r[j];
     }
 }
-// dx of a piece from dy r.
+// dx of a piece, from h r.
 template <int TYPE>
-__device__ __forceinline__ uint4 make_dx(const float (&h)[piece_elements(TYPE)], const float (&w)[piece_elements(TYPE)],
-                                         const float (&dyr)[piece_elements(TYPE)], uint4 dh_raw, float c) {
+__device__ __forceinline__ uint4 make_dx(const float (&hr)[piece_elements(TYPE)], const float (&w)[piece_elements(TYPE)],
+                                         const float (&dy)[piece_elements(TYPE)], uint4 dh_raw, float2 st) {
     constexpr int V = piece_elements(TYPE);
     float dx[V];
     unpack_piece<TYPE>(dh_raw, dx);
 #pragma unroll
-    for (int j = 0; j < V; ++j) dx[j] = fmaf(-h[j], c, fmaf(dyr[j], w[j], dx[j]));
+    for (int j = 0; j < V; ++j) dx[j] = fmaf(-hr[j], st.y, fmaf(dy[j] * w[j], st.x, dx[j]));
     return pack_piece<TYPE>(dx);
 }
 
@@ -192,29 +193,27 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_kernel(const NormGr
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int c = tid * V + i * step, n = p.cols - c;
-            float dyr[V];
+            float dy[V];
             uint4 dh = make_uint4(0, 0, 0, 0);
             if (n > 0) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) h[i][j] *= st.x;
                 if constexpr (kLate) {
-                    unpack_piece<TYPE>(take(ring, 1, i, row), dyr);
+                    unpack_piece<TYPE>(take(ring, 1, i, row), dy);
                     if (p.dh) dh = take(ring, arrays - 1, i, row);
 #pragma unroll
                     for (int k = 0; k < V / 4; ++k) {
                         float4 *at = s_dw + (i * (V / 4) + k) * pitch, d = *at;
-                        dyr[4 * k] *= st.x, dyr[4 * k + 1] *= st.x, dyr[4 * k + 2] *= st.x, dyr[4 * k + 3] *= st.x;
-                        d.x = fmaf(dyr[4 * k], h[i][4 * k], d.x);
-                        d.y = fmaf(dyr[4 * k + 1], h[i][4 * k + 1], d.y);
-                        d.z = fmaf(dyr[4 * k + 2], h[i][4 * k + 2], d.z);
-                        d.w = fmaf(dyr[4 * k + 3], h[i][4 * k + 3], d.w);
+                        d.x = fmaf(dy[4 * k], h[i][4 * k], d.x);
+                        d.y = fmaf(dy[4 * k + 1], h[i][4 * k + 1], d.y);
+                        d.z = fmaf(dy[4 * k + 2], h[i][4 * k + 2], d.z);
+                        d.w = fmaf(dy[4 * k + 3], h[i][4 * k + 3], d.w);
                         *at = d;
                     }
                 } else {
-                    unpack_piece<TYPE>(dy_raw[i], dyr);
+                    unpack_piece<TYPE>(dy_raw[i], dy);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        dyr[j] *= st.x;
-                        dw[i][j] = fmaf(dyr[j], h[i][j], dw[i][j]);
-                    }
+                    for (int j = 0; j < V; ++j) dw[i][j] = fmaf(dy[j], h[i][j], dw[i][j]);
                     if (kAhead) dh = dh_raw[i];
                 }
             }
@@ -225,7 +224,7 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_kernel(const NormGr
                     if (!kAhead && !kLate && p.dh) dh = load_piece<TYPE, ALIGNED>(source(3, row), c * E, n);
                 }
                 store_piece<TYPE, ALIGNED>(static_cast<char *>(p.dx) + ((long long)row * p.lddx + c - lane * V) * E, n,
-                                           make_dx<TYPE>(h[i], w, dyr, dh, st.y), stage);
+                                           make_dx<TYPE>(h[i], w, dy, dh, st), stage);
             }
         }
         if (kLate) start(row + p.stages * stride, ring);
@@ -297,10 +296,10 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_wide_kernel(const N
         sum_h<TYPE>(raw, p.r, h);
         unpack_piece<TYPE>(raw.dy, dy);
 #pragma unroll
-        for (int j = 0; j < V; ++j) dy[j] *= st.x;
+        for (int j = 0; j < V; ++j) h[j] *= st.x;
         if (n > 0) load_weight<TYPE, ALIGNED>(W, p.w_f32, c, n, w);
         store_piece<TYPE, ALIGNED>(static_cast<char *>(p.dx) + (row * p.lddx + c - lane * V) * E, n,
-                                   make_dx<TYPE>(h, w, dy, raw.dh, st.y), stage);
+                                   make_dx<TYPE>(h, w, dy, raw.dh, st), stage);
     }
 }
 
@@ -316,7 +315,7 @@ __global__ void __launch_bounds__(256) norm_grad_columns_kernel(const NormGradPa
     for (long long row = blockIdx.y; row < p.rows; row += p.parts) {
         float h = load_as_float(p.x, TYPE, row * p.ldx + c);
         if (p.r) h += load_as_float(p.r, TYPE, row * p.ldr + c);
-        sum = fmaf(load_as_float(p.dy, TYPE, row * p.lddy + c) * p.stats[row].x, h, sum);
+        sum = fmaf(load_as_float(p.dy, TYPE, row * p.lddy + c), h * p.stats[row].x, sum);
     }
     p.partials[(long long)blockIdx.y * p.cols + c] = sum;
 }

@@ -53,7 +53,7 @@ struct NormGradParams {
     long long lddx;
     void *dw;                 // null: not wanted
     float *partials;          // parts x cols, sums of some rows each
-    float2 *stats;            // rows: r and r^3 mean(n h), where rows do not fit registers
+    float2 *stats;            // rows: r and r^2 mean(n h), where rows do not fit registers
     int parts;
     int device;
     int stages;               // (set by the launch) rows on their way

@@ -79,7 +79,9 @@ SGEMM_API sgemm_status_t sgemm_rms_norm_q8(int64_t T, int64_t D, int type, const
  * residual stream's own).  dx: T x D of `type`, the gradient of x and of the
  * residual alike; it may be dy or dh itself (same address and leading dimension).  dweight: D elements
  * of weight_type.  One of dx and dweight may be NULL.  T == 0: dweight is zero.
- * Sums are held in 32 bits, in an order that depends on sizes and alignment alone.
+ * Sums are held in 32 bits, in an order that depends on sizes and alignment alone:
+ * where the squares' passes FP32's range, r counts as zero (dx is dh there, and the row
+ * adds nothing to dweight); where that of n h does, dx is not finite.
  * Errors as for the forward call.
  */
 SGEMM_API sgemm_status_t sgemm_rms_norm_backward(int64_t T, int64_t D, int type, const void *x,
