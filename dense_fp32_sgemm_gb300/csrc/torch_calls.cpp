@@ -211,7 +211,8 @@ PyObject *rms_norm_backward(PyObject *const *a) {
     const bool need_dx = a[8] == Py_True, need_dw = a[9] == Py_True;
     const at::Tensor *dy = tensor(a[4], ok), *dh = tensor(a[5], ok), *dx = tensor(a[6], ok), *dw = tensor(a[7], ok);
     Rows dyr, dhr, dxr;
-    if (!ok || !dy || !rows_of(dy, n.kind, n.device, n.T, n.D, dyr) || !rows_of(dh, n.kind, n.device, n.T, n.D, dhr) ||
+    if (!ok || !dy || wants_graph({n.x, n.weight, n.residual, dy, dh}) ||
+        !rows_of(dy, n.kind, n.device, n.T, n.D, dyr) || !rows_of(dh, n.kind, n.device, n.T, n.D, dhr) ||
         (need_dx && !rows_of(dx, n.kind, n.device, n.T, n.D, dxr)) ||
         (need_dw && dw && !vector_of(dw, n.weight->scalar_type(), n.device, n.D)) ||
         (a[8] != Py_True && a[8] != Py_False) || (a[9] != Py_True && a[9] != Py_False))

@@ -193,13 +193,16 @@ def rms_norm_backward(dy, x, weight, residual=None, dh=None, eps: float = 1e-6, 
     returned and no residual, which reads one matrix less, for those at the rounded
     sum.  dh: None, or the gradient that reaches h otherwise, which is added.  dx is the gradient of x
     and of the residual alike.  Outputs not given are allocated (dx may be dy or dh
-    itself); ``need_dx`` and ``need_dw`` leave one out (None is returned in its place).
+    itself); ``need_dx`` and ``need_dw`` leave one out (None is returned in its place).  No
+    gradient goes through it: inputs that require one are refused (call it under
+    torch.no_grad(), or let torch call it: rms_norm is part of its graph).
     """
     if stream is None:
         got = (_calls or _load_calls()).rms_norm_backward(x, weight, residual, eps, dy, dh, dx, dweight,
                                                           need_dx, need_dw)
         if got is not None:
             return _done(got, "sgemm_rms_norm_backward")
+    _no_gradient("rms_norm_backward", dy, x, weight, residual, dh)
     _written(dx, dweight)
     T, D, dev, args, _, dha = _norm_args(x, weight, residual, eps, dh, stream, False, "dh")
     dya = _address(dy, "dy", T, D, x.dtype, dev)

@@ -1,0 +1,37 @@
+"""Calls through which no gradient goes refuse inputs that require one; no derivative stops
+without a word.  (On the CPU the refusal comes before the one of the device.)"""
+import pytest
+
+torch = pytest.importorskip("torch")
+from torch.autograd import forward_ad
+
+import dense_fp32_sgemm_gb300 as sg
+
+gpu = pytest.mark.gpu
+
+
+def on(where):
+    if where == "cuda" and not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    sg.build()
+    return where
+
+
+DEVICES = ["cpu", pytest.param("cuda", marks=gpu)]
+
+
+@pytest.mark.parametrize("where", DEVICES)
+@pytest.mark.parametrize("which", range(5))
+def test_gradient_of_the_norms_gradient(where, which):
+    dev = on(where)
+    x, r, dy, dh = (torch.randn(4, 8, device=dev) for _ in range(4))
+    inputs = [dy, x, torch.ones(8, device=dev), r, dh]
+    inputs[which].requires_grad_()
+    dy, x, w, r, dh = inputs
+    for more in ({}, {"need_dx": False}, {"dx": torch.empty(4, 8, device=dev)}):
+        with pytest.raises(ValueError, match="has no gradient"):
+            sg.rms_norm_backward(dy, x, w, residual=r, dh=dh, **more)
+    if where == "cuda":
+        with torch.no_grad():
+            dx, dw = sg.rms_norm_backward(dy, x, w, residual=r, dh=dh)
+        assert not dx.requires_grad and not dw.requires_grad
