@@ -326,7 +326,10 @@ class Q8Matrix:
     def matmul(self, x, x_scales, y=None, stream=None):
         """y[m] = x_scales[m] * (x[m] @ W) for M x K codes x (int8) and M scales, as
         rms_norm_q8, gate_q8 and rows_q8 return them.  The sums are exact.  Returns y
-        (allocated when not given).  No gradient goes through it."""
+        (allocated when not given).  No gradient goes through it: scales that require one,
+        the matrix's own too, are refused."""
+        if self.scales.requires_grad:
+            _no_gradient("Q8Matrix.matmul", self.scales)
         if stream is None:
             got = (_calls or _load_calls()).q8_matmul(x, x_scales, y, self._weights)
             if got is not None:

@@ -35,3 +35,19 @@ def test_gradient_of_the_norms_gradient(where, which):
         with torch.no_grad():
             dx, dw = sg.rms_norm_backward(dy, x, w, residual=r, dh=dh)
         assert not dx.requires_grad and not dw.requires_grad
+
+
+@gpu
+def test_gradient_of_a_matrix_scales():
+    on("cuda")
+    q = torch.ones(16, 64, dtype=torch.int8, device="cuda")
+    x, xs = torch.ones(3, 64, dtype=torch.int8, device="cuda"), torch.ones(3, device="cuda")
+    scales = torch.ones(16, device="cuda")
+    m = sg.Q8Matrix(q, scales)
+    scales.requires_grad_()
+    for stream in (None, torch.cuda.current_stream()):
+        for y in (None, torch.empty(3, 16, dtype=torch.bfloat16, device="cuda")):
+            with pytest.raises(ValueError, match="has no gradient"):
+                m.matmul(x, xs, y, stream=stream)
+    with torch.no_grad():
+        assert bool((m.matmul(x, xs) == 64).all())
