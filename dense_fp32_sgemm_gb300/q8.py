@@ -352,7 +352,8 @@ class Q8Matrix:
 
 def q8_quantize(w, stream=None) -> Q8Matrix:
     """The 8-bit form of a K x N CUDA tensor: a scale for each column; products of w's
-    type."""
+    type.  No gradient goes through it: a w that requires one is refused."""
+    _no_gradient("q8_quantize", w)
     if w.dim() != 2:
         raise ValueError("w must be 2-D")
     K, N = w.shape

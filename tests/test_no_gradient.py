@@ -51,3 +51,15 @@ def test_gradient_of_a_matrix_scales():
                 m.matmul(x, xs, y, stream=stream)
     with torch.no_grad():
         assert bool((m.matmul(x, xs) == 64).all())
+
+
+@pytest.mark.parametrize("where", DEVICES)
+def test_gradient_of_quantised_weights(where):
+    dev = on(where)
+    w = torch.randn(8, 6, device=dev, requires_grad=True)
+    with pytest.raises(ValueError, match="has no gradient"):
+        sg.q8_quantize(w)
+    if where == "cuda":
+        with torch.no_grad():
+            sg.q8_quantize(w)
+        sg.q8_quantize(w.detach())
