@@ -247,7 +247,7 @@ def rms_norm_q8(x, weight, residual=None, eps: float = 1e-6, h=None, q=None, sca
         if got is not None:
             return _done(got, "sgemm_rms_norm_q8")
     _no_gradient("rms_norm_q8", x, weight, residual)
-    _written(h)
+    _written(h, q, scales)
     T, D, dev, args, h, ha = _norm_args(x, weight, residual, eps, h, stream, residual is not None)
     q, scales, qa = _codes(q, scales, T, D, dev, stream)
     _call(_sg.library().sgemm_rms_norm_q8, dev, stream, *args, *ha, *qa)
@@ -265,6 +265,7 @@ def gate_q8(g, u, activation: int = 0, q=None, scales=None, stream=None):
         if got is not None:
             return _done(got, "sgemm_q8_gate")
     _no_gradient("gate_q8", g, u)
+    _written(q, scales)
     if g.dim() != 2:
         raise ValueError("g must be 2-D")
     T, F = g.shape
@@ -284,6 +285,7 @@ def rows_q8(x, q=None, scales=None, stream=None):
         if got is not None:
             return _done(got, "sgemm_q8_gate")
     _no_gradient("rows_q8", x)
+    _written(q, scales)
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     T, D = x.shape
