@@ -64,7 +64,8 @@ bool wants_graph(std::initializer_list<const at::Tensor *> list) {
         if (t && t->requires_grad()) return true;
     return false;
 }
-// A given output: graphs that hold it will know that it was overwritten.
+// A given output (one that requires a gradient is refused in Python): graphs that hold it will
+// know that it was overwritten.
 void written(const at::Tensor *t) {
     if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
 }
@@ -153,7 +154,7 @@ PyObject *rms_norm(PyObject *const *a) {
     if (!ok) Py_RETURN_NONE;
     const at::Tensor *y = tensor(a[4], ok), *h = tensor(a[5], ok);
     Rows yr, hr;
-    if (!ok || wants_graph({n.x, n.weight, n.residual}) || !rows_of(y, n.kind, n.device, n.T, n.D, yr) ||
+    if (!ok || wants_graph({n.x, n.weight, n.residual, y, h}) || !rows_of(y, n.kind, n.device, n.T, n.D, yr) ||
         !rows_of(h, n.kind, n.device, n.T, n.D, hr) || (yr.p && yr.p == hr.p))
         Py_RETURN_NONE;
     at::Tensor new_y, new_h;
@@ -183,7 +184,7 @@ PyObject *rms_norm_q8(PyObject *const *a) {
     if (!ok) Py_RETURN_NONE;
     const at::Tensor *h = tensor(a[4], ok);
     Rows hr;
-    if (!ok || wants_graph({n.x, n.weight, n.residual}) || !rows_of(h, n.kind, n.device, n.T, n.D, hr))
+    if (!ok || wants_graph({n.x, n.weight, n.residual, h}) || !rows_of(h, n.kind, n.device, n.T, n.D, hr))
         Py_RETURN_NONE;
     at::Tensor new_h;
     if (!h && n.residual) {
@@ -211,7 +212,7 @@ PyObject *rms_norm_backward(PyObject *const *a) {
     const bool need_dx = a[8] == Py_True, need_dw = a[9] == Py_True;
     const at::Tensor *dy = tensor(a[4], ok), *dh = tensor(a[5], ok), *dx = tensor(a[6], ok), *dw = tensor(a[7], ok);
     Rows dyr, dhr, dxr;
-    if (!ok || !dy || wants_graph({n.x, n.weight, n.residual, dy, dh}) ||
+    if (!ok || !dy || wants_graph({n.x, n.weight, n.residual, dy, dh, need_dx ? dx : nullptr, need_dw ? dw : nullptr}) ||
         !rows_of(dy, n.kind, n.device, n.T, n.D, dyr) || !rows_of(dh, n.kind, n.device, n.T, n.D, dhr) ||
         (need_dx && !rows_of(dx, n.kind, n.device, n.T, n.D, dxr)) ||
         (need_dw && dw && !vector_of(dw, n.weight->scalar_type(), n.device, n.D)) ||

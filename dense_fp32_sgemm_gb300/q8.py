@@ -77,7 +77,11 @@ def _done(result, name):
 
 
 def _written(*tensors):
-    """Graphs that hold a given output will know that it was overwritten."""
+    """Given outputs: one that requires a gradient is refused (what is written has none), and
+    graphs that hold one will know that it was overwritten."""
+    if _graph(*tensors):
+        raise ValueError("a given output has no gradient, and it requires one: leave it out, "
+                         "or call under torch.no_grad()")
     for t in tensors:
         if t is not None and not t.is_inference():
             torch.autograd.graph.increment_version(t)
@@ -203,7 +207,7 @@ def rms_norm_backward(dy, x, weight, residual=None, dh=None, eps: float = 1e-6, 
         if got is not None:
             return _done(got, "sgemm_rms_norm_backward")
     _no_gradient("rms_norm_backward", dy, x, weight, residual, dh)
-    _written(dx, dweight)
+    _written(dx if need_dx else None, dweight if need_dw else None)
     T, D, dev, args, _, dha = _norm_args(x, weight, residual, eps, dh, stream, False, "dh")
     dya = _address(dy, "dy", T, D, x.dtype, dev)
     dxa, dwa = (None, max(D, 1)), None

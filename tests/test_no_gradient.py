@@ -63,3 +63,26 @@ def test_gradient_of_quantised_weights(where):
         with torch.no_grad():
             sg.q8_quantize(w)
         sg.q8_quantize(w.detach())
+
+
+@pytest.mark.parametrize("where", DEVICES)
+def test_given_outputs_that_require_a_gradient(where):
+    dev = on(where)
+    x, w = torch.randn(4, 8, device=dev), torch.ones(8, device=dev)
+    out = torch.zeros(4, 8, device=dev, requires_grad=True)
+    row = torch.zeros(8, device=dev, requires_grad=True)
+    streams = [None] if where == "cpu" else [None, torch.cuda.current_stream()]
+    for s in streams:
+        for refused in (lambda: sg.rms_norm(x, w, y=out, stream=s), lambda: sg.rms_norm(x, w, h=out, stream=s),
+                        lambda: sg.rms_norm(x, w, residual=x, h=out * 1, stream=s),
+                        lambda: sg.rms_norm_q8(x, w, h=out, stream=s),
+                        lambda: sg.gate_q8(x, x, scales=row[:4], stream=s),
+                        lambda: sg.rows_q8(x, scales=row[:4], stream=s),
+                        lambda: sg.rms_norm_backward(x, x, w, dx=out, stream=s),
+                        lambda: sg.rms_norm_backward(x, x, w, dweight=row, stream=s)):
+            with pytest.raises(ValueError, match="given"):
+                refused()
+    assert bool((out == 0).all()) and bool((row == 0).all())
+    if where == "cuda":
+        with torch.no_grad():
+            assert sg.rms_norm(x, w, y=out) is out
