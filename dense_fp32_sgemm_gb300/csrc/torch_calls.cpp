@@ -58,10 +58,12 @@ bool vector_of(const at::Tensor *t, at::ScalarType type, int64_t device, int64_t
     return t && t->is_cuda() && t->get_device() == device && t->scalar_type() == type && t->dim() == 1 &&
            t->size(0) == n && t->is_contiguous();
 }
+// Whether one requires a gradient to be recorded, or carries a tangent of forward-mode
+// differentiation (of the one level that there is).
 bool wants_graph(std::initializer_list<const at::Tensor *> list) {
-    if (!at::GradMode::is_enabled()) return false;
+    const bool records = at::GradMode::is_enabled();
     for (const at::Tensor *t : list)
-        if (t && t->requires_grad()) return true;
+        if (t && ((records && t->requires_grad()) || t->_fw_grad(0).defined())) return true;
     return false;
 }
 // A given output (one that requires a gradient is refused in Python): graphs that hold it will

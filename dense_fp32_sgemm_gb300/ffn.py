@@ -14,6 +14,7 @@ import contextlib
 import ctypes
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 import dense_fp32_sgemm_gb300 as _sg
@@ -66,6 +67,18 @@ def _call(fn, device, stream, *args):
             status = fn(*args, raw)
     if status != 0:
         raise _sg.SgemmError(status, fn.__name__)
+
+
+def _tangents(*tensors):
+    """Whether one of the tensors (or None) carries a tangent of forward-mode differentiation."""
+    if getattr(forward_ad, "_current_level", 0) < 0:  # (outside of all its levels)
+        return False
+    return any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
+def _no_tangent(what, *tensors):
+    if _tangents(*tensors):
+        raise ValueError(f"{what} has no forward-mode derivative, and a tensor carries a tangent")
 
 
 def _raw_stream(index):

@@ -19,7 +19,7 @@ from torch.autograd.function import once_differentiable
 import dense_fp32_sgemm_gb300 as _sg
 
 from . import _build
-from .ffn import _TYPES, _call, _empty, _matrix, _type_of
+from .ffn import _TYPES, _call, _empty, _matrix, _no_tangent, _tangents, _type_of
 
 _Q8_MOST_K = 131071
 
@@ -79,6 +79,7 @@ def _done(result, name):
 def _written(*tensors):
     """Given outputs: one that requires a gradient is refused (what is written has none), and
     graphs that hold one will know that it was overwritten."""
+    _no_tangent("a given output", *tensors)
     if _graph(*tensors):
         raise ValueError("a given output has no gradient, and it requires one: leave it out, "
                          "or call under torch.no_grad()")
@@ -100,6 +101,7 @@ def _graph(*tensors):
 
 
 def _no_gradient(what, *tensors):
+    _no_tangent(what, *tensors)
     if _graph(*tensors):
         raise ValueError(f"{what} has no gradient, and an input requires one: call it under "
                          "torch.no_grad()")
@@ -141,6 +143,7 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, y=None, h=None, stream
         got = (_calls or _load_calls()).rms_norm(x, weight, residual, eps, y, h)
         if got is not None:
             return _done(got, "sgemm_rms_norm")
+    _no_tangent("rms_norm", x, weight, residual)
     if _graph(x, weight, residual):
         if y is not None or h is not None:
             raise ValueError("a given y or h has no gradient, and an input requires one: "
@@ -334,7 +337,7 @@ class Q8Matrix:
         rms_norm_q8, gate_q8 and rows_q8 return them.  The sums are exact.  Returns y
         (allocated when not given).  No gradient goes through it: scales that require one,
         the matrix's own too, are refused."""
-        if self.scales.requires_grad:
+        if self.scales.requires_grad or _tangents(self.scales):
             _no_gradient("Q8Matrix.matmul", self.scales)
         if stream is None:
             got = (_calls or _load_calls()).q8_matmul(x, x_scales, y, self._weights)

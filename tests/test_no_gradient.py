@@ -86,3 +86,45 @@ def test_given_outputs_that_require_a_gradient(where):
     if where == "cuda":
         with torch.no_grad():
             assert sg.rms_norm(x, w, y=out) is out
+
+
+def tangents(dev):
+    """name -> a call with a tensor that carries a tangent, and the same without one."""
+    x, w = torch.randn(4, 8, device=dev), torch.ones(8, device=dev)
+    calls = {}
+    for which in range(3):
+        def norm(call, which=which):
+            def run(wrap):
+                t = [x, w, x.clone()]
+                t[which] = wrap(t[which])
+                return call(*t)
+            return run
+        calls[f"norm {which}"] = norm(lambda a, b, r: sg.rms_norm(a, b, residual=r))
+        calls[f"norm_q8 {which}"] = norm(lambda a, b, r: sg.rms_norm_q8(a, b, residual=r))
+        calls[f"backward {which}"] = norm(lambda a, b, r: sg.rms_norm_backward(x, a, b, residual=r))
+    calls["backward dy"] = lambda wrap: sg.rms_norm_backward(wrap(x), x, w)
+    calls["backward dh"] = lambda wrap: sg.rms_norm_backward(x, x, w, dh=wrap(x))
+    calls["gate g"] = lambda wrap: sg.gate_q8(wrap(x), x)
+    calls["gate u"] = lambda wrap: sg.gate_q8(x, wrap(x))
+    calls["rows"] = lambda wrap: sg.rows_q8(wrap(x))
+    calls["quantize"] = lambda wrap: sg.q8_quantize(wrap(x))
+    calls["given y"] = lambda wrap: sg.rms_norm(x, w, y=wrap(torch.empty_like(x)))
+    if dev == "cuda":
+        q, s = sg.rows_q8(x)
+        ws = torch.ones(4, device=dev)
+        m = sg.Q8Matrix(q, ws)
+        calls["product"] = lambda wrap: m.matmul(q, wrap(s))
+        calls["product, scales"] = lambda wrap: sg.Q8Matrix(q, wrap(ws)).matmul(q, s)
+    return calls
+
+
+@pytest.mark.parametrize("where", DEVICES)
+def test_tangents_of_forward_mode(where):
+    dev = on(where)
+    for name, call in tangents(dev).items():
+        for grad in (True, False):
+            with forward_ad.dual_level(), torch.set_grad_enabled(grad):
+                with pytest.raises(ValueError, match="forward-mode"):
+                    call(lambda t: forward_ad.make_dual(t, torch.ones_like(t)))
+                if where == "cuda":
+                    call(lambda t: t)  # (a level alone is no tangent)
