@@ -129,8 +129,9 @@ def ffn_forward(x, w_gate, w_up, w_down, y=None, activation: int = 0, saved=None
     Where one of the matrices requires a gradient, y is part of the graph: its
     gradient goes through ffn_backward(), with ``saved`` if given (one for each
     forward pass that waits for its gradient), else from the inputs anew.  A given
-    y is refused then.
+    y is refused then, and so are tensors with a tangent of forward-mode differentiation.
     """
+    _no_tangent("ffn_forward", x, w_gate, w_up, w_down, y)
     if torch.is_grad_enabled() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad
                                     or w_down.requires_grad):
         if y is not None:
@@ -236,6 +237,7 @@ class W4Matrix:
         read once per 16 rows, 8 with float32).  Returns y (allocated when not given).
         No gradient goes through it: where x requires one, a backward pass through y
         raises NotImplementedError, and a given y is refused."""
+        _no_tangent("W4Matrix.matvec", x, y, self.scales)
         if x.requires_grad and torch.is_grad_enabled():
             if y is not None:
                 raise ValueError("a given y has no gradient, and x requires one: "

@@ -128,3 +128,32 @@ def test_tangents_of_forward_mode(where):
                     call(lambda t: forward_ad.make_dual(t, torch.ones_like(t)))
                 if where == "cuda":
                     call(lambda t: t)  # (a level alone is no tangent)
+
+
+@pytest.mark.parametrize("where", DEVICES)
+@pytest.mark.parametrize("which", range(5))
+def test_tangents_through_the_gated_block(where, which):
+    dev = on(where)
+    t = [torch.randn(3, 8, device=dev), torch.randn(8, 16, device=dev), torch.randn(8, 16, device=dev),
+         torch.randn(16, 8, device=dev), torch.empty(3, 8, device=dev)]
+    with forward_ad.dual_level():
+        if where == "cuda":
+            sg.ffn_forward(*t)
+        t[which] = forward_ad.make_dual(t[which], torch.ones_like(t[which]))
+        with pytest.raises(ValueError, match="forward-mode"):
+            sg.ffn_forward(*t)
+
+
+@gpu
+@pytest.mark.parametrize("which", range(3))
+def test_tangents_through_products_with_4_bit_weights(which):
+    on("cuda")
+    x, y = torch.randn(2, 64, device="cuda"), torch.empty(2, 16, device="cuda")
+    m = sg.w4_quantize(torch.randn(64, 16, device="cuda"), group=32)
+    with forward_ad.dual_level():
+        m.matvec(x, y)
+        t = [x, y, m.scales]
+        t[which] = forward_ad.make_dual(t[which], torch.ones_like(t[which]))
+        m = sg.W4Matrix(m.qweight, t[2], 64, 32, zeros=m.zeros)
+        with pytest.raises(ValueError, match="forward-mode"):
+            m.matvec(*t[:2])
