@@ -214,13 +214,16 @@ sgemm_status_t sgemm_rms_norm_backward(int64_t T, int64_t D, int type, const voi
     p.dx = dx; p.lddx = lddx;
     p.dw = dweight;
     p.device = dev.index;
-    p.parts = norm_grad_parts(p, type, vec, dev.num_sms);
-    void *w = nullptr;
-    const size_t stats = up(T * (int64_t)sizeof(float2), 256);
-    s = op_workspace(st, stats + (size_t)p.parts * D * sizeof(float), &w);
-    if (s != SGEMM_OK) return s;
-    p.stats = static_cast<float2 *>(w);
-    p.partials = reinterpret_cast<float *>(static_cast<char *>(w) + stats);
+    const NormGradSpace space = norm_grad_space(p, type, vec, dev.num_sms);
+    p.parts = space.parts;
+    if (dweight) {
+        void *w = nullptr;
+        const size_t stats = space.stats ? up(T * (int64_t)sizeof(float), 256) : 0;
+        s = op_workspace(st, stats + (size_t)p.parts * D * sizeof(float), &w);
+        if (s != SGEMM_OK) return s;
+        p.stats = space.stats ? static_cast<float *>(w) : nullptr;
+        p.partials = reinterpret_cast<float *>(static_cast<char *>(w) + stats);
+    }
     return status(launch_norm_grad(p, type, vec, dev.num_sms, st));
 }
 

@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kMostThreads, 1) norm_grad_wide_kernel(const N
         }
     }
     const float2 st = row_stats(group_sum2(sums, &s_sum, 0, blockDim.x >> 5), p.cols, p.eps);
-    if (tid == 0) p.stats[row] = st;
+    if (tid == 0 && p.stats) p.stats[row] = st.x;
     if (!p.dx) return;
     for (int c = tid * V; c - lane * V < p.cols; c += step) {
         const int n = p.cols - c;
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(256) norm_grad_columns_kernel(const NormGradPa
     for (long long row = blockIdx.y; row < p.rows; row += p.parts) {
         float h = load_as_float(p.x, TYPE, row * p.ldx + c);
         if (p.r) h += load_as_float(p.r, TYPE, row * p.ldr + c);
-        sum = fmaf(load_as_float(p.dy, TYPE, row * p.lddy + c), h * p.stats[row].x, sum);
+        sum = fmaf(load_as_float(p.dy, TYPE, row * p.lddy + c), h * p.stats[row], sum);
     }
     p.partials[(long long)blockIdx.y * p.cols + c] = sum;
 }
@@ -453,9 +453,10 @@ cudaError_t launch_form(const NormGradParams &p, int num_sms, cudaStream_t strea
 
 }  // namespace
 
-int norm_grad_parts(const NormGradParams &p, int type, bool vec, int num_sms) {
+NormGradSpace norm_grad_space(const NormGradParams &p, int type, bool vec, int num_sms) {
+    if (!p.dw) return {0, false};
     const Shape s = shape(p.rows, p.cols, type, vec, p.r, num_sms);
-    return s.depth ? s.ctas : (int)std::min<long long>(p.rows, kWideParts);
+    return {s.depth ? s.ctas : (int)std::min<long long>(p.rows, kWideParts), s.depth == 0};
 }
 
 cudaError_t launch_norm_grad(const NormGradParams &p, int type, bool vec, int num_sms,

@@ -53,13 +53,18 @@ struct NormGradParams {
     long long lddx;
     void *dw;                 // null: not wanted
     float *partials;          // parts x cols, sums of some rows each
-    float2 *stats;            // rows: r and r^2 mean(n h), where rows do not fit registers
+    float *stats;             // rows: r, where rows do not fit registers
     int parts;
     int device;
     int stages;               // (set by the launch) rows on their way
 };
-// Partial rows of the weight's gradient.
-int norm_grad_parts(const NormGradParams &p, int type, bool vec, int num_sms);
+// What a gradient with dw needs beside its operands (one without: nothing): partial rows of dw,
+// and whether the rows' statistics are kept.
+struct NormGradSpace {
+    int parts;
+    bool stats;
+};
+NormGradSpace norm_grad_space(const NormGradParams &p, int type, bool vec, int num_sms);
 cudaError_t launch_norm_grad(const NormGradParams &p, int type, bool vec, int num_sms,
                              cudaStream_t stream);
 

@@ -5,7 +5,7 @@
  * the weights are brought into 8 bits for.
  *
  * Conventions are those of sgemm_ffn.h, its workspace of a device and stream among them
- * (of sgemm_rms_norm_backward and sgemm_q8_matmul here; a call's first use on a
+ * (of sgemm_rms_norm_backward with dweight and of sgemm_q8_matmul here; a call's first use on a
  * stream may allocate, so run it once before capturing it; graphs captured on one
  * stream share its workspace and run one after the other, not at once).  Element types and
  * activations are the constants declared there.  All results are bitwise reproducible.
