@@ -33,7 +33,7 @@ HEADERS = ["device_common.cuh", "kernels.h", "kernels_3xtf32.h", "plan.h",
 PUBLIC_HEADERS = ["sgemm.h", "sgemm_probe.h", "sgemm_ffn.h", "sgemm_q8.h"]
 
 # The usual calls on torch tensors, a Python extension beside the library (not made where
-# there is no torch for CUDA).
+# there is no torch for CUDA; calls take the way through Python then).
 CALLS_SOURCE = "torch_calls.cpp"
 CALLS_PATH = os.path.join(BUILD, "_torch_calls.so")
 
@@ -120,6 +120,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     digest = _digest()
     if (not force and os.path.exists(LIB_PATH) and os.path.exists(stamp)
             and open(stamp).read().strip() == digest):
+        if _torch() and not os.path.exists(CALLS_PATH):
+            _link_calls(_compile_calls())
         return LIB_PATH
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
         calls = pool.submit(_compile_calls)

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import contextlib
 import importlib.util
+import os
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -58,10 +59,22 @@ def _empty_codes(rows, cols, device, stream):
 _calls = None
 
 
+class _NoCalls:
+    """In place of the extension where the library was built without it: no call is usual."""
+
+    def _more(*args):
+        return None
+
+    rms_norm = rms_norm_q8 = rms_norm_backward = gate_q8 = q8_matmul = staticmethod(_more)
+
+
 def _load_calls():
     """The extension, once the library is there."""
     global _calls
     _sg.library()
+    if not os.path.exists(_build.CALLS_PATH):
+        _calls = _NoCalls
+        return _calls
     spec = importlib.util.spec_from_file_location("_torch_calls", _build.CALLS_PATH)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
