@@ -130,11 +130,13 @@ bool q8_plan(Q8GemmParams &p, bool &pair, int num_sms) {
 
 using namespace sgemm;
 
+// (No exception leaves an entry point.  There is one, of a host without memory for the library's own
+// state, which is made before anything is queued.)
 extern "C" {
 
 sgemm_status_t sgemm_rms_norm(int64_t T, int64_t D, int type, const void *x, int64_t ldx,
                               const void *residual, int64_t ldr, const void *weight, int weight_type,
-                              double eps, void *h, int64_t ldh, void *y, int64_t ldy, void *stream) {
+                              double eps, void *h, int64_t ldh, void *y, int64_t ldy, void *stream) try {
     const NormArgs a{T, D, type, x, ldx, residual, ldr, weight, weight_type, eps, h, ldh};
     sgemm_status_t s = check_norm(a);
     if (s != SGEMM_OK) return s;
@@ -150,12 +152,14 @@ sgemm_status_t sgemm_rms_norm(int64_t T, int64_t D, int type, const void *x, int
     p.y = y; p.ldy = ldy;
     return status(launch_norm(p, type, false, norm_vec(a) && rows16(y, ldy, T, type), dev.num_sms,
                               static_cast<cudaStream_t>(stream)));
+} catch (...) {
+    return SGEMM_ERR_ALLOC;
 }
 
 sgemm_status_t sgemm_rms_norm_q8(int64_t T, int64_t D, int type, const void *x, int64_t ldx,
                                  const void *residual, int64_t ldr, const void *weight,
                                  int weight_type, double eps, void *h, int64_t ldh, int8_t *q,
-                                 int64_t ldq, float *scales, void *stream) {
+                                 int64_t ldq, float *scales, void *stream) try {
     const NormArgs a{T, D, type, x, ldx, residual, ldr, weight, weight_type, eps, h, ldh};
     sgemm_status_t s = check_norm(a);
     if (s != SGEMM_OK) return s;
@@ -176,12 +180,14 @@ sgemm_status_t sgemm_rms_norm_q8(int64_t T, int64_t D, int type, const void *x, 
     p.scales = scales;
     return status(launch_norm(p, type, true, norm_vec(a) && p.q_vec,
                               dev.num_sms, static_cast<cudaStream_t>(stream)));
+} catch (...) {
+    return SGEMM_ERR_ALLOC;
 }
 
 sgemm_status_t sgemm_rms_norm_backward(int64_t T, int64_t D, int type, const void *x, int64_t ldx,
                                        const void *residual, int64_t ldr, const void *weight, int weight_type, double eps,
                                        const void *dy, int64_t lddy, const void *dh, int64_t lddh,
-                                       void *dx, int64_t lddx, void *dweight, void *stream) {
+                                       void *dx, int64_t lddx, void *dweight, void *stream) try {
     const NormArgs a{T, D, type, x, ldx, residual, ldr, weight, weight_type, eps, nullptr, 0};
     sgemm_status_t s = check_norm(a);
     if (s != SGEMM_OK) return s;
@@ -225,11 +231,13 @@ sgemm_status_t sgemm_rms_norm_backward(int64_t T, int64_t D, int type, const voi
         p.partials = reinterpret_cast<float *>(static_cast<char *>(w) + stats);
     }
     return status(launch_norm_grad(p, type, vec, dev.num_sms, st));
+} catch (...) {
+    return SGEMM_ERR_ALLOC;
 }
 
 sgemm_status_t sgemm_q8_gate(int64_t T, int64_t F, int type, int activation, const void *g,
                              int64_t ldg, const void *u, int64_t ldu, int8_t *q, int64_t ldq,
-                             float *scales, void *stream) {
+                             float *scales, void *stream) try {
     if (T < 0 || F < 0 || !type_ok(type)) return SGEMM_ERR_INVALID_ARG;
     if (u && activation != SGEMM_GATE_SILU && activation != SGEMM_GATE_GELU &&
         activation != SGEMM_GATE_RELU)
@@ -256,10 +264,12 @@ sgemm_status_t sgemm_q8_gate(int64_t T, int64_t F, int type, int activation, con
     p.scales = scales;
     const bool vec = rows16(g, ldg, T, type) && rows16(u, ldu, T, type) && p.q_vec;
     return status(launch_gate_q8(p, type, vec, dev.num_sms, static_cast<cudaStream_t>(stream)));
+} catch (...) {
+    return SGEMM_ERR_ALLOC;
 }
 
 sgemm_status_t sgemm_q8_quantize(int64_t N, int64_t K, int type, const void *W, int64_t ldw, int8_t *q,
-                                 int64_t ldq, float *scales, void *stream) {
+                                 int64_t ldq, float *scales, void *stream) try {
     if (N < 0 || K < 0 || !type_ok(type)) return SGEMM_ERR_INVALID_ARG;
     if (ldw < at_least_one(N) || ldq < at_least_one(K)) return SGEMM_ERR_INVALID_ARG;
     if (N > kMaxSize || K > kMaxSize) return SGEMM_ERR_UNSUPPORTED;
@@ -276,11 +286,13 @@ sgemm_status_t sgemm_q8_quantize(int64_t N, int64_t K, int type, const void *W, 
     p.q = q; p.ldq = ldq;
     p.scales = scales;
     return status(launch_q8_quantize(p, static_cast<cudaStream_t>(stream)));
+} catch (...) {
+    return SGEMM_ERR_ALLOC;
 }
 
 sgemm_status_t sgemm_q8_matmul(int64_t M, int64_t N, int64_t K, int type, const int8_t *x, int64_t ldx,
                                const float *x_scales, const int8_t *w, int64_t ldw,
-                               const float *w_scales, void *y, int64_t ldy, void *stream) {
+                               const float *w_scales, void *y, int64_t ldy, void *stream) try {
     if (M < 0 || N < 0 || K < 0 || !type_ok(type)) return SGEMM_ERR_INVALID_ARG;
     if (ldx < at_least_one(K) || ldw < at_least_one(K) || ldy < at_least_one(N)) return SGEMM_ERR_INVALID_ARG;
     if (M > kMaxSize || N > kMaxSize || K > kMaxQ8K) return SGEMM_ERR_UNSUPPORTED;
@@ -365,6 +377,8 @@ sgemm_status_t sgemm_q8_matmul(int64_t M, int64_t N, int64_t K, int type, const 
     if (launch_q8_widen(x, ldx, (int)M, (int)K, wide, ld_x, dev.num_sms, st) != cudaSuccess)
         return SGEMM_ERR_LAUNCH;
     return status(launch_q8_gemm(map_w, map_x, p, type, pair, st));
+} catch (...) {
+    return SGEMM_ERR_ALLOC;
 }
 
 }  // extern "C"
