@@ -13,10 +13,10 @@
 // (calls from Python with cold inputs and dh, and in two readings: 1388 x 10504 BF16 63 us, 88;
 // 2048 x 16384 101, 182; 1388 x 10504 off 16 bytes 89, 159).
 //
-// 8192 x 2048 BF16 with dh: 38 us and 5 for the partial rows (its bytes take 20).  Bound:
+// 8192 x 2048 BF16 with residual and dh: 39 us and 5 for the partial rows (its bytes take 25).  Bound:
 // latency, one CTA of 512 threads an SM, which the weight's gradient leaves no registers beside
 // (three of 256 with it in shared memory took 1 us more, 4096 x 4096 5).
-// Rows off 16 bytes: 1023 x 1025 FP32 11 and 5 us.
+// Rows off 16 bytes: 1023 x 1025 FP32 12 and 5 us.
 #include <algorithm>
 #include <atomic>
 

@@ -7,7 +7,8 @@
 // changes them.  x lies in shared memory, zeros from K on.  The loads of three
 // items are under way at a time.  Bound: HBM (1 x 4096 x 12288 11.4 us, 4.4 TB/s of the copy's
 // 6.7, of which a launch and its first loads are 3; 1 x 8192 x 28672 44 us, 5.4 TB/s); from five
-// rows on the multiplications (8 x 8192 x 8192 26 us, 2.5 TB/s).
+// rows on the multiplications too (8 x 4096 x 4096 11.3 us, 1.5 TB/s; larger matrices go to the tensor
+// cores then).
 #include <algorithm>
 #include <atomic>
 

@@ -87,8 +87,8 @@ __device__ __forceinline__ double gate_exact(float g, float u) {
 
 enum : int { kRowNorm, kRowNormQ8, kRowGateQ8 };  // what a row becomes
 
-// A thread's pieces of a row and its registers.  The norm takes two pieces (of 8192 x 8191
-// FP16 108 us, with four 135: fewer warps); what leaves in 8 bits, whose threads have more to
+// A thread's pieces of a row and its registers.  The norm takes two pieces (of 8192 x 8192
+// FP16 55 us, with four 64: fewer warps; 8192 x 2048 BF16 with its residual 24 and 28); what leaves in 8 bits, whose threads have more to
 // do for every row, four (the gate of 4096 x 12288 96 us, with two, which leave one CTA of
 // 768 threads an SM, 132).
 constexpr int row_pieces(int op) { return op == kRowNorm ? 2 : 4; }

@@ -16,8 +16,9 @@
  *
  * round() is to nearest, ties to even; codes lie in -127 .. 127.  The codes are
  * those of exact arithmetic: an element too near a border between two codes for
- * 32 bits is decided with about 48 or 53 bits.  A row with an infinity, a NaN
- * or an element beyond FP32 has the scale NaN and codes of zero.
+ * 32 bits, or not finite in them, is decided with about 48 or 53 bits.  A row with an
+ * infinity, a NaN or an element (in the norm: of h too) beyond FP32 has the scale NaN and
+ * codes of zero.
  */
 #ifndef GB300_SGEMM_Q8_H
 #define GB300_SGEMM_Q8_H
@@ -41,7 +42,8 @@ extern "C" {
  * is taken of the sum in 32 bits, before that rounding.  h may be x or residual
  * itself, and so may y (same address and leading dimension), but not both.
  * weight: D elements of weight_type, which is `type` or SGEMM_TYPE_F32.
- * Squares are summed in FP32: where their sum passes its range, y is zero.
+ * Squares are summed in FP32: where their sum passes its range, y is zero.  eps counts as
+ * rounded to FP32.
  * T == 0 or D == 0: nothing is done.
  * Returns SGEMM_ERR_INVALID_ARG for a negative size, a leading dimension below
  * D, a NULL or misaligned pointer, an unknown type, another weight_type or an
@@ -118,8 +120,8 @@ SGEMM_API sgemm_status_t sgemm_q8_quantize(int64_t N, int64_t K, int type, const
  *
  * x: M x K (ldx >= K), w: N x K (ldw >= K), 8-bit integers, all 256 values of them;
  * x_scales: M floats; w_scales: N floats; y: M x N of `type` (ldy >= N).  The
- * sum is exact, and is rounded to FP32 once; its two scalings and y's rounding
- * follow.  16-byte aligned w whose rows lie a multiple of 16 bytes apart is read in
+ * sum is exact, and is rounded to FP32 once; its two scalings (x's first, in FP32) and y's
+ * rounding follow.  16-byte aligned w whose rows lie a multiple of 16 bytes apart is read in
  * place, other w through a copy made by every call.
  * M == 0 or N == 0: nothing is done.  K == 0: y = 0.
  * Returns SGEMM_ERR_INVALID_ARG for a negative size, a leading dimension below
