@@ -345,6 +345,10 @@ class Q8Matrix:
         self.qweight, self.scales, self.dtype, self.device = qweight, scales, dtype, dev
         self._weights = (self.N, self.K, _TYPES[dtype], w, ldw, s, dev.index)
 
+    def __reduce__(self):
+        # A copy (copy.deepcopy, pickle) has tensors of its own: their addresses are taken anew.
+        return Q8Matrix, (self.qweight, self.scales, self.dtype)
+
     def matmul(self, x, x_scales, y=None, stream=None):
         """y[m] = x_scales[m] * (x[m] @ W) for M x K codes x (int8) and M scales, as
         rms_norm_q8, gate_q8 and rows_q8 return them.  The sums are exact.  Returns y

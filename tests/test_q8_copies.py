@@ -1,0 +1,40 @@
+"""Copies of a matrix of 8-bit weights use tensors of their own, not the memory of the one
+that they were made from."""
+import copy
+import io
+import pickle
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import dense_fp32_sgemm_gb300 as sg
+
+
+def saved(m):
+    file = io.BytesIO()
+    torch.save(m, file)
+    file.seek(0)
+    return torch.load(file, weights_only=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("make", [copy.copy, copy.deepcopy, lambda m: pickle.loads(pickle.dumps(m)), saved])
+def test_copies(make):
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    sg.build()
+    for K in (64, 70):  # (70: rows off 16 bytes were laid out anew)
+        gen = torch.Generator("cuda").manual_seed(K)
+        w = torch.randint(-127, 128, (33, K), generator=gen, device="cuda").to(torch.int8)
+        x = torch.randint(-127, 128, (20, K), generator=gen, device="cuda").to(torch.int8)
+        xs = torch.ones(20, device="cuda")
+        m = sg.Q8Matrix(w, torch.rand(33, generator=gen, device="cuda"), dtype=torch.float32)
+        n = make(m)
+        # (what the calls read, before one is made)
+        assert n._weights[3] == n.qweight.data_ptr() and n._weights[5] == n.scales.data_ptr()
+        assert (n.N, n.K, n.dtype, n.device) == (m.N, m.K, m.dtype, m.device)
+        want = m.matmul(x, xs)
+        assert torch.equal(n.matmul(x, xs), want)
+        n.scales.mul_(2)
+        assert torch.equal(n.matmul(x, xs), 2 * want)
