@@ -322,7 +322,7 @@ class Q8Matrix:
 
     qweight: N x K int8, a row the weights of one channel (output column).  scales: N
     float32.  ``dtype`` is the type of the products.  The tensors are checked once and
-    kept; a qweight whose rows do not start on 16 bytes is copied into rows that do
+    kept (again where their memory is another than it was); a qweight whose rows do not start on 16 bytes is copied into rows that do
     (the copy is waited for, so that products may run on any stream).
     """
 
@@ -345,6 +345,11 @@ class Q8Matrix:
         self.qweight, self.scales, self.dtype, self.device = qweight, scales, dtype, dev
         self._weights = (self.N, self.K, _TYPES[dtype], w, ldw, s, dev.index)
 
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        if name in ("qweight", "scales", "dtype"):
+            super().__setattr__("_weights", (0, 0, 0, -1, 0, -1, 0))  # (no tensors' addresses)
+
     def __reduce__(self):
         # A copy (copy.deepcopy, pickle) has tensors of its own: their addresses are taken anew.
         return Q8Matrix, (self.qweight, self.scales, self.dtype)
@@ -356,6 +361,9 @@ class Q8Matrix:
         the matrix's own too, are refused."""
         if self.scales.requires_grad or _tangents(self.scales):
             _no_gradient("Q8Matrix.matmul", self.scales)
+        if self._weights[3] != self.qweight.data_ptr() or self._weights[5] != self.scales.data_ptr():
+            # (tensors put in the place of these, or a module's that was moved)
+            self.__init__(self.qweight, self.scales, self.dtype)
         if stream is None:
             got = (_calls or _load_calls()).q8_matmul(x, x_scales, y, self._weights)
             if got is not None:

@@ -38,3 +38,35 @@ def test_copies(make):
         assert torch.equal(n.matmul(x, xs), want)
         n.scales.mul_(2)
         assert torch.equal(n.matmul(x, xs), 2 * want)
+
+
+@pytest.mark.gpu
+def test_tensors_that_move_and_tensors_put_in_their_place():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    sg.build()
+    x, xs = torch.ones(20, 64, dtype=torch.int8, device="cuda"), torch.ones(20, device="cuda")
+    weight = torch.nn.Parameter(torch.ones(33, 64, dtype=torch.int8, device="cuda"), requires_grad=False)
+    scales = torch.nn.Parameter(torch.ones(33, device="cuda"), requires_grad=False)
+    m = sg.Q8Matrix(weight, scales, dtype=torch.float32)
+    keep = [weight.data, scales.data]  # (what was read before is there still)
+    for stream in (None, torch.cuda.current_stream()):
+        weight.data = torch.full_like(keep[0], 2)  # as a module's to() does
+        assert bool((m.matmul(x, xs, stream=stream) == 128).all())
+        scales.data = torch.full_like(keep[1], 0.5)
+        assert bool((m.matmul(x, xs, stream=stream) == 64).all())
+        m.scales = torch.full_like(keep[1], 3)
+        assert bool((m.matmul(x, xs, stream=stream) == 384).all())
+        m.qweight, m.scales = weight, scales
+        weight.data, scales.data = keep
+        assert bool((m.matmul(x, xs, stream=stream) == 64).all())
+    m.scales = m.scales[:5]
+    with pytest.raises(ValueError, match="scales"):
+        m.matmul(x, xs)
+    m.scales = scales
+    assert bool((m.matmul(x, xs) == 64).all())
+    m.dtype = torch.bfloat16
+    assert m.matmul(x, xs).dtype == torch.bfloat16
+    m.scales = torch.ones(33)
+    with pytest.raises(ValueError, match="CUDA device"):
+        m.matmul(x, xs)
