@@ -6,7 +6,7 @@ of 8-bit integers).
 Argument checks and marshalling only; all arithmetic runs in the library's
 CUDA kernels (include/sgemm_q8.h).  Streams, new outputs and errors are as in
 ffn.py.  Graphs captured on one stream share that stream's workspace: they may be
-replayed one after the other, not at once.
+replayed one after the other, not at once, nor beside other calls on that stream.
 """
 from __future__ import annotations
 
@@ -317,6 +317,9 @@ def rows_q8(x, q=None, scales=None, stream=None):
     return q, scales
 
 
+_UNCHECKED = (0, 0, 0, -1, 0, -1, 0)  # in place of a Q8Matrix's addresses: no tensor's
+
+
 class Q8Matrix:
     """A K x N matrix of 8-bit weights, W[k][n] = scales[n] * qweight[n][k].
 
@@ -348,11 +351,11 @@ class Q8Matrix:
     def __setattr__(self, name, value):
         super().__setattr__(name, value)
         if name in ("qweight", "scales", "dtype"):
-            super().__setattr__("_weights", (0, 0, 0, -1, 0, -1, 0))  # (no tensors' addresses)
+            super().__setattr__("_weights", _UNCHECKED)
 
-    def __reduce__(self):
-        # A copy (copy.deepcopy, pickle) has tensors of its own: their addresses are taken anew.
-        return Q8Matrix, (self.qweight, self.scales, self.dtype)
+    def __getstate__(self):
+        # A copy (copy.deepcopy, pickle) has tensors of its own: its first product checks them.
+        return {**self.__dict__, "_weights": _UNCHECKED}
 
     def matmul(self, x, x_scales, y=None, stream=None):
         """y[m] = x_scales[m] * (x[m] @ W) for M x K codes x (int8) and M scales, as
@@ -361,26 +364,28 @@ class Q8Matrix:
         the matrix's own too, are refused."""
         if self.scales.requires_grad or _tangents(self.scales):
             _no_gradient("Q8Matrix.matmul", self.scales)
-        if self._weights[3] != self.qweight.data_ptr() or self._weights[5] != self.scales.data_ptr():
+        all_weights = self._weights  # (once: another thread may replace a tensor)
+        if all_weights[3] != self.qweight.data_ptr() or all_weights[5] != self.scales.data_ptr():
             # (tensors put in the place of these, or a module's that was moved)
-            self.__init__(self.qweight, self.scales, self.dtype)
+            Q8Matrix.__init__(self, self.qweight, self.scales, self.dtype)
+            all_weights = self._weights
         if stream is None:
-            got = (_calls or _load_calls()).q8_matmul(x, x_scales, y, self._weights)
+            got = (_calls or _load_calls()).q8_matmul(x, x_scales, y, all_weights)
             if got is not None:
                 return _done(got, "sgemm_q8_matmul")
         _no_gradient("Q8Matrix.matmul", x_scales, y)
         if x.dim() != 2:
             raise ValueError("x must be 2-D")
         M = x.shape[0]
+        N, K, kind, *weights, _ = all_weights
         if y is None:
-            y = _empty(M, self.N, self.dtype, self.device, stream)
+            y = _empty(M, N, self.dtype, self.device, stream)
         else:
             _written(y)
-        xa = _address(x, "x", M, self.K, torch.int8, self.device)
+        xa = _address(x, "x", M, K, torch.int8, self.device)
         sa = _vector(x_scales, "x_scales", M, torch.float32, self.device)
-        N, K, kind, *weights, _ = self._weights
         _call(_sg.library().sgemm_q8_matmul, self.device, stream, M, N, K, kind, *xa, sa, *weights,
-              *_address(y, "y", M, self.N, self.dtype, self.device))
+              *_address(y, "y", M, N, self.dtype, self.device))
         return y
 
 

@@ -30,9 +30,11 @@ def test_copies(make):
         x = torch.randint(-127, 128, (20, K), generator=gen, device="cuda").to(torch.int8)
         xs = torch.ones(20, device="cuda")
         m = sg.Q8Matrix(w, torch.rand(33, generator=gen, device="cuda"), dtype=torch.float32)
+        m.name = "down"
         n = make(m)
-        # (what the calls read, before one is made)
-        assert n._weights[3] == n.qweight.data_ptr() and n._weights[5] == n.scales.data_ptr()
+        assert type(n) is type(m) and n.name == "down"
+        # (what the calls read, before one is made: nothing, or the copy's own)
+        assert n._weights[3] in (-1, n.qweight.data_ptr()) and n._weights[5] in (-1, n.scales.data_ptr())
         assert (n.N, n.K, n.dtype, n.device) == (m.N, m.K, m.dtype, m.device)
         want = m.matmul(x, xs)
         assert torch.equal(n.matmul(x, xs), want)

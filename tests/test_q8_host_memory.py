@@ -84,7 +84,8 @@ def test_entry_points_return_a_status(tmp_path):
     source, lib = tmp_path / "new.cpp", tmp_path / "new.so"
     source.write_text(SOURCE)
     subprocess.run(["g++", "-shared", "-fPIC", "-O1", "-o", str(lib), str(source)], check=True)
-    env = dict(os.environ, LD_PRELOAD=str(lib), PYTHONPATH=ROOT)
+    preload = " ".join(filter(None, [str(lib), os.environ.get("LD_PRELOAD")]))
+    env = dict(os.environ, LD_PRELOAD=preload, PYTHONPATH=ROOT)
     child = subprocess.run([sys.executable, "-c", CHILD], cwd=ROOT, env=env, capture_output=True, text=True,
                            timeout=300)
     assert child.returncode == 0, child.stderr[-2000:]
